@@ -78,11 +78,21 @@ typedef enum biv_dtype { BIV_BF16 = 0, BIV_F32 = 1 } biv_dtype;
 #define BIV_DEVERR_TIMEOUT 1u /* a bounded wait inside a kernel ran out; the kernel returned */
 #define BIV_DEVERR_INDEX 2u   /* a slot / position / token id read from device memory was out of range */
 #define BIV_DEVERR_GROUP 4u   /* rows declared to share a cache slot did not */
+#define BIV_DEVERR_VALUE 8u   /* a row of probabilities could not be sampled from */
 
 /* Build constants. */
 #define BIV_KV_SPLIT 256      /* fixed KV split of the decode attention ([DVR] para 1) */
 #define BIV_HEAD_DIM 128      /* attention head dimension built */
 #define BIV_ATTN_TILE 128     /* rows of one attention MMA tile ([GUIDE] GQA tile rule) */
+
+/* Activations of biv_gemm_bias_act. */
+typedef enum biv_act {
+    BIV_ACT_NONE = 0,
+    BIV_ACT_RELU = 1,
+    BIV_ACT_GELU = 2,      /* x/2 (1 + erf(x / sqrt 2)) */
+    BIV_ACT_GELU_TANH = 3, /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+    BIV_ACT_SILU = 4       /* x / (1 + e^-x) */
+} biv_act;
 
 /* ------------------------------------------------------------- status */
 const char* biv_status_string(int status);           /* static string, never NULL */
@@ -429,6 +439,126 @@ int biv_swiglu_pack_weights(const void* w_gu, void* w_packed, int F, int K, biv_
 
 /* out[i] = bf16(x[i] + y[i]) over n bf16 elements, n % 8 == 0; out may alias x. */
 int biv_residual_add(const void* x, const void* y, void* out, long long n, biv_stream_t stream);
+
+/* The same GEMM with a projection's usual tail in its epilogue:
+ *   C[m][n] = act(sum_k A[m][k] B[n][k] + bias[n]) + residual[m][n]
+ * in fp32, rounded once to C's type (bf16 or fp32, out_dtype).  The sum is
+ * biv_gemm_nosplitk's, bit for bit, so a row does not depend on M.
+ * A: bf16 [M, K]; B: bf16 [N, K]; bias: bf16 [N] or NULL; residual: bf16
+ * [M, N] or NULL; C: [M, N].  act: a biv_act.  C may be the residual itself
+ * when it is bf16 (x += ...); it must not overlap A, B or bias, nor the
+ * residual in any other way.
+ * Requires what biv_gemm_nosplitk requires, and 16-B aligned bias and
+ * residual; BIV_ERR_VALUE for an unknown act or a forbidden alias.         */
+int biv_gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, void* C,
+                      int out_dtype, int act, int M, int N, int K, biv_stream_t stream);
+
+/* ------------------------------------------------- paged key-value cache
+ * The cache of a server whose requests come and go: K and V pools of
+ * n_pages pages, bf16 [n_pages, Hkv, page_size, hd] each (a page holds
+ * page_size consecutive positions of one request, head-major as the slot
+ * cache), and a table, int32 [n_slots, max_pages]: page_table[s][i] holds
+ * positions [i * page_size, (i + 1) * page_size) of cache slot s.  Entries
+ * past a request's last position are never read (-1 by custom); several
+ * slots may name the same page (a shared prefix).  page_size is 16, 32, 64,
+ * 128 or 256.
+ * A row with position -1 is an empty seat of a padded batch: its table and
+ * pages are not read, nothing is written for it but its row of the output,
+ * and no error bit is raised.  Any other position outside [0, max_pages *
+ * page_size), a slot outside [0, n_slots) or a page id outside [0, n_pages)
+ * raises BIV_DEVERR_INDEX.
+ *
+ * biv_rope_kv_write_paged: biv_rope_kv_write over pages.  The q heads of qkv
+ * (bf16 [W, (Hq + 2 Hkv) hd]) are rotated into q_out (bf16 [W, Hq, hd]); the
+ * k heads are rotated and written, with the v heads, to the pages of
+ * (row_slot[w], row_pos[w]).  Row w = r*K + j is written only if rows_keep is
+ * NULL or j < rows_keep[r]; its q always.  Rows that are written must name
+ * different (page, offset) places.  Unlike biv_rope_kv_write, whose angle is
+ * an fp32 product, the angle pos * theta^(-2i/hd) is taken modulo a full turn
+ * in 64-bit integers, so positions of millions lose nothing; the two agree
+ * to that fp32 product's error.
+ * A row whose position is out of range gets q rotated by that position and
+ * writes no K or V.
+ * Requires hd % 16 == 0, hd <= 256, theta > 1 finite, W % K == 0, 16-B
+ * aligned pointers; BIV_ERR_UNSUPPORTED for another page size.             */
+int biv_rope_kv_write_paged(const void* qkv, void* q_out, void* k_pages, void* v_pages,
+                            const int32_t* page_table, const int32_t* row_slot, const int32_t* row_pos,
+                            const int32_t* rows_keep, int W, int K, int Hq, int Hkv, int hd, int n_slots,
+                            int max_pages, int n_pages, int page_size, float theta, biv_stream_t stream);
+
+/* biv_decode_attn_fixedsplit over pages: for each row w and query head h
+ *   o[w][h] = sum_{j <= row_pos[w]} softmax_j(q[w][h] . k_j / sqrt(hd)) v_j
+ * over the keys of slot row_slot[w], KV head h / (Hq/Hkv).  Keys are split at
+ * absolute multiples of BIV_KV_SPLIT and the splits of a row are joined in
+ * increasing order; a row's result depends only on its own q, its keys and
+ * its position -- not on W, on the other rows of its group, on the page size
+ * or on where its pages lie (the same bits).  The softmax weights meet V as a
+ * sum of two bf16 values (16 bits of each weight), so the rounding of o to
+ * bf16 is the only one that counts.
+ * q, o: bf16 [W, Hq, hd].  Rows [g*rows_per_group, (g+1)*rows_per_group) share
+ * one slot: the single row of a decoding step (1) or the rows of a verify
+ * window, which read the cache once.  A row whose slot differs from its
+ * group's first raises BIV_DEVERR_GROUP; such rows, empty rows, rows out of
+ * range and rows that meet a page id out of range come back as zeros.  Cache
+ * rows up to the group's largest position must hold finite values; what lies
+ * behind it (the rest of a page) may hold anything.
+ * workspace: device memory of at least biv_decode_attn_paged_workspace_size
+ * bytes, 16-B aligned, contents ignored on entry and owned by one call at a
+ * time.  row_slot, row_pos and page_table are read before the wait on the
+ * previous kernel of the library (see the conventions above).
+ * Requires hd == 64 or 128 (else BIV_ERR_UNSUPPORTED, as for another page
+ * size), Hq % Hkv == 0, o not q, 16-B aligned pointers.                    */
+size_t biv_decode_attn_paged_workspace_size(int W, int Hq, int hd, int max_pages, int page_size);
+int biv_decode_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                          const int32_t* row_slot, const int32_t* row_pos, void* o, int W, int rows_per_group,
+                          int Hq, int Hkv, int hd, int n_slots, int max_pages, int n_pages, int page_size,
+                          void* workspace, size_t ws_bytes, biv_stream_t stream);
+
+/* --------------------------------------------- sampled verification
+ * For drafters whose tokens were drawn without the shared noise of
+ * biv_gumbel_argmax: probabilities of the target and the drafter, and uniform
+ * numbers, decide (rejection sampling; the emitted tokens follow the target's
+ * distribution whatever the drafter's).
+ *
+ * biv_softmax: p[r][v] = exp(x[r][v] / T) / sum_u exp(x[r][u] / T), fp32, in a
+ * fixed order that depends on V alone (a row's bits do not depend on R).
+ * A NaN counts as -infinity.  A row of nothing but -infinity gives zeros;
+ * entries of +infinity share the whole mass.  T == 0 puts all of it on the
+ * largest entry (the lowest index among equals), the rule of
+ * biv_gumbel_argmax.  logits: fp32 [R, ld]; probs: fp32 [R, ld_p]; probs may
+ * be logits itself (then ld == ld_p).  Columns past V are neither read nor
+ * written.  Requires 1 <= V <= 2^22, ld, ld_p >= V, T >= 0 finite, 4-B
+ * aligned pointers (16-B alignment of pointers and leading dimensions is
+ * faster).                                                                 */
+int biv_softmax(const float* logits, int R, int V, long long ld, float temperature, float* probs,
+                long long ld_p, biv_stream_t stream);
+
+/* biv_verify_sample: request r drafted draft[r][0..K) and holds K + 1 rows of
+ * target probabilities, target[(r (K+1) + j)][.] being the distribution at
+ * draft j's place (j = K: after the last draft).  Draft j is accepted while
+ *   u_accept[r][j] * q[r][j][d_j] < p[r][j][d_j]       (exact, no division).
+ * With n accepted drafts the next token is drawn with u = u_sample[r]:
+ *   token = min { v : S_v > u * S },  S_v = sum_{i <= v} w_i,  S = S_{V-1}
+ *   w = max(p_n - q_n, 0) if n < K (fp32 difference; w = p_n if that is zero
+ *   everywhere), w = p_K if n == K.
+ * draft_probs NULL: the drafter is certain of its tokens (the n-gram
+ * drafter): q is 1 at d_j and 0 elsewhere, and w is p_n without d_n.
+ *   tokens[r][0..K]  = d_0 .. d_{n-1}, token, then -1
+ *   accept_len[r]    = n + 1 (tokens emitted), new_len[r] = p0[r] + n + 1
+ * Sums are taken in 64-bit integers (units of 2^-60), so they are exact to
+ * 2^-60 per entry and do not depend on any order.  Entries are clamped to
+ * [0, 1] and a NaN counts as 0; u_sample is clamped to [0, 1).  Where no entry
+ * is positive, or the entries sum to 8 or more (no distribution: the units
+ * would overflow), the token is 0 and BIV_DEVERR_VALUE is raised; a draft
+ * outside [0, V) is rejected and raises BIV_DEVERR_INDEX.
+ * target: fp32 [N (K+1), V]; draft_probs: fp32 [N K, V]; draft: int32 [N, K];
+ * u_accept: fp32 [N, K]; u_sample: fp32 [N]; p0: int32 [N]; tokens: int32
+ * [N, K+1]; accept_len, new_len: int32 [N].  Requires N >= 0, 0 <= K <= 1024
+ * (K = 0: plain sampling; draft and u_accept may then be NULL),
+ * 1 <= V <= 2^22.                                                          */
+int biv_verify_sample(const float* target, const float* draft_probs, const int32_t* draft,
+                      const float* u_accept, const float* u_sample, const int32_t* p0, int N, int K, int V,
+                      int32_t* tokens, int32_t* accept_len, int32_t* new_len, biv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(HERE, "libbiv.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "biv.h")
 
 BIV_BF16, BIV_F32 = 0, 1
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+DEVERR_TIMEOUT, DEVERR_INDEX, DEVERR_GROUP, DEVERR_VALUE = 1, 2, 4, 8
 KV_SPLIT, HEAD_DIM, ATTN_TILE = 256, 128, 128
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -24,9 +26,9 @@ _lib = None
 
 
 class BivError(RuntimeError):
-    def __init__(self, fn: str, status: int):
+    def __init__(self, fn: str, status: int, what: str = ""):
         msg = _load().biv_status_string(status).decode()
-        extra = ""
+        extra = f": {what}" if what else ""
         if status == 6:
             extra = f" (cudaError {_load().biv_last_cuda_error()})"
         super().__init__(f"{fn}: status {status}: {msg}{extra}")
@@ -73,6 +75,12 @@ SIGNATURES = {
     "biv_swiglu_pack_weights": (_I, [_P, _P, _I, _I, _P]),
     "biv_rope_kv_write": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "biv_residual_add": (_I, [_P, _P, _P, _LL, _P]),
+    "biv_gemm_bias_act": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "biv_rope_kv_write_paged": (_I, [_P] * 8 + [_I] * 9 + [_F, _P]),
+    "biv_decode_attn_paged_workspace_size": (_SZ, [_I] * 5),
+    "biv_decode_attn_paged": (_I, [_P] * 7 + [_I] * 9 + [_P, _SZ, _P]),
+    "biv_softmax": (_I, [_P, _I, _I, _LL, _F, _P, _LL, _P]),
+    "biv_verify_sample": (_I, [_P] * 6 + [_I] * 3 + [_P] * 4),
 }
 
 
@@ -113,6 +121,33 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _dense(fn: str, *tensors) -> None:
+    """(name, tensor, dtype, shape) of each argument: of that type and shape,
+    dense row-major and on the current CUDA device, where the call's stream
+    is; None passes.  Raises BivError with the status that names the fault."""
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise BivError(fn, 4, f"{name} is {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise BivError(fn, 2, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+        if not t.is_contiguous():
+            raise BivError(fn, 2, f"{name} is not dense row-major")
+    for name, t, _, _ in tensors:
+        if t is not None:
+            _on_device(fn, name, t)
+
+
+def _on_device(fn: str, name: str, t) -> None:
+    i = t.get_device()
+    if i < 0 or i != torch.cuda.current_device():
+        raise BivError(fn, 7, f"{name} is on {t.device}, not on the current CUDA device")
 
 
 # ----------------------------------------------------------------- status
@@ -352,3 +387,89 @@ def biv_rope_kv_write(qkv, q_out, k_cache, v_cache, row_slot, row_pos, Hq: int, 
 
 def biv_residual_add(x, y, out, stream=None) -> None:
     _check("biv_residual_add", _load().biv_residual_add(_ptr(x), _ptr(y), _ptr(out), x.numel(), _stream(stream)))
+
+
+def biv_gemm_bias_act(A, B, C_out, bias=None, residual=None, act: str = "none", stream=None) -> None:
+    """C = act(A B^T + bias) + residual; C_out (bf16 or fp32) may be the bf16 residual itself."""
+    M, K = A.shape
+    N = B.shape[0]
+    out = C_out.dtype
+    if out is not _BF16 and out is not _F32:
+        raise BivError("biv_gemm_bias_act", 4, f"C is {out}, not bfloat16 or float32")
+    if act not in ACTS:
+        raise BivError("biv_gemm_bias_act", 4, f"act {act!r} is none of {', '.join(ACTS)}")
+    _dense("biv_gemm_bias_act", ("A", A, _BF16, (M, K)), ("B", B, _BF16, (N, K)), ("bias", bias, _BF16, (N,)),
+           ("residual", residual, _BF16, (M, N)), ("C", C_out, out, (M, N)))
+    _check("biv_gemm_bias_act", _load().biv_gemm_bias_act(
+        _ptr(A), _ptr(B), _ptr(bias), _ptr(residual), _ptr(C_out), BIV_F32 if out is _F32 else BIV_BF16, ACTS[act],
+        M, N, K, _stream(stream)))
+
+
+def biv_rope_kv_write_paged(qkv, q_out, k_pages, v_pages, page_table, row_slot, row_pos, theta: float, K: int,
+                            rows_keep=None, stream=None) -> None:
+    W, Hq, hd = q_out.shape
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    n_slots, max_pages = page_table.shape
+    pool = (n_pages, Hkv, page_size, hd)
+    _dense("biv_rope_kv_write_paged", ("qkv", qkv, _BF16, (W, (Hq + 2 * Hkv) * hd)), ("q_out", q_out, _BF16, (W, Hq, hd)),
+           ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
+           ("page_table", page_table, _I32, (n_slots, max_pages)), ("row_slot", row_slot, _I32, (W,)),
+           ("row_pos", row_pos, _I32, (W,)), ("rows_keep", rows_keep, _I32, (W // max(K, 1),)))
+    _check("biv_rope_kv_write_paged", _load().biv_rope_kv_write_paged(
+        _ptr(qkv), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(row_slot), _ptr(row_pos),
+        _ptr(rows_keep), W, K, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size, theta, _stream(stream)))
+
+
+def biv_decode_attn_paged_workspace_size(W: int, Hq: int, hd: int, max_pages: int, page_size: int) -> int:
+    return _load().biv_decode_attn_paged_workspace_size(W, Hq, hd, max_pages, page_size)
+
+
+def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o, rows_per_group: int, workspace,
+                          stream=None) -> None:
+    W, Hq, hd = q.shape
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    n_slots, max_pages = page_table.shape
+    pool = (n_pages, Hkv, page_size, hd)
+    _dense("biv_decode_attn_paged", ("q", q, _BF16, (W, Hq, hd)), ("k_pages", k_pages, _BF16, pool),
+           ("v_pages", v_pages, _BF16, pool), ("page_table", page_table, _I32, (n_slots, max_pages)),
+           ("row_slot", row_slot, _I32, (W,)), ("row_pos", row_pos, _I32, (W,)), ("o", o, _BF16, (W, Hq, hd)),
+           ("workspace", workspace, workspace.dtype, workspace.shape))
+    _check("biv_decode_attn_paged", _load().biv_decode_attn_paged(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(row_slot), _ptr(row_pos), _ptr(o), W,
+        rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def biv_softmax(logits, probs, temperature: float, V: int | None = None, stream=None) -> None:
+    """probs[:, :V] = softmax(logits[:, :V] / temperature); rows of either may be strided (stride(1) == 1)."""
+    R, ld = logits.shape
+    V = ld if V is None else V
+    for name, t in (("logits", logits), ("probs", probs)):
+        if t.dtype is not _F32 or t.dim() != 2:
+            raise BivError("biv_softmax", 4, f"{name} is no float32 matrix")
+        if t.shape[0] != R or t.shape[1] < V or (V > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < V):
+            raise BivError("biv_softmax", 2, f"{name} is {tuple(t.shape)} with strides {t.stride()}, V = {V}")
+    _on_device("biv_softmax", "logits", logits)
+    _on_device("biv_softmax", "probs", probs)
+    _check("biv_softmax", _load().biv_softmax(
+        _ptr(logits), R, V, max(logits.stride(0), V), temperature, _ptr(probs), max(probs.stride(0), V),
+        _stream(stream)))
+
+
+def biv_verify_sample(target, draft_probs, draft, u_accept, u_sample, p0, tokens, accept_len, new_len,
+                      stream=None) -> None:
+    """target fp32 [N*(K+1), V] (or [N, K+1, V]), draft_probs [N*K, V] or None
+    (a drafter that is certain of its tokens); the other arrays as in the header."""
+    N, K1 = tokens.shape
+    K, V = K1 - 1, target.shape[-1]
+    if target.dim() == 3:
+        target = target.flatten(0, 1)
+    if draft_probs is not None and draft_probs.dim() == 3:
+        draft_probs = draft_probs.flatten(0, 1)
+    _dense("biv_verify_sample", ("target", target, _F32, (N * K1, V)), ("draft_probs", draft_probs, _F32, (N * K, V)),
+           ("draft", draft, _I32, (N, K)), ("u_accept", u_accept, _F32, (N, K)), ("u_sample", u_sample, _F32, (N,)),
+           ("p0", p0, _I32, (N,)), ("tokens", tokens, _I32, (N, K1)), ("accept_len", accept_len, _I32, (N,)),
+           ("new_len", new_len, _I32, (N,)))
+    _check("biv_verify_sample", _load().biv_verify_sample(
+        _ptr(target), _ptr(draft_probs), _ptr(draft), _ptr(u_accept), _ptr(u_sample), _ptr(p0), N, K, V, _ptr(tokens),
+        _ptr(accept_len), _ptr(new_len), _stream(stream)))

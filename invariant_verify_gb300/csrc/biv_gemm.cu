@@ -123,6 +123,14 @@ struct SelectArgs {
     int greedy;
 };
 
+// Bias, activation and residual of the EPI 5 epilogue (biv_gemm_bias_act).
+struct BiasActArgs {
+    const __nv_bfloat16* bias;        // [N] or null
+    const __nv_bfloat16* residual;    // [M, N] or null; may be C itself
+    int act;                          // BIV_ACT_*
+    int out_f32;                      // C is fp32 instead of bf16
+};
+
 BIV_DEV uint32_t pick_word(const U4& w, uint32_t j) {
     return j == 0 ? w.x : (j == 1 ? w.y : (j == 2 ? w.z : w.w));
 }
@@ -545,10 +553,62 @@ BIV_DEV unsigned long long tile_row_winner(uint32_t taddr, int cb, int ce, int n
     return best;
 }
 
+// act(x) in fp32.  erff and tanhf are within 2 ulp, so the result's one rounding
+// to C's type is the only one that counts.
+BIV_DEV float activate(float x, int act) {
+    switch (act) {
+        case BIV_ACT_RELU: return x > 0.0f || x != x ? x : 0.0f;
+        case BIV_ACT_GELU: return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+        case BIV_ACT_GELU_TANH: return 0.5f * x * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * x * x, x, x)));
+        case BIV_ACT_SILU: return silu(x);
+        default: return x;
+    }
+}
+
+// Sixteen bytes of a row that this kernel may overwrite later (a residual that
+// is C itself): an ordinary load, never through the read-only path.
+BIV_DEV uint4 ld_global_16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Eight columns of one row: C = act(acc + bias) + residual, one rounding.
+BIV_DEV void bias_act_store8(const uint32_t* v, int row, int col, int N, void* C, const BiasActArgs& ba) {
+    const long long at = static_cast<long long>(row) * N + col;
+    uint4 rs = make_uint4(0, 0, 0, 0), bs = make_uint4(0, 0, 0, 0);
+    if (ba.residual) rs = ld_global_16(ba.residual + at);
+    if (ba.bias) bs = __ldg(reinterpret_cast<const uint4*>(ba.bias + col));
+    const uint32_t b4[4] = {bs.x, bs.y, bs.z, bs.w}, r4[4] = {rs.x, rs.y, rs.z, rs.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float b = (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
+        x[e] = ba.bias ? __uint_as_float(v[e]) + b : __uint_as_float(v[e]);
+    }
+    if (ba.act != BIV_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
+    }
+    if (ba.residual) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
+    }
+    if (ba.out_f32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+}
+
 // EPI: 0 = bf16 C, 1 = fp32 C, 2 = SwiGLU of gate/up-interleaved B (bf16
 // activation [M, N/2]; see biv_gemm_swiglu), 3 = Gumbel-max selection of each
 // tile-row (optional fp32 C; see biv_lm_head_gumbel), 4 = RoPE of q and k, k
-// and v into the KV cache (see biv_gemm_qkv_rope).
+// and v into the KV cache (see biv_gemm_qkv_rope), 5 = bias, activation and
+// residual (see biv_gemm_bias_act).
 // CG = 1: one CTA per tile of 128 rows.  CG = 2: a cluster of two CTAs per
 // tile of 256 rows (cta_group::2 MMAs of M = 256): each CTA copies its own
 // 128 rows of A and its half of the tile's BN rows of B into its own shared
@@ -562,7 +622,8 @@ template <int EPI, int CG>
 __global__ void __launch_bounds__(64 + epi_threads<EPI>(), 1)
 gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-                     void* __restrict__ C, const GemmArgs g, const SelectArgs sel, const RopeArgs rp) {
+                     void* __restrict__ C, const GemmArgs g, const SelectArgs sel, const RopeArgs rp,
+                     const BiasActArgs ba) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -995,6 +1056,22 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 }
+            } else if constexpr (EPI == 5) {
+                int cb5, ce5;
+                eset_columns(bnt, 16, (warp - 2) >> 2, cb5, ce5);
+#pragma unroll 1
+                for (int c = cb5; c < ce5; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(taddr + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
+                    if (live) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int col = col0 + c + h * 8;
+                            if (col < N) bias_act_store8(r + h * 8, row, col, N, C, ba);
+                        }
+                    }
+                }
             } else {
             int cb0, ce0;
             eset_columns(bnt, 16, (warp - 2) >> 2, cb0, ce0);
@@ -1169,7 +1246,7 @@ inline TailPlan tail_plan(int M, int N, int BN, bool pairs) {
 
 template <int EPI, int CG>
 int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, int BN, cudaStream_t stream,
-                   const SelectArgs& sel, const RopeArgs& rp, int* n_cols) {
+                   const SelectArgs& sel, const RopeArgs& rp, int* n_cols, const BiasActArgs& ba) {
     GemmArgs g;
     g.M = M;
     g.N = N;
@@ -1256,10 +1333,10 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     if (CG == 2) {
         const int grid = 2 * static_cast<int>(std::min<long long>(work, units));
         return launch_cluster_pdl(kern, dim3(grid), block, static_cast<size_t>(smem), stream, 2, ta, tb, ta1, tb1, C,
-                                  g, sel, rp);
+                                  g, sel, rp, ba);
     }
     const int grid = static_cast<int>(std::min<long long>(work, num_sms()));
-    return launch_pdl(kern, dim3(grid), block, static_cast<size_t>(smem), stream, ta, tb, ta1, tb1, C, g, sel, rp);
+    return launch_pdl(kern, dim3(grid), block, static_cast<size_t>(smem), stream, ta, tb, ta1, tb1, C, g, sel, rp, ba);
 }
 
 // Pair tile widths: multiples of 32 in [64, 256] (each CTA copies BN / 2 rows
@@ -1268,10 +1345,11 @@ inline bool pair_bn_ok(int BN) { return BN % 32 == 0 && BN >= 64 && BN <= 256; }
 
 template <int EPI>
 int launch_gemm(const void* A, const void* B, void* C, int M, int N, int K, int BN, cudaStream_t stream,
-                const SelectArgs& sel = SelectArgs{}, const RopeArgs& rp = RopeArgs{}, int* n_cols = nullptr) {
+                const SelectArgs& sel = SelectArgs{}, const RopeArgs& rp = RopeArgs{}, int* n_cols = nullptr,
+                const BiasActArgs& ba = BiasActArgs{}) {
     if (use_pair(M, K) && pair_bn_ok(BN))
-        return launch_gemm_cg<EPI, 2>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols);
-    return launch_gemm_cg<EPI, 1>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols);
+        return launch_gemm_cg<EPI, 2>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols, ba);
+    return launch_gemm_cg<EPI, 1>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols, ba);
 }
 
 int check_gemm(const void* A, const void* B, void* C, int out_dtype, int M, int N, int K) {
@@ -1453,6 +1531,25 @@ extern "C" int biv_gemm_nosplitk(const void* A, const void* B, void* C, int out_
     int st = check_gemm(A, B, C, out_dtype, M, N, K);
     if (st != BIV_OK || M == 0) return st;
     return biv_gemm_nosplitk_bn(A, B, C, out_dtype, M, N, K, biv_gemm_tile_n(M, N, K), stream);
+}
+
+extern "C" int biv_gemm_bias_act(const void* A, const void* B, const void* bias, const void* residual, void* C,
+                                 int out_dtype, int act, int M, int N, int K, biv_stream_t stream) {
+    BIV_TRACE_CALL();
+    const int st = check_gemm(A, B, C, out_dtype, M, N, K);
+    if (st != BIV_OK) return st;
+    if (act < BIV_ACT_NONE || act > BIV_ACT_SILU) return BIV_ERR_VALUE;
+    if (M == 0) return BIV_OK;
+    if ((bias && !aligned16(bias)) || (residual && !aligned16(residual))) return BIV_ERR_ALIGN;
+    // an fp32 C over a bf16 residual would overwrite rows that are still to be read
+    if (C == A || C == B || C == bias || (C == residual && out_dtype == BIV_F32)) return BIV_ERR_VALUE;
+    BiasActArgs ba;
+    ba.bias = static_cast<const __nv_bfloat16*>(bias);
+    ba.residual = static_cast<const __nv_bfloat16*>(residual);
+    ba.act = act;
+    ba.out_f32 = out_dtype == BIV_F32;
+    return launch_gemm<5>(A, B, C, M, N, K, biv_gemm_tile_n(M, N, K), reinterpret_cast<cudaStream_t>(stream),
+                          SelectArgs{}, RopeArgs{}, nullptr, ba);
 }
 
 extern "C" int biv_swiglu_pack_weights(const void* w_gu, void* w_packed, int F, int K, biv_stream_t stream) {
