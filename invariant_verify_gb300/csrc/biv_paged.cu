@@ -2,6 +2,7 @@
 // fixed-split decode attention over them.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "biv_common.cuh"
 
@@ -126,47 +127,62 @@ struct PagedAttnParams {
     float2* ws_ml;             // [W][Hq][s_max] (maximum in units of log 2, sum); sum -1: a page id out of range
     PageTable pt;
     int W, rpg, G, Hq, Hkv, s_max, cap;
+    uint32_t g_magic;          // ceil(2^32 / G) where that divides every query row's number exactly, else 0
     float scale_log2;          // log2(e) / sqrt(hd)
 };
+
+// Window row and head of query row i of a group (i = row * G + head).
+BIV_DEV void row_head(const PagedAttnParams& P, int i, int& row, int& head) {
+    row = P.g_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), P.g_magic)) : P.G == 1 ? i : i / P.G;
+    head = i - row * P.G;
+}
 
 // Position of row w if the row is to be computed, else -1; the first row's slot
 // decides the group's.  flag: raise the error bits (one thread of a grid).
 BIV_DEV int usable_pos(const PagedAttnParams& P, int w, bool flag) {
-    const int pos = P.row_pos[w];
-    if (pos == -1) return -1;
-    const int slot = P.row_slot[w], first = P.row_slot[w - w % P.rpg];
+    const int pos = P.row_pos[w], slot = P.row_slot[w], first = P.row_slot[w - w % P.rpg];
     unsigned int bits = 0;
     if (pos < 0 || pos >= P.cap || slot < 0 || slot >= P.pt.n_slots) bits = BIV_DEVERR_INDEX;
     else if (slot != first) bits = BIV_DEVERR_GROUP;
-    if (bits && flag) atomicOr(&g_paged_err, bits);
+    if (bits && pos != -1 && flag) atomicOr(&g_paged_err, bits);
     return bits ? -1 : pos;
 }
 
-// ---- the split kernel
-// One item is (request, KV head, 256-key split, tile of 8 NT query rows), where
-// the query rows are the request's window rows times the G heads of the KV
-// head.  Keys go along the M side of the tensor core's tile and query rows along
-// N (mma.m16n8k16): S^T = K Q^T and O^T = V^T P^T, so eight rows fill a tile and
+// ---- the split kernels
+// One item is (request, KV head, 256-key split, tile of query rows), where the
+// query rows are the request's window rows times the G heads of the KV head.
+// Keys go along the M side of the tensor core's tile and query rows along N
+// (mma.m16n8k16): S^T = K Q^T and O^T = V^T P^T, so eight rows fill a tile and
 // the four rows of a single token waste half of it instead of the 60 of 64 that
-// a rows-by-keys tile would.  The permutation of the dims inside a product is
-// free, and chosen so that every operand comes straight from global memory in
-// 32-byte loads, a whole 128-byte line per four (K) or eight (V) lanes: no
-// shared memory, no barrier and no address arithmetic between HBM and the
-// tensor core.  Four warps take the 16-key steps of the split in turn, each with
-// its own running maximum and sum, and meet once at the end.
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = 32 * kAttnWarps;
+// a rows-by-keys tile would.  Four classes of warps take the split's 16-key
+// steps in turn (class k: steps k, k + 4, ...), each with its own running maximum
+// and sum, and meet once at the end in class order.  Two kernels run that same
+// program, with the same bits for a row:
+//   direct  up to 8 query rows (one new token): the permutation of the dims
+//           inside a product is free, and chosen so that K and V come straight
+//           from global memory in 32-byte loads, a whole 128-byte line per four
+//           (K) or eight (V) lanes: no shared memory, no barrier and no address
+//           arithmetic between HBM and the tensor core.
+//   staged  more rows (verify windows): K and V pass through a ring in shared
+//           memory, filled by one warp's 16-byte asynchronous copies, so that up
+//           to four tiles of 8 rows share one read of the keys.
+constexpr int kClasses = 4;
 constexpr int kStep = 16;
-constexpr int kStepsPerWarp = kSplit / kStep / kAttnWarps;
+constexpr int kSteps = kSplit / kStep;                 // steps of a split
+constexpr int kStepsPerClass = kSteps / kClasses;
+constexpr int kDirectThreads = 32 * kClasses;
 constexpr int kMaxGroups = 1024;       // entries of the table of live splits; more groups share entries
+constexpr int kMaxRows = 4096;         // rows whose positions are kept in shared memory; with more they are read again
+constexpr int kMaxTiles = 3;           // 8-row tiles of a staged item
+constexpr int kStagedThreads = 32 * kClasses * kMaxTiles + 32;
 
-// 32 bytes of a row of keys or values: read once, so not kept in L1.
-BIV_DEV void ld_row32(const __nv_bfloat16* p, uint32_t (&r)[8]) {
+// 32 or 16 bytes of a row of keys or values: read once, so not kept in L1.
+BIV_DEV void ld_row(const __nv_bfloat16* p, uint32_t (&r)[8]) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
-BIV_DEV void ld_row16(const __nv_bfloat16* p, uint32_t (&r)[4]) {
+BIV_DEV void ld_row(const __nv_bfloat16* p, uint32_t (&r)[4]) {
     asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "l"(p));
@@ -187,418 +203,813 @@ BIV_DEV uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Largest usable position of group g, -1 if it has none.
-BIV_DEV int group_pos(const PagedAttnParams& P, int g, bool flag) {
-    int best = -1;
-    const int w1 = min(P.W, (g + 1) * P.rpg);
-    for (int w = g * P.rpg; w < w1; ++w) best = max(best, usable_pos(P, w, flag));
-    return best;
+BIV_DEV void cp_async16(void* smem, const void* gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+// The same past L1, or sixteen zero bytes (nothing is read then).
+BIV_DEV void cp_async16_or_zero(uint32_t smem, const void* gmem, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(read ? 16 : 0) : "memory");
 }
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 3 : 2)
-paged_attn_kernel(const PagedAttnParams P) {
-    constexpr int KS = HD / 16;            // k-steps of S^T; also the 16-dim tiles of O^T
-    constexpr int KC = HD / 64;            // 64-dim chunks of a key: one 32-byte load per lane each
-    constexpr int TR = 8 * NT;             // query rows of a tile
-    constexpr int HDP = HD + 4;            // padded row of the warps' outputs
-    __shared__ int s_pre[kMaxGroups + 1];  // live splits before each entry
-    __shared__ int s_pos[kMaxGroups];      // largest usable position of each group (one group per entry)
-    __shared__ int s_scan[kAttnWarps];
-    __shared__ __align__(16) float s_o[kAttnWarps][TR][HDP];
-    __shared__ float2 s_ml[kAttnWarps][TR];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g8 = lane >> 2, c4 = lane & 3;       // row of an 8-row fragment, column pair
+// One warp's running softmax over eight query rows: this lane's columns are rows
+// 2 (lane % 4) and the next; acc holds HD / 16 tiles of O^T.
+template <int HD>
+struct RowState {
+    float acc[HD / 16][4];
+    float m[2], l[2];
 
-    // Live splits of every group: computed by each CTA from the positions, which
-    // are not an output of the previous kernel.
-    const int n_groups = (P.W + P.rpg - 1) / P.rpg;
-    const int chunk = (n_groups + kMaxGroups - 1) / kMaxGroups;
-    const int entries = (n_groups + chunk - 1) / chunk;
-    const bool flag = blockIdx.x == 0;
-    if (chunk == 1) {
-        for (int e = tid; e < entries; e += kAttnThreads) s_pos[e] = -1;
+    BIV_DEV void clear() {
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+
+    // Scores of a step (S^T fragment: keys g8 and g8 + 8) to weights: the running
+    // maximum and sum move on, the output is rescaled where a maximum grew (a
+    // factor of a row that did not is exactly 1), and each weight leaves as the
+    // sum of two bf16 values, transposed to the B fragments of O^T += V^T P^T.
+    BIV_DEV void step(float (&st)[4], float scale_log2, uint32_t (&hi)[2], uint32_t (&low)[2]) {
+        float f[2], x[2];
+        bool grew = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[e] = fmaxf(st[e], st[e + 2]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
+            x[0] = fmaxf(x[0], y0);
+            x[1] = fmaxf(x[1], y1);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[e], x[e] * scale_log2);
+            const float mu = mn == -INFINITY ? 0.0f : mn;
+            f[e] = ex2_approx(m[e] - mu);
+            grew |= mn > m[e];
+            m[e] = mn;
+            st[e] = ex2_approx(fmaf(st[e], scale_log2, -mu));
+            st[e + 2] = ex2_approx(fmaf(st[e + 2], scale_log2, -mu));
+            l[e] = fmaf(l[e], f[e], st[e] + st[e + 2]);
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][e] *= f[e & 1];
+        }
+        const uint32_t h0 = pack_bf16x2(st[0], st[1]), h1 = pack_bf16x2(st[2], st[3]);
+        const uint32_t l0 = pack_bf16x2(st[0] - bf16lo(h0), st[1] - bf16hi(h0));
+        const uint32_t l1 = pack_bf16x2(st[2] - bf16lo(h1), st[3] - bf16hi(h1));
+        hi[0] = transpose8(h0);
+        hi[1] = transpose8(h1);
+        low[0] = transpose8(l0);
+        low[1] = transpose8(l1);
+    }
+
+    // O^T += V^T (hi + low); frag(k, a) gives the A fragment of dims tile k.  The
+    // two products of a tile stand kSkew tiles apart, so that the second does not
+    // wait for the first.
+    template <typename F>
+    BIV_DEV void add(const uint32_t (&hi)[2], const uint32_t (&low)[2], F&& frag) {
+        constexpr int KS = HD / 16, kSkew = 2;
+        uint32_t a[KS][4];
+#pragma unroll
+        for (int k = 0; k < KS + kSkew; ++k) {
+            if (k < KS) {
+                frag(k, a[k]);
+                mma_16816(acc[k], a[k][0], a[k][1], a[k][2], a[k][3], hi[0], hi[1]);
+            }
+            if (k >= kSkew) {
+                const int j = k - kSkew;
+                mma_16816(acc[j], a[j][0], a[j][1], a[j][2], a[j][3], low[0], low[1]);
+            }
+        }
+    }
+
+    // The sums over the lanes that share a column.
+    BIV_DEV void sum_lanes(float (&sum)[2]) const {
+        sum[0] = l[0];
+        sum[1] = l[1];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            const float y0 = __shfl_xor_sync(0xffffffffu, sum[0], d), y1 = __shfl_xor_sync(0xffffffffu, sum[1], d);
+            sum[0] += y0;
+            sum[1] += y1;
+        }
+    }
+};
+
+// One item; unit counts (request, split) pairs, sub (KV head, tile).
+struct AttnItem {
+    int unit, sub;
+    int w0, rows;              // first row of the group; its query rows (window rows x G)
+    int kvh, tile, split;
+};
+
+// Shared memory of both kernels: the positions and the live splits of every group.
+struct LiveTable {
+    int pre[kMaxGroups + 1];   // live splits before each entry
+    int pos[kMaxRows];         // usable position of every row, -1: none
+    int scan[32];
+};
+
+// Finds the items of a call: every CTA forms the same table from the rows'
+// positions (not an output of the previous kernel, so before the wait).
+struct Items {
+    const PagedAttnParams& P;
+    LiveTable& t;
+    int n_groups, chunk, entries, tiles, per_unit;
+    bool kept;
+    int units, step_unit, step_sub;        // live splits of all groups; a grid's stride in items
+
+    BIV_DEV Items(const PagedAttnParams& p, LiveTable& table, int tile_rows) : P(p), t(table) {
+        n_groups = (P.W + P.rpg - 1) / P.rpg;
+        chunk = (n_groups + kMaxGroups - 1) / kMaxGroups;
+        entries = (n_groups + chunk - 1) / chunk;
+        kept = P.W <= kMaxRows;
+        tiles = (P.rpg * P.G + tile_rows - 1) / tile_rows;
+        per_unit = P.Hkv * tiles;
+        step_unit = gridDim.x / per_unit;
+        step_sub = gridDim.x - step_unit * per_unit;
+        const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        if (kept)
+            for (int w = tid; w < P.W; w += threads) t.pos[w] = usable_pos(P, w, blockIdx.x == 0);
+        else if (blockIdx.x == 0)
+            for (int w = tid; w < P.W; w += threads) usable_pos(P, w, true);
         __syncthreads();
-        for (int w = tid; w < P.W; w += kAttnThreads) {
-            const int pos = usable_pos(P, w, flag);
-            if (pos >= 0) atomicMax(&s_pos[w / P.rpg], pos);
+        const int ept = (entries + threads - 1) / threads;               // entries of a thread
+        const int e0 = min(entries, tid * ept), e1 = min(entries, e0 + ept);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) sum += live_of(e);
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) t.scan[warp] = incl;
+        __syncthreads();
+        int before = incl - sum;
+        units = 0;
+        for (int k = 0; k < threads / 32; ++k) {
+            if (k < warp) before += t.scan[k];
+            units += t.scan[k];
+        }
+        for (int e = e0; e < e1; ++e) {
+            t.pre[e] = before;
+            before += live_of(e);
         }
         __syncthreads();
     }
-    constexpr int EPT = kMaxGroups / kAttnThreads;         // entries of a thread
-    int mine[EPT], sum = 0;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        const int e = tid * EPT + i;
-        int n = 0;
-        if (e < entries) {
-            if (chunk == 1) n = s_pos[e] / kSplit + (s_pos[e] >= 0);
-            else
-                for (int g = e * chunk; g < min(n_groups, (e + 1) * chunk); ++g) {
-                    const int pos = group_pos(P, g, flag);
-                    n += pos / kSplit + (pos >= 0);
-                }
+
+    BIV_DEV int pos_of(int w) const { return kept ? t.pos[w] : usable_pos(P, w, false); }
+    BIV_DEV int splits_of(int g) const {
+        int best = -1;
+        const int w1 = min(P.W, (g + 1) * P.rpg);
+        for (int w = g * P.rpg; w < w1; ++w) best = max(best, pos_of(w));
+        return best / kSplit + (best >= 0);
+    }
+    BIV_DEV int live_of(int e) const {
+        int k = 0;
+        for (int g = e * chunk; g < min(n_groups, (e + 1) * chunk); ++g) k += splits_of(g);
+        return k;
+    }
+    // The CTA's first item, and the one after an item; false: there is none.
+    // Every lane of a warp asks together.
+    BIV_DEV bool first(AttnItem& it) const {
+        it.unit = blockIdx.x / per_unit;
+        it.sub = blockIdx.x - it.unit * per_unit;
+        return it.unit < units && (find(it), true);
+    }
+    BIV_DEV bool next(const AttnItem& it, AttnItem& nx) const {
+        nx.unit = it.unit + step_unit;
+        nx.sub = it.sub + step_sub;
+        if (nx.sub >= per_unit) {
+            nx.sub -= per_unit;
+            ++nx.unit;
         }
-        mine[i] = sum;
-        sum += n;
+        return nx.unit < units && (find(nx), true);
     }
-    int incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int before = incl - sum, units = 0;
-    for (int k = 0; k < kAttnWarps; ++k) {
-        if (k < warp) before += s_scan[k];
-        units += s_scan[k];
-    }
-#pragma unroll
-    for (int i = 0; i < EPT; ++i)
-        if (tid * EPT + i < entries) s_pre[tid * EPT + i] = before + mine[i];
-    __syncthreads();
-
-    pdl_wait();
-    pdl_trigger();
-
-    // rows that are not computed come back as zeros
-    for (int w = blockIdx.x; w < P.W; w += gridDim.x) {
-        const int pos = chunk == 1 && P.rpg == 1 ? s_pos[w] : usable_pos(P, w, false);
-        if (pos < 0)
-            for (int e = tid; e < P.Hq * HD / 8; e += kAttnThreads)
-                reinterpret_cast<uint4*>(P.o + static_cast<long long>(w) * P.Hq * HD)[e] = make_uint4(0, 0, 0, 0);
-    }
-
-    const int tiles = (P.rpg * P.G + TR - 1) / TR;
-    const int per_unit = P.Hkv * tiles;
-    const long long items = static_cast<long long>(units) * per_unit;
-    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-        const int unit = static_cast<int>(item / per_unit), sub = static_cast<int>(item - static_cast<long long>(unit) * per_unit);
-        const int kvh = sub / tiles, tile = sub - kvh * tiles;
-        int lo = 0, hi = entries - 1;              // the last entry with s_pre <= unit
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pre[mid] <= unit) lo = mid;
-            else hi = mid - 1;
+    BIV_DEV void find(AttnItem& it) const {
+        it.kvh = tiles == 1 ? it.sub : it.sub / tiles;
+        it.tile = it.sub - it.kvh * tiles;
+        // the last entry with pre <= unit, 32 at a time
+        const int lane = threadIdx.x & 31;
+        int e = 0;
+        if (entries > 32) {
+            const bool le = lane * 32 < entries && t.pre[lane * 32] <= it.unit;
+            e = (__popc(__ballot_sync(0xffffffffu, le)) - 1) * 32;
         }
-        int grp = lo, split = unit - s_pre[lo];
+        const bool le = e + lane < entries && t.pre[e + lane] <= it.unit;
+        e += __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        int grp = e;
+        it.split = it.unit - t.pre[e];
         if (chunk > 1) {
-            for (grp = lo * chunk;; ++grp) {
-                const int pos = group_pos(P, grp, false);
-                const int n = pos / kSplit + (pos >= 0);
-                if (split < n) break;
-                split -= n;
+            for (grp = e * chunk;; ++grp) {
+                const int k = splits_of(grp);
+                if (it.split < k) break;
+                it.split -= k;
             }
         }
-        const int w0 = grp * P.rpg;
-        const int rows = min(P.rpg, P.W - w0) * P.G;       // query rows of the group
-        // positions of this thread's columns of S^T (rows 2 c4 and 2 c4 + 1 of each n-tile)
-        int pos2[NT][2], tmax = -1, tmin = 0x7fffffff;
+        it.w0 = grp * P.rpg;
+        it.rows = min(P.rpg, P.W - it.w0) * P.G;
+    }
+    // Largest position of query rows r0 .. r0 + n - 1 of an item, by a whole warp.
+    BIV_DEV int largest_pos(const AttnItem& it, int r0, int n) const {
+        int a, b, h, best = -1;
+        if (r0 >= it.rows) return -1;
+        row_head(P, r0, a, h);
+        row_head(P, min(it.rows, r0 + n) - 1, b, h);
+        for (int w = it.w0 + a + (threadIdx.x & 31); w <= it.w0 + b; w += 32) best = max(best, pos_of(w));
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int d = 16; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+        return best;
+    }
+    BIV_DEV static int steps_to(int tmax, int split) {     // 16-key steps of a split that position tmax reaches
+        return tmax < split * kSplit ? 0 : min(kSteps, (tmax - split * kSplit) / kStep + 1);
+    }
+    // Rows that are not computed come back as zeros.
+    template <int HD>
+    BIV_DEV void zero_rows() const {
+        for (int w = blockIdx.x; w < P.W; w += gridDim.x)
+            if (pos_of(w) < 0)
+                for (int e = threadIdx.x; e < P.Hq * HD / 8; e += blockDim.x)
+                    reinterpret_cast<uint4*>(P.o + static_cast<long long>(w) * P.Hq * HD)[e] = make_uint4(0, 0, 0, 0);
+    }
+};
+
+// Positions of a lane's two query rows of an 8-row tile (first query row r0 of
+// the group), the tile's smallest and largest, and the steps some row reaches.
+struct TilePos {
+    int pos[2], tmin, tmax, nsteps;
+    BIV_DEV TilePos() {}
+    BIV_DEV TilePos(const Items& I, const AttnItem& it, int r0, int c4) {
+        tmax = -1;
+        tmin = 0x7fffffff;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = tile * TR + t * 8 + 2 * c4 + e;
-                int pos = -1;
-                if (i < rows) pos = chunk == 1 && P.rpg == 1 ? s_pos[grp] : usable_pos(P, w0 + i / P.G, false);
-                pos2[t][e] = pos;
-                tmax = max(tmax, pos);
-                tmin = min(tmin, pos);
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int i = r0 + 2 * c4 + e;
+            int row, head;
+            row_head(I.P, i, row, head);
+            pos[e] = i < it.rows ? I.pos_of(it.w0 + row) : -1;
+            tmax = max(tmax, pos[e]);
+            tmin = min(tmin, pos[e]);
+        }
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
             tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, d));
             tmin = min(tmin, __shfl_xor_sync(0xffffffffu, tmin, d));
         }
-        const int key_lo = split * kSplit;
-        if (tmax < key_lo) continue;                       // the same in every warp
-        const int nsteps = min(kSplit / kStep, (tmax - key_lo) / kStep + 1);
+        nsteps = Items::steps_to(tmax, it.split);
+    }
+    // Scores of keys past a row's position count as -infinity.
+    BIV_DEV void mask(float (&st)[4], int key0, int g8) const {
+        if (key0 + kStep - 1 > tmin) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (key0 + g8 + 8 * (e >> 1) > pos[e & 1]) st[e] = -INFINITY;
+        }
+    }
+};
 
-        // pages of this warp's steps (lane i: step warp + 4 i)
-        int page = 0;
-        const int slot = P.row_slot[w0];
-        if (lane < kStepsPerWarp && warp + kAttnWarps * lane < nsteps)
-            page = P.pt.table[static_cast<long long>(slot) * P.pt.max_pages +
-                              ((key_lo + kStep * (warp + kAttnWarps * lane)) >> P.pt.page_shift)];
-        const bool page_ok = page >= 0 && page < P.pt.n_pages;
-        const uint32_t bad_pages = __ballot_sync(0xffffffffu, !page_ok);
-        if (!page_ok) {
-            atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
-            page = 0;
-        }
+// Q of `rows` query rows from r0 on, 16 bytes a thread; rows past the group's
+// read its first row and are never used.
+template <int HD>
+BIV_DEV void load_q(const PagedAttnParams& P, const AttnItem& it, int r0, int rows, __nv_bfloat16* dst, int pitch, int tid,
+                    int threads) {
+    for (int e = tid; e < rows * (HD / 8); e += threads) {
+        const int row = e / (HD / 8), d = (e % (HD / 8)) * 8;
+        const int i = r0 + row;
+        int j, head;
+        row_head(P, i < it.rows ? i : 0, j, head);
+        cp_async16(dst + row * pitch + d,
+                   P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + d);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
 
-        uint32_t qf[NT][KS][2];
+// The classes' shares of each row of an item, joined in class order: o[class][row]
+// and ml[class][row] (sum -infinity: the row met a page id out of range).  A
+// row's only split is finished here, others go to the workspace.
+template <int HD>
+BIV_DEV void join_classes(const Items& I, const AttnItem& it, int r0, int rows, const float* o, const float2* ml, int tid,
+                          int threads) {
+    constexpr int HDP = HD + 4;
+    const PagedAttnParams& P = I.P;
+    for (int x4 = tid; x4 < rows * (HD / 4); x4 += threads) {              // four dims of a row
+        const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4;
+        const int i = r0 + row;
+        if (i >= it.rows) break;
+        int j, head;
+        row_head(P, i, j, head);
+        const int w = it.w0 + j;
+        const int pos = I.pos_of(w);
+        if (pos < it.split * kSplit) continue;
+        float mx = -INFINITY, sum = 0.0f;
+        bool bad = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int i = tile * TR + t * 8 + g8;
-            const bool live = i < rows;
-            const __nv_bfloat16* qr = P.q + (static_cast<long long>(w0 + (live ? i / P.G : 0)) * P.Hq + kvh * P.G +
-                                             (live ? i % P.G : 0)) * HD + 16 * c4;
+        for (int k = 0; k < kClasses; ++k) mx = fmaxf(mx, ml[k * rows + row].x);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int b = 0; b < KC; ++b) {
-                uint32_t r[8];
-                ld_row32(qr + 64 * b, r);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    qf[t][4 * b + k][0] = live ? r[2 * k] : 0u;
-                    qf[t][4 * b + k][1] = live ? r[2 * k + 1] : 0u;
-                }
-            }
+        for (int k = 0; k < kClasses; ++k) {
+            const float2 c = ml[k * rows + row];
+            bad |= c.y == -INFINITY;
+            const float f = c.x == -INFINITY ? 0.0f : ex2_approx(c.x - mx);
+            sum = fmaf(c.y, f, sum);
+            const float4 y = *reinterpret_cast<const float4*>(o + (k * rows + row) * HDP + d);
+            x.x = fmaf(y.x, f, x.x);
+            x.y = fmaf(y.y, f, x.y);
+            x.z = fmaf(y.z, f, x.z);
+            x.w = fmaf(y.w, f, x.w);
         }
-
-        float acc[NT][KS][4], m[NT][2], l[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][k][e] = 0.0f;
-            m[t][0] = m[t][1] = -INFINITY;
-            l[t][0] = l[t][1] = 0.0f;
+        const long long pair = static_cast<long long>(w) * P.Hq + it.kvh * P.G + head;
+        if (pos < kSplit) {
+            const float scale = 1.0f / sum;
+            uint2 y = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
+            if (bad) y = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(P.o + pair * HD + d) = y;
+        } else {
+            const long long part = pair * P.s_max + it.split;
+            if (d == 0) P.ws_ml[part] = make_float2(mx, bad ? -1.0f : sum);
+            *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
         }
-        uint32_t bad_rows = 0;                             // bit 2 t + e: the row met a page id out of range
-        uint32_t kr[2][KC][8];                             // keys g8 and g8 + 8 of the step
-        uint32_t vr[4][KS];                                // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9: dims [KS * 2 g8, ..)
-        const int in_page = P.pt.page_size - 1;
-        auto row_at = [&](int i) {                         // element offset of this warp's i-th step
-            const int pg = __shfl_sync(0xffffffffu, page, i);
-            const int off = (key_lo + kStep * (warp + kAttnWarps * i)) & in_page;
-            return ((static_cast<long long>(pg) * P.Hkv + kvh) * P.pt.page_size + off) * HD;
-        };
-        auto load_k = [&](long long at) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int b = 0; b < KC; ++b) ld_row32(P.kp + at + (g8 + 8 * r) * HD + 64 * b + 16 * c4, kr[r][b]);
-        };
-        auto load_v = [&](long long at) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat16* src = P.vp + at + (2 * c4 + (k & 1) + 8 * (k >> 1)) * HD + 2 * KS * g8;
-                if constexpr (KS == 8) ld_row32(src, vr[k]);
-                else ld_row16(src, vr[k]);
-            }
-        };
-        const int my_steps = (nsteps - warp + kAttnWarps - 1) / kAttnWarps;
-        long long at = 0;
-        if (my_steps > 0) {
-            at = row_at(0);
-            load_k(at);
-            load_v(at);
-        }
-#pragma unroll 1
-        for (int i = 0; i < my_steps; ++i) {
-            const int key0 = key_lo + kStep * (warp + kAttnWarps * i);
-            float st[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st[t][e] = 0.0f;
-                // two chains, so that an MMA does not wait for the one before it
-#pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    const int b = k >> 2, r = 2 * (k & 3);
-                    mma_16816(st[t], kr[0][b][r], kr[1][b][r], kr[0][b][r + 1], kr[1][b][r + 1], qf[t][k][0], qf[t][k][1]);
-                    mma_16816(s1, kr[0][b][r + 2], kr[1][b][r + 2], kr[0][b][r + 3], kr[1][b][r + 3], qf[t][k + 1][0],
-                              qf[t][k + 1][1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st[t][e] += s1[e];
-            }
-            long long next = 0;
-            if (i + 1 < my_steps) {
-                next = row_at(i + 1);
-                load_k(next);
-            }
-            if ((bad_pages >> i) & 1u) {                   // a row that reaches this step cannot be computed
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (pos2[t][e] >= key0) bad_rows |= 1u << (2 * t + e);
-            }
-            if (key0 + kStep - 1 > tmin) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key0 + g8 + 8 * (e >> 1) > pos2[t][e & 1]) st[t][e] = -INFINITY;
-                if (key0 + kStep - 1 > tmax) {             // what lies behind the last key may hold anything
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (key0 + 2 * c4 + (k & 1) + 8 * (k >> 1) > tmax) {
-#pragma unroll
-                            for (int d = 0; d < KS; ++d) vr[k][d] = 0u;
-                        }
-                }
-            }
-            uint32_t hi[NT][2], low[NT][2];                // P^T of the step: keys 0-7 and 8-15, transposed to B fragments
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float f[2];
-                bool grew = false;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(st[t][e], st[t][e + 2]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    const float mn = fmaxf(m[t][e], x * P.scale_log2);
-                    const float mu = mn == -INFINITY ? 0.0f : mn;
-                    f[e] = ex2_approx(m[t][e] - mu);
-                    grew |= mn > m[t][e];
-                    m[t][e] = mn;
-                    const float p0 = ex2_approx(fmaf(st[t][e], P.scale_log2, -mu));
-                    const float p1 = ex2_approx(fmaf(st[t][e + 2], P.scale_log2, -mu));
-                    st[t][e] = p0;
-                    st[t][e + 2] = p1;
-                    l[t][e] = fmaf(l[t][e], f[e], p0 + p1);
-                }
-                if (__any_sync(0xffffffffu, grew)) {       // a factor of a row that did not grow is exactly 1
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[t][k][e] *= f[e & 1];
-                }
-                // each weight as the sum of two bf16 values: 16 of its bits meet V
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t h = pack_bf16x2(st[t][2 * r], st[t][2 * r + 1]);
-                    hi[t][r] = transpose8(h);
-                    low[t][r] = transpose8(pack_bf16x2(st[t][2 * r] - bf16lo(h), st[t][2 * r + 1] - bf16hi(h)));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint32_t a0 = __byte_perm(vr[0][k], vr[1][k], 0x5410), a1 = __byte_perm(vr[0][k], vr[1][k], 0x7632);
-                const uint32_t a2 = __byte_perm(vr[2][k], vr[3][k], 0x5410), a3 = __byte_perm(vr[2][k], vr[3][k], 0x7632);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_16816(acc[t][k], a0, a1, a2, a3, hi[t][0], hi[t][1]);
-                    mma_16816(acc[t][k], a0, a1, a2, a3, low[t][0], low[t][1]);
-                }
-            }
-            if (i + 1 < my_steps) load_v(next);
-        }
-
-        // the warps' shares of each row, joined in warp order
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
-                const int row = t * 8 + 2 * c4 + e;
-                if (g8 == 0)
-                    s_ml[warp][row] = make_float2(m[t][e], (bad_rows >> (2 * t + e)) & 1u ? -INFINITY : l[t][e]);
-                // acc[k][e], acc[k][e + 2]: dims 2 KS g8 + 2 k and + 1 of the row
-#pragma unroll
-                for (int k = 0; k < KS; k += 2)
-                    *reinterpret_cast<float4*>(&s_o[warp][row][2 * KS * g8 + 2 * k]) =
-                        make_float4(acc[t][k][e], acc[t][k][e + 2], acc[t][k + 1][e], acc[t][k + 1][e + 2]);
-            }
-        }
-        __syncthreads();
-        {
-            constexpr int TPR = kAttnThreads / TR;         // threads of a row
-            constexpr int DPT = HD / TPR;                  // dims of a thread
-            const int row = tid / TPR, d0 = (tid % TPR) * 4;
-            const int i = tile * TR + row;
-            const int w = w0 + i / P.G;
-            int pos = -1;
-            if (i < rows) pos = chunk == 1 && P.rpg == 1 ? s_pos[grp] : usable_pos(P, w, false);
-            if (pos >= key_lo) {
-                float mx = -INFINITY, f[kAttnWarps], sum_l = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) mx = fmaxf(mx, s_ml[k][row].x);
-                bool bad = false;
-#pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) {
-                    const float2 ml = s_ml[k][row];
-                    bad |= ml.y == -INFINITY;
-                    f[k] = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mx);
-                    sum_l = fmaf(ml.y, f[k], sum_l);
-                }
-                const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + i % P.G;
-                const bool whole = pos < kSplit;           // the row's only split
-                const float scale = !whole ? 1.0f : bad ? 0.0f : 1.0f / sum_l;
-                const long long part = pair * P.s_max + split;
-                if (!whole && tid % TPR == 0) P.ws_ml[part] = make_float2(mx, bad ? -1.0f : sum_l);
-#pragma unroll
-                for (int j = 0; j < DPT / 4; ++j) {
-                    const int d = d0 + 4 * TPR * j;
-                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                    for (int k = 0; k < kAttnWarps; ++k) {
-                        const float4 y = *reinterpret_cast<const float4*>(&s_o[k][row][d]);
-                        x.x = fmaf(y.x, f[k], x.x);
-                        x.y = fmaf(y.y, f[k], x.y);
-                        x.z = fmaf(y.z, f[k], x.z);
-                        x.w = fmaf(y.w, f[k], x.w);
-                    }
-                    if (whole) {
-                        if (bad) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        *reinterpret_cast<uint2*>(P.o + pair * HD + d) =
-                            make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
-                    } else {
-                        *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
-                    }
-                }
-            }
-        }
-        __syncthreads();
     }
 }
 
-// Joins the splits of one (row, head), in an order that goes by their number
-// alone: warp k takes splits k, k + 8, ..., and the warps' sums are added in warp
-// order.  Rows of a single split were finished by the split kernel.
-constexpr int kCombineWarps = 8;
+template <int HD>
+struct __align__(16) DirectSmem {
+    float o[kClasses][8][HD + 4];          // rows padded against bank conflicts
+    __nv_bfloat16 q[2][8][HD + 8];
+    float2 ml[kClasses][8];
+    LiveTable table;
+};
 
 template <int HD>
-__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const PagedAttnParams P) {
-    constexpr int E = HD / 32;
-    __shared__ float s_acc[kCombineWarps][HD];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long pair = blockIdx.x;
-    const int pos = usable_pos(P, static_cast<int>(pair / P.Hq), false);
+__global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(const PagedAttnParams P) {
+    constexpr int KS = HD / 16;            // k-steps of S^T; also the 16-dim tiles of O^T
+    constexpr int KC = HD / 64;            // 64-dim chunks of a key: one 32-byte load per lane each
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DirectSmem<HD>& sm = *reinterpret_cast<DirectSmem<HD>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
+    const int g8 = lane >> 2, c4 = lane & 3;       // row of an 8-row fragment, column pair
+    const Items I(P, sm.table, 8);
     pdl_wait();
     pdl_trigger();
-    if (pos < kSplit) return;
-    const int ns = pos / kSplit + 1;
-    const float2* ml = P.ws_ml + pair * P.s_max;
-    float m = -INFINITY, l = 0.0f;
-    bool bad = false;
-    for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s].x);
+    I.zero_rows<HD>();
+
+    uint32_t kr[2][KC][8];                         // keys g8 and g8 + 8 of a step
+    uint32_t vr[4][KS];                            // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9: dims [2 KS g8, ..)
+    auto page_of = [&](const AttnItem& it, const TilePos& tp) {        // lane i: page of this class's i-th step
+        int page = 0;
+        if (lane < kStepsPerClass && cls + kClasses * lane < tp.nsteps)
+            page = P.pt.table[static_cast<long long>(P.row_slot[it.w0]) * P.pt.max_pages +
+                              ((it.split * kSplit + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
+        return page;
+    };
+    auto bad_pages_of = [&](int& page) {           // apart from the load, so that nothing waits for it early
+        const bool ok = page >= 0 && page < P.pt.n_pages;
+        if (!ok) {
+            atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
+            page = 0;
+        }
+        return ~__ballot_sync(0xffffffffu, ok);
+    };
+    auto row_at = [&](const AttnItem& it, int page, int i) {           // element offset of this class's i-th step
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+        const int off = (it.split * kSplit + kStep * (cls + kClasses * i)) & (P.pt.page_size - 1);
+        return ((static_cast<long long>(pg) * P.Hkv + it.kvh) * P.pt.page_size + off) * HD;
+    };
+    auto load_k = [&](long long at) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int s = lane; s < ns; s += 32) {
-        const float2 x = ml[s];
-        bad |= x.y == -1.0f;
-        l = fmaf(x.y, ex2_approx(x.x - m), l);
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < KC; ++b) ld_row(P.kp + at + (g8 + 8 * r) * HD + 64 * b + 16 * c4, kr[r][b]);
+    };
+    auto load_v = [&](long long at) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ld_row(P.vp + at + (2 * c4 + (k & 1) + 8 * (k >> 1)) * HD + 2 * KS * g8, vr[k]);
+    };
+    auto steps_of = [&](const TilePos& tp) { return (tp.nsteps - cls + kClasses - 1) / kClasses; };
+
+    AttnItem cur, nxt;
+    if (!I.first(cur)) return;
+    load_q<HD>(P, cur, 0, 8, &sm.q[0][0][0], HD + 8, tid, kDirectThreads);
+    TilePos cur_pos(I, cur, 0, c4), nxt_pos;
+    int cur_page = page_of(cur, cur_pos), nxt_page = 0;
+    uint32_t cur_bad = bad_pages_of(cur_page), nxt_bad = 0;
+    if (steps_of(cur_pos) > 0) {
+        const long long at = row_at(cur, cur_page, 0);
+        load_k(at);
+        load_v(at);
     }
+    for (int buf = 0;; buf ^= 1) {
+        // this item's Q has landed; every class has joined the item before
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        const bool more = I.next(cur, nxt);
+        if (more) {
+            load_q<HD>(P, nxt, 0, 8, &sm.q[buf ^ 1][0][0], HD + 8, tid, kDirectThreads);
+            nxt_pos = TilePos(I, nxt, 0, c4);
+            nxt_page = page_of(nxt, nxt_pos);
+        }
+        RowState<HD> rs;
+        rs.clear();
+        uint32_t bad_rows = 0;                     // bit e: the row met a page id out of range
+        const int my_steps = steps_of(cur_pos);
+        long long next_at = 0;
+        bool next = false;
+#pragma unroll 1
+        for (int i = 0; i < my_steps; ++i) {
+            const int key0 = cur.split * kSplit + kStep * (cls + kClasses * i);
+            // four chains, so that an MMA does not wait for the one before it
+            float s4[4][4] = {}, st[4];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    bad = __any_sync(0xffffffffu, bad);
-    float acc[E] = {};
-    const float* o = P.ws_o + pair * P.s_max * HD + lane * E;
-#pragma unroll 8
-    for (int s = warp; s < ns; s += kCombineWarps) {
-        const float f = ex2_approx(ml[s].x - m);
+            for (int k = 0; k < KS; k += 2) {
+                const int b = k >> 2, r = 2 * (k & 3);
+                const uint4 qv = *reinterpret_cast<const uint4*>(&sm.q[buf][g8][64 * b + 16 * c4 + 2 * r]);
+                mma_16816(s4[k & 3], kr[0][b][r], kr[1][b][r], kr[0][b][r + 1], kr[1][b][r + 1], qv.x, qv.y);
+                mma_16816(s4[(k & 3) + 1], kr[0][b][r + 2], kr[1][b][r + 2], kr[0][b][r + 3], kr[1][b][r + 3], qv.z, qv.w);
+            }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[static_cast<long long>(s) * HD + e], f, acc[e]);
+            for (int e = 0; e < 4; ++e) st[e] = (s4[0][e] + s4[1][e]) + (s4[2][e] + s4[3][e]);
+            // the keys of this class's next step, or of its first step of the next item
+            next = i + 1 < my_steps;
+            if (next) {
+                next_at = row_at(cur, cur_page, i + 1);
+            } else if (more) {
+                nxt_bad = bad_pages_of(nxt_page);
+                next = steps_of(nxt_pos) > 0;
+                if (next) next_at = row_at(nxt, nxt_page, 0);
+            }
+            if (next) load_k(next_at);
+            if ((cur_bad >> i) & 1u)               // a row that reaches this step cannot be computed
+                bad_rows |= (cur_pos.pos[0] >= key0 ? 1u : 0u) | (cur_pos.pos[1] >= key0 ? 2u : 0u);
+            cur_pos.mask(st, key0, g8);
+            if (key0 + kStep - 1 > cur_pos.tmax) { // what lies behind the last key may hold anything
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (key0 + 2 * c4 + (k & 1) + 8 * (k >> 1) > cur_pos.tmax) {
+#pragma unroll
+                        for (int d = 0; d < KS; ++d) vr[k][d] = 0u;
+                    }
+            }
+            uint32_t hi[2], low[2];
+            rs.step(st, P.scale_log2, hi, low);
+            rs.add(hi, low, [&](int k, uint32_t (&a)[4]) {
+                a[0] = __byte_perm(vr[0][k], vr[1][k], 0x5410);
+                a[1] = __byte_perm(vr[0][k], vr[1][k], 0x7632);
+                a[2] = __byte_perm(vr[2][k], vr[3][k], 0x5410);
+                a[3] = __byte_perm(vr[2][k], vr[3][k], 0x7632);
+            });
+            if (next) load_v(next_at);
+        }
+        if (my_steps == 0 && more) {
+            nxt_bad = bad_pages_of(nxt_page);
+            if (steps_of(nxt_pos) > 0) {
+                next_at = row_at(nxt, nxt_page, 0);
+                load_k(next_at);
+                load_v(next_at);
+            }
+        }
+        float l[2];
+        rs.sum_lanes(l);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (g8 == 0) sm.ml[cls][2 * c4 + e] = make_float2(rs.m[e], (bad_rows >> e) & 1u ? -INFINITY : l[e]);
+            // acc[k][e], acc[k][e + 2]: dims 2 KS g8 + 2 k and + 1 of the row
+#pragma unroll
+            for (int k = 0; k < KS; k += 2)
+                *reinterpret_cast<float4*>(&sm.o[cls][2 * c4 + e][2 * KS * g8 + 2 * k]) =
+                    make_float4(rs.acc[k][e], rs.acc[k][e + 2], rs.acc[k + 1][e], rs.acc[k + 1][e + 2]);
+        }
+        __syncthreads();
+        join_classes<HD>(I, cur, 0, 8, &sm.o[0][0][0], &sm.ml[0][0], tid, kDirectThreads);
+        if (!more) break;
+        cur = nxt;
+        cur_pos = nxt_pos;
+        cur_page = nxt_page;
+        cur_bad = nxt_bad;
     }
+}
+
+// ---- staged: T tiles of 8 query rows, warp = 4 tile + class; the last warp fills
+// the ring.  A stage holds the four classes' 16-key steps of a round: K, then V,
+// rows of HD bf16 whose 16-byte chunks are permuted by the key's low three bits
+// (chunk ^ (key & 7)), so that neither the copies nor the fragments' reads meet a
+// bank twice.
+template <int HD>
+struct StagedLayout {
+    static constexpr int kRound = kClasses * kStep;                    // keys of a stage
+    static constexpr int kHalf = kRound * HD * 2;                      // bytes of its K (or V)
+    static constexpr int kStage = 2 * kHalf;
+    int o, q, ml, ring, stages, bytes;                                 // byte offsets; the table comes first
+    __host__ __device__ StagedLayout(int T) {
+        const int rows = 8 * T;
+        o = static_cast<int>(sizeof(LiveTable)) + 256;                 // barriers between
+        o = (o + 15) / 16 * 16;
+        q = o + kClasses * rows * (HD + 4) * 4;
+        ml = q + 2 * rows * (HD + 8) * 2;
+        ring = (ml + kClasses * rows * 8 + 127) / 128 * 128;
+        stages = (227 * 1024 - ring) / kStage;
+        if (stages > 6) stages = 6;
+        bytes = ring + stages * kStage;
+    }
+};
+
+struct StagedBars {
+    uint64_t full[6], empty[6];
+    uint32_t bad[6];            // classes of the stage whose page id is out of range
+    int abort_flag;
+};
+static_assert(sizeof(StagedBars) <= 256, "the layout leaves 256 bytes");
+
+// Sixteen bits by eight by eight of four tiles, transposed: the A fragment of V^T
+// for 16 dims and 16 keys.
+BIV_DEV void ldmatrix_x4_trans(uint32_t addr, uint32_t (&a)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+BIV_DEV void bar_sync_n(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+template <int HD>
+__global__ void __launch_bounds__(kStagedThreads, 1) paged_attn_staged_kernel(const PagedAttnParams P, const int T) {
+    constexpr int KS = HD / 16;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    LiveTable& table = *reinterpret_cast<LiveTable*>(smem_raw);
+    StagedBars& bars = *reinterpret_cast<StagedBars*>(smem_raw + (sizeof(LiveTable) + 7) / 8 * 8);
+    const StagedLayout<HD> L(T);
+    const int rows = 8 * T;
+    float* s_o = reinterpret_cast<float*>(smem_raw + L.o);
+    float2* s_ml = reinterpret_cast<float2*>(smem_raw + L.ml);
+    const uint32_t ring = smem_u32(smem_raw + L.ring);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int consumers = kClasses * T;                    // warps
+    if (tid == 0) {
+        for (int s = 0; s < L.stages; ++s) {
+            mbar_init(&bars.full[s], 33);                  // 32 lanes' copies and one plain arrival
+            mbar_init(&bars.empty[s], consumers);
+        }
+        bars.abort_flag = 0;
+        fence_mbar_init();
+    }
+    const Items I(P, table, rows);                         // its barriers also publish the mbarriers
+    pdl_wait();
+    pdl_trigger();
+    I.zero_rows<HD>();
+    int stage = 0;
+    uint32_t phase = 0;
+    auto advance = [&]() {
+        if (++stage == L.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    };
+
+    if (warp == consumers) {
+        // ------------------------------------------------------- producer
+        const int ck = lane % (HD / 8), rk = lane / (HD / 8);          // chunk of a row, row of a group
+        constexpr int RPI = 32 / (HD / 8);                              // rows of one copy instruction
+        AttnItem it;
+        for (bool more = I.first(it); more; more = I.next(it, it)) {
+            const int tmax = I.largest_pos(it, it.tile * rows, rows);
+            const int key_lo = it.split * kSplit;
+            const int nsteps = Items::steps_to(tmax, it.split);
+            int page = 0;                                  // lane i: page of the split's i-th step
+            if (lane < nsteps)
+                page = P.pt.table[static_cast<long long>(P.row_slot[it.w0]) * P.pt.max_pages +
+                                  ((key_lo + kStep * lane) >> P.pt.page_shift)];
+            const bool ok = page >= 0 && page < P.pt.n_pages;
+            if (!ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
+            const uint32_t bad = ~__ballot_sync(0xffffffffu, ok);
+            for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err, true))) {
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    return;
+                }
+                const uint32_t base = ring + static_cast<uint32_t>(stage * L.kStage);
+#pragma unroll 1
+                for (int k = 0; k < kClasses; ++k) {
+                    const int step = s0 + k;
+                    const int pg = __shfl_sync(0xffffffffu, page, step & 31);
+                    const int key0 = key_lo + kStep * step;
+                    const bool live = step < nsteps && !((bad >> step) & 1u);
+                    const long long at = ((static_cast<long long>(live ? pg : 0) * P.Hkv + it.kvh) * P.pt.page_size +
+                                          (live ? key0 & (P.pt.page_size - 1) : 0)) * HD + ck * 8;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    const int d = threadIdx.x;
-    if (d < HD) {
-        float x = 0.0f;
+                    for (int r = 0; r < kStep; r += RPI) {
+                        const int row = r + rk;            // key of the step; what lies behind the last key reads as zeros
+                        const bool read = live && key0 + row <= tmax;
+                        const uint32_t dst = base + static_cast<uint32_t>((k * kStep + row) * HD * 2 + ((ck ^ (row & 7)) * 16));
+                        cp_async16_or_zero(dst, P.kp + at + row * HD, read);
+                        cp_async16_or_zero(dst + L.kHalf, P.vp + at + row * HD, read);
+                    }
+                }
+                if (lane == 0) {
+                    bars.bad[stage] = (bad >> s0) & ((1u << kClasses) - 1u);
+                    mbar_arrive(&bars.full[stage]);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.full[stage])) : "memory");
+                advance();
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
+
+    // ---------------------------------------------------------- consumers
+    const int g8 = lane >> 2, c4 = lane & 3;
+    const int tile = warp / kClasses, cls = warp % kClasses;
+    const int threads = 32 * consumers;
+    __nv_bfloat16* s_q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L.q);
+    constexpr int QP = HD + 8;
+    // this lane's row of the four 8 x 8 tiles of V^T: key (lane & 7) + 8 (lane / 16), dims 8 ((lane / 8) & 1) on
+    const int vkey = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
+    const uint32_t kbase = static_cast<uint32_t>((cls * kStep + g8) * HD * 2);
+    const uint32_t vbase = static_cast<uint32_t>(StagedLayout<HD>::kHalf + (cls * kStep + vkey) * HD * 2);
+    AttnItem cur, nxt;
+    if (!I.first(cur)) return;
+    load_q<HD>(P, cur, cur.tile * rows, rows, s_q, QP, tid, threads);
+    bool ok = true;                                        // after a wait that ran out: no more waits, every barrier still met
+    for (int buf = 0;; buf ^= 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        bar_sync_n(1, threads);                            // Q has landed; every warp has joined the item before
+        const bool more = I.next(cur, nxt);
+        if (more) load_q<HD>(P, nxt, nxt.tile * rows, rows, s_q + (buf ^ 1) * rows * QP, QP, tid, threads);
+        const int r0 = cur.tile * rows;
+        const TilePos tp(I, cur, r0 + 8 * tile, c4);
+        const int key_lo = cur.split * kSplit;
+        const int nsteps = Items::steps_to(I.largest_pos(cur, r0, rows), cur.split);      // those the producer brings
+        const __nv_bfloat16* q = s_q + (buf * rows + 8 * tile + g8) * QP + 16 * c4;
+        RowState<HD> rs;
+        rs.clear();
+        uint32_t bad_rows = 0;
+#pragma unroll 1
+        for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, &bars.abort_flag, &g_paged_err));
+            if (!ok) break;
+            const int step = s0 + cls, key0 = key_lo + kStep * step;
+            if (step < tp.nsteps) {
+                const uint32_t base = ring + static_cast<uint32_t>(stage * L.kStage);
+                float s4[4][4] = {}, st[4];
 #pragma unroll
-        for (int k = 0; k < kCombineWarps; ++k) x += s_acc[k][d];
-        P.o[pair * HD + d] = __float2bfloat16_rn(bad ? 0.0f : x / l);
+                for (int k = 0; k < KS; k += 2) {
+                    // 16 bytes of keys g8 and g8 + 8: dims 16 c4 + 64 b + 2 r .. as the direct kernel holds them
+                    const int chunk = 8 * (k >> 2) + 2 * c4 + ((k & 2) >> 1);
+                    const uint32_t at = base + kbase + static_cast<uint32_t>((chunk ^ g8) * 16);
+                    uint4 k0, k1;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(k0.x), "=r"(k0.y), "=r"(k0.z), "=r"(k0.w) : "r"(at) : "memory");
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(k1.x), "=r"(k1.y), "=r"(k1.z), "=r"(k1.w) : "r"(at + 8 * HD * 2) : "memory");
+                    const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * (k >> 2) + 4 * (k & 3));
+                    mma_16816(s4[k & 3], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+                    mma_16816(s4[(k & 3) + 1], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[e] = (s4[0][e] + s4[1][e]) + (s4[2][e] + s4[3][e]);
+                if ((bars.bad[stage] >> cls) & 1u)
+                    bad_rows |= (tp.pos[0] >= key0 ? 1u : 0u) | (tp.pos[1] >= key0 ? 2u : 0u);
+                tp.mask(st, key0, g8);
+                uint32_t hi[2], low[2];
+                rs.step(st, P.scale_log2, hi, low);
+                rs.add(hi, low, [&](int k, uint32_t (&a)[4]) {
+                    ldmatrix_x4_trans(base + vbase + static_cast<uint32_t>(((2 * k + vch) ^ (vkey & 7)) * 16), a);
+                });
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.empty[stage]);
+            advance();
+        }
+        float l[2];
+        rs.sum_lanes(l);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = cls * rows + 8 * tile + 2 * c4 + e;
+            if (g8 == 0) s_ml[row] = make_float2(rs.m[e], (bad_rows >> e) & 1u ? -INFINITY : l[e]);
+            // acc[k][e], acc[k][e + 2]: dims 16 k + g8 and + 8 of the row
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                s_o[row * (HD + 4) + 16 * k + g8] = rs.acc[k][e];
+                s_o[row * (HD + 4) + 16 * k + 8 + g8] = rs.acc[k][e + 2];
+            }
+        }
+        bar_sync_n(1, threads);
+        join_classes<HD>(I, cur, r0, rows, s_o, s_ml, tid, threads);
+        if (!more) break;
+        cur = nxt;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Joins the splits of a (row, head) in an order that goes by their number alone:
+// blocks of 16 splits are summed in split order, then the blocks in block order.
+// A row of up to kAlone splits is one warp's work; a longer one is shared by all
+// warps of its CTA, which take a block each, so that one very long row does not
+// wait for one warp's loads.  Rows of a single split were finished by the split
+// kernel.
+constexpr int kCombineWarps = 16;
+constexpr int kBlock = 16;
+constexpr int kAlone = 4 * kBlock;
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const PagedAttnParams P, int per_cta) {
+    constexpr int E = HD / 32;
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    __shared__ float s_acc[kCombineWarps][HD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long pairs = static_cast<long long>(P.W) * P.Hq;
+    const long long first = static_cast<long long>(blockIdx.x) * per_cta;
+    const long long mine = first + warp;
+    const int my_pos = warp < per_cta && mine < pairs ? usable_pos(P, static_cast<int>(mine / P.Hq), false) : -1;
+    pdl_wait();
+    pdl_trigger();
+
+    // maximum and sum over a row's splits, the same in every warp that asks
+    auto head = [&](long long pair, int ns, float& m, float& inv_l) {
+        const float2* ml = P.ws_ml + pair * P.s_max;
+        m = -INFINITY;
+        float l = 0.0f;
+        bool bad = false;
+        for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int s = lane; s < ns; s += 32) {
+            const float2 x = ml[s];
+            bad |= x.y == -1.0f;
+            l = fmaf(x.y, ex2_approx(x.x - m), l);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        inv_l = 1.0f / l;
+        return __any_sync(0xffffffffu, bad);
+    };
+    // a block's sum: all of its loads in flight at once
+    auto block_sum = [&](long long pair, int s0, int ns, float m, float (&acc)[E]) {
+        const float2* ml = P.ws_ml + pair * P.s_max;
+        const float* o = P.ws_o + (pair * P.s_max + s0) * HD + lane * E;
+        Vec v[kBlock];
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k)
+            if (s0 + k < ns) v[k] = *reinterpret_cast<const Vec*>(o + static_cast<long long>(k) * HD);
+        const float f_lane = s0 + (lane & (kBlock - 1)) < ns ? ex2_approx(ml[s0 + (lane & (kBlock - 1))].x - m) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) {
+            const float f = __shfl_sync(0xffffffffu, f_lane, k);
+            if (s0 + k < ns) {
+                const float* x = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+            }
+        }
+    };
+    auto store = [&](long long pair, const float (&x)[E], float inv_l, bool bad) {
+        uint32_t y[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = bad ? 0u : pack_bf16x2(x[2 * e] * inv_l, x[2 * e + 1] * inv_l);
+        __nv_bfloat16* dst = P.o + pair * HD + lane * E;
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = y[0];
+    };
+
+    const int my_ns = my_pos < 0 ? 0 : my_pos / kSplit + 1;
+    if (my_ns > 1 && my_ns <= kAlone) {
+        float m, inv_l, total[E] = {}, acc[E];
+        const bool bad = head(mine, my_ns, m, inv_l);
+        for (int s0 = 0; s0 < my_ns; s0 += kBlock) {
+            block_sum(mine, s0, my_ns, m, acc);
+#pragma unroll
+            for (int e = 0; e < E; ++e) total[e] += acc[e];
+        }
+        store(mine, total, inv_l, bad);
+    }
+    if (!__syncthreads_or(my_ns > kAlone)) return;
+    for (int p = 0; p < per_cta && first + p < pairs; ++p) {
+        const long long pair = first + p;
+        const int pos = usable_pos(P, static_cast<int>(pair / P.Hq), false);
+        const int ns = pos < 0 ? 0 : pos / kSplit + 1;
+        if (ns <= kAlone) continue;
+        float m, inv_l, total[E] = {}, acc[E];
+        const bool bad = head(pair, ns, m, inv_l);
+        for (int s0 = 0; s0 < ns; s0 += kBlock * kCombineWarps) {          // a block of each warp
+            const int mine0 = s0 + kBlock * warp;
+            if (mine0 < ns) {
+                block_sum(pair, mine0, ns, m, acc);
+#pragma unroll
+                for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+            }
+            __syncthreads();
+            if (warp == 0)
+                for (int k = 0; k < kCombineWarps && s0 + kBlock * k < ns; ++k)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) total[e] += s_acc[k][lane * E + e];
+            __syncthreads();
+        }
+        if (warp == 0) store(pair, total, inv_l, bad);
     }
 }
 
@@ -621,21 +1032,41 @@ int check_pages(int n_slots, int max_pages, int n_pages, int page_size, PageTabl
     return BIV_OK;
 }
 
-template <int HD, int NT>
-int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
-    const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
-    const long long tiles = (static_cast<long long>(P.rpg) * P.G + 8 * NT - 1) / (8 * NT);
-    const long long most = n_groups * P.Hkv * tiles * P.s_max;
-    const long long grid = std::min<long long>(most, static_cast<long long>(num_sms()) * (NT == 1 ? 3 : 2));
-    int st = launch_pdl(paged_attn_kernel<HD, NT>, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, s, P);
-    if (st != BIV_OK || P.s_max == 1) return st;
-    const long long pairs = static_cast<long long>(P.W) * P.Hq;
-    return launch_pdl(paged_combine_kernel<HD>, dim3(static_cast<unsigned>(pairs)), dim3(32 * kCombineWarps), 0, s, P);
-}
-
+// The split kernel and, where a row may have several splits, the combine kernel.
 template <int HD>
 int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
-    return static_cast<long long>(P.rpg) * P.G <= 8 ? launch_paged_attn<HD, 1>(P, s) : launch_paged_attn<HD, 2>(P, s);
+    static DeviceOnce once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    int st = once.run(dev, [] {
+        const cudaError_t e1 = cudaFuncSetAttribute(paged_attn_direct_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(sizeof(DirectSmem<HD>)));
+        if (e1 != cudaSuccess) return cuda_status(e1);
+        return cuda_status(cudaFuncSetAttribute(paged_attn_staged_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                227 * 1024));
+    });
+    if (st != BIV_OK) return st;
+    const long long rows = static_cast<long long>(P.rpg) * P.G;
+    const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
+    if (rows <= 8) {
+        const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max, 3LL * num_sms());
+        st = launch_pdl(paged_attn_direct_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(kDirectThreads),
+                        sizeof(DirectSmem<HD>), s, P);
+    } else {
+        // as few passes over the keys as four tiles allow, each with as few tiles as they then need
+        const long long passes = (rows + 8 * kMaxTiles - 1) / (8 * kMaxTiles);
+        const int T = static_cast<int>((rows + 8 * passes - 1) / (8 * passes));
+        const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * passes, num_sms());
+        st = launch_pdl(paged_attn_staged_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(32 * kClasses * T + 32),
+                        static_cast<size_t>(StagedLayout<HD>(T).bytes), s, P, T);
+    }
+    if (st != BIV_OK || P.s_max == 1) return st;
+    // few rows: a CTA each, so that a long row has the whole CTA
+    const long long pairs = static_cast<long long>(P.W) * P.Hq;
+    const int per_cta = static_cast<int>(std::min<long long>(kCombineWarps, (pairs + num_sms() - 1) / num_sms()));
+    return launch_pdl(paged_combine_kernel<HD>, dim3(static_cast<unsigned>((pairs + per_cta - 1) / per_cta)),
+                      dim3(32 * kCombineWarps), 0, s, P, per_cta);
 }
 
 }  // namespace
@@ -711,6 +1142,10 @@ extern "C" int biv_decode_attn_paged(const void* q, const void* k_pages, const v
     P.Hq = Hq;
     P.Hkv = Hkv;
     P.cap = max_pages * page_size;
+    // i / G by a multiplication: exact while i * G stays below 2^32
+    P.g_magic = P.G > 1 && static_cast<double>(P.rpg) * P.G * P.G < 4294967296.0
+                    ? static_cast<uint32_t>((4294967296ull + P.G - 1) / P.G)
+                    : 0u;
     P.s_max = (P.cap + kSplit - 1) / kSplit;
     P.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
     const long long parts = static_cast<long long>(W) * Hq * P.s_max;
