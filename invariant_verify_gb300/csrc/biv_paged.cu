@@ -2,6 +2,7 @@
 // fixed-split decode attention over them.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <type_traits>
 
 #include "biv_common.cuh"
@@ -172,9 +173,7 @@ constexpr int kSteps = kSplit / kStep;                 // steps of a split
 constexpr int kStepsPerClass = kSteps / kClasses;
 constexpr int kDirectThreads = 32 * kClasses;
 constexpr int kMaxGroups = 1024;       // entries of the table of live splits; more groups share entries
-constexpr int kMaxRows = 4096;         // rows whose positions are kept in shared memory; with more they are read again
-constexpr int kMaxTiles = 3;           // 8-row tiles of a staged item
-constexpr int kStagedThreads = 32 * kClasses * kMaxTiles + 32;
+constexpr int kMaxRows = 2048;         // rows whose positions are kept in shared memory; with more they are read again
 
 // 32 or 16 bytes of a row of keys or values: read once, so not kept in L1.
 BIV_DEV void ld_row(const __nv_bfloat16* p, uint32_t (&r)[8]) {
@@ -215,12 +214,13 @@ BIV_DEV void cp_async16_or_zero(uint32_t smem, const void* gmem, bool read) {
 // 2 (lane % 4) and the next; acc holds HD / 16 tiles of O^T.
 template <int HD>
 struct RowState {
-    float acc[HD / 16][4];
+    static constexpr int KS = HD / 16;
+    float acc[KS][4];
     float m[2], l[2];
 
     BIV_DEV void clear() {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
         m[0] = m[1] = -INFINITY;
@@ -228,7 +228,7 @@ struct RowState {
     }
 
     // Scores of a step (S^T fragment: keys g8 and g8 + 8) to weights: the running
-    // maximum and sum move on, the output is rescaled where a maximum grew (a
+    // maxima and sums move on, the output is rescaled where a maximum grew (the
     // factor of a row that did not is exactly 1), and each weight leaves as the
     // sum of two bf16 values, transposed to the B fragments of O^T += V^T P^T.
     BIV_DEV void step(float (&st)[4], float scale_log2, uint32_t (&hi)[2], uint32_t (&low)[2]) {
@@ -253,12 +253,6 @@ struct RowState {
             st[e + 2] = ex2_approx(fmaf(st[e + 2], scale_log2, -mu));
             l[e] = fmaf(l[e], f[e], st[e] + st[e + 2]);
         }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[k][e] *= f[e & 1];
-        }
         const uint32_t h0 = pack_bf16x2(st[0], st[1]), h1 = pack_bf16x2(st[2], st[3]);
         const uint32_t l0 = pack_bf16x2(st[0] - bf16lo(h0), st[1] - bf16hi(h0));
         const uint32_t l1 = pack_bf16x2(st[2] - bf16lo(h1), st[3] - bf16hi(h1));
@@ -266,6 +260,12 @@ struct RowState {
         hi[1] = transpose8(h1);
         low[0] = transpose8(l0);
         low[1] = transpose8(l1);
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][e] *= f[e & 1];
+        }
     }
 
     // O^T += V^T (hi + low); frag(k, a) gives the A fragment of dims tile k.  The
@@ -273,7 +273,7 @@ struct RowState {
     // wait for the first.
     template <typename F>
     BIV_DEV void add(const uint32_t (&hi)[2], const uint32_t (&low)[2], F&& frag) {
-        constexpr int KS = HD / 16, kSkew = 2;
+        constexpr int kSkew = 2;
         uint32_t a[KS][4];
 #pragma unroll
         for (int k = 0; k < KS + kSkew; ++k) {
@@ -288,18 +288,29 @@ struct RowState {
         }
     }
 
-    // The sums over the lanes that share a column.
-    BIV_DEV void sum_lanes(float (&sum)[2]) const {
-        sum[0] = l[0];
-        sum[1] = l[1];
+    // Maximum and sum of every row to ml[row]; a row whose bit e is set in bad met a
+    // page id out of range.
+    BIV_DEV void put_ml(float2* ml, uint32_t bad, int g8, int c4) const {
+        float s0 = l[0], s1 = l[1];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
-            const float y0 = __shfl_xor_sync(0xffffffffu, sum[0], d), y1 = __shfl_xor_sync(0xffffffffu, sum[1], d);
-            sum[0] += y0;
-            sum[1] += y1;
+            const float y0 = __shfl_xor_sync(0xffffffffu, s0, d), y1 = __shfl_xor_sync(0xffffffffu, s1, d);
+            s0 += y0;
+            s1 += y1;
+        }
+        if (g8 == 0) {
+            ml[2 * c4] = make_float2(m[0], bad & 1u ? -INFINITY : s0);
+            ml[2 * c4 + 1] = make_float2(m[1], bad & 2u ? -INFINITY : s1);
         }
     }
 };
+
+// Scores of keys past a row's position count as -infinity.
+BIV_DEV void mask_step(float (&st)[4], const int (&pos)[2], int key0, int g8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (key0 + g8 + 8 * (e >> 1) > pos[e & 1]) st[e] = -INFINITY;
+}
 
 // One item; unit counts (request, split) pairs, sub (KV head, tile).
 struct AttnItem {
@@ -312,6 +323,7 @@ struct AttnItem {
 struct LiveTable {
     int pre[kMaxGroups + 1];   // live splits before each entry
     int pos[kMaxRows];         // usable position of every row, -1: none
+    int slot[kMaxRows];
     int scan[32];
 };
 
@@ -335,7 +347,10 @@ struct Items {
         step_sub = gridDim.x - step_unit * per_unit;
         const int threads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         if (kept)
-            for (int w = tid; w < P.W; w += threads) t.pos[w] = usable_pos(P, w, blockIdx.x == 0);
+            for (int w = tid; w < P.W; w += threads) {
+                t.slot[w] = P.row_slot[w];
+                t.pos[w] = usable_pos(P, w, blockIdx.x == 0);
+            }
         else if (blockIdx.x == 0)
             for (int w = tid; w < P.W; w += threads) usable_pos(P, w, true);
         __syncthreads();
@@ -365,6 +380,7 @@ struct Items {
     }
 
     BIV_DEV int pos_of(int w) const { return kept ? t.pos[w] : usable_pos(P, w, false); }
+    BIV_DEV int slot_of(int w) const { return kept ? t.slot[w] : P.row_slot[w]; }
     BIV_DEV int splits_of(int g) const {
         int best = -1;
         const int w1 = min(P.W, (g + 1) * P.rpg);
@@ -440,39 +456,16 @@ struct Items {
     }
 };
 
-// Positions of a lane's two query rows of an 8-row tile (first query row r0 of
-// the group), the tile's smallest and largest, and the steps some row reaches.
-struct TilePos {
-    int pos[2], tmin, tmax, nsteps;
-    BIV_DEV TilePos() {}
-    BIV_DEV TilePos(const Items& I, const AttnItem& it, int r0, int c4) {
-        tmax = -1;
-        tmin = 0x7fffffff;
+// Positions of a lane's two query rows of an 8-row tile that starts at query row r0.
+BIV_DEV void tile_pos(const Items& I, int w0, int rows, int r0, int c4, int (&pos)[2]) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = r0 + 2 * c4 + e;
-            int row, head;
-            row_head(I.P, i, row, head);
-            pos[e] = i < it.rows ? I.pos_of(it.w0 + row) : -1;
-            tmax = max(tmax, pos[e]);
-            tmin = min(tmin, pos[e]);
-        }
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, d));
-            tmin = min(tmin, __shfl_xor_sync(0xffffffffu, tmin, d));
-        }
-        nsteps = Items::steps_to(tmax, it.split);
+    for (int e = 0; e < 2; ++e) {
+        const int i = r0 + 2 * c4 + e;
+        int row, head;
+        row_head(I.P, i, row, head);
+        pos[e] = i < rows ? I.pos_of(w0 + row) : -1;
     }
-    // Scores of keys past a row's position count as -infinity.
-    BIV_DEV void mask(float (&st)[4], int key0, int g8) const {
-        if (key0 + kStep - 1 > tmin) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (key0 + g8 + 8 * (e >> 1) > pos[e & 1]) st[e] = -INFINITY;
-        }
-    }
-};
+}
 
 // Q of `rows` query rows from r0 on, 16 bytes a thread; rows past the group's
 // read its first row and are never used.
@@ -490,9 +483,29 @@ BIV_DEV void load_q(const PagedAttnParams& P, const AttnItem& it, int r0, int ro
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// The classes' shares of each row of an item, joined in class order: o[class][row]
-// and ml[class][row] (sum -infinity: the row met a page id out of range).  A
-// row's only split is finished here, others go to the workspace.
+// How the classes' shares of a row are joined: the row's maximum, the factor of a
+// class, and the row's sum.  A sum of -infinity marks a class that met a page id out
+// of range; the row's sum is then -1.
+BIV_DEV float classes_max(const float2 (&ml)[kClasses]) {
+    return fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+}
+BIV_DEV float class_factor(const float2& ml, float mx) { return ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mx); }
+BIV_DEV float classes_sum(const float2 (&ml)[kClasses], float mx) {
+    float sum = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kClasses; ++k) {
+        bad |= ml[k].y == -INFINITY;
+        sum = fmaf(ml[k].y, class_factor(ml[k], mx), sum);
+    }
+    return bad ? -1.0f : sum;
+}
+
+// Four classes' scaled outputs of one element, in the order both kernels use.
+BIV_DEV float join4(float c0, float c1, float c2, float c3) { return __fadd_rn(__fadd_rn(c0, c2), __fadd_rn(c1, c3)); }
+
+// The classes' shares of each row of a direct item: o[class][row], ml[class][row].
+// A row's only split is finished here, others go to the workspace.
 template <int HD>
 BIV_DEV void join_classes(const Items& I, const AttnItem& it, int r0, int rows, const float* o, const float2* ml, int tid,
                           int threads) {
@@ -507,32 +520,33 @@ BIV_DEV void join_classes(const Items& I, const AttnItem& it, int r0, int rows, 
         const int w = it.w0 + j;
         const int pos = I.pos_of(w);
         if (pos < it.split * kSplit) continue;
-        float mx = -INFINITY, sum = 0.0f;
-        bool bad = false;
-#pragma unroll
-        for (int k = 0; k < kClasses; ++k) mx = fmaxf(mx, ml[k * rows + row].x);
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float2 c[kClasses];
+        float4 y[kClasses];
 #pragma unroll
         for (int k = 0; k < kClasses; ++k) {
-            const float2 c = ml[k * rows + row];
-            bad |= c.y == -INFINITY;
-            const float f = c.x == -INFINITY ? 0.0f : ex2_approx(c.x - mx);
-            sum = fmaf(c.y, f, sum);
-            const float4 y = *reinterpret_cast<const float4*>(o + (k * rows + row) * HDP + d);
-            x.x = fmaf(y.x, f, x.x);
-            x.y = fmaf(y.y, f, x.y);
-            x.z = fmaf(y.z, f, x.z);
-            x.w = fmaf(y.w, f, x.w);
+            c[k] = ml[k * rows + row];
+            y[k] = *reinterpret_cast<const float4*>(o + (k * rows + row) * HDP + d);
         }
+        const float mx = classes_max(c), sum = classes_sum(c, mx);
+#pragma unroll
+        for (int k = 0; k < kClasses; ++k) {
+            const float f = class_factor(c[k], mx);
+            y[k].x *= f;
+            y[k].y *= f;
+            y[k].z *= f;
+            y[k].w *= f;
+        }
+        const float4 x = make_float4(join4(y[0].x, y[1].x, y[2].x, y[3].x), join4(y[0].y, y[1].y, y[2].y, y[3].y),
+                                     join4(y[0].z, y[1].z, y[2].z, y[3].z), join4(y[0].w, y[1].w, y[2].w, y[3].w));
         const long long pair = static_cast<long long>(w) * P.Hq + it.kvh * P.G + head;
         if (pos < kSplit) {
             const float scale = 1.0f / sum;
-            uint2 y = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
-            if (bad) y = make_uint2(0, 0);
-            *reinterpret_cast<uint2*>(P.o + pair * HD + d) = y;
+            uint2 z = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
+            if (sum == -1.0f) z = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(P.o + pair * HD + d) = z;
         } else {
             const long long part = pair * P.s_max + it.split;
-            if (d == 0) P.ws_ml[part] = make_float2(mx, bad ? -1.0f : sum);
+            if (d == 0) P.ws_ml[part] = make_float2(mx, sum);
             *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
         }
     }
@@ -561,10 +575,10 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
 
     uint32_t kr[2][KC][8];                         // keys g8 and g8 + 8 of a step
     uint32_t vr[4][KS];                            // keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9: dims [2 KS g8, ..)
-    auto page_of = [&](const AttnItem& it, const TilePos& tp) {        // lane i: page of this class's i-th step
+    auto page_of = [&](const AttnItem& it, int nsteps) {        // lane i: page of this class's i-th step
         int page = 0;
-        if (lane < kStepsPerClass && cls + kClasses * lane < tp.nsteps)
-            page = P.pt.table[static_cast<long long>(P.row_slot[it.w0]) * P.pt.max_pages +
+        if (lane < kStepsPerClass && cls + kClasses * lane < nsteps)
+            page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
                               ((it.split * kSplit + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
         return page;
     };
@@ -591,15 +605,28 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
 #pragma unroll
         for (int k = 0; k < 4; ++k) ld_row(P.vp + at + (2 * c4 + (k & 1) + 8 * (k >> 1)) * HD + 2 * KS * g8, vr[k]);
     };
-    auto steps_of = [&](const TilePos& tp) { return (tp.nsteps - cls + kClasses - 1) / kClasses; };
+    auto steps_of = [&](int nsteps) { return (nsteps - cls + kClasses - 1) / kClasses; };
 
     AttnItem cur, nxt;
     if (!I.first(cur)) return;
     load_q<HD>(P, cur, 0, 8, &sm.q[0][0][0], HD + 8, tid, kDirectThreads);
-    TilePos cur_pos(I, cur, 0, c4), nxt_pos;
-    int cur_page = page_of(cur, cur_pos), nxt_page = 0;
+    // the group's largest position, each lane's rows' and the steps that some row reaches
+    auto describe = [&](const AttnItem& it, int (&pos)[2], int& tmax) {
+        tile_pos(I, it.w0, it.rows, 0, c4, pos);
+        tmax = max(pos[0], pos[1]);
+        if (P.rpg > 1) {
+            tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+            tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+        } else {
+            tmax = I.pos_of(it.w0);
+        }
+        return Items::steps_to(tmax, it.split);
+    };
+    int cur_pos[2], nxt_pos[2], cur_tmax, nxt_tmax = -1;
+    int cur_steps = describe(cur, cur_pos, cur_tmax), nxt_steps = 0;
+    int cur_page = page_of(cur, cur_steps), nxt_page = 0;
     uint32_t cur_bad = bad_pages_of(cur_page), nxt_bad = 0;
-    if (steps_of(cur_pos) > 0) {
+    if (steps_of(cur_steps) > 0) {
         const long long at = row_at(cur, cur_page, 0);
         load_k(at);
         load_v(at);
@@ -611,46 +638,46 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         const bool more = I.next(cur, nxt);
         if (more) {
             load_q<HD>(P, nxt, 0, 8, &sm.q[buf ^ 1][0][0], HD + 8, tid, kDirectThreads);
-            nxt_pos = TilePos(I, nxt, 0, c4);
-            nxt_page = page_of(nxt, nxt_pos);
+            nxt_steps = describe(nxt, nxt_pos, nxt_tmax);
+            nxt_page = page_of(nxt, nxt_steps);
         }
         RowState<HD> rs;
         rs.clear();
         uint32_t bad_rows = 0;                     // bit e: the row met a page id out of range
-        const int my_steps = steps_of(cur_pos);
+        const int my_steps = steps_of(cur_steps);
         long long next_at = 0;
         bool next = false;
 #pragma unroll 1
         for (int i = 0; i < my_steps; ++i) {
             const int key0 = cur.split * kSplit + kStep * (cls + kClasses * i);
-            // four chains, so that an MMA does not wait for the one before it
-            float s4[4][4] = {}, st[4];
+            // two chains, so that an MMA does not wait for the one before it
+            float s2[2][4] = {}, st[4];
 #pragma unroll
             for (int k = 0; k < KS; k += 2) {
                 const int b = k >> 2, r = 2 * (k & 3);
                 const uint4 qv = *reinterpret_cast<const uint4*>(&sm.q[buf][g8][64 * b + 16 * c4 + 2 * r]);
-                mma_16816(s4[k & 3], kr[0][b][r], kr[1][b][r], kr[0][b][r + 1], kr[1][b][r + 1], qv.x, qv.y);
-                mma_16816(s4[(k & 3) + 1], kr[0][b][r + 2], kr[1][b][r + 2], kr[0][b][r + 3], kr[1][b][r + 3], qv.z, qv.w);
+                mma_16816(s2[0], kr[0][b][r], kr[1][b][r], kr[0][b][r + 1], kr[1][b][r + 1], qv.x, qv.y);
+                mma_16816(s2[1], kr[0][b][r + 2], kr[1][b][r + 2], kr[0][b][r + 3], kr[1][b][r + 3], qv.z, qv.w);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st[e] = (s4[0][e] + s4[1][e]) + (s4[2][e] + s4[3][e]);
+            for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
             // the keys of this class's next step, or of its first step of the next item
             next = i + 1 < my_steps;
             if (next) {
                 next_at = row_at(cur, cur_page, i + 1);
             } else if (more) {
                 nxt_bad = bad_pages_of(nxt_page);
-                next = steps_of(nxt_pos) > 0;
+                next = steps_of(nxt_steps) > 0;
                 if (next) next_at = row_at(nxt, nxt_page, 0);
             }
             if (next) load_k(next_at);
             if ((cur_bad >> i) & 1u)               // a row that reaches this step cannot be computed
-                bad_rows |= (cur_pos.pos[0] >= key0 ? 1u : 0u) | (cur_pos.pos[1] >= key0 ? 2u : 0u);
-            cur_pos.mask(st, key0, g8);
-            if (key0 + kStep - 1 > cur_pos.tmax) { // what lies behind the last key may hold anything
+                bad_rows |= (cur_pos[0] >= key0 ? 1u : 0u) | (cur_pos[1] >= key0 ? 2u : 0u);
+            mask_step(st, cur_pos, key0, g8);
+            if (key0 + kStep - 1 > cur_tmax) {     // what lies behind the last key may hold anything
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (key0 + 2 * c4 + (k & 1) + 8 * (k >> 1) > cur_pos.tmax) {
+                    if (key0 + 2 * c4 + (k & 1) + 8 * (k >> 1) > cur_tmax) {
 #pragma unroll
                         for (int d = 0; d < KS; ++d) vr[k][d] = 0u;
                     }
@@ -667,17 +694,15 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         }
         if (my_steps == 0 && more) {
             nxt_bad = bad_pages_of(nxt_page);
-            if (steps_of(nxt_pos) > 0) {
+            if (steps_of(nxt_steps) > 0) {
                 next_at = row_at(nxt, nxt_page, 0);
                 load_k(next_at);
                 load_v(next_at);
             }
         }
-        float l[2];
-        rs.sum_lanes(l);
+        rs.put_ml(sm.ml[cls], bad_rows, g8, c4);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            if (g8 == 0) sm.ml[cls][2 * c4 + e] = make_float2(rs.m[e], (bad_rows >> e) & 1u ? -INFINITY : l[e]);
             // acc[k][e], acc[k][e + 2]: dims 2 KS g8 + 2 k and + 1 of the row
 #pragma unroll
             for (int k = 0; k < KS; k += 2)
@@ -688,45 +713,53 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         join_classes<HD>(I, cur, 0, 8, &sm.o[0][0][0], &sm.ml[0][0], tid, kDirectThreads);
         if (!more) break;
         cur = nxt;
-        cur_pos = nxt_pos;
+        cur_pos[0] = nxt_pos[0];
+        cur_pos[1] = nxt_pos[1];
+        cur_tmax = nxt_tmax;
+        cur_steps = nxt_steps;
         cur_page = nxt_page;
         cur_bad = nxt_bad;
     }
 }
 
-// ---- staged: T tiles of 8 query rows, warp = 4 tile + class; the last warp fills
-// the ring.  A stage holds the four classes' 16-key steps of a round: K, then V,
-// rows of HD bf16 whose 16-byte chunks are permuted by the key's low three bits
-// (chunk ^ (key & 7)), so that neither the copies nor the fragments' reads meet a
-// bank twice.
-template <int HD>
+// ---- staged: one CTA per SM; four producer warps, one per class, fill a ring of
+// rounds (the classes' 16-key steps: K, then V) for T groups of four consumer
+// warps, one per class again.  Group g takes tile g of every item.  Rows of HD bf16
+// whose 16-byte chunks are permuted by the key's low three bits (chunk ^ (key & 7)):
+// neither the copies nor the fragments' reads meet a bank twice.
+constexpr int kMaxStages = 6;
+
+struct StagedItem {
+    int w0, rows, kvh, r0, split, nsteps;   // w0 = -1: no more items
+    int stage;
+    uint32_t phase;
+};
+
+template <int HD, int T>
 struct StagedLayout {
-    static constexpr int kRound = kClasses * kStep;                    // keys of a stage
-    static constexpr int kHalf = kRound * HD * 2;                      // bytes of its K (or V)
+    static constexpr int kRows = 8 * T, kSlots = 2, QP = HD + 8, HDP = HD + 4;
+    static constexpr int kHalf = kClasses * kStep * HD * 2;             // bytes of a stage's K (or V)
     static constexpr int kStage = 2 * kHalf;
-    int o, q, ml, ring, stages, bytes;                                 // byte offsets; the table comes first
-    __host__ __device__ StagedLayout(int T) {
-        const int rows = 8 * T;
-        o = static_cast<int>(sizeof(LiveTable)) + 256;                 // barriers between
-        o = (o + 15) / 16 * 16;
-        q = o + kClasses * rows * (HD + 4) * 4;
-        ml = q + 2 * rows * (HD + 8) * 2;
-        ring = (ml + kClasses * rows * 8 + 127) / 128 * 128;
-        stages = (227 * 1024 - ring) / kStage;
-        if (stages > 6) stages = 6;
-        bytes = ring + stages * kStage;
-    }
+    static constexpr int kBars = (static_cast<int>(sizeof(LiveTable)) + 15) / 16 * 16;
+    static constexpr int kQ = kBars + 512;                              // [slots][rows][QP] bf16
+    static constexpr int kMl = kQ + kSlots * kRows * QP * 2;            // [groups][2 items][classes][8] float2
+    static constexpr int kO = kMl + T * 2 * kClasses * 8 * 8;           // [groups][2][8][HDP] float: two exchanges' halves
+    static constexpr int kRing = (kO + T * 2 * 8 * HDP * 4 + 127) / 128 * 128;
+    static constexpr int kFit = (227 * 1024 - kRing) / kStage;
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int kBytes = kRing + kStages * kStage;
+    static_assert(kStages >= 2, "the ring needs two stages");
 };
 
 struct StagedBars {
-    uint64_t full[6], empty[6];
-    uint32_t bad[6];            // classes of the stage whose page id is out of range
+    uint64_t full[kMaxStages], empty[kMaxStages], item_full[2], item_empty[2];
+    uint8_t bad[kMaxStages][kClasses];      // classes of the stage whose page id is out of range
+    StagedItem item[2];
     int abort_flag;
 };
-static_assert(sizeof(StagedBars) <= 256, "the layout leaves 256 bytes");
+static_assert(sizeof(StagedBars) <= 512, "the layout leaves 512 bytes");
 
-// Sixteen bits by eight by eight of four tiles, transposed: the A fragment of V^T
-// for 16 dims and 16 keys.
+// Four 8 x 8 tiles of bf16, transposed: the A fragment of V^T for 16 dims and 16 keys.
 BIV_DEV void ldmatrix_x4_trans(uint32_t addr, uint32_t (&a)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
@@ -734,174 +767,290 @@ BIV_DEV void ldmatrix_x4_trans(uint32_t addr, uint32_t (&a)[4]) {
                  : "memory");
 }
 
-BIV_DEV void bar_sync_n(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+BIV_DEV void group_bar(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+// The barrier and a vote: true if every thread of the group says so.
+BIV_DEV bool group_all(int group, bool ok) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(1 + group), "r"(ok ? 1u : 0u)
+                 : "memory");
+    return r != 0;
+}
+BIV_DEV void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
-template <int HD>
-__global__ void __launch_bounds__(kStagedThreads, 1) paged_attn_staged_kernel(const PagedAttnParams P, const int T) {
+template <int HD, int T>
+__global__ void __launch_bounds__(T * 128 + 128, 1) paged_attn_staged_kernel(const PagedAttnParams P) {
+    using L = StagedLayout<HD, T>;
     constexpr int KS = HD / 16;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     LiveTable& table = *reinterpret_cast<LiveTable*>(smem_raw);
-    StagedBars& bars = *reinterpret_cast<StagedBars*>(smem_raw + (sizeof(LiveTable) + 7) / 8 * 8);
-    const StagedLayout<HD> L(T);
-    const int rows = 8 * T;
-    float* s_o = reinterpret_cast<float*>(smem_raw + L.o);
-    float2* s_ml = reinterpret_cast<float2*>(smem_raw + L.ml);
-    const uint32_t ring = smem_u32(smem_raw + L.ring);
+    StagedBars& bars = *reinterpret_cast<StagedBars*>(smem_raw + L::kBars);
+    const uint32_t ring = smem_u32(smem_raw + L::kRing);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int consumers = kClasses * T;                    // warps
     if (tid == 0) {
-        for (int s = 0; s < L.stages; ++s) {
-            mbar_init(&bars.full[s], 33);                  // 32 lanes' copies and one plain arrival
-            mbar_init(&bars.empty[s], consumers);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&bars.full[s], kClasses * 33);       // of each producer warp 32 lanes' copies and one plain arrival
+            mbar_init(&bars.empty[s], kClasses * T);
+        }
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(&bars.item_full[s], kClasses * 32 + 1);
+            mbar_init(&bars.item_empty[s], kClasses * T);
         }
         bars.abort_flag = 0;
         fence_mbar_init();
     }
-    const Items I(P, table, rows);                         // its barriers also publish the mbarriers
+    const Items I(P, table, L::kRows);                     // its barriers also publish the mbarriers
     pdl_wait();
     pdl_trigger();
     I.zero_rows<HD>();
-    int stage = 0;
-    uint32_t phase = 0;
-    auto advance = [&]() {
-        if (++stage == L.stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
-    };
 
-    if (warp == consumers) {
-        // ------------------------------------------------------- producer
+    if (warp >= T * kClasses) {
+        // ------------------------------------------------------ producers
+        const int cls = warp - T * kClasses;
         const int ck = lane % (HD / 8), rk = lane / (HD / 8);          // chunk of a row, row of a group
         constexpr int RPI = 32 / (HD / 8);                              // rows of one copy instruction
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, slot_phase = 0;
+        bool ok = true;
+        auto hand = [&](const StagedItem& d) {             // publish an item; its Q, if any, was requested before
+            if (cls == 0 && lane == 0) {
+                bars.item[slot] = d;
+                mbar_arrive(&bars.item_full[slot]);
+            }
+            cp_async_arrive(&bars.item_full[slot]);
+            if (++slot == L::kSlots) {
+                slot = 0;
+                slot_phase ^= 1u;
+            }
+        };
+        auto free_slot = [&]() {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.item_empty[slot], slot_phase ^ 1u, &bars.abort_flag, &g_paged_err));
+            return ok;
+        };
         AttnItem it;
-        for (bool more = I.first(it); more; more = I.next(it, it)) {
-            const int tmax = I.largest_pos(it, it.tile * rows, rows);
+        for (bool more = I.first(it); more && ok; more = I.next(it, it)) {
+            const int r0 = it.tile * L::kRows;
+            const int tmax = I.largest_pos(it, r0, L::kRows);
             const int key_lo = it.split * kSplit;
             const int nsteps = Items::steps_to(tmax, it.split);
-            int page = 0;                                  // lane i: page of the split's i-th step
-            if (lane < nsteps)
-                page = P.pt.table[static_cast<long long>(P.row_slot[it.w0]) * P.pt.max_pages +
-                                  ((key_lo + kStep * lane) >> P.pt.page_shift)];
-            const bool ok = page >= 0 && page < P.pt.n_pages;
-            if (!ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
-            const uint32_t bad = ~__ballot_sync(0xffffffffu, ok);
+            if (nsteps == 0) continue;
+            int page = 0;                                  // lane i: page of this class's i-th step
+            if (lane < kStepsPerClass && cls + kClasses * lane < nsteps)
+                page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
+                                  ((key_lo + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
+            if (!free_slot()) break;
+            __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L::kQ) + slot * L::kRows * L::QP;
+            for (int r = cls * RPI + rk; r < L::kRows; r += kClasses * RPI) {      // rows past the group's read its first row and are never used
+                int j, head;
+                row_head(P, r0 + r < it.rows ? r0 + r : 0, j, head);
+                cp_async16(q + r * L::QP + ck * 8,
+                           P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + ck * 8);
+            }
+            hand(StagedItem{it.w0, it.rows, it.kvh, r0, it.split, nsteps, stage, phase});
+            const bool page_ok = page >= 0 && page < P.pt.n_pages;
+            if (!page_ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
+            const uint32_t bad = ~__ballot_sync(0xffffffffu, page_ok);
             for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err, true))) {
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    return;
-                }
-                const uint32_t base = ring + static_cast<uint32_t>(stage * L.kStage);
-#pragma unroll 1
-                for (int k = 0; k < kClasses; ++k) {
-                    const int step = s0 + k;
-                    const int pg = __shfl_sync(0xffffffffu, page, step & 31);
-                    const int key0 = key_lo + kStep * step;
-                    const bool live = step < nsteps && !((bad >> step) & 1u);
-                    const long long at = ((static_cast<long long>(live ? pg : 0) * P.Hkv + it.kvh) * P.pt.page_size +
-                                          (live ? key0 & (P.pt.page_size - 1) : 0)) * HD + ck * 8;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err));
+                if (!ok) break;
+                const int i = s0 / kClasses, step = s0 + cls;
+                const int pg = __shfl_sync(0xffffffffu, page, i);
+                const int key0 = key_lo + kStep * step;
+                const bool step_bad = (bad >> i) & 1u;
+                const bool live = step < nsteps && !step_bad;
+                const long long at = ((static_cast<long long>(live ? pg : 0) * P.Hkv + it.kvh) * P.pt.page_size +
+                                      (live ? key0 & (P.pt.page_size - 1) : 0)) * HD + ck * 8;
+                const __nv_bfloat16* ks = P.kp + at;
+                const __nv_bfloat16* vs = P.vp + at;
+                const uint32_t base = ring + static_cast<uint32_t>(stage * L::kStage + cls * kStep * HD * 2);
+                const int last = live ? tmax - key0 : -1;  // what lies behind the last key reads as zeros
 #pragma unroll
-                    for (int r = 0; r < kStep; r += RPI) {
-                        const int row = r + rk;            // key of the step; what lies behind the last key reads as zeros
-                        const bool read = live && key0 + row <= tmax;
-                        const uint32_t dst = base + static_cast<uint32_t>((k * kStep + row) * HD * 2 + ((ck ^ (row & 7)) * 16));
-                        cp_async16_or_zero(dst, P.kp + at + row * HD, read);
-                        cp_async16_or_zero(dst + L.kHalf, P.vp + at + row * HD, read);
-                    }
+                for (int r = 0; r < kStep; r += RPI) {
+                    const int row = r + rk;
+                    const uint32_t dst = base + static_cast<uint32_t>(row * HD * 2 + ((ck ^ (row & 7)) * 16));
+                    cp_async16_or_zero(dst, ks + row * HD, row <= last);
+                    cp_async16_or_zero(dst + L::kHalf, vs + row * HD, row <= last);
                 }
                 if (lane == 0) {
-                    bars.bad[stage] = (bad >> s0) & ((1u << kClasses) - 1u);
+                    bars.bad[stage][cls] = step_bad;
                     mbar_arrive(&bars.full[stage]);
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.full[stage])) : "memory");
-                advance();
+                cp_async_arrive(&bars.full[stage]);
+                if (++stage == L::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
         }
+        if (free_slot()) hand(StagedItem{-1, 0, 0, 0, 0, 0, 0, 0});
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
 
     // ---------------------------------------------------------- consumers
     const int g8 = lane >> 2, c4 = lane & 3;
-    const int tile = warp / kClasses, cls = warp % kClasses;
-    const int threads = 32 * consumers;
-    __nv_bfloat16* s_q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L.q);
-    constexpr int QP = HD + 8;
+    const int group = warp / kClasses, cls = warp % kClasses;
+    float2* s_ml2 = reinterpret_cast<float2*>(smem_raw + L::kMl) + group * 2 * kClasses * 8;
+    float* s_o = reinterpret_cast<float*>(smem_raw + L::kO) + group * 2 * 8 * L::HDP;
     // this lane's row of the four 8 x 8 tiles of V^T: key (lane & 7) + 8 (lane / 16), dims 8 ((lane / 8) & 1) on
     const int vkey = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
-    const uint32_t kbase = static_cast<uint32_t>((cls * kStep + g8) * HD * 2);
-    const uint32_t vbase = static_cast<uint32_t>(StagedLayout<HD>::kHalf + (cls * kStep + vkey) * HD * 2);
-    AttnItem cur, nxt;
-    if (!I.first(cur)) return;
-    load_q<HD>(P, cur, cur.tile * rows, rows, s_q, QP, tid, threads);
-    bool ok = true;                                        // after a wait that ran out: no more waits, every barrier still met
-    for (int buf = 0;; buf ^= 1) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        bar_sync_n(1, threads);                            // Q has landed; every warp has joined the item before
-        const bool more = I.next(cur, nxt);
-        if (more) load_q<HD>(P, nxt, nxt.tile * rows, rows, s_q + (buf ^ 1) * rows * QP, QP, tid, threads);
-        const int r0 = cur.tile * rows;
-        const TilePos tp(I, cur, r0 + 8 * tile, c4);
-        const int key_lo = cur.split * kSplit;
-        const int nsteps = Items::steps_to(I.largest_pos(cur, r0, rows), cur.split);      // those the producer brings
-        const __nv_bfloat16* q = s_q + (buf * rows + 8 * tile + g8) * QP + 16 * c4;
+    const int kbase = (cls * kStep + g8) * HD * 2;
+    const uint32_t vbase = static_cast<uint32_t>(L::kHalf + (cls * kStep + vkey) * HD * 2);
+    int slot = 0;
+    uint32_t slot_phase = 0;
+    for (int par = 0;; par ^= 1) {
+        // of two items in turn: a warp may still read the last item's while another is done with this one
+        float2* s_ml = s_ml2 + par * kClasses * 8;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.item_full[slot], slot_phase, &bars.abort_flag, &g_paged_err));
+        StagedItem it;
+        if (ok) it = bars.item[slot];
+        else it = StagedItem{0, 0, 0, 0, 0, 0, 0, 0};
+        if (it.w0 < 0) return;                             // the same in every warp
+        int pos[2];
+        tile_pos(I, it.w0, it.rows, it.r0 + 8 * group, c4, pos);
+        const int key_lo = it.split * kSplit;
+        const bool any = __any_sync(0xffffffffu, max(pos[0], pos[1]) >= key_lo);     // the tile has rows in this split
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(smem_raw + L::kQ) + (slot * L::kRows + 8 * group + g8) * L::QP + 16 * c4;
         RowState<HD> rs;
         rs.clear();
-        uint32_t bad_rows = 0;
+        uint32_t bad_rows = 0;                             // bit e: the row met a page id out of range
 #pragma unroll 1
-        for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, &bars.abort_flag, &g_paged_err));
+        for (int s0 = 0; s0 < it.nsteps; s0 += kClasses) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[it.stage], it.phase, &bars.abort_flag, &g_paged_err));
             if (!ok) break;
             const int step = s0 + cls, key0 = key_lo + kStep * step;
-            if (step < tp.nsteps) {
-                const uint32_t base = ring + static_cast<uint32_t>(stage * L.kStage);
-                float s4[4][4] = {}, st[4];
+            if (any && step < it.nsteps) {
+                const uint8_t* base = smem_raw + L::kRing + it.stage * L::kStage;
+                uint4 k0[KS / 2], k1[KS / 2];
 #pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    // 16 bytes of keys g8 and g8 + 8: dims 16 c4 + 64 b + 2 r .. as the direct kernel holds them
-                    const int chunk = 8 * (k >> 2) + 2 * c4 + ((k & 2) >> 1);
-                    const uint32_t at = base + kbase + static_cast<uint32_t>((chunk ^ g8) * 16);
-                    uint4 k0, k1;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(k0.x), "=r"(k0.y), "=r"(k0.z), "=r"(k0.w) : "r"(at) : "memory");
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(k1.x), "=r"(k1.y), "=r"(k1.z), "=r"(k1.w) : "r"(at + 8 * HD * 2) : "memory");
-                    const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * (k >> 2) + 4 * (k & 3));
-                    mma_16816(s4[k & 3], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
-                    mma_16816(s4[(k & 3) + 1], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
+                for (int k = 0; k < KS / 2; ++k) {
+                    // 16 bytes of keys g8 and g8 + 8, the dims that the direct kernel puts into two k-steps
+                    const int chunk = 8 * (k >> 1) + 2 * c4 + (k & 1);
+                    const uint8_t* at = base + kbase + ((chunk ^ g8) * 16);
+                    k0[k] = *reinterpret_cast<const uint4*>(at);
+                    k1[k] = *reinterpret_cast<const uint4*>(at + 8 * HD * 2);
+                }
+                float s2[2][4] = {}, st[4];
+#pragma unroll
+                for (int k = 0; k < KS / 2; ++k) {
+                    const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 8 * (k & 1));
+                    mma_16816(s2[0], k0[k].x, k1[k].x, k0[k].y, k1[k].y, qv.x, qv.y);
+                    mma_16816(s2[1], k0[k].z, k1[k].z, k0[k].w, k1[k].w, qv.z, qv.w);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) st[e] = (s4[0][e] + s4[1][e]) + (s4[2][e] + s4[3][e]);
-                if ((bars.bad[stage] >> cls) & 1u)
-                    bad_rows |= (tp.pos[0] >= key0 ? 1u : 0u) | (tp.pos[1] >= key0 ? 2u : 0u);
-                tp.mask(st, key0, g8);
+                for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
+                if (bars.bad[it.stage][cls]) bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
+                mask_step(st, pos, key0, g8);
                 uint32_t hi[2], low[2];
                 rs.step(st, P.scale_log2, hi, low);
+                const uint32_t vat = smem_u32(base) + vbase;
                 rs.add(hi, low, [&](int k, uint32_t (&a)[4]) {
-                    ldmatrix_x4_trans(base + vbase + static_cast<uint32_t>(((2 * k + vch) ^ (vkey & 7)) * 16), a);
+                    ldmatrix_x4_trans(vat + static_cast<uint32_t>(((2 * k + vch) ^ (vkey & 7)) * 16), a);
                 });
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.empty[stage]);
-            advance();
-        }
-        float l[2];
-        rs.sum_lanes(l);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = cls * rows + 8 * tile + 2 * c4 + e;
-            if (g8 == 0) s_ml[row] = make_float2(rs.m[e], (bad_rows >> e) & 1u ? -INFINITY : l[e]);
-            // acc[k][e], acc[k][e + 2]: dims 16 k + g8 and + 8 of the row
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                s_o[row * (HD + 4) + 16 * k + g8] = rs.acc[k][e];
-                s_o[row * (HD + 4) + 16 * k + 8 + g8] = rs.acc[k][e + 2];
+            if (lane == 0) mbar_arrive(&bars.empty[it.stage]);
+            if (++it.stage == L::kStages) {
+                it.stage = 0;
+                it.phase ^= 1u;
             }
         }
-        bar_sync_n(1, threads);
-        join_classes<HD>(I, cur, r0, rows, s_o, s_ml, tid, threads);
-        if (!more) break;
-        cur = nxt;
+        // join the classes: maxima and sums first
+        rs.put_ml(s_ml + cls * 8, bad_rows, g8, c4);
+        if (!group_all(group, ok)) return;                 // a wait ran out: all four warps leave
+        if (lane == 0) mbar_arrive(&bars.item_empty[slot]);            // Q is no longer needed
+        float2 ml[2][kClasses];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int k = 0; k < kClasses; ++k) ml[e][k] = s_ml[k * 8 + 2 * c4 + e];
+            const float f = class_factor(make_float2(rs.m[e], 0.0f), classes_max(ml[e]));
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                rs.acc[k][e] *= f;
+                rs.acc[k][e + 2] *= f;
+            }
+        }
+        // Classes c and c ^ 2 swap halves of the dims, then c and c ^ 1 quarters: every
+        // warp ends with KS / 4 tiles of 16 dims.  acc[k][e], acc[k][e + 2] are dims
+        // 16 k + g8 and + 8 of row 2 c4 + e.
+        auto put = [&](int half, int k, const float (&x)[4]) {
+            float* o = s_o + (half * 8 + 2 * c4) * L::HDP + 16 * k + g8;
+            o[0] = x[0];
+            o[L::HDP] = x[1];
+            o[8] = x[2];
+            o[L::HDP + 8] = x[3];
+        };
+        auto get = [&](int half, int k, float (&x)[4]) {
+            const float* o = s_o + (half * 8 + 2 * c4) * L::HDP + 16 * k + g8;
+            x[0] = __fadd_rn(x[0], o[0]);
+            x[1] = __fadd_rn(x[1], o[L::HDP]);
+            x[2] = __fadd_rn(x[2], o[8]);
+            x[3] = __fadd_rn(x[3], o[L::HDP + 8]);
+        };
+        float x2[KS / 2][4], x4[KS / 4][4];
+        const bool upper = cls & 2, odd = cls & 1;
+        // region cls & 1: tiles [0, KS/2) written by the upper class, [KS/2, KS) by the lower
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k) {
+            if (upper) put(odd, k, rs.acc[k]);
+            else put(odd, k + KS / 2, rs.acc[k + KS / 2]);
+        }
+        group_bar(group);
+        const int kh = upper ? KS / 2 : 0;
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x2[k][e] = upper ? rs.acc[k + KS / 2][e] : rs.acc[k][e];
+            get(odd, kh + k, x2[k]);
+        }
+        // the even class keeps the lower quarter of its half: what is sent lies where this warp alone has just read
+#pragma unroll
+        for (int k = 0; k < KS / 4; ++k) {
+            if (odd) put(1, kh + k, x2[k]);
+            else put(0, kh + KS / 4 + k, x2[k + KS / 4]);
+        }
+        group_bar(group);
+        const int kq = kh + (odd ? KS / 4 : 0);
+#pragma unroll
+        for (int k = 0; k < KS / 4; ++k) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x4[k][e] = odd ? x2[k + KS / 4][e] : x2[k][e];
+            get(odd ? 0 : 1, kq + k, x4[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = it.r0 + 8 * group + 2 * c4 + e;
+            if (i >= it.rows || pos[e] < key_lo) continue;
+            int j, head;
+            row_head(P, i, j, head);
+            const long long pair = static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head;
+            const float mx = classes_max(ml[e]), sum = classes_sum(ml[e], mx);
+            if (pos[e] < kSplit) {
+                const float scale = 1.0f / sum;
+                __nv_bfloat16* o = P.o + pair * HD + 16 * kq + g8;
+#pragma unroll
+                for (int k = 0; k < KS / 4; ++k) {
+                    o[16 * k] = __float2bfloat16_rn(sum == -1.0f ? 0.0f : x4[k][e] * scale);
+                    o[16 * k + 8] = __float2bfloat16_rn(sum == -1.0f ? 0.0f : x4[k][e + 2] * scale);
+                }
+            } else {
+                const long long part = pair * P.s_max + it.split;
+                float* o = P.ws_o + part * HD + 16 * kq + g8;
+#pragma unroll
+                for (int k = 0; k < KS / 4; ++k) {
+                    o[16 * k] = x4[k][e];
+                    o[16 * k + 8] = x4[k][e + 2];
+                }
+                if (cls == 0 && g8 == 0) P.ws_ml[part] = make_float2(mx, sum);
+            }
+        }
+        slot ^= 1;
+        slot_phase ^= slot == 0 ? 1u : 0u;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Joins the splits of a (row, head) in an order that goes by their number alone:
@@ -1032,34 +1181,47 @@ int check_pages(int n_slots, int max_pages, int n_pages, int page_size, PageTabl
     return BIV_OK;
 }
 
-// The split kernel and, where a row may have several splits, the combine kernel.
-template <int HD>
-int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
+template <int HD, int T>
+int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
+    using L = StagedLayout<HD, T>;
     static DeviceOnce once;
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_status(e);
-    int st = once.run(dev, [] {
-        const cudaError_t e1 = cudaFuncSetAttribute(paged_attn_direct_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    static_cast<int>(sizeof(DirectSmem<HD>)));
-        if (e1 != cudaSuccess) return cuda_status(e1);
-        return cuda_status(cudaFuncSetAttribute(paged_attn_staged_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                227 * 1024));
+    const int st = once.run(dev, [] {
+        return cuda_status(cudaFuncSetAttribute(paged_attn_staged_kernel<HD, T>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes));
     });
     if (st != BIV_OK) return st;
-    const long long rows = static_cast<long long>(P.rpg) * P.G;
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
-    if (rows <= 8) {
+    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * passes, num_sms());
+    return launch_pdl(paged_attn_staged_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(T * 128 + 128), L::kBytes, s, P);
+}
+
+// The split kernel and, where a row may have several splits, the combine kernel.
+template <int HD>
+int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
+    const long long rows = static_cast<long long>(P.rpg) * P.G;
+    int st;
+    if (rows <= 8 && !getenv("BIV_NODIRECT")) {
+        static DeviceOnce once;
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_status(e);
+        st = once.run(dev, [] {
+            return cuda_status(cudaFuncSetAttribute(paged_attn_direct_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    static_cast<int>(sizeof(DirectSmem<HD>))));
+        });
+        if (st != BIV_OK) return st;
+        const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
         const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max, 3LL * num_sms());
         st = launch_pdl(paged_attn_direct_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(kDirectThreads),
                         sizeof(DirectSmem<HD>), s, P);
     } else {
         // as few passes over the keys as four tiles allow, each with as few tiles as they then need
-        const long long passes = (rows + 8 * kMaxTiles - 1) / (8 * kMaxTiles);
-        const int T = static_cast<int>((rows + 8 * passes - 1) / (8 * passes));
-        const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * passes, num_sms());
-        st = launch_pdl(paged_attn_staged_kernel<HD>, dim3(static_cast<unsigned>(grid)), dim3(32 * kClasses * T + 32),
-                        static_cast<size_t>(StagedLayout<HD>(T).bytes), s, P, T);
+        const long long passes = (rows + 31) / 32;
+        const long long T = (rows + 8 * passes - 1) / (8 * passes);
+        st = T == 1 ? launch_staged<HD, 1>(P, passes, s) : T == 2 ? launch_staged<HD, 2>(P, passes, s) : T == 3 ? launch_staged<HD, 3>(P, passes, s) : launch_staged<HD, 4>(P, passes, s);
     }
     if (st != BIV_OK || P.s_max == 1) return st;
     // few rows: a CTA each, so that a long row has the whole CTA
