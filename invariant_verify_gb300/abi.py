@@ -117,7 +117,9 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current device's current stream, without the object that
+        # torch.cuda.current_stream() builds around it (2.9 us on a Grace core)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -126,11 +128,19 @@ def _stream(stream) -> int | None:
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _dense(fn: str, *tensors) -> None:
-    """(name, tensor, dtype, shape) of each argument: of that type and shape,
-    dense row-major and on the current CUDA device, where the call's stream
-    is; None passes.  Raises BivError with the status that names the fault."""
-    for name, t, dtype, shape in tensors:
+def _dense(fn: str, dtype, tensors, shapes, names: str) -> None:
+    """Each of the tensors (None passes) has the type and shape, is dense
+    row-major and lies on the current CUDA device, where the call's stream is;
+    else BivError with the status that names the fault."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    for i, t in enumerate(tensors):
+        if t is not None and (t.dtype is not dtype or t.shape != shapes[i] or not t.is_contiguous()
+                              or t.get_device() != dev):
+            _fault(fn, dtype, tensors, shapes, names.split())
+
+
+def _fault(fn: str, dtype, tensors, shapes, names) -> None:
+    for name, t, shape in zip(names, tensors, shapes):
         if t is None:
             continue
         if t.dtype is not dtype:
@@ -139,15 +149,7 @@ def _dense(fn: str, *tensors) -> None:
             raise BivError(fn, 2, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
         if not t.is_contiguous():
             raise BivError(fn, 2, f"{name} is not dense row-major")
-    for name, t, _, _ in tensors:
-        if t is not None:
-            _on_device(fn, name, t)
-
-
-def _on_device(fn: str, name: str, t) -> None:
-    i = t.get_device()
-    if i < 0 or i != torch.cuda.current_device():
-        raise BivError(fn, 7, f"{name} is on {t.device}, not on the current CUDA device")
+    raise BivError(fn, 7, f"one of {', '.join(names)} is not on the current CUDA device")
 
 
 # ----------------------------------------------------------------- status
@@ -391,33 +393,40 @@ def biv_residual_add(x, y, out, stream=None) -> None:
 
 def biv_gemm_bias_act(A, B, C_out, bias=None, residual=None, act: str = "none", stream=None) -> None:
     """C = act(A B^T + bias) + residual; C_out (bf16 or fp32) may be the bf16 residual itself."""
+    fn = "biv_gemm_bias_act"
     M, K = A.shape
     N = B.shape[0]
     out = C_out.dtype
     if out is not _BF16 and out is not _F32:
-        raise BivError("biv_gemm_bias_act", 4, f"C is {out}, not bfloat16 or float32")
+        raise BivError(fn, 4, f"C is {out}, not bfloat16 or float32")
     if act not in ACTS:
-        raise BivError("biv_gemm_bias_act", 4, f"act {act!r} is none of {', '.join(ACTS)}")
-    _dense("biv_gemm_bias_act", ("A", A, _BF16, (M, K)), ("B", B, _BF16, (N, K)), ("bias", bias, _BF16, (N,)),
-           ("residual", residual, _BF16, (M, N)), ("C", C_out, out, (M, N)))
-    _check("biv_gemm_bias_act", _load().biv_gemm_bias_act(
-        _ptr(A), _ptr(B), _ptr(bias), _ptr(residual), _ptr(C_out), BIV_F32 if out is _F32 else BIV_BF16, ACTS[act],
-        M, N, K, _stream(stream)))
+        raise BivError(fn, 4, f"act {act!r} is none of {', '.join(ACTS)}")
+    _dense(fn, _BF16, (A, B, bias, residual), ((M, K), (N, K), (N,), (M, N)), "A B bias residual")
+    _dense(fn, out, (C_out,), ((M, N),), "C")
+    st = _load().biv_gemm_bias_act(
+        A.data_ptr(), B.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), C_out.data_ptr(), BIV_F32 if out is _F32 else BIV_BF16,
+        ACTS[act], M, N, K, _stream(stream))
+    if st:
+        raise BivError(fn, st)
 
 
 def biv_rope_kv_write_paged(qkv, q_out, k_pages, v_pages, page_table, row_slot, row_pos, theta: float, K: int,
                             rows_keep=None, stream=None) -> None:
+    fn = "biv_rope_kv_write_paged"
     W, Hq, hd = q_out.shape
-    n_pages, Hkv, page_size, _ = k_pages.shape
+    pool = n_pages, Hkv, page_size, _ = k_pages.shape
     n_slots, max_pages = page_table.shape
-    pool = (n_pages, Hkv, page_size, hd)
-    _dense("biv_rope_kv_write_paged", ("qkv", qkv, _BF16, (W, (Hq + 2 * Hkv) * hd)), ("q_out", q_out, _BF16, (W, Hq, hd)),
-           ("k_pages", k_pages, _BF16, pool), ("v_pages", v_pages, _BF16, pool),
-           ("page_table", page_table, _I32, (n_slots, max_pages)), ("row_slot", row_slot, _I32, (W,)),
-           ("row_pos", row_pos, _I32, (W,)), ("rows_keep", rows_keep, _I32, (W // max(K, 1),)))
-    _check("biv_rope_kv_write_paged", _load().biv_rope_kv_write_paged(
-        _ptr(qkv), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(row_slot), _ptr(row_pos),
-        _ptr(rows_keep), W, K, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size, theta, _stream(stream)))
+    _dense(fn, _BF16, (qkv, q_out, k_pages, v_pages),
+           ((W, (Hq + 2 * Hkv) * hd), (W, Hq, hd), (n_pages, Hkv, page_size, hd), pool), "qkv q_out k_pages v_pages")
+    _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), ((n_slots, max_pages), (W,), (W,), (W // max(K, 1),)),
+           "page_table row_slot row_pos rows_keep")
+    st = _load().biv_rope_kv_write_paged(
+        qkv.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        row_slot.data_ptr(), row_pos.data_ptr(), None if rows_keep is None else rows_keep.data_ptr(), W, K, Hq, Hkv,
+        hd, n_slots, max_pages, n_pages, page_size, theta, _stream(stream))
+    if st:
+        raise BivError(fn, st)
 
 
 def biv_decode_attn_paged_workspace_size(W: int, Hq: int, hd: int, max_pages: int, page_size: int) -> int:
@@ -426,50 +435,59 @@ def biv_decode_attn_paged_workspace_size(W: int, Hq: int, hd: int, max_pages: in
 
 def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o, rows_per_group: int, workspace,
                           stream=None) -> None:
-    W, Hq, hd = q.shape
-    n_pages, Hkv, page_size, _ = k_pages.shape
+    fn = "biv_decode_attn_paged"
+    rows = W, Hq, hd = q.shape
+    pool = n_pages, Hkv, page_size, _ = k_pages.shape
     n_slots, max_pages = page_table.shape
-    pool = (n_pages, Hkv, page_size, hd)
-    _dense("biv_decode_attn_paged", ("q", q, _BF16, (W, Hq, hd)), ("k_pages", k_pages, _BF16, pool),
-           ("v_pages", v_pages, _BF16, pool), ("page_table", page_table, _I32, (n_slots, max_pages)),
-           ("row_slot", row_slot, _I32, (W,)), ("row_pos", row_pos, _I32, (W,)), ("o", o, _BF16, (W, Hq, hd)),
-           ("workspace", workspace, workspace.dtype, workspace.shape))
-    _check("biv_decode_attn_paged", _load().biv_decode_attn_paged(
-        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(row_slot), _ptr(row_pos), _ptr(o), W,
-        rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    _dense(fn, _BF16, (q, k_pages, v_pages, o), (rows, (n_pages, Hkv, page_size, hd), pool, rows), "q k_pages v_pages o")
+    _dense(fn, _I32, (page_table, row_slot, row_pos), ((n_slots, max_pages), (W,), (W,)), "page_table row_slot row_pos")
+    _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")
+    st = _load().biv_decode_attn_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), row_slot.data_ptr(),
+        row_pos.data_ptr(), o.data_ptr(), W, rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size,
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        raise BivError(fn, st)
 
 
 def biv_softmax(logits, probs, temperature: float, V: int | None = None, stream=None) -> None:
     """probs[:, :V] = softmax(logits[:, :V] / temperature); rows of either may be strided (stride(1) == 1)."""
+    fn = "biv_softmax"
     R, ld = logits.shape
-    V = ld if V is None else V
+    if V is None:
+        V = ld
     for name, t in (("logits", logits), ("probs", probs)):
         if t.dtype is not _F32 or t.dim() != 2:
-            raise BivError("biv_softmax", 4, f"{name} is no float32 matrix")
-        if t.shape[0] != R or t.shape[1] < V or (V > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < V):
-            raise BivError("biv_softmax", 2, f"{name} is {tuple(t.shape)} with strides {t.stride()}, V = {V}")
-    _on_device("biv_softmax", "logits", logits)
-    _on_device("biv_softmax", "probs", probs)
-    _check("biv_softmax", _load().biv_softmax(
-        _ptr(logits), R, V, max(logits.stride(0), V), temperature, _ptr(probs), max(probs.stride(0), V),
-        _stream(stream)))
+            raise BivError(fn, 4, f"{name} is no float32 matrix")
+        if t.shape != (R, V) or not t.is_contiguous():     # rows of a larger matrix?
+            if t.shape[0] != R or t.shape[1] < V or (V > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < V):
+                raise BivError(fn, 2, f"{name} is {tuple(t.shape)} with strides {t.stride()}, V = {V}")
+    if not logits.is_cuda or not probs.is_cuda or logits.get_device() != (dev := torch._C._cuda_getDevice()) \
+            or probs.get_device() != dev:
+        raise BivError(fn, 7, "logits or probs is not on the current CUDA device")
+    st = _load().biv_softmax(
+        logits.data_ptr(), R, V, logits.stride(0) if R > 1 else max(ld, V), temperature, probs.data_ptr(),
+        probs.stride(0) if R > 1 else max(probs.shape[1], V), _stream(stream))
+    if st:
+        raise BivError(fn, st)
 
 
 def biv_verify_sample(target, draft_probs, draft, u_accept, u_sample, p0, tokens, accept_len, new_len,
                       stream=None) -> None:
     """target fp32 [N*(K+1), V] (or [N, K+1, V]), draft_probs [N*K, V] or None
     (a drafter that is certain of its tokens); the other arrays as in the header."""
+    fn = "biv_verify_sample"
     N, K1 = tokens.shape
     K, V = K1 - 1, target.shape[-1]
-    if target.dim() == 3:
-        target = target.flatten(0, 1)
-    if draft_probs is not None and draft_probs.dim() == 3:
-        draft_probs = draft_probs.flatten(0, 1)
-    _dense("biv_verify_sample", ("target", target, _F32, (N * K1, V)), ("draft_probs", draft_probs, _F32, (N * K, V)),
-           ("draft", draft, _I32, (N, K)), ("u_accept", u_accept, _F32, (N, K)), ("u_sample", u_sample, _F32, (N,)),
-           ("p0", p0, _I32, (N,)), ("tokens", tokens, _I32, (N, K1)), ("accept_len", accept_len, _I32, (N,)),
-           ("new_len", new_len, _I32, (N,)))
-    _check("biv_verify_sample", _load().biv_verify_sample(
-        _ptr(target), _ptr(draft_probs), _ptr(draft), _ptr(u_accept), _ptr(u_sample), _ptr(p0), N, K, V, _ptr(tokens),
-        _ptr(accept_len), _ptr(new_len), _stream(stream)))
+    _dense(fn, _F32, (target, draft_probs, u_accept, u_sample),
+           ((N, K1, V) if target.dim() == 3 else (N * K1, V),
+            (N, K, V) if draft_probs is not None and draft_probs.dim() == 3 else (N * K, V), (N, K), (N,)),
+           "target draft_probs u_accept u_sample")
+    _dense(fn, _I32, (draft, p0, tokens, accept_len, new_len), ((N, K), (N,), (N, K1), (N,), (N,)),
+           "draft p0 tokens accept_len new_len")
+    st = _load().biv_verify_sample(
+        target.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(), draft.data_ptr(),
+        u_accept.data_ptr(), u_sample.data_ptr(), p0.data_ptr(), N, K, V, tokens.data_ptr(), accept_len.data_ptr(),
+        new_len.data_ptr(), _stream(stream))
+    if st:
+        raise BivError(fn, st)

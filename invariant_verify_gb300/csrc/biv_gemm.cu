@@ -65,6 +65,7 @@ struct GemmArgs {
                      // MMAs start as soon as it lands; the others hold KS k-blocks
     int m64;         // one row tile of at most 64 rows: M = 64 MMAs
     int a_rows;      // rows of A copied per k-block (multiple of 8, <= 128)
+    int row_step;    // rows of the tile that belong to one CTA: 128, or a_rows where a pair halves one row tile
     uint32_t idesc;  // tcgen05 instruction descriptor for M=128, N=BN
     uint32_t tmem_cols;
     // Narrow tail (CTA pairs, fused selection): column tiles [0, nt_full) are
@@ -553,12 +554,26 @@ BIV_DEV unsigned long long tile_row_winner(uint32_t taddr, int cb, int ce, int n
     return best;
 }
 
-// act(x) in fp32.  erff and tanhf are within 2 ulp, so the result's one rounding
-// to C's type is the only one that counts.
+// 1 + erf(x / sqrt 2) by Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7: one branch-free
+// form for all x, where erff takes both of its branches in nearly every warp (the
+// epilogue of the last tile is not hidden behind any product).
+BIV_DEV float one_plus_erf_half(float x) {
+    const float z = fabsf(x) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float e = p * t * ex2_approx(-1.4426950408889634f * z * z);      // erfc(z)
+    return x < 0.0f ? e : 2.0f - e;
+}
+
+// act(x) in fp32.  tanhf is within 2 ulp and the others' errors below 2^-21 of |x|, so
+// the result's one rounding to C's type is the one that counts.
 BIV_DEV float activate(float x, int act) {
     switch (act) {
         case BIV_ACT_RELU: return x > 0.0f || x != x ? x : 0.0f;
-        case BIV_ACT_GELU: return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+        case BIV_ACT_GELU: return 0.5f * x * one_plus_erf_half(x);
         case BIV_ACT_GELU_TANH: return 0.5f * x * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * x * x, x, x)));
         case BIV_ACT_SILU: return silu(x);
         default: return x;
@@ -761,7 +776,7 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     if constexpr (CG == 2) {
                         const uint32_t fb = mapa_shared(&full[stage], 0);
                         if (!b_done && rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * tx_t);
-                        tma_load_3d_pair(sa, &tmA, fb, 0, m_blk * TM + rank * kBM, kb0, pol_a);
+                        tma_load_3d_pair(sa, &tmA, fb, 0, m_blk * TM + rank * g.row_step, kb0, pol_a);
                         if (!b_done) tma_load_3d_pair(sa + A_BYTES, tmBt, fb, 0, ti.col0 + rank * bnl_t, kb0, pol_b);
                     } else if (g.first1 && sb == 0) {
                         if (!b_done) mbar_arrive_expect_tx(&full[stage], tx_bytes1);
@@ -904,7 +919,7 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const TileAt ti = tile_at(g, t, m_tiles);
             const int m_blk = ti.m_blk;
             const int bnt = ti.bn, col0 = ti.col0;                 // this tile's width and first column
-            const int row_base = m_blk * TM + rank * kBM;          // first row of this CTA's 128
+            const int row_base = m_blk * TM + rank * g.row_step;   // first row of this CTA's share
             if constexpr (EPI == 3 && CG == 1) {
                 // This tile's noise buckets while its MMAs run; the vote below is
                 // also the barrier that makes them (and the table) visible.
@@ -925,7 +940,7 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             // lane 32 (r / 16) + r % 16, so each warp owns 16 rows in lanes 0..15.
             const int rloc = g.m64 ? q * 16 + lane : q * 32 + lane;
             const int row = row_base + rloc;
-            const bool live = row < M && (!g.m64 || lane < 16);
+            const bool live = row < M && rloc < g.row_step && (!g.m64 || lane < 16);
             const uint32_t taddr =
                 tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
             if constexpr (EPI == 3) {
@@ -1252,7 +1267,10 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     g.N = N;
     g.K = K;
     g.BN = BN;
-    g.a_rows = (CG == 2 || M >= kBM) ? kBM : ((M + 7) / 8) * 8;
+    // A pair that halves one row tile: each CTA copies half of the rows.
+    const bool halves = CG == 2 && M <= kBM;
+    g.a_rows = halves ? ((M + 1) / 2 + 7) / 8 * 8 : (CG == 2 || M >= kBM) ? kBM : ((M + 7) / 8) * 8;
+    g.row_step = halves ? g.a_rows : kBM;
     g.KB = (K + kBK - 1) / kBK;
     g.three_d = (K % kBK == 0) ? 1 : 0;
     const int BNL = BN / CG;                        // B rows one CTA copies per tile
@@ -1281,7 +1299,10 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     int units = 0;
     const int st = kernel_setup<EPI, CG>(dev, smem_max, &units);
     if (st != BIV_OK) return st;
-    if (CG == 2) {
+    if (halves) {
+        // weight streaming: as many k-blocks per box as three stages allow
+        ks = std::min(g.KB, std::max(1, (ring - tail) / (3 * (g.a_rows + BNL) * kRowBytes)));
+    } else if (CG == 2) {
         // Pairs: two k-blocks per box while the ring holds three stages.
         if (ring / (2 * (g.a_rows + BNL) * kRowBytes) >= 3) ks = 2;
     } else if (g.three_d && M <= kBM) {        // one row tile: weight streaming
@@ -1299,7 +1320,7 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     // A one-k-block first stage pays off where the MMA chain, not the copy,
     // sets the pace (narrow tiles with many k-blocks per stage).
     g.first1 = (CG == 1 && g.three_d && ks >= 4 && g.KB > 1) ? 1 : 0;
-    g.m64 = g.a_rows <= 64 ? 1 : 0;
+    g.m64 = CG == 1 && g.a_rows <= 64 ? 1 : 0;
     g.stages = std::min(kMaxStages, std::max(1, (ring - tail) / stage_bytes(ks, g.a_rows, BNL)));
     g.idesc = idesc_bf16_f32(CG == 2 ? 2 * kBM : (g.m64 ? 64 : kBM), BN);
     g.tmem_cols = tmem_cols_for(BN);
@@ -1350,6 +1371,17 @@ int launch_gemm(const void* A, const void* B, void* C, int M, int N, int K, int 
     if (use_pair(M, K) && pair_bn_ok(BN))
         return launch_gemm_cg<EPI, 2>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols, ba);
     return launch_gemm_cg<EPI, 1>(A, B, C, M, N, K, BN, stream, sel, rp, n_cols, ba);
+}
+
+// One row tile (M <= 128) as CTA pairs that halve it: a CTA then takes M / 2 rows of
+// A and BN / 2 rows of B out of L2 for every k-block instead of M and bn, and what an
+// SM can take (about 120 GB/s) is what bounds these GEMMs once A is no small part.
+// M = 64, N = 4096, K = 14336: 96 rows a k-block per CTA, 35.6 us, against 64 rows.
+inline int halves_tile_n(int N) {
+    return static_cast<int>(std::min<long long>(256, std::max<long long>(64, ceil_div(ceil_div(N, kPairWave), 32) * 32)));
+}
+inline bool halves_pay(int M, int N, int K) {
+    return M > 32 && M <= kBM && K % kBK == 0 && N >= 2048 && ceil_div(N, halves_tile_n(N)) <= kPairWave;
 }
 
 int check_gemm(const void* A, const void* B, void* C, int out_dtype, int M, int N, int K) {
@@ -1548,8 +1580,10 @@ extern "C" int biv_gemm_bias_act(const void* A, const void* B, const void* bias,
     ba.residual = static_cast<const __nv_bfloat16*>(residual);
     ba.act = act;
     ba.out_f32 = out_dtype == BIV_F32;
-    return launch_gemm<5>(A, B, C, M, N, K, biv_gemm_tile_n(M, N, K), reinterpret_cast<cudaStream_t>(stream),
-                          SelectArgs{}, RopeArgs{}, nullptr, ba);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (halves_pay(M, N, K))
+        return launch_gemm_cg<5, 2>(A, B, C, M, N, K, halves_tile_n(N), s, SelectArgs{}, RopeArgs{}, nullptr, ba);
+    return launch_gemm<5>(A, B, C, M, N, K, biv_gemm_tile_n(M, N, K), s, SelectArgs{}, RopeArgs{}, nullptr, ba);
 }
 
 extern "C" int biv_swiglu_pack_weights(const void* w_gu, void* w_packed, int F, int K, biv_stream_t stream) {

@@ -2,7 +2,6 @@
 // fixed-split decode attention over them.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "biv_common.cuh"
@@ -1203,7 +1202,7 @@ template <int HD>
 int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
     const long long rows = static_cast<long long>(P.rpg) * P.G;
     int st;
-    if (rows <= 8 && !getenv("BIV_NODIRECT")) {
+    if (rows <= 8) {
         static DeviceOnce once;
         int dev = 0;
         const cudaError_t e = cudaGetDevice(&dev);
@@ -1221,7 +1220,7 @@ int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
         // as few passes over the keys as four tiles allow, each with as few tiles as they then need
         const long long passes = (rows + 31) / 32;
         const long long T = (rows + 8 * passes - 1) / (8 * passes);
-        st = T == 1 ? launch_staged<HD, 1>(P, passes, s) : T == 2 ? launch_staged<HD, 2>(P, passes, s) : T == 3 ? launch_staged<HD, 3>(P, passes, s) : launch_staged<HD, 4>(P, passes, s);
+        st = T == 2 ? launch_staged<HD, 2>(P, passes, s) : T == 3 ? launch_staged<HD, 3>(P, passes, s) : launch_staged<HD, 4>(P, passes, s);
     }
     if (st != BIV_OK || P.s_max == 1) return st;
     // few rows: a CTA each, so that a long row has the whole CTA

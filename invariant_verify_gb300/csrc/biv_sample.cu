@@ -12,81 +12,243 @@ BIV_DEFINE_ERR_WORD(g_sample_err)
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPerLoad = 4 * kThreads;        // entries that one 16-byte load a thread covers
 
-// A NaN logit counts as -infinity.
-BIV_DEV float no_nan(float x) { return x == x ? x : -INFINITY; }
+// A NaN logit counts as -infinity (fmaxf returns the operand that is a number).
+BIV_DEV float no_nan(float x) { return fmaxf(x, -INFINITY); }
+BIV_DEV float4 no_nan(float4 r) { return make_float4(no_nan(r.x), no_nan(r.y), no_nan(r.z), no_nan(r.w)); }
 
-// One CTA per row, three passes.
-__global__ void __launch_bounds__(kThreads)
-softmax_kernel(const float* logits, int V, long long ld, float scale, int greedy, float* probs, long long ld_p) {
-    __shared__ float s_m[kWarps], s_l[kWarps];
-    __shared__ int s_i[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_trigger();
-    const float* x = logits + blockIdx.x * ld;
-    float* p = probs + blockIdx.x * ld_p;
-    float m = -INFINITY;
-    int at = 0x7fffffff;
-    for (int v = threadIdx.x; v < V; v += kThreads) {
-        const float y = no_nan(x[v]);
-        if (y > m) m = y, at = v;
+// Four entries of a row from v on, `fill` past its end.  VEC: rows are 16-byte
+// aligned and whole groups are read at once; else one by one.  The same entries
+// either way, so the same bits.
+template <bool VEC>
+BIV_DEV float4 load4(const float* x, int v, int V, float fill) {
+    if (VEC && v + 4 <= V) {
+        float4 r;
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(x + v));
+        return r;
     }
-    for (int d = 16; d > 0; d >>= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, d);
-        const int oi = __shfl_xor_sync(0xffffffffu, at, d);
-        if (om > m || (om == m && oi < at)) m = om, at = oi;
-    }
-    if (lane == 0) s_m[warp] = m, s_i[warp] = at;
-    __syncthreads();
-    for (int k = 0; k < kWarps; ++k)
-        if (s_m[k] > m || (s_m[k] == m && s_i[k] < at)) m = s_m[k], at = s_i[k];
-    if (greedy || m == -INFINITY) {
-        for (int v = threadIdx.x; v < V; v += kThreads) p[v] = v == at ? 1.0f : 0.0f;
+    float4 r = make_float4(fill, fill, fill, fill);
+    if (v < V) r.x = x[v];
+    if (v + 1 < V) r.y = x[v + 1];
+    if (v + 2 < V) r.z = x[v + 2];
+    if (v + 3 < V) r.w = x[v + 3];
+    return r;
+}
+template <bool VEC>
+BIV_DEV void store4(float* p, int v, int V, float4 r) {
+    if (VEC && v + 4 <= V) {
+        *reinterpret_cast<float4*>(p + v) = r;
         return;
     }
-    float l = 0.0f;
-    for (int v = threadIdx.x; v < V; v += kThreads) {
-        const float y = no_nan(x[v]);
-        l += m == INFINITY ? (y == INFINITY ? 1.0f : 0.0f) : exp2f((y - m) * scale);
+    if (v < V) p[v] = r.x;
+    if (v + 1 < V) p[v + 1] = r.y;
+    if (v + 2 < V) p[v + 2] = r.z;
+    if (v + 3 < V) p[v + 3] = r.w;
+}
+
+// A CTA's shared memory may be written by the others of its cluster once all have
+// started: each says so as it begins and waits for the others before its first write.
+BIV_DEV void cluster_started() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+BIV_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// A shared variable of the cluster's CTA `rank`.
+BIV_DEV void put_cluster(const void* p, uint32_t rank, float x) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(p, rank)), "f"(x) : "memory");
+}
+BIV_DEV void put_cluster(const void* p, uint32_t rank, int x) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(mapa_shared(p, rank)), "r"(x) : "memory");
+}
+BIV_DEV void put_cluster(const void* p, uint32_t rank, unsigned long long x) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(p, rank)), "l"(x) : "memory");
+}
+
+// ---------------------------------------------------------------- softmax
+// A row belongs to a cluster of C CTAs, each of which keeps its slice in registers
+// (NV groups of four per thread): one read and one write of the row, and one
+// exchange of (maximum, sum) between the CTAs.  p = e^((x - m_c) / T) / S_c's share:
+// each CTA's exponentials stand on its own maximum m_c and are scaled once by
+// e^((m_c - m) / T) / S.  C and NV go by V alone, so a row's bits do not depend on the
+// batch.  Rows past 8 x 16 x 2048 entries are read twice.
+constexpr int kMaxCluster = 8;
+
+template <bool VEC, int NV, bool LONG>
+__global__ void __launch_bounds__(kThreads, LONG || NV > 10 ? 1 : NV > 4 ? 2 : 3)
+softmax_kernel(const float* logits, int V, long long ld, float scale, float* probs, long long ld_p, int C) {
+    __shared__ float s_m[kWarps], s_l[kWarps];
+    __shared__ float c_m[kMaxCluster], c_l[kMaxCluster];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long row = blockIdx.x / C;
+    if (C > 1) cluster_started();
+    pdl_wait();
+    pdl_trigger();
+    const float* x = logits + row * ld;
+    float* p = probs + row * ld_p;
+    // slices of whole rounds of NV loads; a CTA's are consecutive
+    const int per = LONG ? (V + C * kPerLoad - 1) / (C * kPerLoad) * kPerLoad : NV * kPerLoad;
+    const int v0 = rank * per + 4 * tid;
+    const int end = min(V, (rank + 1) * per);
+
+    float4 r[NV];
+    float m_cta = -INFINITY;
+    for (int base = 0; base < per; base += NV * kPerLoad) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) r[k] = load4<VEC>(x, v0 + base + k * kPerLoad, end, -INFINITY);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            r[k] = no_nan(r[k]);
+            m_cta = fmaxf(m_cta, fmaxf(fmaxf(r[k].x, r[k].y), fmaxf(r[k].z, r[k].w)));
+        }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m_cta = fmaxf(m_cta, __shfl_xor_sync(0xffffffffu, m_cta, d));
+    if (lane == 0) s_m[warp] = m_cta;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) m_cta = fmaxf(m_cta, s_m[k]);
+
+    // An infinite maximum: its entries share the mass (differences would be NaN).  A
+    // slice of nothing but -infinity: zeros.
+    const bool infinite = m_cta == INFINITY, empty = m_cta == -INFINITY;
+    const float zero_at = infinite || empty ? 0.0f : m_cta;
+    auto power4 = [&](float4 y) {
+        if (infinite)
+            y = make_float4(y.x == INFINITY ? 0.0f : -INFINITY, y.y == INFINITY ? 0.0f : -INFINITY,
+                            y.z == INFINITY ? 0.0f : -INFINITY, y.w == INFINITY ? 0.0f : -INFINITY);
+        return make_float4(ex2_approx((y.x - zero_at) * scale), ex2_approx((y.y - zero_at) * scale),
+                           ex2_approx((y.z - zero_at) * scale), ex2_approx((y.w - zero_at) * scale));
+    };
+    float l = 0.0f;
+    for (int base = 0; base < per; base += NV * kPerLoad) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if constexpr (LONG) r[k] = no_nan(load4<VEC>(x, v0 + base + k * kPerLoad, end, -INFINITY));
+            r[k] = power4(r[k]);
+            l += (r[k].x + r[k].y) + (r[k].z + r[k].w);
+        }
+    }
+#pragma unroll
     for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     if (lane == 0) s_l[warp] = l;
     __syncthreads();
     l = 0.0f;
+#pragma unroll
     for (int k = 0; k < kWarps; ++k) l += s_l[k];
-    for (int v = threadIdx.x; v < V; v += kThreads) {
-        const float y = no_nan(x[v]);
-        p[v] = (m == INFINITY ? (y == INFINITY ? 1.0f : 0.0f) : exp2f((y - m) * scale)) / l;
+
+    float m = m_cta, factor = 1.0f / l;                    // of this CTA's exponentials
+    if (C > 1) {
+        cluster_wait();
+        if (tid < C) {
+            put_cluster(&c_m[rank], tid, m_cta);
+            put_cluster(&c_l[rank], tid, l);
+        }
+        cluster_sync();
+        for (int k = 0; k < C; ++k) m = fmaxf(m, c_m[k]);
+        float sum = 0.0f;
+        auto share = [&](float mk) { return mk == -INFINITY ? 0.0f : mk == m ? 1.0f : m == INFINITY ? 0.0f : ex2_approx((mk - m) * scale); };
+        for (int k = 0; k < C; ++k) sum = fmaf(c_l[k], share(c_m[k]), sum);
+        factor = share(m_cta) / sum;
+    }
+    if (m == -INFINITY) factor = 0.0f;
+
+    for (int base = 0; base < per; base += NV * kPerLoad) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = v0 + base + k * kPerLoad;
+            if constexpr (LONG) r[k] = power4(no_nan(load4<VEC>(x, v, end, -INFINITY)));
+            if (v < end) store4<VEC>(p, v, end, make_float4(r[k].x * factor, r[k].y * factor, r[k].z * factor, r[k].w * factor));
+        }
     }
 }
 
+// T == 0: one CTA per row finds the lowest index of its largest entry and writes the row.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads)
+softmax_greedy_kernel(const float* logits, int V, long long ld, float* probs, long long ld_p) {
+    __shared__ float s_m[kWarps];
+    __shared__ int s_i[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const float* x = logits + static_cast<long long>(blockIdx.x) * ld;
+    float* p = probs + static_cast<long long>(blockIdx.x) * ld_p;
+    float m = -INFINITY;
+    int at = 0x7fffffff;
+    auto take = [&](float om, int oi) {
+        if (om > m || (om == m && oi < at)) m = om, at = oi;
+    };
+    for (int v = 4 * tid; v < V; v += kPerLoad) {
+        const float4 r = no_nan(load4<VEC>(x, v, V, -INFINITY));
+        const float m4 = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
+        if (m4 > m) m = m4, at = v + (r.x == m4 ? 0 : r.y == m4 ? 1 : r.z == m4 ? 2 : 3);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, d);
+        const int oi = __shfl_xor_sync(0xffffffffu, at, d);
+        take(om, oi);
+    }
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_i[warp] = at;
+    }
+    __syncthreads();
+    for (int k = 0; k < kWarps; ++k) take(s_m[k], s_i[k]);
+    for (int v = 4 * tid; v < V; v += kPerLoad)
+        store4<VEC>(p, v, V, make_float4(v == at ? 1.0f : 0.0f, v + 1 == at ? 1.0f : 0.0f, v + 2 == at ? 1.0f : 0.0f, v + 3 == at ? 1.0f : 0.0f));
+}
+
+// ----------------------------------------------------------------- verify
 // A weight in units of 2^-60 (truncated), clamped to [0, 1]; a NaN counts as 0.
 BIV_DEV float clamp01(float w) { return fminf(fmaxf(w, 0.0f), 1.0f); }
-BIV_DEV unsigned long long units(float w) { return __float2ull_rz(w * 1152921504606846976.0f); }
+// By shifts of the significand: conversions to 64-bit integers run at the rate of
+// this part's few FP64 units (64 x 128256 entries: 44 us with them, 21 us without).
+BIV_DEV unsigned long long units(float w) {
+    const uint32_t b = __float_as_uint(w), down = 130u - (b >> 23);
+    const unsigned long long top = static_cast<unsigned long long>((b << 8) | 0x80000000u) << 32;      // 2^63 (1 + fraction)
+    return down < 64u ? top >> down : 0ull;
+}
 
-// One CTA per request.
-__global__ void __launch_bounds__(kThreads)
+BIV_DEV unsigned long long warp_sum(unsigned long long x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// One request per cluster of C CTAs, a contiguous chunk of the row per warp.  Every
+// CTA finds the first rejected draft (a few gathered numbers), each warp sums the
+// weights of its chunk in 64-bit integers, and the warp that holds the border reads
+// its chunk again (from L2) and walks down to the entry.  Sums of integers do not
+// depend on their order, so C may follow the batch.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads, 2)
 verify_sample_kernel(const float* __restrict__ target, const float* __restrict__ draft_probs,
                      const int32_t* __restrict__ draft, const float* __restrict__ u_accept,
                      const float* __restrict__ u_sample, const int32_t* __restrict__ p0, int K, int V,
-                     int32_t* __restrict__ tokens, int32_t* __restrict__ accept_len, int32_t* __restrict__ new_len) {
-    __shared__ int s_n, s_found;
-    __shared__ unsigned long long s_sum[kThreads];
-    __shared__ float s_f[kThreads];
-    const int r = blockIdx.x, t = threadIdx.x;
+                     int32_t* __restrict__ tokens, int32_t* __restrict__ accept_len, int32_t* __restrict__ new_len, int C) {
+    __shared__ int s_n;
+    __shared__ unsigned long long s_sum[kWarps];
+    __shared__ float s_f[kWarps];
+    __shared__ unsigned long long c_sum[2][kMaxCluster];
+    __shared__ float c_f[2][kMaxCluster];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long r = blockIdx.x / C;
+    if (tid == 0) s_n = K;
+    if (C > 1) cluster_started();
     pdl_wait();
     pdl_trigger();
-    if (t == 0) s_n = K;
+    const float u = fminf(fmaxf(u_sample[r], 0.0f), 0.99999994f);
     __syncthreads();
-    for (int j = t; j < K; j += kThreads) {
-        const long long row = static_cast<long long>(r) * K + j;
+    for (int j = tid; j < K; j += kThreads) {
+        const long long row = r * K + j;
         const int d = draft[row];
         bool ok = false;
         if (d < 0 || d >= V) {
-            atomicOr(&g_sample_err, BIV_DEVERR_INDEX);
+            if (rank == 0) atomicOr(&g_sample_err, BIV_DEVERR_INDEX);
         } else {
-            const float p = clamp01(target[(static_cast<long long>(r) * (K + 1) + j) * V + d]);
+            const float p = clamp01(target[(r * (K + 1) + j) * V + d]);
             const float q = draft_probs ? clamp01(draft_probs[row * V + d]) : 1.0f;
             // the product of two 24-bit numbers is exact in 64 bits
             ok = static_cast<double>(u_accept[row]) * static_cast<double>(q) < static_cast<double>(p);
@@ -95,59 +257,164 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
     }
     __syncthreads();
     const int n = s_n;
-    const float* p = target + (static_cast<long long>(r) * (K + 1) + n) * V;
-    const float* q = draft_probs && n < K ? draft_probs + (static_cast<long long>(r) * K + n) * V : nullptr;
-    const int skip = !draft_probs && n < K ? draft[static_cast<long long>(r) * K + n] : -1;
-    const int per = (V + kThreads - 1) / kThreads, v0 = min(V, t * per), v1 = min(V, v0 + per);
+    const float* p = target + (r * (K + 1) + n) * V;
+    const float* q = draft_probs && n < K ? draft_probs + (r * K + n) * V : nullptr;
+    const int skip = !draft_probs && n < K ? draft[r * K + n] : -1;
+    constexpr int kRound = 128;                            // entries of one load of a warp
+    const int parts = C * kWarps;
+    const int chunk = (V + parts * kRound - 1) / (parts * kRound) * kRound;
+    const int v0 = min(V, (rank * kWarps + warp) * chunk), end = min(V, v0 + chunk);
+
+    // kDeep rounds of weights, all their loads first
+    constexpr int kDeep = 4;
+    auto weights = [&](int v, bool plain, float4 (&w)[kDeep]) {
+        float4 y[kDeep];
+        const bool diff = q && !plain;
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) w[k] = load4<VEC>(p, v + k * kRound, end, 0.0f);
+        if (diff) {
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) y[k] = load4<VEC>(q, v + k * kRound, end, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            if (diff) w[k] = make_float4(w[k].x - y[k].x, w[k].y - y[k].y, w[k].z - y[k].z, w[k].w - y[k].w);
+            w[k] = make_float4(clamp01(w[k].x), clamp01(w[k].y), clamp01(w[k].z), clamp01(w[k].w));
+        }
+        if (skip >= 0 && !plain) {
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                const int at = skip - v - k * kRound;
+                if (at == 0) w[k].x = 0.0f;
+                if (at == 1) w[k].y = 0.0f;
+                if (at == 2) w[k].z = 0.0f;
+                if (at == 3) w[k].w = 0.0f;
+            }
+        }
+    };
     unsigned long long total = 0, before = 0;
-    bool plain = false, valid = true;
+    float all = 0.0f;
+    bool plain = false;
     for (int round = 0; round < 2; ++round) {
         unsigned long long sum = 0;
         float f = 0.0f;
-        for (int v = v0; v < v1; ++v) {
-            const float w = plain ? clamp01(p[v]) : v == skip ? 0.0f : q ? clamp01(p[v] - q[v]) : clamp01(p[v]);
-            sum += units(w);
-            f += w;
-        }
-        __syncthreads();
-        s_sum[t] = sum;
-        s_f[t] = f;
-        __syncthreads();
-        total = before = 0;
-        float all = 0.0f;
-        for (int k = 0; k < kThreads; ++k) {
-            if (k == t) before = total;
-            total += s_sum[k];
-            all += s_f[k];
-        }
-        valid = total > 0 && all < 8.0f;
-        if (total > 0 || plain) break;
-        plain = true;
-    }
-    if (t == 0) s_found = 0;
-    __syncthreads();
-    const float u = fminf(fmaxf(u_sample[r], 0.0f), 0.99999994f);
-    const unsigned long long border = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
-    if (valid && before <= border) {
-        unsigned long long sum = before;
-        for (int v = v0; v < v1; ++v) {
-            const float w = plain ? clamp01(p[v]) : v == skip ? 0.0f : q ? clamp01(p[v] - q[v]) : clamp01(p[v]);
-            sum += units(w);
-            if (sum > border) {
-                s_found = v;
-                break;
+        for (int v = v0 + 4 * lane; v < end; v += kDeep * kRound) {
+            float4 w[kDeep];
+            weights(v, plain, w);
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                sum += (units(w[k].x) + units(w[k].y)) + (units(w[k].z) + units(w[k].w));
+                f += (w[k].x + w[k].y) + (w[k].z + w[k].w);
             }
         }
+        sum = warp_sum(sum);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
+        __syncthreads();                                   // the round before has read s_sum
+        if (lane == 0) {
+            s_sum[warp] = sum;
+            s_f[warp] = f;
+        }
+        __syncthreads();
+        sum = 0;
+        f = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            sum += s_sum[k];
+            f += s_f[k];
+        }
+        before = 0;
+        if (C > 1) {
+            if (round == 0) cluster_wait();
+            if (tid < C) {
+                put_cluster(&c_sum[round][rank], tid, sum);
+                put_cluster(&c_f[round][rank], tid, f);
+            }
+            cluster_sync();
+            total = 0;
+            all = 0.0f;
+            for (int k = 0; k < C; ++k) {
+                if (k == rank) before = total;
+                total += c_sum[round][k];
+                all += c_f[round][k];
+            }
+            sum = c_sum[round][rank];
+        } else {
+            total = sum;
+            all = f;
+        }
+        if (total > 0 || plain) break;                     // the same in every CTA
+        plain = true;
     }
-    __syncthreads();
-    if (!valid && t == 0) atomicOr(&g_sample_err, BIV_DEVERR_VALUE);
-    for (int j = t; j <= K; j += kThreads)
-        tokens[static_cast<long long>(r) * (K + 1) + j] =
-            j < n ? draft[static_cast<long long>(r) * K + j] : j == n ? s_found : -1;
-    if (t == 0) {
-        accept_len[r] = n + 1;
-        new_len[r] = p0[r] + n + 1;
+    const bool valid = total > 0 && all < 8.0f;
+    const unsigned long long border = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
+    if (rank == 0) {
+        for (int j = tid; j <= K; j += kThreads)
+            if (j != n || !valid) tokens[r * (K + 1) + j] = j < n ? draft[r * K + j] : j == n ? 0 : -1;
+        if (tid == 0) {
+            if (!valid) atomicOr(&g_sample_err, BIV_DEVERR_VALUE);
+            accept_len[r] = n + 1;
+            new_len[r] = p0[r] + n + 1;
+        }
     }
+    if (!valid) return;
+    // s_sum still holds the warps' sums: the warp whose share holds the border walks its chunk
+    unsigned long long at = before;
+    for (int k = 0; k < warp; ++k) at += s_sum[k];
+    if (border < at || border >= at + s_sum[warp]) return;
+    for (int v = v0; v < end; v += kDeep * kRound) {
+        float4 w[kDeep];
+        weights(v + 4 * lane, plain, w);
+        unsigned long long four[kDeep], incl[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) incl[k] = four[k] = (units(w[k].x) + units(w[k].y)) + (units(w[k].z) + units(w[k].w));
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                const unsigned long long o = __shfl_up_sync(0xffffffffu, incl[k], s);
+                if (lane >= s) incl[k] += o;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const unsigned long long pre = at + incl[k] - four[k];
+            if (border >= pre && border < pre + four[k]) {
+                const unsigned long long a = pre + units(w[k].x), b = a + units(w[k].y), c = b + units(w[k].z);
+                tokens[r * (K + 1) + n] = v + 4 * lane + k * kRound + (border < a ? 0 : border < b ? 1 : border < c ? 2 : 3);
+            }
+            at += __shfl_sync(0xffffffffu, incl[k], 31);
+        }
+        if (border < at) return;
+    }
+}
+
+bool aligned_rows(const float* p, long long ld) { return aligned16(p) && ld % 4 == 0; }
+
+template <bool VEC, int NV, bool LONG>
+int launch_softmax(const float* x, int R, int V, long long ld, float scale, float* p, long long ld_p, int C,
+                   cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(R) * C);
+    if (C == 1)
+        return launch_pdl(softmax_kernel<VEC, NV, LONG>, grid, dim3(kThreads), 0, s, x, V, ld, scale, p, ld_p, C);
+    return launch_cluster_pdl(softmax_kernel<VEC, NV, LONG>, grid, dim3(kThreads), 0, s, C, x, V, ld, scale, p, ld_p, C);
+}
+
+// Loads a thread and CTAs a row, by V alone: up to four loads a thread, then up to
+// eight CTAs, then more loads.
+template <bool VEC>
+int launch_softmax(const float* x, int R, int V, long long ld, float scale, bool greedy, float* p, long long ld_p,
+                   cudaStream_t s) {
+    if (greedy)
+        return launch_pdl(softmax_greedy_kernel<VEC>, dim3(static_cast<unsigned>(R)), dim3(kThreads), 0, s, x, V, ld, p, ld_p);
+    const int loads = (V + kPerLoad - 1) / kPerLoad;
+    if (loads <= 1) return launch_softmax<VEC, 1, false>(x, R, V, ld, scale, p, ld_p, 1, s);
+    if (loads <= 4) return launch_softmax<VEC, 4, false>(x, R, V, ld, scale, p, ld_p, 1, s);
+    if (loads <= 32) return launch_softmax<VEC, 4, false>(x, R, V, ld, scale, p, ld_p, loads <= 8 ? 2 : loads <= 16 ? 4 : 8, s);
+    if (loads <= 64) return launch_softmax<VEC, 8, false>(x, R, V, ld, scale, p, ld_p, 8, s);
+    if (loads <= 80) return launch_softmax<VEC, 10, false>(x, R, V, ld, scale, p, ld_p, 8, s);
+    if (loads <= 128) return launch_softmax<VEC, 16, false>(x, R, V, ld, scale, p, ld_p, 8, s);
+    return launch_softmax<VEC, 8, true>(x, R, V, ld, scale, p, ld_p, 8, s);
 }
 
 }  // namespace
@@ -168,9 +435,12 @@ extern "C" int biv_softmax(const float* logits, int R, int V, long long ld, floa
     // log2(e) / T; a T so small that it would overflow leaves the largest entries alone, as it should
     const float scale = temperature == 0.0f ? 0.0f
                                             : static_cast<float>(std::min(1.4426950408889634 / temperature, 3.4028234663852886e38));
-    return launch_pdl(softmax_kernel, dim3(static_cast<unsigned>(R)), dim3(kThreads), 0,
-                      reinterpret_cast<cudaStream_t>(stream), logits, V, ld, scale, temperature == 0.0f ? 1 : 0,
-                      probs, ld_p);
+    if (static_cast<long long>(R) * kMaxCluster > 0x7fffffffLL) return BIV_ERR_SHAPE;
+    const bool greedy = temperature == 0.0f;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return aligned_rows(logits, ld) && aligned_rows(probs, ld_p)
+               ? launch_softmax<true>(logits, R, V, ld, scale, greedy, probs, ld_p, s)
+               : launch_softmax<false>(logits, R, V, ld, scale, greedy, probs, ld_p, s);
 }
 
 extern "C" int biv_verify_sample(const float* target, const float* draft_probs, const int32_t* draft,
@@ -182,7 +452,17 @@ extern "C" int biv_verify_sample(const float* target, const float* draft_probs, 
     if (N == 0) return BIV_OK;
     if (!target || !u_sample || !p0 || !tokens || !accept_len || !new_len) return BIV_ERR_NULL;
     if (K > 0 && (!draft || !u_accept)) return BIV_ERR_NULL;
-    return launch_pdl(verify_sample_kernel, dim3(static_cast<unsigned>(N)), dim3(kThreads), 0,
-                      reinterpret_cast<cudaStream_t>(stream), target, draft_probs, draft, u_accept, u_sample, p0, K, V,
-                      tokens, accept_len, new_len);
+    if (static_cast<long long>(N) * kMaxCluster > 0x7fffffffLL) return BIV_ERR_SHAPE;
+    // CTAs of a request: as many as its row gives work, fewer where the requests alone fill the machine
+    int C = 1;
+    while (C < kMaxCluster && C * kPerLoad < V && 2LL * N * C <= 2LL * num_sms()) C *= 2;
+    const bool vec = aligned_rows(target, V) && (!draft_probs || aligned_rows(draft_probs, V));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto kernel = vec ? verify_sample_kernel<true> : verify_sample_kernel<false>;
+    const dim3 grid(static_cast<unsigned>(N) * C);
+    if (C == 1)
+        return launch_pdl(kernel, grid, dim3(kThreads), 0, s, target, draft_probs, draft, u_accept, u_sample, p0, K, V, tokens,
+                          accept_len, new_len, C);
+    return launch_cluster_pdl(kernel, grid, dim3(kThreads), 0, s, C, target, draft_probs, draft, u_accept, u_sample, p0, K, V,
+                              tokens, accept_len, new_len, C);
 }

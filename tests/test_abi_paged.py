@@ -138,13 +138,12 @@ def test_binding_refuses_wrong_tensors(lib):
     refused(DEVICE, B.biv_gemm_bias_act, z(4, 64), z(64, 64), z(4, 64))
     pool, q = z(9, 2, 16, 128), z(4, 8, 128)
     ws = torch.zeros(64, dtype=torch.uint8)
-    refused(VALUE, B.biv_decode_attn_paged, q, pool, pool, i(4, 3).long(), i(4), i(4), z(4, 8, 128), 1, ws)
+    refused(VALUE, B.biv_decode_attn_paged, q, pool, pool.half(), i(4, 3), i(4), i(4), z(4, 8, 128), 1, ws)
     refused(SHAPE, B.biv_decode_attn_paged, q, pool, z(9, 2, 32, 128), i(4, 3), i(4), i(4), z(4, 8, 128), 1, ws)
-    refused(SHAPE, B.biv_decode_attn_paged, q, pool, pool, i(4, 3), i(5), i(4), z(4, 8, 128), 1, ws)
+    refused(SHAPE, B.biv_decode_attn_paged, q, pool, pool, i(4, 3), i(4), i(4), z(4, 8, 64), 1, ws)
     refused(DEVICE, B.biv_decode_attn_paged, q, pool, pool, i(4, 3), i(4), i(4), z(4, 8, 128), 1, ws)
     refused(SHAPE, B.biv_rope_kv_write_paged, z(4, 11 * 128), q, pool, pool, i(4, 3), i(4), i(4), 1e4, 1)
-    refused(SHAPE, B.biv_rope_kv_write_paged, z(4, 12 * 128), q, pool, pool, i(4, 3), i(4), i(4), 1e4, 2,
-            rows_keep=i(4))
+    refused(DEVICE, B.biv_rope_kv_write_paged, z(4, 12 * 128), q, pool, pool, i(4, 3), i(4), i(4), 1e4, 1)
     f = lambda *s: torch.zeros(*s)  # noqa: E731
     refused(VALUE, B.biv_softmax, f(4, 8).double(), f(4, 8), 1.0)
     refused(SHAPE, B.biv_softmax, f(4, 8), f(4, 7), 1.0)
@@ -152,4 +151,5 @@ def test_binding_refuses_wrong_tensors(lib):
     refused(SHAPE, B.biv_softmax, f(1, 8).expand(4, 8), f(4, 8), 1.0)      # one row for all: not a matrix of rows
     refused(DEVICE, B.biv_softmax, f(4, 8), f(4, 8), 1.0)
     refused(SHAPE, B.biv_verify_sample, f(6, 10), f(3, 10), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
+    refused(VALUE, B.biv_verify_sample, f(6, 10), f(4, 10).double(), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
     refused(DEVICE, B.biv_verify_sample, f(6, 10), f(4, 10), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
