@@ -1374,14 +1374,17 @@ int launch_gemm(const void* A, const void* B, void* C, int M, int N, int K, int 
 }
 
 // One row tile (M <= 128) as CTA pairs that halve it: a CTA then takes M / 2 rows of
-// A and BN / 2 rows of B out of L2 for every k-block instead of M and bn, and what an
-// SM can take (about 120 GB/s) is what bounds these GEMMs once A is no small part.
-// M = 64, N = 4096, K = 14336: 96 rows a k-block per CTA, 35.6 us, against 64 rows.
+// A and BN / 2 rows of B out of L2 for every k-block instead of M and bn rows, and an
+// SM takes about 120 GB/s.  A pair costs about 2 us more to start, so it pays where A
+// is long (pairs against single CTAs, us): M = 64, N = 4096, K = 14336: 32.8 / 35.5;
+// M = 128 there: 38.1 / 48.0; M = 128, N = 4096, K = 4096: 15.0 / 16.2; but M = 64
+// there: 13.5 / 12.4, K = 1024: 7.1 / 5.5, and with wide tiles (N = 14336, K = 4096,
+// M = 128), whose ring holds few k-blocks: 27.5 / 24.7.
 inline int halves_tile_n(int N) {
     return static_cast<int>(std::min<long long>(256, std::max<long long>(64, ceil_div(ceil_div(N, kPairWave), 32) * 32)));
 }
 inline bool halves_pay(int M, int N, int K) {
-    return M > 32 && M <= kBM && K % kBK == 0 && N >= 2048 && ceil_div(N, halves_tile_n(N)) <= kPairWave;
+    return M >= 48 && M <= kBM && K % kBK == 0 && static_cast<long long>(M) * K >= 380000 && N >= 2048 && N <= 128 * kPairWave;
 }
 
 int check_gemm(const void* A, const void* B, void* C, int out_dtype, int M, int N, int K) {

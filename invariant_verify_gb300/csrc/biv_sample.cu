@@ -2,6 +2,7 @@
 // drafted tokens from given uniform numbers.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "biv_common.cuh"
 
@@ -72,12 +73,65 @@ BIV_DEV void put_cluster(const void* p, uint32_t rank, unsigned long long x) {
 // batch.  Rows past 8 x 16 x 2048 entries are read twice.
 constexpr int kMaxCluster = 8;
 
+// Exponentials of a slice on its own maximum: an infinite maximum's entries share the
+// mass (differences would be NaN), a slice of nothing but -infinity gives zeros.
+struct SlicePower {
+    float zero_at, scale;
+    bool infinite;
+    BIV_DEV SlicePower(float m, float s) : zero_at(m == INFINITY || m == -INFINITY ? 0.0f : m), scale(s), infinite(m == INFINITY) {}
+    BIV_DEV float4 operator()(float4 y) const {
+        if (infinite)
+            y = make_float4(y.x == INFINITY ? 0.0f : -INFINITY, y.y == INFINITY ? 0.0f : -INFINITY,
+                            y.z == INFINITY ? 0.0f : -INFINITY, y.w == INFINITY ? 0.0f : -INFINITY);
+        return make_float4(ex2_approx((y.x - zero_at) * scale), ex2_approx((y.y - zero_at) * scale),
+                           ex2_approx((y.z - zero_at) * scale), ex2_approx((y.w - zero_at) * scale));
+    }
+};
+
+BIV_DEV float max4(float m, float4 r) { return fmaxf(m, fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w))); }
+
+// Largest value (sum) over the CTA, in an order that goes by the thread alone.
+BIV_DEV float cta_max(float m, float* s_m) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, s_m[k]);
+    return m;
+}
+BIV_DEV float cta_sum(float l, float* s_l) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if ((threadIdx.x & 31) == 0) s_l[threadIdx.x >> 5] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) l += s_l[k];
+    return l;
+}
+
+// The factor of this CTA's exponentials, from (maximum, sum) of all C CTAs.
+BIV_DEV float slice_factor(float m_cta, float scale, const float2* ml, int C) {
+    float m = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k].x);
+    auto share = [&](float mk) { return mk == -INFINITY ? 0.0f : mk == m ? 1.0f : m == INFINITY ? 0.0f : ex2_approx((mk - m) * scale); };
+    for (int k = 0; k < C; ++k) sum = fmaf(ml[k].y, share(ml[k].x), sum);
+    return m == -INFINITY ? 0.0f : share(m_cta) / sum;
+}
+
+BIV_DEV unsigned long long pack2(float a, float b) {
+    return static_cast<unsigned long long>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+
+BIV_DEV float4 times(float4 r, float f) { return make_float4(r.x * f, r.y * f, r.z * f, r.w * f); }
+
 template <bool VEC, int NV, bool LONG>
 __global__ void __launch_bounds__(kThreads, LONG || NV > 10 ? 1 : NV > 4 ? 2 : 3)
 softmax_kernel(const float* logits, int V, long long ld, float scale, float* probs, long long ld_p, int C) {
     __shared__ float s_m[kWarps], s_l[kWarps];
-    __shared__ float c_m[kMaxCluster], c_l[kMaxCluster];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ __align__(8) float2 c_ml[kMaxCluster];
+    const int tid = threadIdx.x;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const long long row = blockIdx.x / C;
     if (C > 1) cluster_started();
@@ -91,74 +145,122 @@ softmax_kernel(const float* logits, int V, long long ld, float scale, float* pro
     const int end = min(V, (rank + 1) * per);
 
     float4 r[NV];
-    float m_cta = -INFINITY;
+    float m = -INFINITY;
     for (int base = 0; base < per; base += NV * kPerLoad) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) r[k] = load4<VEC>(x, v0 + base + k * kPerLoad, end, -INFINITY);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            r[k] = no_nan(r[k]);
-            m_cta = fmaxf(m_cta, fmaxf(fmaxf(r[k].x, r[k].y), fmaxf(r[k].z, r[k].w)));
-        }
+        for (int k = 0; k < NV; ++k) m = max4(m, r[k] = no_nan(r[k]));
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m_cta = fmaxf(m_cta, __shfl_xor_sync(0xffffffffu, m_cta, d));
-    if (lane == 0) s_m[warp] = m_cta;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) m_cta = fmaxf(m_cta, s_m[k]);
-
-    // An infinite maximum: its entries share the mass (differences would be NaN).  A
-    // slice of nothing but -infinity: zeros.
-    const bool infinite = m_cta == INFINITY, empty = m_cta == -INFINITY;
-    const float zero_at = infinite || empty ? 0.0f : m_cta;
-    auto power4 = [&](float4 y) {
-        if (infinite)
-            y = make_float4(y.x == INFINITY ? 0.0f : -INFINITY, y.y == INFINITY ? 0.0f : -INFINITY,
-                            y.z == INFINITY ? 0.0f : -INFINITY, y.w == INFINITY ? 0.0f : -INFINITY);
-        return make_float4(ex2_approx((y.x - zero_at) * scale), ex2_approx((y.y - zero_at) * scale),
-                           ex2_approx((y.z - zero_at) * scale), ex2_approx((y.w - zero_at) * scale));
-    };
+    m = cta_max(m, s_m);
+    const SlicePower power(m, scale);
     float l = 0.0f;
     for (int base = 0; base < per; base += NV * kPerLoad) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if constexpr (LONG) r[k] = no_nan(load4<VEC>(x, v0 + base + k * kPerLoad, end, -INFINITY));
-            r[k] = power4(r[k]);
+            r[k] = power(r[k]);
             l += (r[k].x + r[k].y) + (r[k].z + r[k].w);
         }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) l += s_l[k];
-
-    float m = m_cta, factor = 1.0f / l;                    // of this CTA's exponentials
+    l = cta_sum(l, s_l);
+    float factor = m == -INFINITY ? 0.0f : 1.0f / l;
     if (C > 1) {
         cluster_wait();
-        if (tid < C) {
-            put_cluster(&c_m[rank], tid, m_cta);
-            put_cluster(&c_l[rank], tid, l);
-        }
+        if (tid < C) put_cluster(&c_ml[rank], tid, pack2(m, l));
         cluster_sync();
-        for (int k = 0; k < C; ++k) m = fmaxf(m, c_m[k]);
-        float sum = 0.0f;
-        auto share = [&](float mk) { return mk == -INFINITY ? 0.0f : mk == m ? 1.0f : m == INFINITY ? 0.0f : ex2_approx((mk - m) * scale); };
-        for (int k = 0; k < C; ++k) sum = fmaf(c_l[k], share(c_m[k]), sum);
-        factor = share(m_cta) / sum;
+        factor = slice_factor(m, scale, c_ml, C);
     }
-    if (m == -INFINITY) factor = 0.0f;
-
     for (int base = 0; base < per; base += NV * kPerLoad) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int v = v0 + base + k * kPerLoad;
-            if constexpr (LONG) r[k] = power4(no_nan(load4<VEC>(x, v, end, -INFINITY)));
-            if (v < end) store4<VEC>(p, v, end, make_float4(r[k].x * factor, r[k].y * factor, r[k].z * factor, r[k].w * factor));
+            if constexpr (LONG) r[k] = power(no_nan(load4<VEC>(x, v, end, -INFINITY)));
+            if (v < end) store4<VEC>(p, v, end, times(r[k], factor));
         }
+    }
+}
+
+// Many rows of a large vocabulary: the clusters stay and take row after row, and the
+// next row's slice is on its way into shared memory (one bulk copy, as soon as the
+// threads hold the row before) while a row is summed and written.  The same slices,
+// orders and bits as softmax_kernel, whose CTAs read, wait for one another and write
+// in turn.  (Maximum, sum) travel by asynchronous stores that count on a barrier of
+// the receiving CTA: a cluster barrier's release would wait until the row before has
+// been written out.
+template <int NV>
+__global__ void __launch_bounds__(kThreads, 2)
+softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale, float* probs, long long ld_p) {
+    constexpr int kSlice = NV * kPerLoad, C = kMaxCluster;
+    extern __shared__ __align__(16) float s_x[];           // [kSlice]
+    __shared__ float s_m[kWarps], s_l[kWarps];
+    __shared__ __align__(8) float2 c_ml[2][C];
+    __shared__ uint64_t full, heard[2];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int step = gridDim.x / C;
+    const int start = rank * kSlice, n = min(max(V - start, 0), kSlice);      // this CTA's slice of every row
+    if (tid == 0) {
+        mbar_init(&full, 1);
+        mbar_init(&heard[0], 1);
+        mbar_init(&heard[1], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    cluster_started();
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    auto fetch = [&](int row) {                            // by one thread
+        mbar_arrive_expect_tx(&full, static_cast<uint32_t>(n) * 4u);
+        if (n > 0)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(s_x)),
+                         "l"(logits + static_cast<long long>(row) * ld + start), "r"(n * 4), "r"(smem_u32(&full))
+                         : "memory");
+    };
+    int row = blockIdx.x / C;
+    if (tid == 0) fetch(row);                              // the grid holds no more clusters than rows
+    cluster_wait();
+    uint32_t heard_phase = 0;
+    for (uint32_t phase = 0; row < R; row += step, phase ^= 1u) {
+        mbar_wait(&full, phase, &abort_flag, &g_sample_err);           // one that runs out raises its bit; the row is lost
+        const float* x = s_x + 4 * tid;
+        float4 r[NV];
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            r[k] = 4 * tid + k * kPerLoad < n ? no_nan(*reinterpret_cast<const float4*>(x + k * kPerLoad))
+                                              : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            m = max4(m, r[k]);
+        }
+        m = cta_max(m, s_m);                               // its barrier: every thread has read the buffer
+        if (tid == 0 && row + step < R) fetch(row + step);
+        const SlicePower power(m, scale);
+        float l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            r[k] = power(r[k]);
+            l += (r[k].x + r[k].y) + (r[k].z + r[k].w);
+        }
+        l = cta_sum(l, s_l);
+        // to every CTA's buffer of this row (two in turn: a CTA sends a row's only after
+        // all its threads are done with the one before, so none is overwritten early)
+        if (tid == 0) mbar_arrive_expect_tx(&heard[phase], C * 8);
+        if (tid < C)
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                             mapa_shared(&c_ml[phase][rank], tid)),
+                         "l"(pack2(m, l)), "r"(mapa_shared(&heard[phase], tid))
+                         : "memory");
+        mbar_wait(&heard[phase], heard_phase, &abort_flag, &g_sample_err, false, true);
+        if (phase) heard_phase ^= 1u;
+        const float factor = slice_factor(m, scale, c_ml[phase], C);
+        float* p = probs + static_cast<long long>(row) * ld_p + start + 4 * tid;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (4 * tid + k * kPerLoad < n) *reinterpret_cast<float4*>(p + k * kPerLoad) = times(r[k], factor);
     }
 }
 
@@ -400,6 +502,48 @@ int launch_softmax(const float* x, int R, int V, long long ld, float scale, floa
     return launch_cluster_pdl(softmax_kernel<VEC, NV, LONG>, grid, dim3(kThreads), 0, s, C, x, V, ld, scale, p, ld_p, C);
 }
 
+// Many rows: as many clusters of softmax_rows_kernel as the device holds at once.
+// *done = false: the rows fit softmax_kernel's one wave (or the device holds none).
+template <int NV>
+int launch_softmax_rows(const float* x, int R, int V, long long ld, float scale, float* p, long long ld_p, bool* done,
+                        cudaStream_t s) {
+    constexpr int smem = NV * kPerLoad * 4;
+    static std::mutex mu;
+    static int resident[kMaxDevices] = {};                 // clusters, 0: not yet asked, -1: none
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (dev < 0 || dev >= kMaxDevices) return BIV_ERR_DEVICE;
+    int n = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (resident[dev] == 0) {
+            e = cudaFuncSetAttribute(softmax_rows_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return cuda_status(e);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms() / kMaxCluster * kMaxCluster));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = kMaxCluster;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int most = 0;
+            e = cudaOccupancyMaxActiveClusters(&most, softmax_rows_kernel<NV>, &cfg);
+            if (e != cudaSuccess) return cuda_status(e);
+            resident[dev] = most > 0 ? most : -1;
+        }
+        n = resident[dev];
+    }
+    *done = n > 0 && R > n;
+    if (!*done) return BIV_OK;
+    return launch_cluster_pdl(softmax_rows_kernel<NV>, dim3(static_cast<unsigned>(n) * kMaxCluster), dim3(kThreads), smem, s,
+                              kMaxCluster, x, R, V, ld, scale, p, ld_p);
+}
+
 // Loads a thread and CTAs a row, by V alone: up to four loads a thread, then up to
 // eight CTAs, then more loads.
 template <bool VEC>
@@ -410,6 +554,13 @@ int launch_softmax(const float* x, int R, int V, long long ld, float scale, bool
     const int loads = (V + kPerLoad - 1) / kPerLoad;
     if (loads <= 1) return launch_softmax<VEC, 1, false>(x, R, V, ld, scale, p, ld_p, 1, s);
     if (loads <= 4) return launch_softmax<VEC, 4, false>(x, R, V, ld, scale, p, ld_p, 1, s);
+    if (VEC && loads > 16 && loads <= 80) {
+        bool done = false;
+        const int st = loads <= 32   ? launch_softmax_rows<4>(x, R, V, ld, scale, p, ld_p, &done, s)
+                       : loads <= 64 ? launch_softmax_rows<8>(x, R, V, ld, scale, p, ld_p, &done, s)
+                                     : launch_softmax_rows<10>(x, R, V, ld, scale, p, ld_p, &done, s);
+        if (st != BIV_OK || done) return st;
+    }
     if (loads <= 32) return launch_softmax<VEC, 4, false>(x, R, V, ld, scale, p, ld_p, loads <= 8 ? 2 : loads <= 16 ? 4 : 8, s);
     if (loads <= 64) return launch_softmax<VEC, 8, false>(x, R, V, ld, scale, p, ld_p, 8, s);
     if (loads <= 80) return launch_softmax<VEC, 10, false>(x, R, V, ld, scale, p, ld_p, 8, s);

@@ -290,7 +290,8 @@ def test_gemm_bias_act(M, N, K, act):
     assert B.biv_device_error() == 0
 
 
-@pytest.mark.parametrize("M,N,K", [(7, 1024, 1024), (64, 4096, 512), (300, 512, 256)])
+@pytest.mark.parametrize("M,N,K", [(7, 1024, 1024), (64, 4096, 512), (300, 512, 256), (48, 2056, 8192), (65, 2048, 6400),
+                                    (127, 9728, 4096), (128, 4104, 2976)])
 def test_gemm_bias_act_bits(M, N, K):
     """No bias, activation or residual: the plain GEMM's bits; in place over the
     residual the same as apart; a row does not depend on M."""

@@ -49,14 +49,16 @@ def test_softmax_special_rows(V):
     x[7] = 3e38
     x[7, 2] = -3e38
     for T in (1.0, 0.3, 0.0):
-        check_softmax(softmax(x, T), x, T)
+        p = softmax(x, T)
+        check_softmax(p, x, T)
+        assert same_bits(softmax(x.repeat(12, 1), T), p.repeat(12, 1))
     check_softmax(softmax(x[:1], 1e-45), x[:1], 1e-45)
     y = torch.tensor([[1.0, 3.0, 3.0, 2.0]])
     assert softmax(y, 1e-42).tolist() == [[0.0, 0.5, 0.5, 0.0]]
     assert softmax(y, 0.0).tolist() == [[0.0, 1.0, 0.0, 0.0]]
 
 
-@pytest.mark.parametrize("V", [3, 1000, 33333, 128256])
+@pytest.mark.parametrize("V", [3, 1000, 33333, 40004, 128256, 152064])
 def test_softmax_layouts_give_the_same_bits(V):
     """Strided rows, rows off 16-byte alignment, in place, one row alone; columns past V stay."""
     R = 4
@@ -74,8 +76,11 @@ def test_softmax_layouts_give_the_same_bits(V):
         B.biv_softmax(wide[:, off:], wide[:, off:], 0.7, V=V)
         assert same_bits(wide[:, off:off + V].contiguous(), base)
         assert bool((wide[:, off + V:] == 50).all())
-    many = x.repeat(100, 1)
-    assert same_bits(softmax(many, 0.7)[396:400], base)
+    many = x.repeat(100, 1)                        # row after row by clusters that stay
+    out = softmax(many, 0.7)
+    assert same_bits(out, base.repeat(100, 1))
+    B.biv_softmax(many, many, 0.7)                 # in place
+    assert same_bits(many, out)
 
 
 # ------------------------------------------------------------------ verify
