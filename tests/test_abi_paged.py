@@ -150,6 +150,6 @@ def test_binding_refuses_wrong_tensors(lib):
     refused(SHAPE, B.biv_softmax, f(8, 4).t(), f(4, 8), 1.0)
     refused(SHAPE, B.biv_softmax, f(1, 8).expand(4, 8), f(4, 8), 1.0)      # one row for all: not a matrix of rows
     refused(DEVICE, B.biv_softmax, f(4, 8), f(4, 8), 1.0)
-    refused(SHAPE, B.biv_verify_sample, f(6, 10), f(3, 10), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
-    refused(VALUE, B.biv_verify_sample, f(6, 10), f(4, 10).double(), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
+    refused(SHAPE, B.biv_verify_sample, f(5, 10), f(4, 10), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
+    refused(VALUE, B.biv_verify_sample, f(6, 10), f(4, 10), i(2, 2), f(2, 2).double(), f(2), i(2), i(2, 3), i(2), i(2))
     refused(DEVICE, B.biv_verify_sample, f(6, 10), f(4, 10), i(2, 2), f(2, 2), f(2), i(2), i(2, 3), i(2), i(2))
