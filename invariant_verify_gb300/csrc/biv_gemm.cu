@@ -568,14 +568,19 @@ BIV_DEV float one_plus_erf_half(float x) {
     return x < 0.0f ? e : 2.0f - e;
 }
 
-// act(x) in fp32.  tanhf is within 2 ulp and the others' errors below 2^-21 of |x|, so
-// the result's one rounding to C's type is the one that counts.
+// x / (1 + e^-y), a few ulp (silu with y = x).  e^-y = infinity gives 0.
+BIV_DEV float times_sigmoid(float x, float y) { return __fdividef(x, 1.0f + ex2_approx(-1.4426950408889634f * y)); }
+
+// act(x) in fp32, without branches: the epilogue of a CTA's last tile is not hidden
+// behind any product.  Errors stay below 2^-20 of |x|, so the result's one rounding to
+// bf16 is the one that counts.  x/2 (1 + tanh u) = x / (1 + e^-2u) loses nothing to
+// cancellation.
 BIV_DEV float activate(float x, int act) {
     switch (act) {
         case BIV_ACT_RELU: return x > 0.0f || x != x ? x : 0.0f;
         case BIV_ACT_GELU: return 0.5f * x * one_plus_erf_half(x);
-        case BIV_ACT_GELU_TANH: return 0.5f * x * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * x * x, x, x)));
-        case BIV_ACT_SILU: return silu(x);
+        case BIV_ACT_GELU_TANH: return times_sigmoid(x, 1.5957691216057308f * fmaf(0.044715f * x * x, x, x));
+        case BIV_ACT_SILU: return times_sigmoid(x, x);
         default: return x;
     }
 }
@@ -588,34 +593,48 @@ BIV_DEV uint4 ld_global_16(const void* p) {
     return v;
 }
 
-// Eight columns of one row: C = act(acc + bias) + residual, one rounding.
-BIV_DEV void bias_act_store8(const uint32_t* v, int row, int col, int N, void* C, const BiasActArgs& ba) {
+// Sixteen columns of one row: C = act(acc + bias) + residual, one rounding.  The
+// operands from memory are requested before the accumulators are waited for.
+BIV_DEV void bias_act_16(uint32_t taddr, bool live, int row, int col, int N, void* C, const BiasActArgs& ba) {
     const long long at = static_cast<long long>(row) * N + col;
-    uint4 rs = make_uint4(0, 0, 0, 0), bs = make_uint4(0, 0, 0, 0);
-    if (ba.residual) rs = ld_global_16(ba.residual + at);
-    if (ba.bias) bs = __ldg(reinterpret_cast<const uint4*>(ba.bias + col));
-    const uint32_t b4[4] = {bs.x, bs.y, bs.z, bs.w}, r4[4] = {rs.x, rs.y, rs.z, rs.w};
-    float x[8];
+    uint4 bs[2], rs[2];
+    bool in[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float b = (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
-        x[e] = ba.bias ? __uint_as_float(v[e]) + b : __uint_as_float(v[e]);
+    for (int h = 0; h < 2; ++h) {
+        in[h] = live && col + 8 * h < N;
+        bs[h] = rs[h] = make_uint4(0, 0, 0, 0);
+        if (in[h] && ba.bias) bs[h] = __ldg(reinterpret_cast<const uint4*>(ba.bias + col + 8 * h));
+        if (in[h] && ba.residual) rs[h] = ld_global_16(ba.residual + at + 8 * h);
     }
-    if (ba.act != BIV_ACT_NONE) {
+    uint32_t v[16];
+    tmem_ld16(taddr, v);
+    tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
-    }
-    if (ba.residual) {
+    for (int h = 0; h < 2; ++h) {
+        if (!in[h]) continue;
+        const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
-    }
-    if (ba.out_f32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        for (int e = 0; e < 8; ++e) {
+            x[e] = __uint_as_float(v[8 * h + e]);
+            if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
+        }
+        if (ba.act != BIV_ACT_NONE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
+        }
+        if (ba.residual) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
+        }
+        if (ba.out_f32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at + 8 * h);
+            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at + 8 * h) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        }
     }
 }
 
@@ -1076,16 +1095,7 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 eset_columns(bnt, 16, (warp - 2) >> 2, cb5, ce5);
 #pragma unroll 1
                 for (int c = cb5; c < ce5; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(taddr + static_cast<uint32_t>(c), r);
-                    tmem_ld_wait();
-                    if (live) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int col = col0 + c + h * 8;
-                            if (col < N) bias_act_store8(r + h * 8, row, col, N, C, ba);
-                        }
-                    }
+                    bias_act_16(taddr + static_cast<uint32_t>(c), live, row, col0 + c, N, C, ba);
                 }
             } else {
             int cb0, ce0;
