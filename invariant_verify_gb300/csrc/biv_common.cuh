@@ -297,6 +297,12 @@ BIV_DEV uint64_t policy_evict_last() {
     return p;
 }
 
+BIV_DEV uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // ------------------------------------------------------------ clusters
 // Rank of this CTA in its cluster.
 BIV_DEV uint32_t cluster_ctarank() {
