@@ -1503,7 +1503,7 @@ extern "C" int biv_decode_attn_paged(const void* q, const void* k_pages, const v
     P.g_magic = P.G > 1 && static_cast<double>(P.rpg) * P.G * P.G < 4294967296.0
                     ? static_cast<uint32_t>((4294967296ull + P.G - 1) / P.G)
                     : 0u;
-    P.s_max = (P.cap + kSplit - 1) / kSplit;
+    P.s_max = (P.cap - 1) / kSplit + 1;                    // no sum that passes 31 bits
     P.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
     const long long parts = static_cast<long long>(W) * Hq * P.s_max;
     // partial outputs 32-byte aligned

@@ -554,7 +554,7 @@ int launch_softmax(const float* x, int R, int V, long long ld, float scale, bool
     const int loads = (V + kPerLoad - 1) / kPerLoad;
     if (loads <= 1) return launch_softmax<VEC, 1, false>(x, R, V, ld, scale, p, ld_p, 1, s);
     if (loads <= 4) return launch_softmax<VEC, 4, false>(x, R, V, ld, scale, p, ld_p, 1, s);
-    if (VEC && loads > 16 && loads <= 80) {
+    if (VEC && V % 4 == 0 && loads > 16 && loads <= 80) {           // a bulk copy takes whole 16-byte groups
         bool done = false;
         const int st = loads <= 32   ? launch_softmax_rows<4>(x, R, V, ld, scale, p, ld_p, &done, s)
                        : loads <= 64 ? launch_softmax_rows<8>(x, R, V, ld, scale, p, ld_p, &done, s)

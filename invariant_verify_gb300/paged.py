@@ -207,6 +207,8 @@ def paged_generate(ver: PagedVerifier, prompts: list, n_tokens: int, generator: 
     n, K = len(prompts), ver.K
     if n > ver.N:
         raise ValueError(f"{n} prompts, the verifier has {ver.N} seats")
+    if not all(len(p) for p in prompts):
+        raise ValueError("a prompt has at least one token")
     text = [[int(t) for t in p] for p in prompts]
     for r, p in enumerate(text):
         ver.prefill(r, p[:-1])                    # the last token is the first window's row 0

@@ -92,6 +92,39 @@ def test_attention_does_not_depend_on_batch_pages_or_workspace():
         assert same_bits(attend(q, pool, range(4), [n - 1 for n in lengths], table=wide), base)
 
 
+def test_attention_more_rows_than_the_tables_hold():
+    """Thousands of single rows, and one prompt's rows as a single group (their first
+    ones see one key, their last ones all)."""
+    Hq, Hkv, hd, page = 4, 2, 64, 16
+    W = 2600
+    lengths = [1 + (37 * r) % 90 for r in range(W)]
+    pool = U.Pool(lengths, Hkv, hd, page, seed=6)
+    q = U.bf16(U.gen(7), W, Hq, hd)
+    pos = [n - 1 for n in lengths]
+    o = attend(q, pool, range(W), pos)
+    some = list(range(0, W, 131))
+    within(o[some], *U.attention(q[some], pool.rows, some, [pos[r] for r in some]))
+    assert same_bits(attend(q[some], pool, some, [pos[r] for r in some]), o[some])
+    pool = U.Pool([W], Hkv, hd, page, seed=8)
+    pos, slot = list(range(W)), [0] * W
+    o = attend(q, pool, slot, pos, rpg=W)
+    some = [0, 1, 15, 16, 255, 256, 257, 1000, 2047, 2048, W - 1]
+    within(o[some], *U.attention(q[some], pool.rows, [0] * len(some), some))
+    assert same_bits(attend(q[some], pool, [0] * len(some), some), o[some])
+    assert B.biv_device_error() == 0
+
+
+def test_attention_widest_table():
+    """A table for every position below 2^31: nothing but its width is large."""
+    small = U.Pool([300], 1, 64, 16, seed=3)
+    wide = (1 << 27) - 1
+    table = torch.full((1, wide), -1, dtype=torch.int32, device="cuda")
+    table[0, :small.table.shape[1]] = small.table[0].cuda()
+    q = U.bf16(U.gen(2), 1, 1, 64)
+    o = attend(q, small, [0], [299], table=table)
+    assert B.biv_device_error() == 0 and same_bits(o, attend(q, small, [0], [299]))
+
+
 def test_attention_shared_prefix_pages():
     """Two slots that name the same pages read the same keys."""
     pool = U.Pool([300, 300], 2, 128, 64, seed=1)
@@ -180,7 +213,8 @@ def test_attention_pool_past_two_gib_of_elements():
 
 # ------------------------------------------------------------------ write
 @pytest.mark.parametrize("Hq,Hkv,hd,page,K,N", [(8, 2, 128, 16, 1, 5), (4, 4, 64, 64, 3, 4), (6, 2, 256, 32, 1, 3),
-                                                 (32, 8, 128, 128, 700, 1), (5, 1, 16, 256, 2, 2)])
+                                                 (32, 8, 128, 128, 700, 1), (5, 1, 16, 256, 2, 2), (3, 3, 48, 16, 2, 3),
+                                                 (7, 1, 80, 32, 4, 200)])
 def test_rope_write(Hq, Hkv, hd, page, K, N):
     starts = [3 + 37 * r for r in range(N)]
     pool = U.Pool([s + K for s in starts], Hkv, hd, page, seed=K)

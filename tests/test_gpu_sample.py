@@ -83,6 +83,19 @@ def test_softmax_layouts_give_the_same_bits(V):
     assert same_bits(many, out)
 
 
+@pytest.mark.parametrize("V", [33001, 40003, 128254, 152061])
+def test_softmax_many_rows_with_a_ragged_end(V):
+    """Rows that start on 16 bytes and end off them, as many as persistent clusters would take."""
+    R, ld = 60, V + (-V) % 4
+    wide = torch.full((R, ld), 50.0, device="cuda")
+    wide[:, :V] = torch.randn(3, V, generator=U.gen(V)).cuda().repeat(20, 1)
+    out = torch.full((R, ld), 7.0, device="cuda")
+    B.biv_softmax(wide, out, 0.7, V=V)
+    check_softmax(out[:3, :V], wide[:3, :V].cpu(), 0.7)
+    assert same_bits(out[:, :V].contiguous(), out[:3, :V].repeat(20, 1))
+    assert bool((out[:, V:] == 7).all()) and B.biv_device_error() == 0
+
+
 # ------------------------------------------------------------------ verify
 def case(N, K, V, seed, point=False, near=0.7, T=1.0):
     g = U.gen(seed)
