@@ -124,13 +124,22 @@ struct SelectArgs {
     int greedy;
 };
 
-// Bias, activation and residual of the EPI 5 epilogue (biv_gemm_bias_act).
+// Bias, activation and residual of the EPI 5 and 6 epilogues (biv_gemm_bias_act).
 struct BiasActArgs {
     const __nv_bfloat16* bias;        // [N] or null
     const __nv_bfloat16* residual;    // [M, N] or null; may be C itself
     int act;                          // BIV_ACT_*
-    int out_f32;                      // C is fp32 instead of bf16
 };
+
+// EPI 6 (fp32 C): the tensor core cuts what it adds to an fp32 accumulator, an error that
+// grows with K (relative to the result's norm: 0.9e-6 at K = 1024, 3.9e-6 at 4096, 1.5e-5
+// at 14336; rounded sums of 32 bits have 3e-7), far below a bf16 C's rounding but not an
+// fp32 C's.  So every kSumBlocks k-blocks (768 terms) the accumulator moves on to rounded
+// fp32 sums in registers: 5.7e-7 to 6.5e-7 at any of these K.  It costs, in us with one
+// accumulator / with the sums: 10.2 / 13.2 at 1 x 4096 x 4096, 36 / 42 at 64 x 4096 x 14336,
+// 75 / 86 at 1023 x 4096 x 14336, 75 / 89 at 1023 x 14336 x 4096 (M x N x K; 8 k-blocks
+// instead of 12 take the same; tiles of 192 columns, which need no spills, 148 and 97 there).
+constexpr int kSumBlocks = 12;
 
 BIV_DEV uint32_t pick_word(const U4& w, uint32_t j) {
     return j == 0 ? w.x : (j == 1 ? w.y : (j == 2 ? w.z : w.w));
@@ -593,56 +602,61 @@ BIV_DEV uint4 ld_global_16(const void* p) {
     return v;
 }
 
-// Sixteen columns of one row: C = act(acc + bias) + residual, one rounding.  The
-// operands from memory are requested before the accumulators are waited for.
-BIV_DEV void bias_act_16(uint32_t taddr, bool live, int row, int col, int N, void* C, const BiasActArgs& ba) {
-    const long long at = static_cast<long long>(row) * N + col;
+// Sixteen columns of one row: C = act(acc + bias) + residual, one rounding.
+struct BiasActRow {
     uint4 bs[2], rs[2];
     bool in[2];
+    long long at;
+
+    // The operands from memory (requested before the accumulators are waited for).
+    BIV_DEV BiasActRow(bool live, int row, int col, int N, const BiasActArgs& ba) {
+        at = static_cast<long long>(row) * N + col;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        in[h] = live && col + 8 * h < N;
-        bs[h] = rs[h] = make_uint4(0, 0, 0, 0);
-        if (in[h] && ba.bias) bs[h] = __ldg(reinterpret_cast<const uint4*>(ba.bias + col + 8 * h));
-        if (in[h] && ba.residual) rs[h] = ld_global_16(ba.residual + at + 8 * h);
-    }
-    uint32_t v[16];
-    tmem_ld16(taddr, v);
-    tmem_ld_wait();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (!in[h]) continue;
-        const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = __uint_as_float(v[8 * h + e]);
-            if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
-        }
-        if (ba.act != BIV_ACT_NONE) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
-        }
-        if (ba.residual) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
-        }
-        if (ba.out_f32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at + 8 * h);
-            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at + 8 * h) =
-                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        for (int h = 0; h < 2; ++h) {
+            in[h] = live && col + 8 * h < N;
+            bs[h] = rs[h] = make_uint4(0, 0, 0, 0);
+            if (in[h] && ba.bias) bs[h] = __ldg(reinterpret_cast<const uint4*>(ba.bias + col + 8 * h));
+            if (in[h] && ba.residual) rs[h] = ld_global_16(ba.residual + at + 8 * h);
         }
     }
-}
+    template <bool F32, typename V>
+    BIV_DEV void store(V&& v, void* C, const BiasActArgs& ba) const {      // v(e): accumulator of column e
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!in[h]) continue;
+            const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = v(8 * h + e);
+                if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
+            }
+            if (ba.act != BIV_ACT_NONE) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
+            }
+            if (ba.residual) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
+            }
+            if constexpr (F32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at + 8 * h);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at + 8 * h) =
+                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            }
+        }
+    }
+};
 
 // EPI: 0 = bf16 C, 1 = fp32 C, 2 = SwiGLU of gate/up-interleaved B (bf16
 // activation [M, N/2]; see biv_gemm_swiglu), 3 = Gumbel-max selection of each
 // tile-row (optional fp32 C; see biv_lm_head_gumbel), 4 = RoPE of q and k, k
 // and v into the KV cache (see biv_gemm_qkv_rope), 5 = bias, activation and
-// residual (see biv_gemm_bias_act).
+// residual (see biv_gemm_bias_act), 6 = the same with an fp32 C and sums that are
+// rounded every kSumBlocks k-blocks.
 // CG = 1: one CTA per tile of 128 rows.  CG = 2: a cluster of two CTAs per
 // tile of 256 rows (cta_group::2 MMAs of M = 256): each CTA copies its own
 // 128 rows of A and its half of the tile's BN rows of B into its own shared
@@ -855,8 +869,8 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const TileAt ti = tile_at(g, t, m_tiles);
                 const uint32_t idesc_t = ti.bn == BN ? g.idesc : g.idesc_tail;
                 const int bnl_t = ti.bn / CG;
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                for (int sb = 0; sb < n_stage_blocks; ++sb) {
+                uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int sb = 0; sb < n_stage_blocks && ok; ++sb) {
                     if (!__all_sync(0xffffffffu,
                                     mbar_wait(&full[stage], phase, abort_flag, &g_gemm_err, true, CG == 2))) {
                         ok = false;
@@ -867,22 +881,50 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     const uint32_t b_addr = a_addr + static_cast<uint32_t>(A_BYTES);
                     int kb0, nkb;
                     stage_range(g, sb, kb0, nkb);
-                    for (int j = 0; j < nkb; ++j) {
-                        const int kb = kb0 + j;
-                        const uint64_t a_desc = sw128_kmajor_desc(a_addr + static_cast<uint32_t>(j * g.a_rows * kRowBytes));
-                        const uint64_t b_desc = sw128_kmajor_desc(b_addr + static_cast<uint32_t>(j * bnl_t * kRowBytes));
+                    // EPI 6: runs of k-blocks that end where the accumulator changes; the inner
+                    // loop stays as tight as the others' (it sets the rate of narrow tiles)
+                    for (int j = 0; j < nkb;) {
+                        int run = nkb, kb_first = 0;       // first k-block of the accumulator
+                        if constexpr (EPI == 6) {
+                            const int in_sum = (kb0 + j) % kSumBlocks;
+                            if (kb0 + j > 0 && in_sum == 0) {              // on to the other accumulator
+                                if constexpr (CG == 2) {
+                                    umma_commit_pair_elect(mapa_shared(&tfull[acc], 0));
+                                    umma_commit_pair_elect(mapa_shared(&tfull[acc], 1));
+                                } else {
+                                    umma_commit_elect(&tfull[acc]);
+                                }
+                                acc ^= 1;
+                                if (acc == 0) acc_phase ^= 1u;
+                                if (!__all_sync(0xffffffffu,
+                                                mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, &g_gemm_err, true, CG == 2))) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                            }
+                            run = min(nkb, j + kSumBlocks - in_sum);
+                            kb_first = kb0 + j - in_sum;
+                        }
+                        for (; j < run; ++j) {
+                            const int kb = kb0 + j;
+                            const uint64_t a_desc = sw128_kmajor_desc(a_addr + static_cast<uint32_t>(j * g.a_rows * kRowBytes));
+                            const uint64_t b_desc = sw128_kmajor_desc(b_addr + static_cast<uint32_t>(j * bnl_t * kRowBytes));
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k) {
-                            // +32 bytes along K inside the swizzle row = +2 in 16-byte units.
-                            if constexpr (CG == 2)
-                                umma_bf16_pair_elect(d_tmem, a_desc + 2u * k, b_desc + 2u * k, idesc_t,
-                                                     (kb > 0 || k > 0) ? 1u : 0u);
-                            else
-                                umma_bf16_elect(d_tmem, a_desc + 2u * k, b_desc + 2u * k, idesc_t,
-                                                (kb > 0 || k > 0) ? 1u : 0u);
+                            for (int k = 0; k < kBK / 16; ++k) {
+                                // +32 bytes along K inside the swizzle row = +2 in 16-byte units.
+                                if constexpr (CG == 2)
+                                    umma_bf16_pair_elect(d_tmem, a_desc + 2u * k, b_desc + 2u * k, idesc_t,
+                                                         (kb > kb_first || k > 0) ? 1u : 0u);
+                                else
+                                    umma_bf16_elect(d_tmem, a_desc + 2u * k, b_desc + 2u * k, idesc_t,
+                                                    (kb > kb_first || k > 0) ? 1u : 0u);
+                            }
                         }
                     }
                     any = true;
+                    if (!ok) break;
                     if constexpr (CG == 2) {
                         // the stage is free in both CTAs once these MMAs are done
                         umma_commit_pair_elect(mapa_shared(&empty[stage], 0));
@@ -946,6 +988,50 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 // under the next tile's MMAs.)
                 if (!sel.greedy)
                     tile_buckets<NT>(bk, g.a_rows, min(kBM, M - m_blk * kBM), bnt, col0, N, m_blk * kBM, sel);
+            }
+            if constexpr (EPI == 6) {
+                // Sums of the tile in registers (128 a thread in the widest): one
+                // accumulator after the other is added and handed back.
+                int cb6, ce6;
+                eset_columns(bnt, 16, (warp - 2) >> 2, cb6, ce6);
+                const int rloc = g.m64 ? q * 16 + lane : q * 32 + lane, row = row_base + rloc;
+                const bool live = row < M && rloc < g.row_step && (!g.m64 || lane < 16);
+                constexpr int kParts = 256 / 32;
+                float sum[kParts][16];
+                bool ok = true;
+                for (int kb = 0; kb < KB; kb += kSumBlocks) {
+                    ok = threadIdx.x == 64 ? mbar_wait(&tfull[acc], acc_phase, abort_flag, &g_gemm_err, false, CG == 2) : true;
+                    ok = epilogue_all<NT>(ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN + cb6);
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i)
+                        if (cb6 + 16 * i < ce6) {
+                            uint32_t r[16];
+                            tmem_ld16_sync(taddr + static_cast<uint32_t>(16 * i), r);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                sum[i][e] = kb == 0 ? __uint_as_float(r[e]) : sum[i][e] + __uint_as_float(r[e]);
+                        }
+                    tc_fence_before();
+                    if constexpr (CG == 2) {
+                        epilogue_bar<NT>();
+                        if (threadIdx.x == 64) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));
+                    } else {
+                        mbar_arrive(&tempty[acc]);
+                    }
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    if (cb6 + 16 * i < ce6) {
+                        const BiasActRow operands(live, row, col0 + cb6 + 16 * i, N, ba);
+                        operands.template store<true>([&](int e) { return sum[i][e]; }, C, ba);
+                    }
+                continue;
             }
             // One thread polls the accumulator barrier; the vote hands its
             // outcome to the other epilogue threads (no polling traffic beside
@@ -1095,7 +1181,11 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 eset_columns(bnt, 16, (warp - 2) >> 2, cb5, ce5);
 #pragma unroll 1
                 for (int c = cb5; c < ce5; c += 16) {
-                    bias_act_16(taddr + static_cast<uint32_t>(c), live, row, col0 + c, N, C, ba);
+                    const BiasActRow operands(live, row, col0 + c, N, ba);
+                    uint32_t r[16];
+                    tmem_ld16(taddr + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
+                    operands.template store<false>([&](int e) { return __uint_as_float(r[e]); }, C, ba);
                 }
             } else {
             int cb0, ce0;
@@ -1592,11 +1682,17 @@ extern "C" int biv_gemm_bias_act(const void* A, const void* B, const void* bias,
     ba.bias = static_cast<const __nv_bfloat16*>(bias);
     ba.residual = static_cast<const __nv_bfloat16*>(residual);
     ba.act = act;
-    ba.out_f32 = out_dtype == BIV_F32;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (halves_pay(M, N, K))
-        return launch_gemm_cg<5, 2>(A, B, C, M, N, K, halves_tile_n(N), s, SelectArgs{}, RopeArgs{}, nullptr, ba);
-    return launch_gemm<5>(A, B, C, M, N, K, biv_gemm_tile_n(M, N, K), s, SelectArgs{}, RopeArgs{}, nullptr, ba);
+    const SelectArgs sel{};
+    const RopeArgs rp{};
+    if (halves_pay(M, N, K)) {
+        const int bn = halves_tile_n(N);
+        return out_dtype == BIV_F32 ? launch_gemm_cg<6, 2>(A, B, C, M, N, K, bn, s, sel, rp, nullptr, ba)
+                                    : launch_gemm_cg<5, 2>(A, B, C, M, N, K, bn, s, sel, rp, nullptr, ba);
+    }
+    const int bn = biv_gemm_tile_n(M, N, K);
+    return out_dtype == BIV_F32 ? launch_gemm<6>(A, B, C, M, N, K, bn, s, sel, rp, nullptr, ba)
+                                : launch_gemm<5>(A, B, C, M, N, K, bn, s, sel, rp, nullptr, ba);
 }
 
 extern "C" int biv_swiglu_pack_weights(const void* w_gu, void* w_packed, int F, int K, biv_stream_t stream) {

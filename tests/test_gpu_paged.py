@@ -325,18 +325,24 @@ def test_gemm_bias_act(M, N, K, act):
 
 
 @pytest.mark.parametrize("M,N,K", [(7, 1024, 1024), (64, 4096, 512), (300, 512, 256), (48, 2056, 8192), (65, 2048, 6400),
-                                    (127, 9728, 4096), (128, 4104, 2976)])
+                                    (127, 9728, 4096), (128, 4104, 2976), (300, 264, 2000), (700, 512, 4096)])
 def test_gemm_bias_act_bits(M, N, K):
-    """No bias, activation or residual: the plain GEMM's bits; in place over the
-    residual the same as apart; a row does not depend on M."""
+    """No bias, activation or residual, bf16: the plain GEMM's bits; in place over the
+    residual the same as apart; a row does not depend on M, in either type."""
     g = U.gen(M)
     A, W = U.bf16(g, M, K).cuda(), U.bf16(g, N, K, std=0.05).cuda()
     bias, res = U.bf16(g, N).cuda(), U.bf16(g, M, N).cuda()
-    for dt in (torch.bfloat16, torch.float32):
-        a, b = nan_like(M, N, dtype=dt), nan_like(M, N, dtype=dt)
-        B.biv_gemm_bias_act(A, W, a)
-        B.biv_gemm_nosplitk(A, W, b)
-        assert same_bits(a, b)
+    a, b = nan_like(M, N), nan_like(M, N)
+    B.biv_gemm_bias_act(A, W, a)
+    B.biv_gemm_nosplitk(A, W, b)
+    assert same_bits(a, b)
+    full = nan_like(M, N, dtype=torch.float32)
+    B.biv_gemm_bias_act(A, W, full, bias=bias, residual=res)
+    # fp32 sums: blocks of 768 terms cut in the tensor core (48 additions, 2^-23 each at
+    # most), then at most K / 768 + 1 rounded additions
+    s = A.double() @ W.double().T
+    tol = (48 * 2.0 ** -23 + (K / 768 + 5) * 2.0 ** -24) * (A.double().abs() @ W.double().abs().T + bias.double().abs() + res.double().abs())
+    within(full, (s + bias.double() + res.double()).cpu(), tol.cpu(), "fp32")
     apart, over = nan_like(M, N), res.clone()
     B.biv_gemm_bias_act(A, W, apart, bias=bias, residual=res, act="gelu")
     B.biv_gemm_bias_act(A, W, over, bias=bias, residual=over, act="gelu")
@@ -345,6 +351,9 @@ def test_gemm_bias_act_bits(M, N, K):
         few = nan_like(len(rows), N)
         B.biv_gemm_bias_act(A[rows].contiguous(), W, few, bias=bias, residual=res[rows].contiguous(), act="gelu")
         assert same_bits(few, apart[rows])
+        few = nan_like(len(rows), N, dtype=torch.float32)
+        B.biv_gemm_bias_act(A[rows].contiguous(), W, few, bias=bias, residual=res[rows].contiguous())
+        assert same_bits(few, full[rows])
 
 
 def test_gemm_bias_act_not_a_number():
