@@ -180,8 +180,8 @@ BIV_DEV int usable_pos(const PagedAttnParams& P, int w, bool flag) {
 //           (K) or eight (V) lanes: no shared memory, no barrier and no address
 //           arithmetic between HBM and the tensor core.
 //   staged  more rows (verify windows): K and V pass through a ring in shared
-//           memory, filled by one warp's 16-byte asynchronous copies, so that up
-//           to four tiles of 8 rows share one read of the keys.
+//           memory, filled by TMA, so that up to four tiles of 8 rows share one
+//           read of the keys.
 constexpr int kClasses = 4;
 constexpr int kStep = 16;
 constexpr int kSteps = kSplit / kStep;                 // steps of a split
@@ -222,12 +222,6 @@ BIV_DEV uint32_t transpose8(uint32_t x) {
 BIV_DEV void cp_async16(void* smem, const void* gmem) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
 }
-// The same past L1, or sixteen zero bytes (nothing is read then).
-BIV_DEV void cp_async16_or_zero(uint32_t smem, const void* gmem, bool read, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem), "l"(gmem),
-                 "r"(read ? 16 : 0), "l"(policy)
-                 : "memory");
-}
 
 // One warp's running softmax over eight query rows: this lane's columns are rows
 // 2 (lane % 4) and the next; acc holds HD / 16 tiles of O^T.
@@ -246,31 +240,47 @@ struct RowState {
         l[0] = l[1] = 0.0f;
     }
 
-    // Scores of a step (S^T fragment: keys g8 and g8 + 8) to weights: the running
-    // maxima and sums move on, the output is rescaled where a maximum grew (the
-    // factor of a row that did not is exactly 1), and each weight leaves as the
-    // sum of two bf16 values, transposed to the B fragments of O^T += V^T P^T.
+    // Scores of a step (S^T fragment: keys g8 and g8 + 8) to weights: each weight leaves
+    // as the sum of two bf16 values, transposed to the B fragments of O^T += V^T P^T.
+    // A row's reference m follows its running maximum only when a score passes it by
+    // more than kSlack (weights of up to 2^kSlack are as exact as those up to 1), so that
+    // most steps need one vote and no exchange of maxima or scaling of the output (32
+    // windows of 5 rows: 71.4 -> 68.3 us, one request of 700 keys: 5.8 -> 5.4).
+    // Whether a row moves on depends on that row's scores alone (the factor of a row that
+    // does not is exactly 1).
+    static constexpr float kSlack = 8.0f;
     BIV_DEV void step(float (&st)[4], float scale_log2, uint32_t (&hi)[2], uint32_t (&low)[2]) {
-        float f[2], x[2];
-        bool grew = false;
+        float x[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) x[e] = fmaxf(st[e], st[e + 2]);
+        for (int e = 0; e < 2; ++e) x[e] = fmaxf(st[e], st[e + 2]) * scale_log2;
+        if (__any_sync(0xffffffffu, x[0] > m[0] + kSlack || x[1] > m[1] + kSlack)) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
-            x[0] = fmaxf(x[0], y0);
-            x[1] = fmaxf(x[1], y1);
+            for (int d = 4; d < 32; d <<= 1) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
+                x[0] = fmaxf(x[0], y0);
+                x[1] = fmaxf(x[1], y1);
+            }
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[e] = 1.0f;
+                if (x[e] > m[e] + kSlack) {
+                    f[e] = ex2_approx(m[e] - x[e]);
+                    m[e] = x[e];
+                }
+                l[e] *= f[e];
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][e] *= f[e & 1];
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[e], x[e] * scale_log2);
-            const float mu = mn == -INFINITY ? 0.0f : mn;
-            f[e] = ex2_approx(m[e] - mu);
-            grew |= mn > m[e];
-            m[e] = mn;
+            const float mu = m[e] == -INFINITY ? 0.0f : m[e];
             st[e] = ex2_approx(fmaf(st[e], scale_log2, -mu));
             st[e + 2] = ex2_approx(fmaf(st[e + 2], scale_log2, -mu));
-            l[e] = fmaf(l[e], f[e], st[e] + st[e + 2]);
+            l[e] += st[e] + st[e + 2];
         }
         const uint32_t h0 = pack_bf16x2(st[0], st[1]), h1 = pack_bf16x2(st[2], st[3]);
         const uint32_t l0 = pack_bf16x2(st[0] - bf16lo(h0), st[1] - bf16hi(h0));
@@ -279,12 +289,6 @@ struct RowState {
         hi[1] = transpose8(h1);
         low[0] = transpose8(l0);
         low[1] = transpose8(l1);
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[k][e] *= f[e & 1];
-        }
     }
 
     // O^T += V^T (hi + low); frag(k, a) gives the A fragment of dims tile k.  The
@@ -548,29 +552,31 @@ BIV_DEV float4 join_dims(const float (*o)[8][HD + 4], const float2 (*ml)[8], int
                        join4(y[0].z, y[1].z, y[2].z, y[3].z), join4(y[0].w, y[1].w, y[2].w, y[3].w));
 }
 
-// The rows of a direct item: a row's only split is finished here, others go to the
-// workspace.
+// Query rows r0 .. r0 + 7 of an item: a row's only split is finished here, others go to
+// the workspace.  By the kDirectThreads threads that computed them.
 template <int HD>
-BIV_DEV void join_classes(const Items& I, const AttnItem& it, const float (*o)[8][HD + 4], const float2 (*ml)[8], int tid) {
+BIV_DEV void join_classes(const Items& I, int w0, int rows, int kvh, int split, int r0, const float (*o)[8][HD + 4],
+                          const float2 (*ml)[8], int tid) {
     const PagedAttnParams& P = I.P;
+#pragma unroll
     for (int x4 = tid; x4 < 8 * (HD / 4); x4 += kDirectThreads) {
         const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4;
-        if (row >= it.rows) break;
+        if (r0 + row >= rows) break;
         int j, head;
-        row_head(P, row, j, head);
-        const int w = it.w0 + j;
+        row_head(P, r0 + row, j, head);
+        const int w = w0 + j;
         const int pos = I.pos_of(w);
-        if (pos < it.split * kSplit) continue;
+        if (pos < split * kSplit) continue;
         float mx, sum;
         const float4 x = join_dims<HD>(o, ml, row, d, mx, sum);
-        const long long pair = static_cast<long long>(w) * P.Hq + it.kvh * P.G + head;
+        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + head;
         if (pos < kSplit) {
             const float scale = 1.0f / sum;
             uint2 z = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
             if (sum == -1.0f) z = make_uint2(0, 0);
             *reinterpret_cast<uint2*>(P.o + pair * HD + d) = z;
         } else {
-            const long long part = pair * P.s_max + it.split;
+            const long long part = pair * P.s_max + split;
             if (d == 0) P.ws_ml[part] = make_float2(mx, sum);
             *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
         }
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         rs.put_ml(sm.ml[cls], bad_rows, g8, c4);
         DirectKeys<HD>::put(rs, sm.o[cls], g8, c4);
         __syncthreads();
-        join_classes<HD>(I, cur, sm.o, sm.ml, tid);
+        join_classes<HD>(I, cur.w0, cur.rows, cur.kvh, cur.split, 0, sm.o, sm.ml, tid);
         if (!more) break;
         cur = nxt;
         cur_pos[0] = nxt_pos[0];
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
 // ---- small calls: a cluster of eight CTAs per (request, KV head), CTA c taking splits
 // c and c + 8; the partials stay in shared memory, and CTA c joins query row c of all
 // splits.  One launch and no workspace traffic where the direct kernel and the combine
-// kernel would mostly wait for one another (1 request of 700 keys: 7.9 us for the two).
+// kernel would mostly wait for one another (1 request of 700 keys: 7.9 us for the two, 5.5 so).
 // The same steps, joins and bits.
 constexpr int kSmallCluster = 8;
 constexpr int kSmallSplits = 16;                   // of a row: two a CTA
@@ -913,15 +919,20 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     cluster_sync();                                        // nobody leaves while its shared memory is read
 }
 
-// ---- staged: one CTA per SM; four producer warps, one per class, fill a ring of
-// rounds (the classes' 16-key steps: K, then V) for T groups of four consumer
-// warps, one per class again.  Group g takes tile g of every item.  Rows of HD bf16
-// whose 16-byte chunks are permuted by the key's low three bits (chunk ^ (key & 7)):
-// neither the copies nor the fragments' reads meet a bank twice.
+// ---- staged: one CTA per SM; a producer warp fills a ring of rounds (the classes'
+// 16-key steps: K, then V) for T groups of four consumer warps, one per class.  Group
+// g takes tile g of every item.  A step's K, and its V, come in one TMA box of 16 keys:
+// HD / 64 tiles of 16 rows of 128 bytes, swizzled, so that the fragments' reads meet
+// no bank twice (a bulk copy per key's row instead: 240 us for the windows below, 82
+// cycles a copy).  32 windows of 5 rows (20 query rows a KV head, 3 tiles; 1024 keys at
+// the median): 66 us with the join of the splits, 3.25 TB/s of keys.  What is left is
+// the serial chain of a step (scores, weights, values: some 400 + 400 + 300 cycles with
+// three consumer warps a scheduler, all that the registers allow) and of the classes'
+// join after four of them; the tensor pipe is 18 % busy, shared memory 50 %.
 constexpr int kMaxStages = 6;
 
 struct StagedItem {
-    int w0, rows, kvh, r0, split, nsteps;   // w0 = -1: no more items
+    int w0, rows, kvh, r0, split, nsteps, tmax;    // w0 = -1: no more items
     int stage;
     uint32_t phase;
 };
@@ -929,16 +940,17 @@ struct StagedItem {
 template <int HD, int T>
 struct StagedLayout {
     static constexpr int kRows = 8 * T, kSlots = 2, QP = HD + 8, HDP = HD + 4;
-    static constexpr int kHalf = kClasses * kStep * HD * 2;             // bytes of a stage's K (or V)
+    static constexpr int kBox = kStep * HD * 2;                         // bytes of a step's K (or V)
+    static constexpr int kHalf = kClasses * kBox;                       // of a stage's
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kBars = (static_cast<int>(sizeof(LiveTable)) + 15) / 16 * 16;
     static constexpr int kQ = kBars + 512;                              // [slots][rows][QP] bf16
-    static constexpr int kMl = kQ + kSlots * kRows * QP * 2;            // [groups][2 items][classes][8] float2
-    static constexpr int kO = kMl + T * 2 * kClasses * 8 * 8;           // [groups][2][8][HDP] float: two exchanges' halves
-    static constexpr int kRing = (kO + T * 2 * 8 * HDP * 4 + 127) / 128 * 128;
-    static constexpr int kFit = (227 * 1024 - kRing) / kStage;
+    static constexpr int kMl = kQ + kSlots * kRows * QP * 2;            // [groups][classes][8] float2
+    static constexpr int kO = kMl + T * kClasses * 8 * 8;               // [groups][classes][8][HDP] float
+    static constexpr int kRing = (kO + T * kClasses * 8 * HDP * 4 + 1023) / 1024 * 1024;   // the swizzle goes by the address
+    static constexpr int kFit = (226 * 1024 - kRing) / kStage;
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    static constexpr int kBytes = kRing + kStages * kStage;
+    static constexpr int kBytes = kRing + kStages * kStage + 1024;      // the base is aligned to 1024
     static_assert(kStages >= 2, "the ring needs two stages");
 };
 
@@ -973,112 +985,128 @@ BIV_DEV void cp_async_arrive(uint64_t* bar) {
 }
 
 template <int HD, int T>
-__global__ void __launch_bounds__(T * 128 + 128, 1) paged_attn_staged_kernel(const PagedAttnParams P) {
+__global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                            const __grid_constant__ CUtensorMap tmV, const PagedAttnParams P) {
     using L = StagedLayout<HD, T>;
     constexpr int KS = HD / 16;
-    extern __shared__ __align__(128) uint8_t smem_raw[];
+    extern __shared__ uint8_t smem_base[];
+    uint8_t* smem_raw = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_base) + 1023) & ~static_cast<uintptr_t>(1023));
     LiveTable& table = *reinterpret_cast<LiveTable*>(smem_raw);
     StagedBars& bars = *reinterpret_cast<StagedBars*>(smem_raw + L::kBars);
-    const uint32_t ring = smem_u32(smem_raw + L::kRing);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&bars.full[s], kClasses * 33);       // of each producer warp 32 lanes' copies and one plain arrival
+            mbar_init(&bars.full[s], 1);
             mbar_init(&bars.empty[s], kClasses * T);
         }
         for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(&bars.item_full[s], kClasses * 32 + 1);
+            mbar_init(&bars.item_full[s], 33);            // the producer's 32 lanes' copies and one plain arrival
             mbar_init(&bars.item_empty[s], kClasses * T);
         }
         bars.abort_flag = 0;
         fence_mbar_init();
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
     }
     const Items I(P, table, L::kRows);                     // its barriers also publish the mbarriers
     pdl_wait();
     pdl_trigger();
     I.zero_rows<HD>();
 
-    if (warp >= T * kClasses) {
-        // ------------------------------------------------------ producers
-        const int cls = warp - T * kClasses;
-        const int ck = lane % (HD / 8), rk = lane / (HD / 8);          // chunk of a row, row of a group
-        constexpr int RPI = 32 / (HD / 8);                              // rows of one copy instruction
+    if (warp == T * kClasses) {
+        // ------------------------------------------------------ producer
+        const int cls = lane & (kClasses - 1);             // lanes 0-3 bring K of a class's step, 4-7 V
+        const bool is_v = lane & kClasses;
         // keys that one item alone reads leave L2 first; other tiles of the rows read them again
         const uint64_t policy = I.tiles == 1 ? policy_evict_first() : policy_evict_normal();
-        int stage = 0, slot = 0;
+        int stage = 0, slot = 0, fills = 0;
         uint32_t phase = 0, slot_phase = 0;
         bool ok = true;
-        auto hand = [&](const StagedItem& d) {             // publish an item; its Q, if any, was requested before
-            if (cls == 0 && lane == 0) {
+        auto free_slot = [&]() {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.item_empty[slot], slot_phase ^ 1u, &bars.abort_flag, &g_paged_err));
+            return ok;
+        };
+        auto hand = [&](const StagedItem& d) {             // publish an item; every lane's copies of Q were requested before
+            if (lane == 0) {
                 bars.item[slot] = d;
                 mbar_arrive(&bars.item_full[slot]);
             }
             cp_async_arrive(&bars.item_full[slot]);
+        };
+        auto next_slot = [&]() {
             if (++slot == L::kSlots) {
                 slot = 0;
                 slot_phase ^= 1u;
             }
         };
-        auto free_slot = [&]() {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.item_empty[slot], slot_phase ^ 1u, &bars.abort_flag, &g_paged_err));
-            return ok;
-        };
-        AttnItem it;
-        for (bool more = I.first(it); more && ok; more = I.next(it, it)) {
-            const int r0 = it.tile * L::kRows;
-            const int tmax = I.largest_pos(it, r0, L::kRows);
-            const int key_lo = it.split * kSplit;
-            const int nsteps = Items::steps_to(tmax, it.split);
-            if (nsteps == 0) continue;
-            int page = 0;                                  // lane i: page of this class's i-th step
-            if (lane < kStepsPerClass && cls + kClasses * lane < nsteps)
+        // an item's last position, its steps, and the page of step i in lane i
+        auto describe = [&](const AttnItem& it, int& tmax, int& nsteps, int& page) {
+            tmax = I.largest_pos(it, it.tile * L::kRows, L::kRows);
+            nsteps = Items::steps_to(tmax, it.split);
+            page = 0;
+            if (lane < nsteps)
                 page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
-                                  ((key_lo + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
-            if (!free_slot()) break;
-            __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L::kQ) + slot * L::kRows * L::QP;
-            for (int r = cls * RPI + rk; r < L::kRows; r += kClasses * RPI) {      // rows past the group's read its first row and are never used
+                                  ((it.split * kSplit + kStep * lane) >> P.pt.page_shift)];
+        };
+        AttnItem it, nxt;
+        int tmax = 0, nsteps = 0, page = 0, nxt_tmax = 0, nxt_nsteps = 0, nxt_page = 0;
+        bool more = I.first(it);
+        if (more) describe(it, tmax, nsteps, page);
+        while (more) {
+            const bool again = I.next(it, nxt);
+            if (again) describe(nxt, nxt_tmax, nxt_nsteps, nxt_page);  // its pages are looked up while this item is copied
+            if (nsteps > 0) {
+                if (!free_slot()) break;
+                const int r0 = it.tile * L::kRows, key_lo = it.split * kSplit;
+                // rows past the group's read its first row and are never used
                 int j, head;
-                row_head(P, r0 + r < it.rows ? r0 + r : 0, j, head);
-                cp_async16(q + r * L::QP + ck * 8,
-                           P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + ck * 8);
-            }
-            hand(StagedItem{it.w0, it.rows, it.kvh, r0, it.split, nsteps, stage, phase});
-            const bool page_ok = page >= 0 && page < P.pt.n_pages;
-            if (!page_ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
-            const uint32_t bad = ~__ballot_sync(0xffffffffu, page_ok);
-            for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err));
-                if (!ok) break;
-                const int i = s0 / kClasses, step = s0 + cls;
-                const int pg = __shfl_sync(0xffffffffu, page, i);
-                const int key0 = key_lo + kStep * step;
-                const bool step_bad = (bad >> i) & 1u;
-                const bool live = step < nsteps && !step_bad;
-                const long long at = ((static_cast<long long>(live ? pg : 0) * P.Hkv + it.kvh) * P.pt.page_size +
-                                      (live ? key0 & (P.pt.page_size - 1) : 0)) * HD + ck * 8;
-                const __nv_bfloat16* ks = P.kp + at;
-                const __nv_bfloat16* vs = P.vp + at;
-                const uint32_t base = ring + static_cast<uint32_t>(stage * L::kStage + cls * kStep * HD * 2);
-                const int last = live ? tmax - key0 : -1;  // what lies behind the last key reads as zeros
+                row_head(P, r0 + lane < it.rows ? r0 + lane : 0, j, head);
+                const long long q_at = (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD;   // of row `lane`
+                constexpr int RPI = 32 / (HD / 8);         // rows of one copy instruction
+                const int ck = lane % (HD / 8), rk = lane / (HD / 8);
+                __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L::kQ) + slot * L::kRows * L::QP;
 #pragma unroll
-                for (int r = 0; r < kStep; r += RPI) {
-                    const int row = r + rk;
-                    const uint32_t dst = base + static_cast<uint32_t>(row * HD * 2 + ((ck ^ (row & 7)) * 16));
-                    cp_async16_or_zero(dst, ks + row * HD, row <= last, policy);
-                    cp_async16_or_zero(dst + L::kHalf, vs + row * HD, row <= last, policy);
+                for (int r = 0; r < L::kRows; r += RPI)
+                    cp_async16(q + (r + rk) * L::QP + ck * 8, P.q + __shfl_sync(0xffffffffu, q_at, r + rk) + ck * 8);
+                hand(StagedItem{it.w0, it.rows, it.kvh, r0, it.split, nsteps, tmax, stage, phase});
+                next_slot();
+                const bool page_ok = page >= 0 && page < P.pt.n_pages;
+                if (!page_ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
+                const uint32_t bad = ~__ballot_sync(0xffffffffu, page_ok);
+                for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err));
+                    if (!ok) break;
+                    // steps that no row reaches, or whose page is none, are not copied
+                    const int pg = __shfl_sync(0xffffffffu, page, s0 + cls);
+                    const bool step_bad = (bad >> (s0 + cls)) & 1u;
+                    const bool live = lane < kClasses * 2 && s0 + cls < nsteps && !step_bad;
+                    if (lane < kClasses) bars.bad[stage][cls] = step_bad;
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, live));
+                    if (lane == 0) mbar_arrive_expect_tx(&bars.full[stage], static_cast<uint32_t>(boxes * L::kBox));
+                    __syncwarp();
+                    if (live)
+                        tma_load_5d(smem_raw + L::kRing + stage * L::kStage + (is_v ? L::kHalf : 0) + cls * L::kBox, is_v ? &tmV : &tmK,
+                                    &bars.full[stage], 0, (key_lo + kStep * (s0 + cls)) & (P.pt.page_size - 1), 0, it.kvh, pg, policy);
+                    ++fills;
+                    if (++stage == L::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (lane == 0) {
-                    bars.bad[stage][cls] = step_bad;
-                    mbar_arrive(&bars.full[stage]);
-                }
-                cp_async_arrive(&bars.full[stage]);
-                if (++stage == L::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (!ok) break;
             }
+            it = nxt;
+            tmax = nxt_tmax;
+            nsteps = nxt_nsteps;
+            page = nxt_page;
+            more = again;
         }
-        if (free_slot()) hand(StagedItem{-1, 0, 0, 0, 0, 0, 0, 0});
+        if (free_slot()) hand(StagedItem{-1, 0, 0, 0, 0, 0, 0, 0, 0});
+        // no copy may land after the CTA has left (the consumers see all of them complete,
+        // unless a wait ran out)
+        if (lane == 0)
+            for (int s = 0; s < L::kStages; ++s)
+                if (fills > s) mbar_wait_drain(&bars.full[s], s < stage ? phase : phase ^ 1u);
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
@@ -1086,161 +1114,95 @@ __global__ void __launch_bounds__(T * 128 + 128, 1) paged_attn_staged_kernel(con
     // ---------------------------------------------------------- consumers
     const int g8 = lane >> 2, c4 = lane & 3;
     const int group = warp / kClasses, cls = warp % kClasses;
-    float2* s_ml2 = reinterpret_cast<float2*>(smem_raw + L::kMl) + group * 2 * kClasses * 8;
-    float* s_o = reinterpret_cast<float*>(smem_raw + L::kO) + group * 2 * 8 * L::HDP;
+    float2(*s_ml)[8] = reinterpret_cast<float2(*)[8]>(smem_raw + L::kMl) + group * kClasses;
+    float(*s_o)[8][L::HDP] = reinterpret_cast<float(*)[8][L::HDP]>(smem_raw + L::kO) + group * kClasses;
     // this lane's row of the four 8 x 8 tiles of V^T: key (lane & 7) + 8 (lane / 16), dims 8 ((lane / 8) & 1) on
     const int vkey = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
-    const int kbase = (cls * kStep + g8) * HD * 2;
-    const uint32_t vbase = static_cast<uint32_t>(L::kHalf + (cls * kStep + vkey) * HD * 2);
+    const int kbase = cls * L::kBox + g8 * 128;
+    const uint32_t vbase = static_cast<uint32_t>(L::kHalf + cls * L::kBox + vkey * 128);
     int slot = 0;
     uint32_t slot_phase = 0;
-    for (int par = 0;; par ^= 1) {
-        // of two items in turn: a warp may still read the last item's while another is done with this one
-        float2* s_ml = s_ml2 + par * kClasses * 8;
+    while (true) {
         bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.item_full[slot], slot_phase, &bars.abort_flag, &g_paged_err));
-        StagedItem it;
-        if (ok) it = bars.item[slot];
-        else it = StagedItem{0, 0, 0, 0, 0, 0, 0, 0};
-        if (it.w0 < 0) return;                             // the same in every warp
-        int pos[2];
-        tile_pos(I, it.w0, it.rows, it.r0 + 8 * group, c4, pos);
-        const int key_lo = it.split * kSplit;
+        const StagedItem& it = bars.item[slot];            // read again at the end: registers are short
+        if (ok && it.w0 < 0) return;                       // the same in every warp
+        const int nsteps = ok ? it.nsteps : 0, tmax = ok ? it.tmax : 0, key_lo = ok ? it.split * kSplit : 0;
+        int stage = ok ? it.stage : 0;
+        uint32_t phase = ok ? it.phase : 0;
+        int pos[2] = {-1, -1};
+        if (ok) tile_pos(I, it.w0, it.rows, it.r0 + 8 * group, c4, pos);
         const bool any = __any_sync(0xffffffffu, max(pos[0], pos[1]) >= key_lo);     // the tile has rows in this split
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(smem_raw + L::kQ) + (slot * L::kRows + 8 * group + g8) * L::QP + 16 * c4;
         RowState<HD> rs;
         rs.clear();
         uint32_t bad_rows = 0;                             // bit e: the row met a page id out of range
 #pragma unroll 1
-        for (int s0 = 0; s0 < it.nsteps; s0 += kClasses) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[it.stage], it.phase, &bars.abort_flag, &g_paged_err));
+        for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, &bars.abort_flag, &g_paged_err));
             if (!ok) break;
             const int step = s0 + cls, key0 = key_lo + kStep * step;
-            if (any && step < it.nsteps) {
-                const uint8_t* base = smem_raw + L::kRing + it.stage * L::kStage;
-                uint4 k0[KS / 2], k1[KS / 2];
-#pragma unroll
-                for (int k = 0; k < KS / 2; ++k) {
-                    // 16 bytes of keys g8 and g8 + 8, the dims that the direct kernel puts into two k-steps
-                    const int chunk = 8 * (k >> 1) + 2 * c4 + (k & 1);
-                    const uint8_t* at = base + kbase + ((chunk ^ g8) * 16);
-                    k0[k] = *reinterpret_cast<const uint4*>(at);
-                    k1[k] = *reinterpret_cast<const uint4*>(at + 8 * HD * 2);
-                }
+            if (any && step < nsteps) {
+                const uint8_t* base = smem_raw + L::kRing + stage * L::kStage;
                 float s2[2][4] = {}, st[4];
 #pragma unroll
                 for (int k = 0; k < KS / 2; ++k) {
                     const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 8 * (k & 1));
-                    mma_16816(s2[0], k0[k].x, k1[k].x, k0[k].y, k1[k].y, qv.x, qv.y);
-                    mma_16816(s2[1], k0[k].z, k1[k].z, k0[k].w, k1[k].w, qv.z, qv.w);
+                    // 16 bytes of keys g8 and g8 + 8: the dims that the direct kernel puts into two k-steps
+                    const uint8_t* at = base + kbase + (k >> 1) * (kStep * 128) + ((2 * c4 + (k & 1)) ^ g8) * 16;
+                    const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
+                    mma_16816(s2[0], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
+                    mma_16816(s2[1], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
-                if (bars.bad[it.stage][cls]) bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
+                int live_keys = tmax - key0 + 1;
+                if (bars.bad[stage][cls]) {                // the rows that reach the step cannot be computed
+                    bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
+                    live_keys = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[e] = 0.0f;
+                }
+                if (live_keys < kStep) {
+                    // values behind the last key may be anything; every group that reads them writes these zeros first
+                    const uint32_t v0 = smem_u32(base) + static_cast<uint32_t>(L::kHalf + cls * L::kBox);
+                    for (int h = 0; h < HD / 64; ++h)
+                        for (int e = live_keys * 8 + lane; e < kStep * 8; e += 32)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + static_cast<uint32_t>(h * kStep * 128 + e * 16)), "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();              // before the next box in this place
+                    __syncwarp();
+                }
                 mask_step(st, pos, key0, g8);
                 uint32_t hi[2], low[2];
                 rs.step(st, P.scale_log2, hi, low);
                 const uint32_t vat = smem_u32(base) + vbase;
                 rs.add(hi, low, [&](int k, uint32_t (&a)[4]) {
-                    ldmatrix_x4_trans(vat + static_cast<uint32_t>(((2 * k + vch) ^ (vkey & 7)) * 16), a);
+                    ldmatrix_x4_trans(vat + static_cast<uint32_t>((k >> 2) * (kStep * 128) + (((2 * k + vch) & 7) ^ (vkey & 7)) * 16), a);
                 });
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.empty[it.stage]);
-            if (++it.stage == L::kStages) {
-                it.stage = 0;
-                it.phase ^= 1u;
+            if (lane == 0) mbar_arrive(&bars.empty[stage]);
+            if (++stage == L::kStages) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
-        // join the classes: maxima and sums first
-        rs.put_ml(s_ml + cls * 8, bad_rows, g8, c4);
-        if (!group_all(group, ok)) return;                 // a wait ran out: all four warps leave
-        if (lane == 0) mbar_arrive(&bars.item_empty[slot]);            // Q is no longer needed
-        float2 ml[2][kClasses];
+        if (!group_all(group, ok)) return;                 // a wait ran out: all four warps leave (else the last join has been read)
+        rs.put_ml(s_ml[cls], bad_rows, g8, c4);
+        // acc[k][e], acc[k][e + 2] are dims 16 k + g8 and + 8 of row 2 c4 + e
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int k = 0; k < kClasses; ++k) ml[e][k] = s_ml[k * 8 + 2 * c4 + e];
-            const float f = class_factor(make_float2(rs.m[e], 0.0f), classes_max(ml[e]));
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                rs.acc[k][e] *= f;
-                rs.acc[k][e + 2] *= f;
-            }
-        }
-        // Classes c and c ^ 2 swap halves of the dims, then c and c ^ 1 quarters: every
-        // warp ends with KS / 4 tiles of 16 dims.  acc[k][e], acc[k][e + 2] are dims
-        // 16 k + g8 and + 8 of row 2 c4 + e.
-        auto put = [&](int half, int k, const float (&x)[4]) {
-            float* o = s_o + (half * 8 + 2 * c4) * L::HDP + 16 * k + g8;
-            o[0] = x[0];
-            o[L::HDP] = x[1];
-            o[8] = x[2];
-            o[L::HDP + 8] = x[3];
-        };
-        auto get = [&](int half, int k, float (&x)[4]) {
-            const float* o = s_o + (half * 8 + 2 * c4) * L::HDP + 16 * k + g8;
-            x[0] = __fadd_rn(x[0], o[0]);
-            x[1] = __fadd_rn(x[1], o[L::HDP]);
-            x[2] = __fadd_rn(x[2], o[8]);
-            x[3] = __fadd_rn(x[3], o[L::HDP + 8]);
-        };
-        float x2[KS / 2][4], x4[KS / 4][4];
-        const bool upper = cls & 2, odd = cls & 1;
-        // region cls & 1: tiles [0, KS/2) written by the upper class, [KS/2, KS) by the lower
-#pragma unroll
-        for (int k = 0; k < KS / 2; ++k) {
-            if (upper) put(odd, k, rs.acc[k]);
-            else put(odd, k + KS / 2, rs.acc[k + KS / 2]);
+        for (int k = 0; k < KS; ++k) {
+            float* o = &s_o[cls][2 * c4][16 * k + g8];
+            o[0] = rs.acc[k][0];
+            o[L::HDP] = rs.acc[k][1];
+            o[8] = rs.acc[k][2];
+            o[L::HDP + 8] = rs.acc[k][3];
         }
         group_bar(group);
-        const int kh = upper ? KS / 2 : 0;
-#pragma unroll
-        for (int k = 0; k < KS / 2; ++k) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x2[k][e] = upper ? rs.acc[k + KS / 2][e] : rs.acc[k][e];
-            get(odd, kh + k, x2[k]);
-        }
-        // the even class keeps the lower quarter of its half: what is sent lies where this warp alone has just read
-#pragma unroll
-        for (int k = 0; k < KS / 4; ++k) {
-            if (odd) put(1, kh + k, x2[k]);
-            else put(0, kh + KS / 4 + k, x2[k + KS / 4]);
-        }
-        group_bar(group);
-        const int kq = kh + (odd ? KS / 4 : 0);
-#pragma unroll
-        for (int k = 0; k < KS / 4; ++k) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x4[k][e] = odd ? x2[k + KS / 4][e] : x2[k][e];
-            get(odd ? 0 : 1, kq + k, x4[k]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = it.r0 + 8 * group + 2 * c4 + e;
-            if (i >= it.rows || pos[e] < key_lo) continue;
-            int j, head;
-            row_head(P, i, j, head);
-            const long long pair = static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head;
-            const float mx = classes_max(ml[e]), sum = classes_sum(ml[e], mx);
-            if (pos[e] < kSplit) {
-                const float scale = 1.0f / sum;
-                __nv_bfloat16* o = P.o + pair * HD + 16 * kq + g8;
-#pragma unroll
-                for (int k = 0; k < KS / 4; ++k) {
-                    o[16 * k] = __float2bfloat16_rn(sum == -1.0f ? 0.0f : x4[k][e] * scale);
-                    o[16 * k + 8] = __float2bfloat16_rn(sum == -1.0f ? 0.0f : x4[k][e + 2] * scale);
-                }
-            } else {
-                const long long part = pair * P.s_max + it.split;
-                float* o = P.ws_o + part * HD + 16 * kq + g8;
-#pragma unroll
-                for (int k = 0; k < KS / 4; ++k) {
-                    o[16 * k] = x4[k][e];
-                    o[16 * k + 8] = x4[k][e + 2];
-                }
-                if (cls == 0 && g8 == 0) P.ws_ml[part] = make_float2(mx, sum);
-            }
-        }
+        const int w0 = it.w0, rows = it.rows, kvh = it.kvh, split = it.split, r0 = it.r0 + 8 * group;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.item_empty[slot]);            // neither the item nor Q is needed any more
+        join_classes<HD>(I, w0, rows, kvh, split, r0, s_o, s_ml, threadIdx.x & (kDirectThreads - 1));
         slot ^= 1;
         slot_phase ^= slot == 0 ? 1u : 0u;
     }
@@ -1256,52 +1218,36 @@ constexpr int kCombineWarps = 16;
 constexpr int kBlock = 16;
 constexpr int kAlone = 4 * kBlock;
 
-template <int HD>
-__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const PagedAttnParams P, int per_cta) {
+// WARPS: 16 for a long row's sake; with more rows than 16 warps on every SM can take at
+// once, half of that, so that an SM takes new rows more often (5120 rows of 1 to 32
+// splits: 1 us less than with 16; 32 rows of 512 splits: 2 us more).
+template <int HD, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, kCombineWarps / WARPS) paged_combine_kernel(const PagedAttnParams P, int per_cta) {
     constexpr int E = HD / 32;
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
-    __shared__ float s_acc[kCombineWarps][HD];
+    __shared__ float s_acc[WARPS][HD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long pairs = static_cast<long long>(P.W) * P.Hq;
     const long long first = static_cast<long long>(blockIdx.x) * per_cta;
-    const long long mine = first + warp;
-    const int my_pos = warp < per_cta && mine < pairs ? usable_pos(P, static_cast<int>(mine / P.Hq), false) : -1;
+    auto splits_of = [&](int p) {                          // of the CTA's p-th row
+        const int pos = p < per_cta && first + p < pairs ? usable_pos(P, static_cast<int>((first + p) / P.Hq), false) : -1;
+        return pos < 0 ? 0 : pos / kSplit + 1;
+    };
+    int ns = splits_of(warp);                              // a row a warp: per_cta <= WARPS
     pdl_wait();
     pdl_trigger();
 
-    // maximum and sum over a row's splits, the same in every warp that asks
-    auto head = [&](long long pair, int ns, float& m, float& inv_l) {
-        const float2* ml = P.ws_ml + pair * P.s_max;
-        m = -INFINITY;
-        float l = 0.0f;
-        bool bad = false;
-        for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int s = lane; s < ns; s += 32) {
-            const float2 x = ml[s];
-            bad |= x.y == -1.0f;
-            l = fmaf(x.y, ex2_approx(x.x - m), l);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        inv_l = 1.0f / l;
-        return __any_sync(0xffffffffu, bad);
-    };
-    // a block's sum: all of its loads in flight at once
-    auto block_sum = [&](long long pair, int s0, int ns, float m, float (&acc)[E]) {
-        const float2* ml = P.ws_ml + pair * P.s_max;
+    // a block's outputs, all under way at once, and their sum in split order
+    auto load = [&](long long pair, int s0, int ns, Vec (&v)[kBlock]) {
         const float* o = P.ws_o + (pair * P.s_max + s0) * HD + lane * E;
-        Vec v[kBlock];
 #pragma unroll
         for (int k = 0; k < kBlock; ++k)
             if (s0 + k < ns) v[k] = *reinterpret_cast<const Vec*>(o + static_cast<long long>(k) * HD);
-        const float f_lane = s0 + (lane & (kBlock - 1)) < ns ? ex2_approx(ml[s0 + (lane & (kBlock - 1))].x - m) : 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    };
+    auto add = [&](const Vec (&v)[kBlock], int s0, int ns, float factors, int lane0, float (&acc)[E]) {     // lane lane0 + k: split k's factor
 #pragma unroll
         for (int k = 0; k < kBlock; ++k) {
-            const float f = __shfl_sync(0xffffffffu, f_lane, k);
+            const float f = __shfl_sync(0xffffffffu, factors, lane0 + k);
             if (s0 + k < ns) {
                 const float* x = reinterpret_cast<const float*>(&v[k]);
 #pragma unroll
@@ -1318,40 +1264,73 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
         else *reinterpret_cast<uint32_t*>(dst) = y[0];
     };
 
-    const int my_ns = my_pos < 0 ? 0 : my_pos / kSplit + 1;
-    if (my_ns > 1 && my_ns <= kAlone) {
-        float m, inv_l, total[E] = {}, acc[E];
-        const bool bad = head(mine, my_ns, m, inv_l);
-        for (int s0 = 0; s0 < my_ns; s0 += kBlock) {
-            block_sum(mine, s0, my_ns, m, acc);
+    if (ns > 1 && ns <= kAlone) {
+        const long long pair = first + warp;
+        // (maximum, sum) of splits lane and lane + 32 and the first outputs, all under way at once
+        const float2* ml = P.ws_ml + pair * P.s_max;
+        const float2 none = make_float2(-INFINITY, 0.0f);
+        const float2 ml0 = lane < ns ? ml[lane] : none, ml1 = lane + 32 < ns ? ml[lane + 32] : none;
+        Vec v[kBlock];
+        load(pair, 0, ns, v);
+        float m = fmaxf(ml0.x, ml1.x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float f0 = lane < ns ? ex2_approx(ml0.x - m) : 0.0f, f1 = lane + 32 < ns ? ex2_approx(ml1.x - m) : 0.0f;
+        float l = fmaf(ml1.y, f1, ml0.y * f0);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const bool bad = __any_sync(0xffffffffu, ml0.y == -1.0f || ml1.y == -1.0f);
+        float total[E] = {};
+        for (int s0 = 0; s0 < ns; s0 += kBlock) {
+            float acc[E] = {};
+            if (s0 > 0) load(pair, s0, ns, v);
+            add(v, s0, ns, s0 < 32 ? f0 : f1, s0 & 31, acc);
 #pragma unroll
             for (int e = 0; e < E; ++e) total[e] += acc[e];
         }
-        store(mine, total, inv_l, bad);
+        store(pair, total, 1.0f / l, bad);
     }
-    if (!__syncthreads_or(my_ns > kAlone)) return;
+    if (!__syncthreads_or(ns > kAlone)) return;
     for (int p = 0; p < per_cta && first + p < pairs; ++p) {
         const long long pair = first + p;
-        const int pos = usable_pos(P, static_cast<int>(pair / P.Hq), false);
-        const int ns = pos < 0 ? 0 : pos / kSplit + 1;
+        ns = splits_of(p);
         if (ns <= kAlone) continue;
-        float m, inv_l, total[E] = {}, acc[E];
-        const bool bad = head(pair, ns, m, inv_l);
-        for (int s0 = 0; s0 < ns; s0 += kBlock * kCombineWarps) {          // a block of each warp
-            const int mine0 = s0 + kBlock * warp;
-            if (mine0 < ns) {
-                block_sum(pair, mine0, ns, m, acc);
+        // maximum and sum over the row's splits, the same in every warp
+        const float2* ml = P.ws_ml + pair * P.s_max;
+        float m = -INFINITY, l = 0.0f;
+        bool bad = false;
+        for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int s = lane; s < ns; s += 32) {
+            const float2 x = ml[s];
+            bad |= x.y == -1.0f;
+            l = fmaf(x.y, ex2_approx(x.x - m), l);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        bad = __any_sync(0xffffffffu, bad);
+        float total[E] = {};
+        for (int s0 = 0; s0 < ns; s0 += kBlock * WARPS) {          // a block of each warp
+            const int mine = s0 + kBlock * warp;
+            if (mine < ns) {
+                const int at = mine + (lane & (kBlock - 1));
+                const float f = at < ns ? ex2_approx(ml[at].x - m) : 0.0f;
+                float acc[E] = {};
+                Vec v[kBlock];
+                load(pair, mine, ns, v);
+                add(v, mine, ns, f, 0, acc);
 #pragma unroll
                 for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
             }
             __syncthreads();
             if (warp == 0)
-                for (int k = 0; k < kCombineWarps && s0 + kBlock * k < ns; ++k)
+                for (int k = 0; k < WARPS && s0 + kBlock * k < ns; ++k)
 #pragma unroll
                     for (int e = 0; e < E; ++e) total[e] += s_acc[k][lane * E + e];
             __syncthreads();
         }
-        if (warp == 0) store(pair, total, inv_l, bad);
+        if (warp == 0) store(pair, total, 1.0f / l, bad);
     }
 }
 
@@ -1374,6 +1353,21 @@ int check_pages(int n_slots, int max_pages, int n_pages, int page_size, PageTabl
     return BIV_OK;
 }
 
+// A pool of pages [n_pages][Hkv][page_size][HD] seen in boxes of 16 keys.
+template <int HD>
+bool encode_pages(CUtensorMap* map, const __nv_bfloat16* pool, const PagedAttnParams& P) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = HD * 2, page = row * static_cast<cuuint64_t>(P.pt.page_size);
+    const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(P.pt.page_size), HD / 64, static_cast<cuuint64_t>(P.Hkv),
+                                static_cast<cuuint64_t>(P.pt.n_pages)};
+    const cuuint64_t strides[4] = {row, 128, page, page * static_cast<cuuint64_t>(P.Hkv)};
+    const cuuint32_t box[5] = {64, kStep, HD / 64, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<__nv_bfloat16*>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD, int T>
 int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
     using L = StagedLayout<HD, T>;
@@ -1386,9 +1380,14 @@ int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes));
     });
     if (st != BIV_OK) return st;
+    CUtensorMap tk, tv;
+    if (!encode_pages<HD>(&tk, P.kp, P) || !encode_pages<HD>(&tv, P.vp, P)) {
+        set_cuda_error(cudaErrorNotSupported);
+        return BIV_ERR_CUDA;
+    }
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
     const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * passes, num_sms());
-    return launch_pdl(paged_attn_staged_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(T * 128 + 128), L::kBytes, s, P);
+    return launch_pdl(paged_attn_staged_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(T * 128 + 32), L::kBytes, s, tk, tv, P);
 }
 
 // The split kernel and, where a row may have several splits, the combine kernel.
@@ -1425,9 +1424,11 @@ int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
     if (st != BIV_OK || P.s_max == 1) return st;
     // few rows: a CTA each, so that a long row has the whole CTA
     const long long pairs = static_cast<long long>(P.W) * P.Hq;
-    const int per_cta = static_cast<int>(std::min<long long>(kCombineWarps, (pairs + num_sms() - 1) / num_sms()));
-    return launch_pdl(paged_combine_kernel<HD>, dim3(static_cast<unsigned>((pairs + per_cta - 1) / per_cta)),
-                      dim3(32 * kCombineWarps), 0, s, P, per_cta);
+    const bool few = pairs <= static_cast<long long>(kCombineWarps) * num_sms();
+    const int per_cta = few ? static_cast<int>((pairs + num_sms() - 1) / num_sms()) : kCombineWarps / 2;
+    return launch_pdl(few ? paged_combine_kernel<HD, kCombineWarps> : paged_combine_kernel<HD, kCombineWarps / 2>,
+                      dim3(static_cast<unsigned>((pairs + per_cta - 1) / per_cta)),
+                      dim3(32 * (few ? kCombineWarps : kCombineWarps / 2)), 0, s, P, per_cta);
 }
 
 }  // namespace

@@ -191,6 +191,31 @@ def test_attention_extreme_scores():
     within(o, *U.attention(q, pool.rows, [0, 0, 0], [599, 598, 300]))
 
 
+@pytest.mark.parametrize("slope", [0.05, 0.4, 3.0, -0.4])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_scores_that_rise_or_fall(slope, hd):
+    """Scores that grow from key to key by little (a row's reference stays behind its
+    maximum for a while) or much (it moves on in every step), for some heads only."""
+    lengths, Hq, Hkv, page, K = [700, 90], 4, 2, 32, 5
+    pool = U.Pool(lengths, Hkv, hd, page, seed=11)
+    for r, (k, v) in enumerate(pool.rows):
+        # head 0 of every KV head's two: dim 0 of q is 4, of the keys the trend (in units of ln 2)
+        k[:, :, 0] = (torch.arange(lengths[r]) * (slope * 0.6931 * hd ** 0.5 / 4)).to(torch.bfloat16)
+        for i in range(-(-lengths[r] // page)):
+            m = min(page, lengths[r] - i * page)
+            pool.k[pool.table[r, i], :, :m] = k[:, i * page:i * page + m]
+    q = U.bf16(U.gen(12), 2 * K, Hq, hd)
+    q[:, :, 0] = torch.tensor([4.0, 0.0, 4.0, 0.0])
+    slot = [r for r in range(2) for _ in range(K)]
+    pos = [n - K + j for n in lengths for j in range(K)]
+    o = attend(q, pool, slot, pos, rpg=K)
+    assert B.biv_device_error() == 0
+    within(o, *U.attention(q, pool.rows, slot, pos))
+    assert same_bits(attend(q, pool, slot, pos, rpg=1), o)
+    for w in (0, 3, 9):
+        assert same_bits(attend(q[w:w + 1], pool, [slot[w]], [pos[w]])[0], o[w])
+
+
 def test_attention_pool_past_two_gib_of_elements():
     """Pages whose offsets pass 32 bits."""
     page, Hkv, hd = 256, 8, 128
