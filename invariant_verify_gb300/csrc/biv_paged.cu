@@ -230,6 +230,7 @@ struct RowState {
     static constexpr int KS = HD / 16;
     float acc[KS][4];
     float m[2], l[2];
+    float mu[2];               // m, or 0 while no key has counted
 
     BIV_DEV void clear() {
 #pragma unroll
@@ -237,7 +238,7 @@ struct RowState {
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
         m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.0f;
+        l[0] = l[1] = mu[0] = mu[1] = 0.0f;
     }
 
     // Scores of a step (S^T fragment: keys g8 and g8 + 8) to weights: each weight leaves
@@ -266,7 +267,7 @@ struct RowState {
                 f[e] = 1.0f;
                 if (x[e] > m[e] + kSlack) {
                     f[e] = ex2_approx(m[e] - x[e]);
-                    m[e] = x[e];
+                    m[e] = mu[e] = x[e];
                 }
                 l[e] *= f[e];
             }
@@ -277,9 +278,8 @@ struct RowState {
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float mu = m[e] == -INFINITY ? 0.0f : m[e];
-            st[e] = ex2_approx(fmaf(st[e], scale_log2, -mu));
-            st[e + 2] = ex2_approx(fmaf(st[e + 2], scale_log2, -mu));
+            st[e] = ex2_approx(fmaf(st[e], scale_log2, -mu[e]));
+            st[e + 2] = ex2_approx(fmaf(st[e + 2], scale_log2, -mu[e]));
             l[e] += st[e] + st[e + 2];
         }
         const uint32_t h0 = pack_bf16x2(st[0], st[1]), h1 = pack_bf16x2(st[2], st[3]);
@@ -552,34 +552,22 @@ BIV_DEV float4 join_dims(const float (*o)[8][HD + 4], const float2 (*ml)[8], int
                        join4(y[0].z, y[1].z, y[2].z, y[3].z), join4(y[0].w, y[1].w, y[2].w, y[3].w));
 }
 
-// Query rows r0 .. r0 + 7 of an item: a row's only split is finished here, others go to
-// the workspace.  By the kDirectThreads threads that computed them.
+// Dims d .. d + 3 of one row of a split, joined: a row's only split is finished here,
+// others go to the workspace.
 template <int HD>
-BIV_DEV void join_classes(const Items& I, int w0, int rows, int kvh, int split, int r0, const float (*o)[8][HD + 4],
-                          const float2 (*ml)[8], int tid) {
-    const PagedAttnParams& P = I.P;
-#pragma unroll
-    for (int x4 = tid; x4 < 8 * (HD / 4); x4 += kDirectThreads) {
-        const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4;
-        if (r0 + row >= rows) break;
-        int j, head;
-        row_head(P, r0 + row, j, head);
-        const int w = w0 + j;
-        const int pos = I.pos_of(w);
-        if (pos < split * kSplit) continue;
-        float mx, sum;
-        const float4 x = join_dims<HD>(o, ml, row, d, mx, sum);
-        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + head;
-        if (pos < kSplit) {
-            const float scale = 1.0f / sum;
-            uint2 z = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
-            if (sum == -1.0f) z = make_uint2(0, 0);
-            *reinterpret_cast<uint2*>(P.o + pair * HD + d) = z;
-        } else {
-            const long long part = pair * P.s_max + split;
-            if (d == 0) P.ws_ml[part] = make_float2(mx, sum);
-            *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
-        }
+BIV_DEV void join_row(const PagedAttnParams& P, const float (*o)[8][HD + 4], const float2 (*ml)[8], int row, int d, int pos,
+                      long long pair, int split) {
+    float mx, sum;
+    const float4 x = join_dims<HD>(o, ml, row, d, mx, sum);
+    if (pos < kSplit) {
+        const float scale = 1.0f / sum;
+        uint2 z = make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(x.z * scale, x.w * scale));
+        if (sum == -1.0f) z = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(P.o + pair * HD + d) = z;
+    } else {
+        const long long part = pair * P.s_max + split;
+        if (d == 0) P.ws_ml[part] = make_float2(mx, sum);
+        *reinterpret_cast<float4*>(P.ws_o + part * HD + d) = x;
     }
 }
 
@@ -766,7 +754,15 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         rs.put_ml(sm.ml[cls], bad_rows, g8, c4);
         DirectKeys<HD>::put(rs, sm.o[cls], g8, c4);
         __syncthreads();
-        join_classes<HD>(I, cur.w0, cur.rows, cur.kvh, cur.split, 0, sm.o, sm.ml, tid);
+        for (int x4 = tid; x4 < 8 * (HD / 4); x4 += kDirectThreads) {
+            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4;
+            if (row >= cur.rows) break;
+            int j, head;
+            row_head(P, row, j, head);
+            const int pos = I.pos_of(cur.w0 + j);
+            if (pos >= cur.split * kSplit)
+                join_row<HD>(P, sm.o, sm.ml, row, d, pos, static_cast<long long>(cur.w0 + j) * P.Hq + cur.kvh * P.G + head, cur.split);
+        }
         if (!more) break;
         cur = nxt;
         cur_pos[0] = nxt_pos[0];
@@ -919,32 +915,37 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     cluster_sync();                                        // nobody leaves while its shared memory is read
 }
 
-// ---- staged: one CTA per SM; a producer warp fills a ring of rounds (the classes'
-// 16-key steps: K, then V) for T groups of four consumer warps, one per class.  Group
-// g takes tile g of every item.  A step's K, and its V, come in one TMA box of 16 keys:
-// HD / 64 tiles of 16 rows of 128 bytes, swizzled, so that the fragments' reads meet
-// no bank twice (a bulk copy per key's row instead: 240 us for the windows below, 82
-// cycles a copy).  32 windows of 5 rows (20 query rows a KV head, 3 tiles; 1024 keys at
-// the median): 66 us with the join of the splits, 3.25 TB/s of keys.  What is left is
-// the serial chain of a step (scores, weights, values: some 400 + 400 + 300 cycles with
-// three consumer warps a scheduler, all that the registers allow) and of the classes'
-// join after four of them; the tensor pipe is 18 % busy, shared memory 50 %.
+// ---- staged: one CTA per SM; one producer warp prepares items (Q and the pages), the
+// next fills a ring of rounds (the classes' 16-key steps, 64 keys: K, then V) for T
+// groups of four consumer warps, one per class.  Group g takes tile g of every item.
+// K and V come in TMA boxes of a page's keys, up to a round's: HD / 64 tiles of rows of
+// 128 bytes, swizzled, so that the fragments' reads meet no bank twice.
+// FIGURES
 constexpr int kMaxStages = 6;
 
 struct StagedItem {
-    int w0, rows, kvh, r0, split, nsteps, tmax;    // w0 = -1: no more items
-    int stage;
-    uint32_t phase;
+    int kvh, split, nsteps, tmax;           // nsteps = 0: no more items
+    uint32_t bad;                           // bit i: the page id of step i is out of range
+    int page[kSteps];
+    alignas(8) int pos[32];                 // of the rows of all tiles, -1: no row (read two at a time)
+    long long pair[32];                     // their (row, head)
 };
+
+struct StagedBars {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t item_set[3], item_full[3], item_empty[3];     // the item alone, the item and its Q, free
+    StagedItem item[3];
+    int abort_flag;
+};
+constexpr int kBarBytes = (static_cast<int>(sizeof(StagedBars)) + 15) / 16 * 16;
 
 template <int HD, int T>
 struct StagedLayout {
-    static constexpr int kRows = 8 * T, kSlots = 2, QP = HD + 8, HDP = HD + 4;
-    static constexpr int kBox = kStep * HD * 2;                         // bytes of a step's K (or V)
-    static constexpr int kHalf = kClasses * kBox;                       // of a stage's
+    static constexpr int kRows = 8 * T, kSlots = 3, QP = HD + 8, HDP = HD + 4;
+    static constexpr int kHalf = kClasses * kStep * HD * 2;             // bytes of a stage's K (or V)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kBars = (static_cast<int>(sizeof(LiveTable)) + 15) / 16 * 16;
-    static constexpr int kQ = kBars + 512;                              // [slots][rows][QP] bf16
+    static constexpr int kQ = kBars + kBarBytes;                              // [slots][rows][QP] bf16
     static constexpr int kMl = kQ + kSlots * kRows * QP * 2;            // [groups][classes][8] float2
     static constexpr int kO = kMl + T * kClasses * 8 * 8;               // [groups][classes][8][HDP] float
     static constexpr int kRing = (kO + T * kClasses * 8 * HDP * 4 + 1023) / 1024 * 1024;   // the swizzle goes by the address
@@ -954,13 +955,7 @@ struct StagedLayout {
     static_assert(kStages >= 2, "the ring needs two stages");
 };
 
-struct StagedBars {
-    uint64_t full[kMaxStages], empty[kMaxStages], item_full[2], item_empty[2];
-    uint8_t bad[kMaxStages][kClasses];      // classes of the stage whose page id is out of range
-    StagedItem item[2];
-    int abort_flag;
-};
-static_assert(sizeof(StagedBars) <= 512, "the layout leaves 512 bytes");
+constexpr int kRoundKeys = kClasses * kStep;
 
 // Four 8 x 8 tiles of bf16, transposed: the A fragment of V^T for 16 dims and 16 keys.
 BIV_DEV void ldmatrix_x4_trans(uint32_t addr, uint32_t (&a)[4]) {
@@ -985,7 +980,7 @@ BIV_DEV void cp_async_arrive(uint64_t* bar) {
 }
 
 template <int HD, int T>
-__global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(T * 128 + 64, 1) paged_attn_staged_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                             const __grid_constant__ CUtensorMap tmV, const PagedAttnParams P) {
     using L = StagedLayout<HD, T>;
     constexpr int KS = HD / 16;
@@ -1000,7 +995,8 @@ __global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(cons
             mbar_init(&bars.empty[s], kClasses * T);
         }
         for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(&bars.item_full[s], 33);            // the producer's 32 lanes' copies and one plain arrival
+            mbar_init(&bars.item_set[s], 1);
+            mbar_init(&bars.item_full[s], 33);             // 32 lanes' copies and one plain arrival
             mbar_init(&bars.item_empty[s], kClasses * T);
         }
         bars.abort_flag = 0;
@@ -1013,101 +1009,119 @@ __global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(cons
     pdl_trigger();
     I.zero_rows<HD>();
 
+    const int box_keys = min(P.pt.page_size, kRoundKeys);
+    int slot = 0;
+    uint32_t slot_phase = 0;
+    auto next_slot = [&]() {
+        if (++slot == L::kSlots) {
+            slot = 0;
+            slot_phase ^= 1u;
+        }
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&]() {
+        if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+               __all_sync(0xffffffffu, mbar_wait(bar, parity, &bars.abort_flag, &g_paged_err));
+    };
     if (warp == T * kClasses) {
-        // ------------------------------------------------------ producer
-        const int cls = lane & (kClasses - 1);             // lanes 0-3 bring K of a class's step, 4-7 V
-        const bool is_v = lane & kClasses;
-        // keys that one item alone reads leave L2 first; other tiles of the rows read them again
-        const uint64_t policy = I.tiles == 1 ? policy_evict_first() : policy_evict_normal();
-        int stage = 0, slot = 0, fills = 0;
-        uint32_t phase = 0, slot_phase = 0;
+        // -------------------------------------------------- items and their Q
+        AttnItem it;
         bool ok = true;
-        auto free_slot = [&]() {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.item_empty[slot], slot_phase ^ 1u, &bars.abort_flag, &g_paged_err));
-            return ok;
-        };
-        auto hand = [&](const StagedItem& d) {             // publish an item; every lane's copies of Q were requested before
-            if (lane == 0) {
-                bars.item[slot] = d;
-                mbar_arrive(&bars.item_full[slot]);
-            }
-            cp_async_arrive(&bars.item_full[slot]);
-        };
-        auto next_slot = [&]() {
-            if (++slot == L::kSlots) {
-                slot = 0;
-                slot_phase ^= 1u;
-            }
-        };
-        // an item's last position, its steps, and the page of step i in lane i
-        auto describe = [&](const AttnItem& it, int& tmax, int& nsteps, int& page) {
-            tmax = I.largest_pos(it, it.tile * L::kRows, L::kRows);
-            nsteps = Items::steps_to(tmax, it.split);
-            page = 0;
+        for (bool more = I.first(it); more; more = I.next(it, it)) {
+            const int r0 = it.tile * L::kRows;
+            const int tmax = I.largest_pos(it, r0, L::kRows), nsteps = Items::steps_to(tmax, it.split);
+            if (nsteps == 0) continue;
+            int page = 0;                                  // lane i: page of step i
             if (lane < nsteps)
                 page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
                                   ((it.split * kSplit + kStep * lane) >> P.pt.page_shift)];
-        };
-        AttnItem it, nxt;
-        int tmax = 0, nsteps = 0, page = 0, nxt_tmax = 0, nxt_nsteps = 0, nxt_page = 0;
-        bool more = I.first(it);
-        if (more) describe(it, tmax, nsteps, page);
-        while (more) {
-            const bool again = I.next(it, nxt);
-            if (again) describe(nxt, nxt_tmax, nxt_nsteps, nxt_page);  // its pages are looked up while this item is copied
-            if (nsteps > 0) {
-                if (!free_slot()) break;
-                const int r0 = it.tile * L::kRows, key_lo = it.split * kSplit;
-                // rows past the group's read its first row and are never used
-                int j, head;
-                row_head(P, r0 + lane < it.rows ? r0 + lane : 0, j, head);
-                const long long q_at = (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD;   // of row `lane`
-                constexpr int RPI = 32 / (HD / 8);         // rows of one copy instruction
-                const int ck = lane % (HD / 8), rk = lane / (HD / 8);
-                __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L::kQ) + slot * L::kRows * L::QP;
+            const bool real = lane < L::kRows && r0 + lane < it.rows;
+            int j, head;                                   // of row `lane`; rows past the group's read its first row and are never used
+            row_head(P, real ? r0 + lane : 0, j, head);
+            const long long pair = static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head;
+            ok = wait(&bars.item_empty[slot], slot_phase ^ 1u);
+            if (!ok) break;
+            constexpr int RPI = 32 / (HD / 8);             // rows of one copy instruction
+            const int ck = lane % (HD / 8), rk = lane / (HD / 8);
+            __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(smem_raw + L::kQ) + slot * L::kRows * L::QP;
 #pragma unroll
-                for (int r = 0; r < L::kRows; r += RPI)
-                    cp_async16(q + (r + rk) * L::QP + ck * 8, P.q + __shfl_sync(0xffffffffu, q_at, r + rk) + ck * 8);
-                hand(StagedItem{it.w0, it.rows, it.kvh, r0, it.split, nsteps, tmax, stage, phase});
-                next_slot();
-                const bool page_ok = page >= 0 && page < P.pt.n_pages;
-                if (!page_ok) atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
-                const uint32_t bad = ~__ballot_sync(0xffffffffu, page_ok);
-                for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars.empty[stage], phase ^ 1u, &bars.abort_flag, &g_paged_err));
-                    if (!ok) break;
-                    // steps that no row reaches, or whose page is none, are not copied
-                    const int pg = __shfl_sync(0xffffffffu, page, s0 + cls);
-                    const bool step_bad = (bad >> (s0 + cls)) & 1u;
-                    const bool live = lane < kClasses * 2 && s0 + cls < nsteps && !step_bad;
-                    if (lane < kClasses) bars.bad[stage][cls] = step_bad;
-                    const int boxes = __popc(__ballot_sync(0xffffffffu, live));
-                    if (lane == 0) mbar_arrive_expect_tx(&bars.full[stage], static_cast<uint32_t>(boxes * L::kBox));
-                    __syncwarp();
-                    if (live)
-                        tma_load_5d(smem_raw + L::kRing + stage * L::kStage + (is_v ? L::kHalf : 0) + cls * L::kBox, is_v ? &tmV : &tmK,
-                                    &bars.full[stage], 0, (key_lo + kStep * (s0 + cls)) & (P.pt.page_size - 1), 0, it.kvh, pg, policy);
-                    ++fills;
-                    if (++stage == L::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (!ok) break;
+            for (int r = 0; r < L::kRows; r += RPI)
+                cp_async16(q + (r + rk) * L::QP + ck * 8, P.q + __shfl_sync(0xffffffffu, pair, r + rk) * HD + ck * 8);
+            const uint32_t bad = bad_pages(P, page);
+            StagedItem& d = bars.item[slot];
+            if (lane < kSteps) d.page[lane] = page;
+            d.pos[lane] = real ? I.pos_of(it.w0 + j) : -1;
+            d.pair[lane] = pair;
+            if (lane == 0) {
+                d.kvh = it.kvh;
+                d.split = it.split;
+                d.nsteps = nsteps;
+                d.tmax = tmax;
+                d.bad = bad;
             }
-            it = nxt;
-            tmax = nxt_tmax;
-            nsteps = nxt_nsteps;
-            page = nxt_page;
-            more = again;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.item_set[slot]);
+                mbar_arrive(&bars.item_full[slot]);
+            }
+            cp_async_arrive(&bars.item_full[slot]);
+            next_slot();
         }
-        if (free_slot()) hand(StagedItem{-1, 0, 0, 0, 0, 0, 0, 0, 0});
+        if (ok && wait(&bars.item_empty[slot], slot_phase ^ 1u)) {
+            if (lane == 0) {
+                bars.item[slot].nsteps = 0;
+                mbar_arrive(&bars.item_set[slot]);
+                mbar_arrive(&bars.item_full[slot]);
+            }
+            cp_async_arrive(&bars.item_full[slot]);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
+    if (warp > T * kClasses) {
+        // ------------------------------------------------------ keys and values
+        // keys that one item alone reads leave L2 first; other tiles of the rows read them again
+        const uint64_t policy = I.tiles == 1 ? policy_evict_first() : policy_evict_normal();
+        const int boxes = kRoundKeys / box_keys, box_bytes = box_keys * HD * 2;
+        const bool is_v = lane >= boxes;                   // a lane per box: K, then V
+        const int box = is_v ? lane - boxes : lane, box_step = box * (box_keys / kStep);
+        int fills = 0;
+        bool ok = true;
+        while (ok && wait(&bars.item_set[slot], slot_phase)) {
+            const StagedItem& it = bars.item[slot];
+            const int nsteps = it.nsteps, kvh = it.kvh;    // after the last copy the item may be another
+            if (nsteps == 0) break;
+            const uint32_t bad = it.bad;
+            for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
+                const int step = s0 + box_step;
+                // boxes that no row reaches, or whose page is none, are not copied
+                const bool live = lane < 2 * boxes && step < nsteps && !((bad >> step) & 1u);
+                const int page = live ? it.page[step] : 0, key = (kStep * step) & (P.pt.page_size - 1);
+                const int n = __popc(__ballot_sync(0xffffffffu, live));
+                ok = wait(&bars.empty[stage], phase ^ 1u);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bars.full[stage], static_cast<uint32_t>(n * box_bytes));
+                __syncwarp();
+                if (live)
+                    tma_load_5d(smem_raw + L::kRing + stage * L::kStage + (is_v ? L::kHalf : 0) + box * box_bytes, is_v ? &tmV : &tmK,
+                                &bars.full[stage], 0, key, 0, kvh, page, policy);
+                ++fills;
+                next_stage();
+            }
+            next_slot();
+        }
         // no copy may land after the CTA has left (the consumers see all of them complete,
         // unless a wait ran out)
         if (lane == 0)
             for (int s = 0; s < L::kStages; ++s)
                 if (fills > s) mbar_wait_drain(&bars.full[s], s < stage ? phase : phase ^ 1u);
-        asm volatile("cp.async.wait_all;" ::: "memory");
         return;
     }
 
@@ -1118,27 +1132,35 @@ __global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(cons
     float(*s_o)[8][L::HDP] = reinterpret_cast<float(*)[8][L::HDP]>(smem_raw + L::kO) + group * kClasses;
     // this lane's row of the four 8 x 8 tiles of V^T: key (lane & 7) + 8 (lane / 16), dims 8 ((lane / 8) & 1) on
     const int vkey = (lane & 7) + 8 * (lane >> 4), vch = (lane >> 3) & 1;
-    const int kbase = cls * L::kBox + g8 * 128;
-    const uint32_t vbase = static_cast<uint32_t>(L::kHalf + cls * L::kBox + vkey * 128);
-    int slot = 0;
-    uint32_t slot_phase = 0;
+    const int half = box_keys * 128;                       // bytes of a box's 64 dims
+    const int cls_at = cls * kStep / box_keys * (box_keys * HD * 2) + cls * kStep % box_keys * 128;
+    const int kbase = cls_at + g8 * 128;
+    const uint32_t vbase = static_cast<uint32_t>(L::kHalf + cls_at + vkey * 128);
     while (true) {
-        bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.item_full[slot], slot_phase, &bars.abort_flag, &g_paged_err));
+        bool ok = wait(&bars.item_full[slot], slot_phase);
         const StagedItem& it = bars.item[slot];            // read again at the end: registers are short
-        if (ok && it.w0 < 0) return;                       // the same in every warp
-        const int nsteps = ok ? it.nsteps : 0, tmax = ok ? it.tmax : 0, key_lo = ok ? it.split * kSplit : 0;
-        int stage = ok ? it.stage : 0;
-        uint32_t phase = ok ? it.phase : 0;
-        int pos[2] = {-1, -1};
-        if (ok) tile_pos(I, it.w0, it.rows, it.r0 + 8 * group, c4, pos);
+        const int nsteps = ok ? it.nsteps : 0, tmax = it.tmax, key_lo = it.split * kSplit;
+        if (ok && nsteps == 0) return;                     // the same in every warp
+        const int2 pos2 = *reinterpret_cast<const int2*>(&it.pos[8 * group + 2 * c4]);
+        const int pos[2] = {pos2.x, pos2.y};
         const bool any = __any_sync(0xffffffffu, max(pos[0], pos[1]) >= key_lo);     // the tile has rows in this split
+        // the last key that every such row sees; up to there nothing is masked
+        int all_see = min(pos[0] >= key_lo ? pos[0] : 0x7fffffff, pos[1] >= key_lo ? pos[1] : 0x7fffffff);
+        all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 1));
+        all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 2));
+        if (it.bad) all_see = -1;
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(smem_raw + L::kQ) + (slot * L::kRows + 8 * group + g8) * L::QP + 16 * c4;
+        constexpr bool kHold = T < 4;                      // Q stays in registers where there are enough
+        uint4 qh[KS / 2];
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k)
+            if (kHold) qh[k] = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 8 * (k & 1));
         RowState<HD> rs;
         rs.clear();
         uint32_t bad_rows = 0;                             // bit e: the row met a page id out of range
 #pragma unroll 1
         for (int s0 = 0; s0 < nsteps; s0 += kClasses) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars.full[stage], phase, &bars.abort_flag, &g_paged_err));
+            ok = wait(&bars.full[stage], phase);
             if (!ok) break;
             const int step = s0 + cls, key0 = key_lo + kStep * step;
             if (any && step < nsteps) {
@@ -1146,46 +1168,45 @@ __global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(cons
                 float s2[2][4] = {}, st[4];
 #pragma unroll
                 for (int k = 0; k < KS / 2; ++k) {
-                    const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 8 * (k & 1));
+                    const uint4 qv = kHold ? qh[k] : *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 8 * (k & 1));
                     // 16 bytes of keys g8 and g8 + 8: the dims that the direct kernel puts into two k-steps
-                    const uint8_t* at = base + kbase + (k >> 1) * (kStep * 128) + ((2 * c4 + (k & 1)) ^ g8) * 16;
+                    const uint8_t* at = base + kbase + (k >> 1) * half + ((2 * c4 + (k & 1)) ^ g8) * 16;
                     const uint4 k0 = *reinterpret_cast<const uint4*>(at), k1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
                     mma_16816(s2[0], k0.x, k1.x, k0.y, k1.y, qv.x, qv.y);
                     mma_16816(s2[1], k0.z, k1.z, k0.w, k1.w, qv.z, qv.w);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
-                int live_keys = tmax - key0 + 1;
-                if (bars.bad[stage][cls]) {                // the rows that reach the step cannot be computed
-                    bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
-                    live_keys = 0;
+                if (key0 + kStep - 1 > all_see) {
+                    int live_keys = tmax - key0 + 1;
+                    if ((it.bad >> step) & 1u) {               // the rows that reach the step cannot be computed
+                        bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
+                        live_keys = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st[e] = 0.0f;
+                        for (int e = 0; e < 4; ++e) st[e] = 0.0f;
+                    }
+                    if (live_keys < kStep) {
+                        // values behind the last key may be anything; every group that reads them writes these zeros first
+                        const uint32_t v0 = smem_u32(base) + static_cast<uint32_t>(L::kHalf + cls_at);
+                        for (int h = 0; h < HD / 64; ++h)
+                            for (int e = live_keys * 8 + lane; e < kStep * 8; e += 32)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + static_cast<uint32_t>(h * half + e * 16)), "r"(0)
+                                             : "memory");
+                        fence_proxy_async_smem();              // before the next box in this place
+                        __syncwarp();
+                    }
+                    mask_step(st, pos, key0, g8);
                 }
-                if (live_keys < kStep) {
-                    // values behind the last key may be anything; every group that reads them writes these zeros first
-                    const uint32_t v0 = smem_u32(base) + static_cast<uint32_t>(L::kHalf + cls * L::kBox);
-                    for (int h = 0; h < HD / 64; ++h)
-                        for (int e = live_keys * 8 + lane; e < kStep * 8; e += 32)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + static_cast<uint32_t>(h * kStep * 128 + e * 16)), "r"(0)
-                                         : "memory");
-                    fence_proxy_async_smem();              // before the next box in this place
-                    __syncwarp();
-                }
-                mask_step(st, pos, key0, g8);
                 uint32_t hi[2], low[2];
                 rs.step(st, P.scale_log2, hi, low);
                 const uint32_t vat = smem_u32(base) + vbase;
                 rs.add(hi, low, [&](int k, uint32_t (&a)[4]) {
-                    ldmatrix_x4_trans(vat + static_cast<uint32_t>((k >> 2) * (kStep * 128) + (((2 * k + vch) & 7) ^ (vkey & 7)) * 16), a);
+                    ldmatrix_x4_trans(vat + static_cast<uint32_t>((k >> 2) * half + (((2 * k + vch) & 7) ^ (vkey & 7)) * 16), a);
                 });
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.empty[stage]);
-            if (++stage == L::kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            next_stage();
         }
         if (!group_all(group, ok)) return;                 // a wait ran out: all four warps leave (else the last join has been read)
         rs.put_ml(s_ml[cls], bad_rows, g8, c4);
@@ -1199,12 +1220,15 @@ __global__ void __launch_bounds__(T * 128 + 32, 1) paged_attn_staged_kernel(cons
             o[L::HDP + 8] = rs.acc[k][3];
         }
         group_bar(group);
-        const int w0 = it.w0, rows = it.rows, kvh = it.kvh, split = it.split, r0 = it.r0 + 8 * group;
+        const int t = threadIdx.x & (kDirectThreads - 1), split = it.split;
+#pragma unroll
+        for (int x4 = t; x4 < 8 * (HD / 4); x4 += kDirectThreads) {
+            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4, row_pos = it.pos[8 * group + row];
+            if (row_pos >= key_lo) join_row<HD>(P, s_o, s_ml, row, d, row_pos, it.pair[8 * group + row], split);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.item_empty[slot]);            // neither the item nor Q is needed any more
-        join_classes<HD>(I, w0, rows, kvh, split, r0, s_o, s_ml, threadIdx.x & (kDirectThreads - 1));
-        slot ^= 1;
-        slot_phase ^= slot == 0 ? 1u : 0u;
+        next_slot();
     }
 }
 
@@ -1353,7 +1377,7 @@ int check_pages(int n_slots, int max_pages, int n_pages, int page_size, PageTabl
     return BIV_OK;
 }
 
-// A pool of pages [n_pages][Hkv][page_size][HD] seen in boxes of 16 keys.
+// A pool of pages [n_pages][Hkv][page_size][HD] seen in boxes of a page's keys, up to a round's.
 template <int HD>
 bool encode_pages(CUtensorMap* map, const __nv_bfloat16* pool, const PagedAttnParams& P) {
     EncodeTiledFn fn = encode_fn();
@@ -1362,7 +1386,7 @@ bool encode_pages(CUtensorMap* map, const __nv_bfloat16* pool, const PagedAttnPa
     const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(P.pt.page_size), HD / 64, static_cast<cuuint64_t>(P.Hkv),
                                 static_cast<cuuint64_t>(P.pt.n_pages)};
     const cuuint64_t strides[4] = {row, 128, page, page * static_cast<cuuint64_t>(P.Hkv)};
-    const cuuint32_t box[5] = {64, kStep, HD / 64, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(std::min(P.pt.page_size, kRoundKeys)), HD / 64, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<__nv_bfloat16*>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1387,7 +1411,7 @@ int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
     }
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg;
     const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * passes, num_sms());
-    return launch_pdl(paged_attn_staged_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(T * 128 + 32), L::kBytes, s, tk, tv, P);
+    return launch_pdl(paged_attn_staged_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(T * 128 + 64), L::kBytes, s, tk, tv, P);
 }
 
 // The split kernel and, where a row may have several splits, the combine kernel.
