@@ -328,6 +328,14 @@ struct RowState {
     }
 };
 
+// The last key that every row of an 8-row tile with keys in the split sees: up to there
+// nothing needs a mask.  (Rows without keys there are not used.)
+BIV_DEV int all_see(const int (&pos)[2], int key_lo) {
+    int x = min(pos[0] >= key_lo ? pos[0] : 0x7fffffff, pos[1] >= key_lo ? pos[1] : 0x7fffffff);
+    x = min(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return min(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
 // Scores of keys past a row's position count as -infinity.
 BIV_DEV void mask_step(float (&st)[4], const int (&pos)[2], int key0, int g8) {
 #pragma unroll
@@ -604,10 +612,11 @@ struct DirectKeys {
         for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
     }
     // The step's weights and O^T; what lies behind the last key (tmax) may hold anything.
-    BIV_DEV void accumulate(RowState<HD>& rs, float (&st)[4], const int (&pos)[2], int tmax, int key0, int g8, int c4,
+    // see: all_see of the rows.
+    BIV_DEV void accumulate(RowState<HD>& rs, float (&st)[4], const int (&pos)[2], int see, int tmax, int key0, int g8, int c4,
                             float scale_log2) {
-        mask_step(st, pos, key0, g8);
-        if (key0 + kStep - 1 > tmax) {
+        if (key0 + kStep - 1 > see) {
+            mask_step(st, pos, key0, g8);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (key0 + 2 * c4 + (k & 1) + 8 * (k >> 1) > tmax) {
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
         RowState<HD> rs;
         rs.clear();
         uint32_t bad_rows = 0;                     // bit e: the row met a page id out of range
-        const int my_steps = steps_of(cur_steps);
+        const int my_steps = steps_of(cur_steps), see = all_see(cur_pos, cur.split * kSplit);
         long long next_at = 0;
         bool next = false;
 #pragma unroll 1
@@ -738,9 +747,9 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
                 if (next) next_at = row_at(nxt, nxt_page, 0);
             }
             if (next) keys.load_k(P, next_at, g8, c4);
-            if ((cur_bad >> i) & 1u)               // a row that reaches this step cannot be computed
-                bad_rows |= (cur_pos[0] >= key0 ? 1u : 0u) | (cur_pos[1] >= key0 ? 2u : 0u);
-            keys.accumulate(rs, st, cur_pos, cur_tmax, key0, g8, c4, P.scale_log2);
+            const bool bad = (cur_bad >> i) & 1u;  // a row that reaches this step cannot be computed; for the others its values are none
+            if (bad) bad_rows |= (cur_pos[0] >= key0 ? 1u : 0u) | (cur_pos[1] >= key0 ? 2u : 0u);
+            keys.accumulate(rs, st, cur_pos, see, bad ? -1 : cur_tmax, key0, g8, c4, P.scale_log2);
             if (next) keys.load_v(P, next_at, g8, c4);
         }
         if (my_steps == 0 && more) {
@@ -843,6 +852,7 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
         const int split = rank + kSmallCluster * j;
         const int steps = (Items::steps_to(tmax, split) - cls + kClasses - 1) / kClasses;
         if (split * kSplit > tmax) break;                  // the same in every warp
+        const int see = all_see(pos, split * kSplit);
         auto at = [&](int i) {
             return step_at<HD>(P, __shfl_sync(0xffffffffu, page, 4 * j + i), kvh, split * kSplit + kStep * (cls + kClasses * i));
         };
@@ -866,8 +876,9 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
                 next = at(i + 1);
                 keys.load_k(P, next, g8, c4);
             }
-            if ((bad >> (4 * j + i)) & 1u) bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
-            keys.accumulate(rs, st, pos, tmax, key0, g8, c4, P.scale_log2);
+            const bool step_bad = (bad >> (4 * j + i)) & 1u;
+            if (step_bad) bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
+            keys.accumulate(rs, st, pos, see, step_bad ? -1 : tmax, key0, g8, c4, P.scale_log2);
             if (i + 1 < steps) keys.load_v(P, next, g8, c4);
         }
         rs.put_ml(sm.ml[cls], bad_rows, g8, c4);
@@ -920,7 +931,14 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
 // groups of four consumer warps, one per class.  Group g takes tile g of every item.
 // K and V come in TMA boxes of a page's keys, up to a round's: HD / 64 tiles of rows of
 // 128 bytes, swizzled, so that the fragments' reads meet no bank twice.
-// FIGURES
+// 32 windows of 5 rows (20 query rows a KV head: 3 tiles; 8 KV heads of 128, 1024 keys at
+// the median): 61 us with the join of the splits, 3.5 TB/s of keys.  Larger boxes and a
+// warp for the items, since one TMA instruction keeps its warp some 85 cycles (a copy
+// per key's row: 240 us).  What bounds it is the serial work of a consumer warp, of
+// which registers allow three a scheduler: a step takes some 400 + 360 + 340 cycles
+// (scores, weights, values), an item's join 2000 more after four of them; the tensor
+// pipe is a fifth busy, shared memory half.  Splits of 512 keys would take a tenth off,
+// and add a third to one request's step on a short context.
 constexpr int kMaxStages = 6;
 
 struct StagedItem {
@@ -1144,11 +1162,7 @@ __global__ void __launch_bounds__(T * 128 + 64, 1) paged_attn_staged_kernel(cons
         const int2 pos2 = *reinterpret_cast<const int2*>(&it.pos[8 * group + 2 * c4]);
         const int pos[2] = {pos2.x, pos2.y};
         const bool any = __any_sync(0xffffffffu, max(pos[0], pos[1]) >= key_lo);     // the tile has rows in this split
-        // the last key that every such row sees; up to there nothing is masked
-        int all_see = min(pos[0] >= key_lo ? pos[0] : 0x7fffffff, pos[1] >= key_lo ? pos[1] : 0x7fffffff);
-        all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 1));
-        all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 2));
-        if (it.bad) all_see = -1;
+        const int see = it.bad ? -1 : all_see(pos, key_lo);
         const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(smem_raw + L::kQ) + (slot * L::kRows + 8 * group + g8) * L::QP + 16 * c4;
         constexpr bool kHold = T < 4;                      // Q stays in registers where there are enough
         uint4 qh[KS / 2];
@@ -1177,7 +1191,7 @@ __global__ void __launch_bounds__(T * 128 + 64, 1) paged_attn_staged_kernel(cons
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[e] = s2[0][e] + s2[1][e];
-                if (key0 + kStep - 1 > all_see) {
+                if (key0 + kStep - 1 > see) {
                     int live_keys = tmax - key0 + 1;
                     if ((it.bad >> step) & 1u) {               // the rows that reach the step cannot be computed
                         bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);

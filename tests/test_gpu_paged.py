@@ -176,6 +176,25 @@ def test_attention_page_ids_out_of_range():
         assert same_bits(o[keep], good[keep])
 
 
+@pytest.mark.parametrize("path", ["one launch", "direct", "staged"])
+def test_attention_page_out_of_range_for_some_rows_of_a_window(path):
+    """Rows that do not reach the bad page are computed, whatever page 0 holds."""
+    G, K = (4, 5) if path == "staged" else (2, 4)
+    pool = U.Pool([34], 1, 128, 16, seed=13)
+    nan = torch.full_like(pool.k[:1], float("nan"))
+    pool.k, pool.v, pool.table = torch.cat([nan, pool.k]), torch.cat([nan, pool.v]), pool.table + 1
+    if path == "direct":                                   # a table too wide for the one-launch form
+        pool.table = torch.cat([pool.table, torch.zeros(1, 600, dtype=torch.int32)], 1)
+    q = U.bf16(U.gen(2), K, G, 128)
+    pos = [30, 31, 32, 33, 33][:K]
+    table = pool.table.clone()
+    table[0, 2] = -3
+    o = attend(q, pool, [0] * K, pos, rpg=K, table=table)
+    assert B.biv_device_error() == 2
+    within(o[:2], *U.attention(q[:2], pool.rows, [0, 0], pos[:2]))
+    assert bool((o[2:] == 0).all())
+
+
 def test_attention_extreme_scores():
     """One key far above the others, far below, and scores of a thousand."""
     pool = U.Pool([600], 1, 128, 64, seed=8)
