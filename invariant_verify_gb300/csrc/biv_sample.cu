@@ -305,7 +305,7 @@ softmax_greedy_kernel(const float* logits, int V, long long ld, float* probs, lo
 // A weight in units of 2^-60 (truncated), clamped to [0, 1]; a NaN counts as 0.
 BIV_DEV float clamp01(float w) { return fminf(fmaxf(w, 0.0f), 1.0f); }
 // By shifts of the significand: conversions to 64-bit integers run at the rate of
-// this part's few FP64 units (64 x 128256 entries: 44 us with them, 21 us without).
+// this part's few FP64 units (64 x 128256 entries: 44 us with them, 32 without).
 BIV_DEV unsigned long long units(float w) {
     const uint32_t b = __float_as_uint(w), down = 130u - (b >> 23);
     const unsigned long long top = static_cast<unsigned long long>((b << 8) | 0x80000000u) << 32;      // 2^63 (1 + fraction)
@@ -321,8 +321,9 @@ BIV_DEV unsigned long long warp_sum(unsigned long long x) {
 // One request per cluster of C CTAs, a contiguous chunk of the row per warp.  Every
 // CTA finds the first rejected draft (a few gathered numbers), each warp sums the
 // weights of its chunk in 64-bit integers, and the warp that holds the border reads
-// its chunk again (from L2) and walks down to the entry.  Sums of integers do not
-// depend on their order, so C may follow the batch.
+// the part of its chunk again (from L2) where its kept sums pass the border, down to the
+// entry.  Sums of integers do not depend on their order, so C may follow the batch.
+constexpr int kKeptGoes = 4;           // goes of 512 entries whose sums are kept (64 x 128256 entries, four to a warp: 18.4 -> 16.3 us)
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads, 2)
 verify_sample_kernel(const float* __restrict__ target, const float* __restrict__ draft_probs,
@@ -334,6 +335,7 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
     __shared__ float s_f[kWarps];
     __shared__ unsigned long long c_sum[2][kMaxCluster];
     __shared__ float c_f[2][kMaxCluster];
+    __shared__ unsigned long long s_go[kWarps][kKeptGoes][32];     // the lanes' sums of a warp's first goes
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const long long r = blockIdx.x / C;
@@ -368,7 +370,7 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
     const int v0 = min(V, (rank * kWarps + warp) * chunk), end = min(V, v0 + chunk);
 
     // kDeep rounds of weights, all their loads first
-    constexpr int kDeep = 4;
+    constexpr int kDeep = 4, kGo = kDeep * kRound;
     auto weights = [&](int v, bool plain, float4 (&w)[kDeep]) {
         float4 y[kDeep];
         const bool diff = q && !plain;
@@ -400,14 +402,17 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
     for (int round = 0; round < 2; ++round) {
         unsigned long long sum = 0;
         float f = 0.0f;
-        for (int v = v0 + 4 * lane; v < end; v += kDeep * kRound) {
+        for (int go = 0; v0 + go * kGo < end; ++go) {
             float4 w[kDeep];
-            weights(v, plain, w);
+            unsigned long long part = 0;
+            weights(v0 + go * kGo + 4 * lane, plain, w);
 #pragma unroll
             for (int k = 0; k < kDeep; ++k) {
-                sum += (units(w[k].x) + units(w[k].y)) + (units(w[k].z) + units(w[k].w));
+                part += (units(w[k].x) + units(w[k].y)) + (units(w[k].z) + units(w[k].w));
                 f += (w[k].x + w[k].y) + (w[k].z + w[k].w);
             }
+            if (go < kKeptGoes && end - v0 > kGo) s_go[warp][go][lane] = part;
+            sum += part;
         }
         sum = warp_sum(sum);
 #pragma unroll
@@ -464,7 +469,21 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
     unsigned long long at = before;
     for (int k = 0; k < warp; ++k) at += s_sum[k];
     if (border < at || border >= at + s_sum[warp]) return;
-    for (int v = v0; v < end; v += kDeep * kRound) {
+    int go0 = 0;                                           // the go that holds the border, or the first one not kept
+    if (end - v0 > kGo) {
+        unsigned long long kept[kKeptGoes];
+#pragma unroll
+        for (int k = 0; k < kKeptGoes; ++k) kept[k] = v0 + k * kGo < end ? warp_sum(s_go[warp][k][lane]) : 0;
+        while (go0 < kKeptGoes) {
+            unsigned long long here = 0;
+#pragma unroll
+            for (int k = 0; k < kKeptGoes; ++k) here = k == go0 ? kept[k] : here;
+            if (border < at + here) break;
+            at += here;
+            ++go0;
+        }
+    }
+    for (int v = v0 + go0 * kGo; v < end; v += kGo) {
         float4 w[kDeep];
         weights(v + 4 * lane, plain, w);
         unsigned long long four[kDeep], incl[kDeep];

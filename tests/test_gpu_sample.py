@@ -168,6 +168,18 @@ def test_verify_borders():
         assert a[0] == want + 1
 
 
+def test_verify_draws_from_every_part_of_a_long_row():
+    """Many requests share the device, so that a warp goes over its part of a row in several goes."""
+    N, V = 160, 36004
+    g = U.gen(21)
+    p = torch.rand(V, generator=g, dtype=torch.float64) ** 4
+    p = (p / p.sum()).float()
+    c = dict(target=p.expand(N, 1, V).contiguous(), draft_probs=None, draft=torch.zeros(N, 0, dtype=torch.int32),
+             u_accept=torch.zeros(N, 0), u_sample=(torch.arange(N) + torch.rand(N, generator=g)) / N, p0=torch.zeros(N, dtype=torch.int32))
+    tokens, _, _ = check(c)
+    assert len(set(tokens[:, 0].tolist())) > N * 0.9
+
+
 def test_verify_special_probabilities():
     nan, inf = float("nan"), float("inf")
     V = 3000
