@@ -603,6 +603,9 @@ BIV_DEV uint4 ld_global_16(const void* p) {
 }
 
 // Sixteen columns of one row: C = act(acc + bias) + residual, one rounding.
+// 1023 x 14336 x 4096 with bias and GELU: 77 us, the plain product 71 (the last tile's
+// epilogue is not covered by MMAs); operands after the accumulators and the C library's
+// erff: 80.
 struct BiasActRow {
     uint4 bs[2], rs[2];
     bool in[2];

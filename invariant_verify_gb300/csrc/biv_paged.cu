@@ -50,7 +50,8 @@ constexpr int kRopeThreads = 256;
 // cosines of the rows' angles (one each, in shared memory), then rotate: an
 // item is eight pairs of one head, two 16-byte loads and two 16-byte stores, so
 // every sector that is touched is used whole.  Bound by memory: 2 x (Hq + 2 Hkv)
-// hd x 2 bytes per row.
+// hd x 2 bytes per row (4095 rows of 32 + 16 heads of 128: 19.8 us, 5.1 TB/s; all loads
+// first, or the rows brought into L2 while the angles are computed, is not faster).
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kv_write_paged_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ q_out,
                            __nv_bfloat16* __restrict__ kp, __nv_bfloat16* __restrict__ vp, const PageTable pt,
@@ -172,13 +173,16 @@ BIV_DEV int usable_pos(const PagedAttnParams& P, int w, bool flag) {
 // the four rows of a single token waste half of it instead of the 60 of 64 that
 // a rows-by-keys tile would.  Four classes of warps take the split's 16-key
 // steps in turn (class k: steps k, k + 4, ...), each with its own running maximum
-// and sum, and meet once at the end in class order.  Two kernels run that same
+// and sum, and meet once at the end in class order.  These kernels run that same
 // program, with the same bits for a row:
 //   direct  up to 8 query rows (one new token): the permutation of the dims
 //           inside a product is free, and chosen so that K and V come straight
 //           from global memory in 32-byte loads, a whole 128-byte line per four
 //           (K) or eight (V) lanes: no shared memory, no barrier and no address
-//           arithmetic between HBM and the tensor core.
+//           arithmetic between HBM and the tensor core.  Bound by memory: 64
+//           requests of 256 to 8192 keys 60.4 us, one of 131071 keys 90.3,
+//           both 5.9 TB/s with the join (a plain copy: 6.8).
+//   small   few of them with short tables: the same loads, in one launch.
 //   staged  more rows (verify windows): K and V pass through a ring in shared
 //           memory, filled by TMA, so that up to four tiles of 8 rows share one
 //           read of the keys.
@@ -192,7 +196,7 @@ constexpr int kMaxRows = 2048;         // rows whose positions are kept in share
 
 // 32 or 16 bytes of a row of keys or values: read once, so not kept in L1, and first to
 // leave L2 (the 32-byte form has that hint), where the splits' partials shall stay for
-// the join (64 requests: 65.7 -> 61.2 us).
+// the join (64 requests: 65.7 us without the hint, 61.2 with it).
 BIV_DEV void ld_row(const __nv_bfloat16* p, uint32_t (&r)[8]) {
     asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
