@@ -512,7 +512,8 @@ int biv_rope_kv_write_paged(const void* qkv, void* q_out, void* k_pages, void* v
  * time.  row_slot, row_pos and page_table are read before the wait on the
  * previous kernel of the library (see the conventions above).
  * Requires hd == 64 or 128 (else BIV_ERR_UNSUPPORTED, as for another page
- * size), Hq % Hkv == 0, o not q, 16-B aligned pointers.                    */
+ * size), Hq % Hkv == 0, o not q, 16-B aligned q, o and workspace, 32-B
+ * aligned k_pages and v_pages.                                             */
 size_t biv_decode_attn_paged_workspace_size(int W, int Hq, int hd, int max_pages, int page_size);
 int biv_decode_attn_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                           const int32_t* row_slot, const int32_t* row_pos, void* o, int W, int rows_per_group,

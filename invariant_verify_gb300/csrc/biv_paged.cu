@@ -1525,8 +1525,8 @@ extern "C" int biv_decode_attn_paged(const void* q, const void* k_pages, const v
     if (static_cast<long long>(W) * Hq > 0x7fffffffLL) return BIV_ERR_SHAPE;
     if (W == 0) return BIV_OK;
     if (!q || !k_pages || !v_pages || !page_table || !row_slot || !row_pos || !o || !workspace) return BIV_ERR_NULL;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned16(workspace))
-        return BIV_ERR_ALIGN;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return BIV_ERR_ALIGN;
+    if (((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 31u) != 0) return BIV_ERR_ALIGN;   // ld_row
     if (ws_bytes < biv_decode_attn_paged_workspace_size(W, Hq, hd, max_pages, page_size)) return BIV_ERR_SHAPE;
     if (o == q) return BIV_ERR_VALUE;
     P.q = static_cast<const __nv_bfloat16*>(q);

@@ -78,6 +78,8 @@ def test_decode_attn_paged(lib):
     assert f(Hq=7) == SHAPE
     assert f(hd=96) == UNSUP
     assert f(hd=256) == UNSUP
+    for name in ("k", "v"):                        # read 32 bytes at a time
+        assert f(**{name: FAKE + 16}) == ALIGN
     assert f(page=8) == UNSUP
     assert f(n_slots=0) == SHAPE
     assert f(ws_bytes=size(8, 8, 128, 8, 64) - 1) == SHAPE

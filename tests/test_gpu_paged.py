@@ -68,6 +68,23 @@ def test_attention_windows(K, hd, Hq, Hkv):
     assert same_bits(o[perm], o1)
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("hd,G,K", [(128, 4, 5), (64, 4, 5), (128, 8, 4), (64, 2, 40)])
+def test_attention_windows_over_pages(page, hd, G, K):
+    """Windows of every page size end inside a page, a round of 64 keys and a split."""
+    lengths = [K, 66, 259, 530, 1000]
+    pool = U.Pool(lengths, 2, hd, page, seed=page + K)
+    N, Hq = len(lengths), 2 * G
+    q = U.bf16(U.gen(14), N * K, Hq, hd)
+    slot = [r for r in range(N) for _ in range(K)]
+    pos = [n - K + j for n in lengths for j in range(K)]
+    pos[0] = -1                                            # an empty seat within a window
+    o = attend(q, pool, slot, pos, rpg=K)
+    assert B.biv_device_error() == 0
+    within(o, *U.attention(q, pool.rows, slot, pos))
+    assert same_bits(attend(q, pool, slot, pos, rpg=1), o)
+
+
 def test_attention_does_not_depend_on_batch_pages_or_workspace():
     lengths, Hq, Hkv, hd = [900, 33, 511, 2000], 8, 2, 128
     q = U.bf16(U.gen(3), 4, Hq, hd)
@@ -248,6 +265,8 @@ def test_attention_pool_past_two_gib_of_elements():
         vp[int(table[0, i])] = small.v[int(small.table[0, i])].cuda()
     q = U.bf16(U.gen(2), 1, 8, hd)
     assert same_bits(attend(q, small, [0], [399], k=kp, v=vp, table=table), attend(q, small, [0], [399]))
+    window = U.bf16(U.gen(5), 5, 32, hd), small, [0] * 5, [395, 396, 397, 398, 399], 5
+    assert same_bits(attend(*window, k=kp, v=vp, table=table), attend(*window))
     qkv = U.bf16(U.gen(4), 1, (8 + 2 * Hkv) * hd).cuda()
     q_out = nan_like(1, 8, hd)
     i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
