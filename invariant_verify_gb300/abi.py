@@ -4,6 +4,12 @@ Each ``biv_*`` function takes torch CUDA tensors, passes their raw device
 pointers, sizes and the current CUDA stream to the C entry point of the same
 name, and raises ``BivError`` on a non-zero status.  There is no fallback:
 if ``libbiv.so`` has not been built, loading raises immediately.
+
+The paged and sampled calls, whose small cases take less time on the GPU than
+ctypes and these checks on the host, go through ``_biv_torch.so`` first
+(``csrc/biv_torch.cpp``: the same checks and the same entry points); what it
+does not take (a named stream, rows_keep, strided rows, a tensor at fault)
+comes back here.
 """
 from __future__ import annotations
 
@@ -23,6 +29,7 @@ KV_SPLIT, HEAD_DIM, ATTN_TILE = 256, 128, 128
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lib = None
+_fast = None      # the binding of the small calls: -1 where a call needs this file's own checks
 
 
 class BivError(RuntimeError):
@@ -85,7 +92,7 @@ SIGNATURES = {
 
 
 def _load():
-    global _lib
+    global _lib, _fast
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libbiv.so is not built ({LIB_PATH}); run __graft_entry__.build()")
@@ -94,8 +101,23 @@ def _load():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        _lib = lib
+        from . import _biv_torch
+        _biv_torch.bind(*(C.cast(getattr(lib, "biv_" + n), C.c_void_p).value for n in (
+            "rope_kv_write_paged", "decode_attn_paged", "gemm_bias_act", "softmax", "verify_sample")))
+        _lib, _fast = lib, _biv_torch
     return _lib
+
+
+def _done(fn: str, status: int) -> bool:
+    """What the binding of the small calls answered: done, not for it, or a fault."""
+    if status > 0:
+        raise BivError(fn, status)
+    return status == 0
+
+
+def _load_fast():
+    _load()
+    return _fast
 
 
 def lib():
@@ -394,6 +416,8 @@ def biv_residual_add(x, y, out, stream=None) -> None:
 def biv_gemm_bias_act(A, B, C_out, bias=None, residual=None, act: str = "none", stream=None) -> None:
     """C = act(A B^T + bias) + residual; C_out (bf16 or fp32) may be the bf16 residual itself."""
     fn = "biv_gemm_bias_act"
+    if stream is None and act in ACTS and _done(fn, (_fast or _load_fast()).gemm_bias_act(A, B, C_out, bias, residual, ACTS[act])):
+        return
     M, K = A.shape
     N = B.shape[0]
     out = C_out.dtype
@@ -414,23 +438,16 @@ def biv_gemm_bias_act(A, B, C_out, bias=None, residual=None, act: str = "none", 
 def biv_rope_kv_write_paged(qkv, q_out, k_pages, v_pages, page_table, row_slot, row_pos, theta: float, K: int,
                             rows_keep=None, stream=None) -> None:
     fn = "biv_rope_kv_write_paged"
+    if stream is None and rows_keep is None and _done(fn, (_fast or _load_fast()).rope_kv_write_paged(
+            qkv, q_out, k_pages, v_pages, page_table, row_slot, row_pos, theta, K)):
+        return
     rows = W, Hq, hd = q_out.shape
     pool = n_pages, Hkv, page_size, _ = k_pages.shape
     table = n_slots, max_pages = page_table.shape
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
-    if not (qkv.dtype is _BF16 and q_out.dtype is _BF16 and k_pages.dtype is _BF16 and v_pages.dtype is _BF16
-            and page_table.dtype is _I32 and row_slot.dtype is _I32 and row_pos.dtype is _I32
-            and qkv.shape == (W, (Hq + 2 * Hkv) * hd) and pool[3] == hd and v_pages.shape == pool
-            and row_slot.shape == (W,) and row_pos.shape == (W,) and rows_keep is None
-            and qkv.is_contiguous() and q_out.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and page_table.is_contiguous() and row_slot.is_contiguous() and row_pos.is_contiguous()
-            and qkv.get_device() == dev and q_out.get_device() == dev and k_pages.get_device() == dev
-            and v_pages.get_device() == dev and page_table.get_device() == dev and row_slot.get_device() == dev
-            and row_pos.get_device() == dev):
-        _dense(fn, _BF16, (qkv, q_out, k_pages, v_pages),
-               ((W, (Hq + 2 * Hkv) * hd), rows, (n_pages, Hkv, page_size, hd), pool), "qkv q_out k_pages v_pages")
-        _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), (table, (W,), (W,), (W // max(K, 1),)),
-               "page_table row_slot row_pos rows_keep")
+    _dense(fn, _BF16, (qkv, q_out, k_pages, v_pages),
+           ((W, (Hq + 2 * Hkv) * hd), rows, (n_pages, Hkv, page_size, hd), pool), "qkv q_out k_pages v_pages")
+    _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), (table, (W,), (W,), (W // max(K, 1),)),
+           "page_table row_slot row_pos rows_keep")
     st = _load().biv_rope_kv_write_paged(
         qkv.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
         row_slot.data_ptr(), row_pos.data_ptr(), None if rows_keep is None else rows_keep.data_ptr(), W, K, Hq, Hkv,
@@ -446,23 +463,15 @@ def biv_decode_attn_paged_workspace_size(W: int, Hq: int, hd: int, max_pages: in
 def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o, rows_per_group: int, workspace,
                           stream=None) -> None:
     fn = "biv_decode_attn_paged"
+    if stream is None and _done(fn, (_fast or _load_fast()).decode_attn_paged(
+            q, k_pages, v_pages, page_table, row_slot, row_pos, o, rows_per_group, workspace)):
+        return
     rows = W, Hq, hd = q.shape
     pool = n_pages, Hkv, page_size, _ = k_pages.shape
     table = n_slots, max_pages = page_table.shape
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
-    if not (q.dtype is _BF16 and k_pages.dtype is _BF16 and v_pages.dtype is _BF16 and o.dtype is _BF16
-            and page_table.dtype is _I32 and row_slot.dtype is _I32 and row_pos.dtype is _I32
-            and pool[3] == hd and v_pages.shape == pool and o.shape == rows
-            and row_slot.shape == (W,) and row_pos.shape == (W,)
-            and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous() and o.is_contiguous()
-            and page_table.is_contiguous() and row_slot.is_contiguous() and row_pos.is_contiguous()
-            and workspace.is_contiguous() and q.get_device() == dev and k_pages.get_device() == dev
-            and v_pages.get_device() == dev and o.get_device() == dev and page_table.get_device() == dev
-            and row_slot.get_device() == dev and row_pos.get_device() == dev and workspace.get_device() == dev):
-        _dense(fn, _BF16, (q, k_pages, v_pages, o), (rows, (n_pages, Hkv, page_size, hd), pool, rows),
-               "q k_pages v_pages o")
-        _dense(fn, _I32, (page_table, row_slot, row_pos), (table, (W,), (W,)), "page_table row_slot row_pos")
-        _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")
+    _dense(fn, _BF16, (q, k_pages, v_pages, o), (rows, (n_pages, Hkv, page_size, hd), pool, rows), "q k_pages v_pages o")
+    _dense(fn, _I32, (page_table, row_slot, row_pos), (table, (W,), (W,)), "page_table row_slot row_pos")
+    _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")
     st = _load().biv_decode_attn_paged(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), row_slot.data_ptr(),
         row_pos.data_ptr(), o.data_ptr(), W, rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size,
@@ -474,6 +483,8 @@ def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o,
 def biv_softmax(logits, probs, temperature: float, V: int | None = None, stream=None) -> None:
     """probs[:, :V] = softmax(logits[:, :V] / temperature); rows of either may be strided (stride(1) == 1)."""
     fn = "biv_softmax"
+    if V is None and stream is None and _done(fn, (_fast or _load_fast()).softmax(logits, probs, temperature)):
+        return
     R, ld = logits.shape
     if V is None:
         V = ld
@@ -498,24 +509,16 @@ def biv_verify_sample(target, draft_probs, draft, u_accept, u_sample, p0, tokens
     """target fp32 [N*(K+1), V] (or [N, K+1, V]), draft_probs [N*K, V] or None
     (a drafter that is certain of its tokens); the other arrays as in the header."""
     fn = "biv_verify_sample"
+    if stream is None and _done(fn, (_fast or _load_fast()).verify_sample(
+            target, draft_probs, draft, u_accept, u_sample, p0, tokens, accept_len, new_len)):
+        return
     N, K1 = emitted = tokens.shape
     K, V = K1 - 1, target.shape[-1]
     per_draft, per_req = (N, K), (N,)
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
-    if not (target.dtype is _F32 and u_accept.dtype is _F32 and u_sample.dtype is _F32 and draft.dtype is _I32
-            and p0.dtype is _I32 and tokens.dtype is _I32 and accept_len.dtype is _I32 and new_len.dtype is _I32
-            and target.shape == (N * K1, V) and draft.shape == per_draft and u_accept.shape == per_draft
-            and u_sample.shape == per_req and p0.shape == per_req and accept_len.shape == per_req
-            and new_len.shape == per_req and target.is_contiguous() and draft.is_contiguous()
-            and u_accept.is_contiguous() and u_sample.is_contiguous() and p0.is_contiguous()
-            and tokens.is_contiguous() and accept_len.is_contiguous() and new_len.is_contiguous()
-            and target.get_device() == dev and draft.get_device() == dev and u_accept.get_device() == dev
-            and u_sample.get_device() == dev and p0.get_device() == dev and tokens.get_device() == dev
-            and accept_len.get_device() == dev and new_len.get_device() == dev):
-        _dense(fn, _F32, (target, u_accept, u_sample),
-               ((N, K1, V) if target.dim() == 3 else (N * K1, V), per_draft, per_req), "target u_accept u_sample")
-        _dense(fn, _I32, (draft, p0, tokens, accept_len, new_len), (per_draft, per_req, emitted, per_req, per_req),
-               "draft p0 tokens accept_len new_len")
+    _dense(fn, _F32, (target, u_accept, u_sample),
+           ((N, K1, V) if target.dim() == 3 else (N * K1, V), per_draft, per_req), "target u_accept u_sample")
+    _dense(fn, _I32, (draft, p0, tokens, accept_len, new_len), (per_draft, per_req, emitted, per_req, per_req),
+           "draft p0 tokens accept_len new_len")
     if draft_probs is not None:
         _dense(fn, _F32, (draft_probs,), ((N, K, V) if draft_probs.dim() == 3 else (N * K, V),), "draft_probs")
     st = _load().biv_verify_sample(

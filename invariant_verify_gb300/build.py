@@ -3,19 +3,23 @@
 One translation unit per kernel family, compiled in parallel, then linked
 into ``invariant_verify_gb300/libbiv.so`` (git-ignored).  The CUDA runtime
 is linked statically, so the library only needs the driver at run time.
+Beside it ``_biv_torch.so``, the Python binding of the small calls.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbiv.so")
+TORCH_LIB = os.path.join(HERE, "_biv_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["biv_api.cu", "biv_gemm.cu", "biv_select.cu", "biv_attn.cu", "biv_rowops.cu", "biv_draft.cu",
@@ -56,13 +60,35 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_torch() -> None:
+    """The binding of the small calls (csrc/biv_torch.cpp), for the torch and the
+    Python that run this."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    src = os.path.join(CSRC, "biv_torch.cpp")
+    if not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "biv.h"), os.path.join(torch_dir, "version.py")]):
+        return
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-I{d}" for d in inc), src, "-o", TORCH_LIB + ".tmp",
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on biv_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for f in os.listdir(BUILD):
             os.remove(os.path.join(BUILD, f))
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    if force and os.path.exists(TORCH_LIB):
+        os.remove(TORCH_LIB)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_torch)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        binding.result()
     if force or _stale(LIB, objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
