@@ -66,6 +66,8 @@ struct GemmArgs {
     int m64;         // one row tile of at most 64 rows: M = 64 MMAs
     int a_rows;      // rows of A copied per k-block (multiple of 8, <= 128)
     int row_step;    // rows of the tile that belong to one CTA: 128, or a_rows where a pair halves one row tile
+    int halves;      // that pair: M = 128 MMAs, 64 rows a CTA, whose columns lie in TMEM lanes 0-63 (the lower
+                     // half of the tile's) and 64-127 (the upper half)
     uint32_t idesc;  // tcgen05 instruction descriptor for M=128, N=BN
     uint32_t tmem_cols;
     // Narrow tail (CTA pairs, fused selection): column tiles [0, nt_full) are
@@ -137,7 +139,7 @@ struct BiasActArgs {
 // fp32 C's.  So every kSumBlocks k-blocks (768 terms) the accumulator moves on to rounded
 // fp32 sums in registers: 5.7e-7 to 6.5e-7 at any of these K.  It costs, in us with one
 // accumulator / with the sums: 10.2 / 13.2 at 1 x 4096 x 4096, 36 / 42 at 64 x 4096 x 14336,
-// 75 / 86 at 1023 x 4096 x 14336, 75 / 89 at 1023 x 14336 x 4096 (M x N x K; 8 k-blocks
+// 75 / 85 at 1023 x 4096 x 14336, 75 / 88 at 1023 x 14336 x 4096 (M x N x K; 8 k-blocks
 // instead of 12 take the same; tiles of 192 columns, which need no spills, 148 and 97 there).
 constexpr int kSumBlocks = 12;
 
@@ -996,8 +998,9 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 // Sums of the tile in registers (128 a thread in the widest): one
                 // accumulator after the other is added and handed back.
                 int cb6, ce6;
-                eset_columns(bnt, 16, (warp - 2) >> 2, cb6, ce6);
-                const int rloc = g.m64 ? q * 16 + lane : q * 32 + lane, row = row_base + rloc;
+                eset_columns(g.halves ? bnt / 2 : bnt, 16, (warp - 2) >> 2, cb6, ce6);
+                const int rloc = g.m64 ? q * 16 + lane : g.halves ? (q & 1) * 32 + lane : q * 32 + lane, row = row_base + rloc;
+                const int col6 = col0 + (g.halves ? (q >> 1) * (bnt / 2) : 0);
                 const bool live = row < M && rloc < g.row_step && (!g.m64 || lane < 16);
                 constexpr int kParts = 256 / 32;
                 float sum[kParts][16];
@@ -1031,7 +1034,7 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 #pragma unroll
                 for (int i = 0; i < kParts; ++i)
                     if (cb6 + 16 * i < ce6) {
-                        const BiasActRow operands(live, row, col0 + cb6 + 16 * i, N, ba);
+                        const BiasActRow operands(live, row, col6 + cb6 + 16 * i, N, ba);
                         operands.template store<true>([&](int e) { return sum[i][e]; }, C, ba);
                     }
                 continue;
@@ -1181,10 +1184,13 @@ gemm_nosplitk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
             } else if constexpr (EPI == 5) {
                 int cb5, ce5;
-                eset_columns(bnt, 16, (warp - 2) >> 2, cb5, ce5);
+                eset_columns(g.halves ? bnt / 2 : bnt, 16, (warp - 2) >> 2, cb5, ce5);
+                const int row5 = g.halves ? row_base + (q & 1) * 32 + lane : row;
+                const bool live5 = g.halves ? row5 < M && (q & 1) * 32 + lane < g.row_step : live;
+                const int col5 = col0 + (g.halves ? (q >> 1) * (bnt / 2) : 0);
 #pragma unroll 1
                 for (int c = cb5; c < ce5; c += 16) {
-                    const BiasActRow operands(live, row, col0 + c, N, ba);
+                    const BiasActRow operands(live5, row5, col5 + c, N, ba);
                     uint32_t r[16];
                     tmem_ld16(taddr + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
@@ -1371,9 +1377,10 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     g.K = K;
     g.BN = BN;
     // A pair that halves one row tile: each CTA copies half of the rows.
-    const bool halves = CG == 2 && M <= kBM;
+    const bool halves = (EPI == 5 || EPI == 6) && CG == 2 && M <= kBM;
     g.a_rows = halves ? ((M + 1) / 2 + 7) / 8 * 8 : (CG == 2 || M >= kBM) ? kBM : ((M + 7) / 8) * 8;
     g.row_step = halves ? g.a_rows : kBM;
+    g.halves = halves ? 1 : 0;
     g.KB = (K + kBK - 1) / kBK;
     g.three_d = (K % kBK == 0) ? 1 : 0;
     const int BNL = BN / CG;                        // B rows one CTA copies per tile
@@ -1425,7 +1432,7 @@ int launch_gemm_cg(const void* A, const void* B, void* C, int M, int N, int K, i
     g.first1 = (CG == 1 && g.three_d && ks >= 4 && g.KB > 1) ? 1 : 0;
     g.m64 = CG == 1 && g.a_rows <= 64 ? 1 : 0;
     g.stages = std::min(kMaxStages, std::max(1, (ring - tail) / stage_bytes(ks, g.a_rows, BNL)));
-    g.idesc = idesc_bf16_f32(CG == 2 ? 2 * kBM : (g.m64 ? 64 : kBM), BN);
+    g.idesc = idesc_bf16_f32(CG == 2 && !halves ? 2 * kBM : (g.m64 ? 64 : kBM), BN);
     g.tmem_cols = tmem_cols_for(BN);
     // the narrow tail: the fused selection on pairs, when the wave it is
     // planned for is the resident one (a unit's first tile is then a full one)
@@ -1479,10 +1486,12 @@ int launch_gemm(const void* A, const void* B, void* C, int M, int N, int K, int 
 // One row tile (M <= 128) as CTA pairs that halve it: a CTA then takes M / 2 rows of
 // A and BN / 2 rows of B out of L2 for every k-block instead of M and bn rows, and an
 // SM takes about 120 GB/s.  A pair costs about 2 us more to start, so it pays where A
-// is long (pairs against single CTAs, us): M = 64, N = 4096, K = 14336: 32.8 / 35.5;
-// M = 128 there: 38.1 / 48.0; M = 128, N = 4096, K = 4096: 15.0 / 16.2; but M = 64
+// is long (pairs against single CTAs, us): M = 64, N = 4096, K = 14336: 31.7 / 35.5;
+// M = 128 there: 37.3 / 48.0; M = 128, N = 4096, K = 4096: 14.1 / 16.2; but M = 64
 // there: 13.5 / 12.4, K = 1024: 7.1 / 5.5, and with wide tiles (N = 14336, K = 4096,
-// M = 128), whose ring holds few k-blocks: 27.5 / 24.7.
+// M = 128), whose ring holds few k-blocks: 27.5 / 24.7.  Pair MMAs of M = 128, which read
+// 64 rows of each CTA's shared memory, instead of M = 256: 1 to 3 % less; what is left at
+// M = 64 is the chain of 896 MMAs on one accumulator, some 58 cycles each (26 us).
 inline int halves_tile_n(int N) {
     return static_cast<int>(std::min<long long>(256, std::max<long long>(64, ceil_div(ceil_div(N, kPairWave), 32) * 32)));
 }
