@@ -1259,6 +1259,7 @@ __global__ void __launch_bounds__(T * 128 + 64, 1) paged_attn_staged_kernel(cons
 constexpr int kCombineWarps = 16;
 constexpr int kBlock = 16;
 constexpr int kAlone = 4 * kBlock;
+constexpr int kAsk = 32 * kCombineWarps;
 
 // WARPS: 16 for a long row's sake; with more rows than 16 warps on every SM can take at
 // once, half of that, so that an SM takes new rows more often (5120 rows of 1 to 32
@@ -1267,7 +1268,7 @@ template <int HD, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, kCombineWarps / WARPS) paged_combine_kernel(const PagedAttnParams P, int per_cta) {
     constexpr int E = HD / 32;
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
-    __shared__ float s_acc[WARPS][HD];
+    __shared__ float s_acc[WARPS][HD], s_red[WARPS], s_sum[kAsk / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long pairs = static_cast<long long>(P.W) * P.Hq;
     const long long first = static_cast<long long>(blockIdx.x) * per_cta;
@@ -1337,21 +1338,34 @@ __global__ void __launch_bounds__(32 * WARPS, kCombineWarps / WARPS) paged_combi
         const long long pair = first + p;
         ns = splits_of(p);
         if (ns <= kAlone) continue;
-        // maximum and sum over the row's splits, the same in every warp
+        // maximum and sum over the row's splits: kAsk threads ask for one each at a time,
+        // whatever the CTA's size, so that the order of the sum goes by ns alone
         const float2* ml = P.ws_ml + pair * P.s_max;
-        float m = -INFINITY, l = 0.0f;
-        bool bad = false;
-        for (int s = lane; s < ns; s += 32) m = fmaxf(m, ml[s].x);
+        float m = -INFINITY;
+        for (int s = threadIdx.x; s < ns; s += 32 * WARPS) m = fmaxf(m, ml[s].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int s = lane; s < ns; s += 32) {
-            const float2 x = ml[s];
-            bad |= x.y == -1.0f;
-            l = fmaf(x.y, ex2_approx(x.x - m), l);
-        }
+        if (lane == 0) s_red[warp] = m;
+        __syncthreads();
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        bad = __any_sync(0xffffffffu, bad);
+        for (int k = 0; k < WARPS; ++k) m = fmaxf(m, s_red[k]);
+        bool bad = false;
+#pragma unroll
+        for (int t = 0; t < kAsk; t += 32 * WARPS) {
+            float l = 0.0f;
+            for (int s = t + threadIdx.x; s < ns; s += kAsk) {
+                const float2 x = ml[s];
+                bad |= x.y == -1.0f;
+                l = fmaf(x.y, ex2_approx(x.x - m), l);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+            if (lane == 0) s_sum[t / 32 + warp] = l;
+        }
+        bad = __syncthreads_or(bad);
+        float l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAsk / 32; ++k) l += s_sum[k];
         float total[E] = {};
         for (int s0 = 0; s0 < ns; s0 += kBlock * WARPS) {          // a block of each warp
             const int mine = s0 + kBlock * warp;

@@ -68,6 +68,25 @@ def test_attention_windows(K, hd, Hq, Hkv):
     assert same_bits(o[perm], o1)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_long_rows_alone_and_among_many(hd):
+    """More splits than one warp joins (64), in calls of few and of very many rows."""
+    n = 18001
+    pool = U.Pool([n, 300], 1, hd, 256, seed=15)
+    q = U.bf16(U.gen(16), 1300, 2, hd)
+    slot, pos = [0, 1, 0, 0], [n - 1, 299, 16384, 16383]
+    o = attend(q[:4], pool, slot, pos)
+    assert B.biv_device_error() == 0
+    within(o, *U.attention(q[:4], pool.rows, slot, pos))
+    many = attend(q, pool, slot + [1] * 1296, pos + [r % 300 for r in range(1296)])
+    assert same_bits(many[:4], o)
+    table = pool.table.clone()
+    table[0, 70] = -1                                      # page 70 starts at key 17920
+    bad = attend(q[:4], pool, slot, pos, table=table)
+    assert B.biv_device_error() == 2
+    assert bool((bad[0] == 0).all()) and same_bits(bad[1:], o[1:])
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("hd,G,K", [(128, 4, 5), (64, 4, 5), (128, 8, 4), (64, 2, 40)])
 def test_attention_windows_over_pages(page, hd, G, K):
