@@ -182,7 +182,7 @@ BIV_DEV int usable_pos(const PagedAttnParams& P, int w, bool flag) {
 //           arithmetic between HBM and the tensor core.  Bound by memory: 64
 //           requests of 256 to 8192 keys 60.4 us, one of 131071 keys 90.3,
 //           both 5.9 TB/s with the join (a plain copy: 6.8).
-//   small   few of them with short tables: the same loads, in one launch.
+//   small   few tiles of eight rows and short tables: the same loads, in one launch.
 //   staged  more rows (verify windows): K and V pass through a ring in shared
 //           memory, filled by TMA, so that up to four tiles of 8 rows share one
 //           read of the keys.
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
     }
 }
 
-// ---- small calls: a cluster of eight CTAs per (request, KV head), CTA c taking splits
+// ---- small calls: a cluster of eight CTAs per (request, KV head, 8 query rows), CTA c taking splits
 // c and c + 8; the partials stay in shared memory, and CTA c joins query row c of all
 // splits.  One launch and no workspace traffic where the direct kernel and the combine
 // kernel would mostly wait for one another (1 request of 700 keys: 7.9 us for the two, 5.5 so).
@@ -825,13 +825,14 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int p = blockIdx.x / kSmallCluster, grp = p / P.Hkv, kvh = p - grp * P.Hkv;
-    const int w0 = grp * P.rpg, rows = min(P.rpg, P.W - w0) * P.G;
+    const int tiles = (P.rpg * P.G + 7) / 8, p = blockIdx.x / kSmallCluster / tiles, tile = blockIdx.x / kSmallCluster - p * tiles;
+    const int grp = p / P.Hkv, kvh = p - grp * P.Hkv;
+    const int w0 = grp * P.rpg, r0 = 8 * tile, rows = min(8, min(P.rpg, P.W - w0) * P.G - r0);   // none: a last group that is not full
     int pos[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = 2 * c4 + e;
-        pos[e] = i < rows ? usable_pos(P, w0 + i / P.G, rank == 0 && kvh == 0) : -1;
+        pos[e] = i < rows ? usable_pos(P, w0 + (r0 + i) / P.G, rank == 0 && kvh == 0) : -1;
     }
     int tmax = max(pos[0], pos[1]);
     tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     pdl_wait();
     pdl_trigger();
     for (int e = tid; e < 8 * (HD / 8); e += kDirectThreads) {         // rows past the group's read its first row and are never used
-        const int row = e / (HD / 8), d = (e % (HD / 8)) * 8, i = row < rows ? row : 0;
+        const int row = e / (HD / 8), d = (e % (HD / 8)) * 8, i = row < rows ? r0 + row : 0;
         cp_async16(&sm.q[row][d], P.q + (static_cast<long long>(w0 + i / P.G) * P.Hq + kvh * P.G + i % P.G) * HD + d);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -900,9 +901,9 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     cluster_sync();
     // query row `rank`, joined as the combine kernel does (up to 16 splits: one block)
     if (rank < rows) {
-        const int w = w0 + rank / P.G;
+        const int w = w0 + (r0 + rank) / P.G;
         const int row_pos = usable_pos(P, w, false), ns = row_pos < 0 ? 0 : row_pos / kSplit + 1;
-        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + rank % P.G;
+        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + (r0 + rank) % P.G;
         const float2 mine = lane < ns ? ld_cluster(&sm.part_ml[lane / kSmallCluster][rank], lane % kSmallCluster)
                                       : make_float2(-INFINITY, 0.0f);
         float x[kSmallSplits] = {};
@@ -1450,10 +1451,12 @@ int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
 template <int HD>
 int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
     const long long rows = static_cast<long long>(P.rpg) * P.G;
-    // Few (request, KV head) pairs and short tables: one launch.  With more of them, or
-    // longer ones, eight CTAs a pair would leave SMs idle or make several rounds.
-    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * kSmallCluster;
-    if (rows <= 8 && P.s_max <= kSmallSplits && small <= 2LL * num_sms())
+    // Few tiles (of 8 query rows of a request and KV head) and short tables: one launch.  With
+    // more of them, or longer ones, eight CTAs a tile would leave SMs idle or make several rounds
+    // (windows of 5 rows, 32 and 8 heads, 700 keys: one request takes 6.7 us, with two kernels
+    // 10.1; two requests would take 12.7 and take 10.5).
+    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((rows + 7) / 8) * kSmallCluster;
+    if (P.s_max <= kSmallSplits && small <= 2LL * num_sms())
         return launch_cluster_pdl(paged_attn_small_kernel<HD>, dim3(static_cast<unsigned>(small)), dim3(kDirectThreads), 0, s,
                                   kSmallCluster, P);
     int st;

@@ -35,6 +35,11 @@ def attend(q, pool, slot, pos, rpg=1, ws_fill=255, **kw):
     return o
 
 
+def wide(pool):
+    """The pool's table with columns for 5000 more keys: too many splits for the one-launch form."""
+    return torch.cat([pool.table, torch.full((pool.table.shape[0], -(-5000 // pool.page)), -1, dtype=torch.int32)], 1)
+
+
 LENGTHS = [1, 2, 15, 16, 17, 255, 256, 257, 700, 1030]
 
 
@@ -62,6 +67,7 @@ def test_attention_windows(K, hd, Hq, Hkv):
     o = attend(q, pool, slot, pos, rpg=K)
     assert B.biv_device_error() == 0
     within(o, *U.attention(q, pool.rows, slot, pos))
+    assert same_bits(attend(q, pool, slot, pos, rpg=K, table=wide(pool)), o)
     # the same rows one at a time, in another order: the same bits
     perm = torch.randperm(N * K, generator=U.gen(K)).tolist()
     o1 = attend(q[perm], pool, [slot[i] for i in perm], [pos[i] for i in perm], rpg=1)
@@ -101,7 +107,11 @@ def test_attention_windows_over_pages(page, hd, G, K):
     o = attend(q, pool, slot, pos, rpg=K)
     assert B.biv_device_error() == 0
     within(o, *U.attention(q, pool.rows, slot, pos))
+    assert same_bits(attend(q, pool, slot, pos, rpg=K, table=wide(pool)), o)
     assert same_bits(attend(q, pool, slot, pos, rpg=1), o)
+    assert same_bits(attend(q[:-2], pool, slot[:-2], pos[:-2], rpg=K, table=wide(pool)), o[:-2])     # a last window that is not full
+    assert same_bits(attend(q[:-2], pool, slot[:-2], pos[:-2], rpg=K), o[:-2])
+    assert B.biv_device_error() == 0
 
 
 def test_attention_does_not_depend_on_batch_pages_or_workspace():
@@ -212,15 +222,15 @@ def test_attention_page_ids_out_of_range():
         assert same_bits(o[keep], good[keep])
 
 
-@pytest.mark.parametrize("path", ["one launch", "direct", "staged"])
+@pytest.mark.parametrize("path", ["one launch", "one launch, tiles", "direct", "staged"])
 def test_attention_page_out_of_range_for_some_rows_of_a_window(path):
     """Rows that do not reach the bad page are computed, whatever page 0 holds."""
-    G, K = (4, 5) if path == "staged" else (2, 4)
+    G, K = (4, 5) if path in ("staged", "one launch, tiles") else (2, 4)
     pool = U.Pool([34], 1, 128, 16, seed=13)
     nan = torch.full_like(pool.k[:1], float("nan"))
     pool.k, pool.v, pool.table = torch.cat([nan, pool.k]), torch.cat([nan, pool.v]), pool.table + 1
-    if path == "direct":                                   # a table too wide for the one-launch form
-        pool.table = torch.cat([pool.table, torch.zeros(1, 600, dtype=torch.int32)], 1)
+    if path in ("direct", "staged"):
+        pool.table = wide(pool)
     q = U.bf16(U.gen(2), K, G, 128)
     pos = [30, 31, 32, 33, 33][:K]
     table = pool.table.clone()
@@ -267,6 +277,7 @@ def test_attention_scores_that_rise_or_fall(slope, hd):
     assert B.biv_device_error() == 0
     within(o, *U.attention(q, pool.rows, slot, pos))
     assert same_bits(attend(q, pool, slot, pos, rpg=1), o)
+    assert same_bits(attend(q, pool, slot, pos, rpg=K, table=wide(pool)), o)
     for w in (0, 3, 9):
         assert same_bits(attend(q[w:w + 1], pool, [slot[w]], [pos[w]])[0], o[w])
 
@@ -286,6 +297,8 @@ def test_attention_pool_past_two_gib_of_elements():
     assert same_bits(attend(q, small, [0], [399], k=kp, v=vp, table=table), attend(q, small, [0], [399]))
     window = U.bf16(U.gen(5), 5, 32, hd), small, [0] * 5, [395, 396, 397, 398, 399], 5
     assert same_bits(attend(*window, k=kp, v=vp, table=table), attend(*window))
+    far = torch.cat([table, torch.full((1, 20), -1, dtype=torch.int32)], 1)
+    assert same_bits(attend(*window, k=kp, v=vp, table=far), attend(*window))
     qkv = U.bf16(U.gen(4), 1, (8 + 2 * Hkv) * hd).cuda()
     q_out = nan_like(1, 8, hd)
     i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
