@@ -787,19 +787,18 @@ __global__ void __launch_bounds__(kDirectThreads, 3) paged_attn_direct_kernel(co
     }
 }
 
-// ---- small calls: a cluster of eight CTAs per (request, KV head, 8 query rows), CTA c taking splits
-// c and c + 8; the partials stay in shared memory, and CTA c joins query row c of all
-// splits.  One launch and no workspace traffic where the direct kernel and the combine
-// kernel would mostly wait for one another (1 request of 700 keys: 7.9 us for the two, 5.5 so).
-// The same steps, joins and bits.
-constexpr int kSmallCluster = 8;
-constexpr int kSmallSplits = 16;                   // of a row: two a CTA
+// ---- small calls: a cluster of C CTAs per (request, KV head, 8 query rows), CTA c taking
+// splits c and c + C; the partials stay in shared memory, and CTA c joins query rows c,
+// c + C, ... of all splits.  One launch and no workspace traffic where the direct kernel
+// and the combine kernel would mostly wait for one another (1 request of 700 keys: 7.9 us
+// for the two, 5.5 so).  The same steps, joins and bits.
+constexpr int kSmallTurns = 2;                     // splits a CTA takes at most
 
-template <int HD>
+template <int HD, int C>
 struct __align__(16) SmallSmem {
     float o[kClasses][8][HD + 4];
-    float part[kSmallSplits / kSmallCluster][8][HD];       // this CTA's splits' outputs
-    float2 part_ml[kSmallSplits / kSmallCluster][8];
+    float part[kSmallTurns][8][HD];        // this CTA's splits' outputs
+    float2 part_ml[kSmallTurns][8];
     __nv_bfloat16 q[8][HD + 8];
     float2 ml[kClasses][8];
 };
@@ -819,13 +818,13 @@ BIV_DEV float2 ld_cluster<float2>(const float2* p, uint32_t rank) {
     return x;
 }
 
-template <int HD>
+template <int HD, int C>
 __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(const PagedAttnParams P) {
-    __shared__ SmallSmem<HD> sm;
+    __shared__ SmallSmem<HD, C> sm;
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int tiles = (P.rpg * P.G + 7) / 8, p = blockIdx.x / kSmallCluster / tiles, tile = blockIdx.x / kSmallCluster - p * tiles;
+    const int tiles = (P.rpg * P.G + 7) / 8, p = blockIdx.x / C / tiles, tile = blockIdx.x / C - p * tiles;
     const int grp = p / P.Hkv, kvh = p - grp * P.Hkv;
     const int w0 = grp * P.rpg, r0 = 8 * tile, rows = min(8, min(P.rpg, P.W - w0) * P.G - r0);   // none: a last group that is not full
     int pos[2];
@@ -840,8 +839,8 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     // pages of this class's steps of both splits (lane 4 j + i: step i of split rank + 8 j)
     int page = 0;
     {
-        const int key0 = (rank + kSmallCluster * (lane >> 2)) * kSplit + kStep * (cls + kClasses * (lane & 3));
-        if (lane < 4 * (kSmallSplits / kSmallCluster) && key0 <= tmax)
+        const int key0 = (rank + C * (lane >> 2)) * kSplit + kStep * (cls + kClasses * (lane & 3));
+        if (lane < kStepsPerClass * kSmallTurns && key0 <= tmax)
             page = P.pt.table[static_cast<long long>(P.row_slot[w0]) * P.pt.max_pages + (key0 >> P.pt.page_shift)];
     }
     const uint32_t bad = bad_pages(P, page);
@@ -853,8 +852,8 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     DirectKeys<HD> keys;
-    for (int j = 0; j < kSmallSplits / kSmallCluster; ++j) {
-        const int split = rank + kSmallCluster * j;
+    for (int j = 0; j < kSmallTurns; ++j) {
+        const int split = rank + C * j;
         const int steps = (Items::steps_to(tmax, split) - cls + kClasses - 1) / kClasses;
         if (split * kSplit > tmax) break;                  // the same in every warp
         const int see = all_see(pos, split * kSplit);
@@ -899,18 +898,18 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     cluster_sync();
-    // query row `rank`, joined as the combine kernel does (up to 16 splits: one block)
-    if (rank < rows) {
-        const int w = w0 + (r0 + rank) / P.G;
+    // query rows rank, rank + C, ..., joined as the combine kernel does (up to 16 splits: one block)
+    for (int r = rank; r < rows; r += C) {
+        const int w = w0 + (r0 + r) / P.G;
         const int row_pos = usable_pos(P, w, false), ns = row_pos < 0 ? 0 : row_pos / kSplit + 1;
-        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + (r0 + rank) % P.G;
-        const float2 mine = lane < ns ? ld_cluster(&sm.part_ml[lane / kSmallCluster][rank], lane % kSmallCluster)
+        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + (r0 + r) % P.G;
+        const float2 mine = lane < ns ? ld_cluster(&sm.part_ml[lane / C][r], lane % C)
                                       : make_float2(-INFINITY, 0.0f);
-        float x[kSmallSplits] = {};
+        float x[kSmallTurns * C] = {};
         if (tid < HD) {
 #pragma unroll
-            for (int k = 0; k < kSmallSplits; ++k)
-                if (k < ns) x[k] = ld_cluster(&sm.part[k / kSmallCluster][rank][tid], k % kSmallCluster);
+            for (int k = 0; k < kSmallTurns * C; ++k)
+                if (k < ns) x[k] = ld_cluster(&sm.part[k / C][r][tid], k % C);
         }
         float m = mine.x, l;
 #pragma unroll
@@ -922,7 +921,7 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
         const bool broken = __any_sync(0xffffffffu, lane < ns && mine.y == -1.0f);
         float acc = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kSmallSplits; ++k) {
+        for (int k = 0; k < kSmallTurns * C; ++k) {
             const float f = __shfl_sync(0xffffffffu, f_lane, k);
             if (k < ns) acc = fmaf(x[k], f, acc);
         }
@@ -1451,14 +1450,17 @@ int launch_staged(const PagedAttnParams& P, long long passes, cudaStream_t s) {
 template <int HD>
 int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
     const long long rows = static_cast<long long>(P.rpg) * P.G;
-    // Few tiles (of 8 query rows of a request and KV head) and short tables: one launch.  With
-    // more of them, or longer ones, eight CTAs a tile would leave SMs idle or make several rounds
-    // (windows of 5 rows, 32 and 8 heads, 700 keys: one request takes 6.7 us, with two kernels
-    // 10.1; two requests would take 12.7 and take 10.5).
-    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((rows + 7) / 8) * kSmallCluster;
-    if (P.s_max <= kSmallSplits && small <= 2LL * num_sms())
-        return launch_cluster_pdl(paged_attn_small_kernel<HD>, dim3(static_cast<unsigned>(small)), dim3(kDirectThreads), 0, s,
-                                  kSmallCluster, P);
+    // Few tiles (of 8 query rows of a request and KV head) and short tables: one launch, with
+    // as many CTAs a tile as one round of them holds.  A CTA takes its splits one after the
+    // other, some 3 to 5 us each, so two at most.  32 and 8 heads, us, with two kernels in
+    // brackets: a window of 5 rows, 700 keys, 1 request 6.7 (10.1), 3 requests (C = 4) 7.8 (11.0);
+    // 5 single tokens 6.5 (9.0), of 1500 keys 12.8 (11.7), 9 of them 14.7 (14.5).  In several
+    // rounds (2 windows, C = 8): 12.7 (10.5).
+    const long long tiles = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((rows + 7) / 8), slots = 2LL * num_sms();
+    if (P.s_max <= kSmallTurns * 8 && tiles * 8 <= slots)
+        return launch_cluster_pdl(paged_attn_small_kernel<HD, 8>, dim3(static_cast<unsigned>(tiles * 8)), dim3(kDirectThreads), 0, s, 8, P);
+    if (P.s_max <= kSmallTurns * 4 && tiles * 4 <= slots)
+        return launch_cluster_pdl(paged_attn_small_kernel<HD, 4>, dim3(static_cast<unsigned>(tiles * 4)), dim3(kDirectThreads), 0, s, 4, P);
     int st;
     if (rows <= 8) {
         static DeviceOnce once;

@@ -111,6 +111,8 @@ def test_attention_windows_over_pages(page, hd, G, K):
     assert same_bits(attend(q, pool, slot, pos, rpg=1), o)
     assert same_bits(attend(q[:-2], pool, slot[:-2], pos[:-2], rpg=K, table=wide(pool)), o[:-2])     # a last window that is not full
     assert same_bits(attend(q[:-2], pool, slot[:-2], pos[:-2], rpg=K), o[:-2])
+    # twice the requests: clusters of four where eight do not fit one round
+    assert same_bits(attend(torch.cat([q, q]), pool, slot + slot, pos + pos, rpg=K), torch.cat([o, o]))
     assert B.biv_device_error() == 0
 
 
