@@ -836,10 +836,10 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     int tmax = max(pos[0], pos[1]);
     tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
     tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-    // pages of this class's steps of both splits (lane 4 j + i: step i of split rank + 8 j)
+    // pages of this class's steps of both splits (lane kStepsPerClass j + i: step i of split rank + C j)
     int page = 0;
     {
-        const int key0 = (rank + C * (lane >> 2)) * kSplit + kStep * (cls + kClasses * (lane & 3));
+        const int key0 = (rank + C * (lane / kStepsPerClass)) * kSplit + kStep * (cls + kClasses * (lane % kStepsPerClass));
         if (lane < kStepsPerClass * kSmallTurns && key0 <= tmax)
             page = P.pt.table[static_cast<long long>(P.row_slot[w0]) * P.pt.max_pages + (key0 >> P.pt.page_shift)];
     }
@@ -852,19 +852,22 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     DirectKeys<HD> keys;
+    auto steps_of = [&](int j) {                           // of this class, of the j-th split; a later split has no more
+        return j < kSmallTurns ? (Items::steps_to(tmax, rank + C * j) - cls + kClasses - 1) / kClasses : 0;
+    };
+    auto at = [&](int j, int i) {
+        return step_at<HD>(P, __shfl_sync(0xffffffffu, page, kStepsPerClass * j + i), kvh,
+                           (rank + C * j) * kSplit + kStep * (cls + kClasses * i));
+    };
+    if (steps_of(0) > 0) {
+        const long long a = at(0, 0);
+        keys.load_k(P, a, g8, c4);
+        keys.load_v(P, a, g8, c4);
+    }
     for (int j = 0; j < kSmallTurns; ++j) {
-        const int split = rank + C * j;
-        const int steps = (Items::steps_to(tmax, split) - cls + kClasses - 1) / kClasses;
+        const int split = rank + C * j, steps = steps_of(j);
         if (split * kSplit > tmax) break;                  // the same in every warp
         const int see = all_see(pos, split * kSplit);
-        auto at = [&](int i) {
-            return step_at<HD>(P, __shfl_sync(0xffffffffu, page, 4 * j + i), kvh, split * kSplit + kStep * (cls + kClasses * i));
-        };
-        if (steps > 0) {
-            const long long a = at(0);
-            keys.load_k(P, a, g8, c4);
-            keys.load_v(P, a, g8, c4);
-        }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                                   // Q has landed; the split before is joined
         RowState<HD> rs;
@@ -875,15 +878,17 @@ __global__ void __launch_bounds__(kDirectThreads, 2) paged_attn_small_kernel(con
             const int key0 = split * kSplit + kStep * (cls + kClasses * i);
             float st[4];
             keys.scores(&sm.q[g8][16 * c4], st);
+            // the next step, or the next split's first
+            const bool here = i + 1 < steps, more = here || steps_of(j + 1) > 0;
             long long next = 0;
-            if (i + 1 < steps) {
-                next = at(i + 1);
+            if (more) {
+                next = here ? at(j, i + 1) : at(j + 1, 0);
                 keys.load_k(P, next, g8, c4);
             }
-            const bool step_bad = (bad >> (4 * j + i)) & 1u;
+            const bool step_bad = (bad >> (kStepsPerClass * j + i)) & 1u;
             if (step_bad) bad_rows |= (pos[0] >= key0 ? 1u : 0u) | (pos[1] >= key0 ? 2u : 0u);
             keys.accumulate(rs, st, pos, see, step_bad ? -1 : tmax, key0, g8, c4, P.scale_log2);
-            if (i + 1 < steps) keys.load_v(P, next, g8, c4);
+            if (more) keys.load_v(P, next, g8, c4);
         }
         rs.put_ml(sm.ml[cls], bad_rows, g8, c4);
         DirectKeys<HD>::put(rs, sm.o[cls], g8, c4);
