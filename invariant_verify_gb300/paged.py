@@ -202,8 +202,10 @@ class PagedVerifier:
 def paged_generate(ver: PagedVerifier, prompts: list, n_tokens: int, generator: torch.Generator | None = None,
                    ngram=(3, 1)) -> tuple[list, float]:
     """``n_tokens`` tokens after each prompt (slots 0..), with n-gram drafts
-    (``biv_ngram_draft``; none if the verifier's K is 0) verified by sampling.
-    Returns the tokens and the mean number emitted per request and step."""
+    (``biv_ngram_draft``; none if the verifier's K is 0) verified by sampling.  The
+    pool and its table have to hold a prompt, ``n_tokens`` and K more positions of each.
+    Returns the tokens and the mean number emitted per request and step that it took
+    part in."""
     n, K = len(prompts), ver.K
     if n > ver.N:
         raise ValueError(f"{n} prompts, the verifier has {ver.N} seats")
@@ -214,28 +216,32 @@ def paged_generate(ver: PagedVerifier, prompts: list, n_tokens: int, generator: 
         ver.prefill(r, p[:-1])                    # the last token is the first window's row 0
     done, emitted, steps = [0] * n, 0, 0
     dev = ver.tokens.device
-    while min(done) < n_tokens:
-        draft = torch.zeros(n, K, dtype=torch.int32)
+    while min(done, default=n_tokens) < n_tokens:
+        # a request that has its tokens leaves its seat: its text, pages and share of the mean stay as they are
+        live = [r for r in range(n) if done[r] < n_tokens]
+        m = len(live)
+        draft = torch.zeros(m, K, dtype=torch.int32)
         if K > 0:
-            longest = max(len(p) for p in text)
-            hist = torch.zeros(n, longest, dtype=torch.int32)
-            for r, p in enumerate(text):
-                hist[r, :len(p)] = torch.tensor(p, dtype=torch.int32)
-            out, src = torch.empty(n, K, dtype=torch.int32, device=dev), torch.empty(n, dtype=torch.int32, device=dev)
-            B.biv_ngram_draft(hist.to(dev), torch.tensor([len(p) for p in text], dtype=torch.int32, device=dev),
+            longest = max(len(text[r]) for r in live)
+            hist = torch.zeros(m, longest, dtype=torch.int32)
+            for i, r in enumerate(live):
+                hist[i, :len(text[r])] = torch.tensor(text[r], dtype=torch.int32)
+            out, src = torch.empty(m, K, dtype=torch.int32, device=dev), torch.empty(m, dtype=torch.int32, device=dev)
+            B.biv_ngram_draft(hist.to(dev), torch.tensor([len(text[r]) for r in live], dtype=torch.int32, device=dev),
                               ngram[0], ngram[1], out, src)
             draft = out.cpu()
-        p0 = [len(p) - 1 for p in text]
-        for r in range(n):
-            ver.pool.reserve(r, p0[r] + K + 1)
-        ver.set_window(list(range(n)), [p[-1] for p in text], p0, draft, torch.rand(n, K, generator=generator),
-                       torch.rand(n, generator=generator))
+        p0 = [len(text[r]) - 1 for r in live]
+        for r, p in zip(live, p0):
+            ver.pool.reserve(r, p + K + 1)
+        # numbers for every request, so that one's do not depend on which others have ended
+        u_accept, u_sample = torch.rand(n, K, generator=generator), torch.rand(n, generator=generator)
+        ver.set_window(live, [text[r][-1] for r in live], p0, draft, u_accept[live], u_sample[live])
         ver.step()
         tokens, count = ver.emitted.cpu(), ver.accept_len.cpu()
-        steps += 1
-        for r in range(n):
-            c = int(count[r])
-            text[r] += tokens[r, :c].tolist()
+        steps += m
+        for i, r in enumerate(live):
+            c = int(count[i])
+            text[r] += tokens[i, :c].tolist()
             done[r] += c
             emitted += c
-    return [p[len(prompts[r]):len(prompts[r]) + n_tokens] for r, p in enumerate(text)], emitted / max(1, steps * n)
+    return [p[len(prompts[r]):len(prompts[r]) + n_tokens] for r, p in enumerate(text)], emitted / max(1, steps)
