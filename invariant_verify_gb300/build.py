@@ -10,6 +10,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -62,20 +63,29 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 
 def _compile_torch() -> None:
     """The binding of the small calls (csrc/biv_torch.cpp), for the torch and the
-    Python that run this."""
+    Python that run this.  A file beside it holds the command that made it, with
+    torch's version: another one rebuilds it, whatever the files' times say."""
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     src = os.path.join(CSRC, "biv_torch.cpp")
-    if not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "biv.h"), os.path.join(torch_dir, "version.py")]):
-        return
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        version = re.search(r"__version__ = ['\"]([^'\"]+)['\"]", f.read()).group(1)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-I{d}" for d in inc), src, "-o", TORCH_LIB + ".tmp",
-           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f'-DBIV_TORCH_VERSION="{version}"', *(f"-I{d}" for d in inc),
+           src, "-o", TORCH_LIB + ".tmp", "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    made = "\n".join([*cmd, sysconfig.get_config_var("SOABI") or ""])
+    if not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "biv.h")]) and os.path.exists(TORCH_LIB + ".cmd"):
+        with open(TORCH_LIB + ".cmd") as f:
+            if f.read() == made:
+                return
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on biv_torch.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    with open(TORCH_LIB + ".cmd", "w") as f:
+        f.write(made)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:

@@ -235,4 +235,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_biv_torch", nullptr, -1, kMethod
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__biv_torch() { return PyModule_Create(&kModule); }
+// torch_version: the torch whose tensors this code reads (build.py gives it).
+PyMODINIT_FUNC PyInit__biv_torch() {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m && PyModule_AddStringConstant(m, "torch_version", BIV_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
