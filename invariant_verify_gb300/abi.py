@@ -9,12 +9,14 @@ The paged and sampled calls, whose small cases take less time on the GPU than
 ctypes and these checks on the host, go through ``_biv_torch.so`` first
 (``csrc/biv_torch.cpp``: the same checks and the same entry points); what it
 does not take (a named stream, rows_keep, strided rows, a tensor at fault)
-comes back here.
+comes back here.  Without it, or with one that was built for another torch, all
+of them go this way, after a warning.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
+import warnings
 
 import torch
 
@@ -29,7 +31,7 @@ KV_SPLIT, HEAD_DIM, ATTN_TILE = 256, 128, 128
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lib = None
-_fast = None      # the binding of the small calls: -1 where a call needs this file's own checks
+_fast = None      # the binding of the small calls (or _NoBinding): -1 where a call needs this file's own checks
 
 
 class BivError(RuntimeError):
@@ -101,11 +103,30 @@ def _load():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        from . import _biv_torch
-        _biv_torch.bind(*(C.cast(getattr(lib, "biv_" + n), C.c_void_p).value for n in (
-            "rope_kv_write_paged", "decode_attn_paged", "gemm_bias_act", "softmax", "verify_sample")))
-        _lib, _fast = lib, _biv_torch
+        _lib, _fast = lib, _binding(lib)
     return _lib
+
+
+class _NoBinding:
+    """In the binding's place where there is none: every call is for this file."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
+def _binding(lib):
+    try:
+        from . import _biv_torch
+        built = getattr(_biv_torch, "torch_version", "an unknown version")
+        if built != str(torch.__version__):
+            raise ImportError(f"built for torch {built}, this is {torch.__version__}")
+    except ImportError as e:
+        warnings.warn(f"_biv_torch.so is not used ({e}): small calls take longer on the host; run __graft_entry__.build()",
+                      RuntimeWarning, stacklevel=3)
+        return _NoBinding()
+    _biv_torch.bind(*(C.cast(getattr(lib, "biv_" + n), C.c_void_p).value for n in (
+        "rope_kv_write_paged", "decode_attn_paged", "gemm_bias_act", "softmax", "verify_sample")))
+    return _biv_torch
 
 
 def _done(fn: str, status: int) -> bool:
