@@ -64,8 +64,12 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 def _compile_torch() -> None:
     """The binding of the small calls (csrc/biv_torch.cpp), for the torch and the
     Python that run this.  A file beside it holds the command that made it, with
-    torch's version: another one rebuilds it, whatever the files' times say."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch's version: another one rebuilds it, whatever the files' times say.  The
+    library itself needs no torch: without one there is nothing to bind."""
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return
+    torch_dir = torch.submodule_search_locations[0]
     src = os.path.join(CSRC, "biv_torch.cpp")
     with open(os.path.join(torch_dir, "version.py")) as f:
         version = re.search(r"__version__ = ['\"]([^'\"]+)['\"]", f.read()).group(1)

@@ -41,3 +41,12 @@ def test_another_torch_or_python_rebuilds_the_binding(monkeypatch, tmp_path, cha
         soabi[0] = "cpython-313"
     build._compile_torch()
     assert len(ran) == 2
+
+
+def test_the_library_builds_without_torch(monkeypatch, tmp_path):
+    from invariant_verify_gb300 import build
+    monkeypatch.setattr(build, "TORCH_LIB", str(tmp_path / "_biv_torch.so"))
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    monkeypatch.setattr(build.subprocess, "run", lambda *a, **kw: pytest.fail("nothing is compiled"))
+    build._compile_torch()
+    assert not os.listdir(tmp_path)
