@@ -182,6 +182,12 @@ def _dense(fn: str, dtype, tensors, shapes, names: str) -> None:
             _fault(fn, dtype, tensors, shapes, names.split())
 
 
+def _int32(fn: str, *sizes) -> None:
+    """Every size goes through the C interface as it is: ctypes would cut it to 32 bits."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise BivError(fn, 2, f"one of the sizes {', '.join(map(str, sizes))} passes 31 bits")
+
+
 def _fault(fn: str, dtype, tensors, shapes, names) -> None:
     for name, t, shape in zip(names, tensors, shapes):
         if t is None:
@@ -441,6 +447,7 @@ def biv_gemm_bias_act(A, B, C_out, bias=None, residual=None, act: str = "none", 
         return
     M, K = A.shape
     N = B.shape[0]
+    _int32(fn, M, N, K)
     out = C_out.dtype
     if out is not _BF16 and out is not _F32:
         raise BivError(fn, 4, f"C is {out}, not bfloat16 or float32")
@@ -465,6 +472,7 @@ def biv_rope_kv_write_paged(qkv, q_out, k_pages, v_pages, page_table, row_slot, 
     rows = W, Hq, hd = q_out.shape
     pool = n_pages, Hkv, page_size, _ = k_pages.shape
     table = n_slots, max_pages = page_table.shape
+    _int32(fn, W, K, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size)
     _dense(fn, _BF16, (qkv, q_out, k_pages, v_pages),
            ((W, (Hq + 2 * Hkv) * hd), rows, (n_pages, Hkv, page_size, hd), pool), "qkv q_out k_pages v_pages")
     _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), (table, (W,), (W,), (W // max(K, 1),)),
@@ -478,6 +486,7 @@ def biv_rope_kv_write_paged(qkv, q_out, k_pages, v_pages, page_table, row_slot, 
 
 
 def biv_decode_attn_paged_workspace_size(W: int, Hq: int, hd: int, max_pages: int, page_size: int) -> int:
+    _int32("biv_decode_attn_paged_workspace_size", W, Hq, hd, max_pages, page_size)
     return _load().biv_decode_attn_paged_workspace_size(W, Hq, hd, max_pages, page_size)
 
 
@@ -490,6 +499,7 @@ def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o,
     rows = W, Hq, hd = q.shape
     pool = n_pages, Hkv, page_size, _ = k_pages.shape
     table = n_slots, max_pages = page_table.shape
+    _int32(fn, W, rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size)
     _dense(fn, _BF16, (q, k_pages, v_pages, o), (rows, (n_pages, Hkv, page_size, hd), pool, rows), "q k_pages v_pages o")
     _dense(fn, _I32, (page_table, row_slot, row_pos), (table, (W,), (W,)), "page_table row_slot row_pos")
     _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")
@@ -509,6 +519,7 @@ def biv_softmax(logits, probs, temperature: float, V: int | None = None, stream=
     R, ld = logits.shape
     if V is None:
         V = ld
+    _int32(fn, R, V)
     for name, t in (("logits", logits), ("probs", probs)):
         if t.dtype is not _F32 or t.dim() != 2:
             raise BivError(fn, 4, f"{name} is no float32 matrix")
@@ -535,6 +546,7 @@ def biv_verify_sample(target, draft_probs, draft, u_accept, u_sample, p0, tokens
         return
     N, K1 = emitted = tokens.shape
     K, V = K1 - 1, target.shape[-1]
+    _int32(fn, N, K, V)
     per_draft, per_req = (N, K), (N,)
     _dense(fn, _F32, (target, u_accept, u_sample),
            ((N, K1, V) if target.dim() == 3 else (N * K1, V), per_draft, per_req), "target u_accept u_sample")
