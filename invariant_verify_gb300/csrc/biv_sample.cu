@@ -314,6 +314,16 @@ BIV_DEV unsigned long long units(float w) {
     return down < 64u ? top >> down : 0ull;
 }
 
+// floor(u x) for 0 <= u < 1, exactly: the product of u's 24-bit significand and x, in 128
+// bits, shifted down.  (A double keeps 53 of the product's up to 88 bits.)
+BIV_DEV unsigned long long floor_share(float u, unsigned long long x) {
+    const uint32_t b = __float_as_uint(u) & 0x7fffffffu, e = b >> 23;      // a zero may be a negative one
+    const unsigned long long m = e ? (b & 0x7fffffu) | 0x800000u : b;
+    const uint32_t down = 150u - (e ? e : 1u);             // u = m 2^-down, 24 <= down
+    const unsigned long long lo = m * x, hi = __umul64hi(m, x);
+    return down < 64u ? hi << (64u - down) | lo >> down : down < 128u ? hi >> (down - 64u) : 0ull;
+}
+
 BIV_DEV unsigned long long warp_sum(unsigned long long x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
@@ -459,7 +469,7 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
         plain = true;
     }
     const bool valid = total > 0 && all < 8.0f;
-    const unsigned long long border = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
+    const unsigned long long border = floor_share(u, total);       // S_v > u S where S_v is above it: both are integers
     if (rank == 0) {
         for (int j = tid; j <= K; j += kThreads)
             if (j != n || !valid) tokens[r * (K + 1) + j] = j < n ? draft[r * K + j] : j == n ? 0 : -1;
