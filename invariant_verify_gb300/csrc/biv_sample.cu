@@ -468,7 +468,10 @@ verify_sample_kernel(const float* __restrict__ target, const float* __restrict__
         if (total > 0 || plain) break;                     // the same in every CTA
         plain = true;
     }
-    const bool valid = total > 0 && all < 8.0f;
+    // Below 8 by the exact sum, whatever order `all` was added in: that sum, some 2^-10 off at
+    // most (8192 additions a thread of the largest row), only tells whether total has passed
+    // its 64 bits, at 16.
+    const bool valid = total > 0 && all < 12.0f && total < 8ull << 60;
     const unsigned long long border = floor_share(u, total);       // S_v > u S where S_v is above it: both are integers
     if (rank == 0) {
         for (int j = tid; j <= K; j += kThreads)

@@ -7,7 +7,7 @@ import torch
 
 import paged_util as U
 from invariant_verify_gb300 import abi as B
-from test_gpu_sample import check
+from test_gpu_sample import check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,22 @@ def test_border_is_exact_to_the_last_unit(pad):
     c = plain(torch.tensor([r + [0.0] * (V - len(r)) for r in rows]), us)
     check(c)
     assert B.biv_device_error() == 0
+
+
+@pytest.mark.parametrize("N", [1, 9, 300])
+def test_a_sum_of_eight_is_the_first_that_is_refused(N):
+    """Decided on the exact sum: whatever order the entries are added in, however many
+    requests share the device."""
+    V = 9000
+    under = [1.0] * 7 + [1 - 2.0 ** -24]           # rounds to 8 when it is added up in fp32
+    spread = [1.0] * 7 + [2.0 ** -13] * 8191       # 8 - 2^-13, in parts that rounded sums may lose
+    even = [1.0] * 8
+    over = [1.0] * 8 + [2.0 ** -40]
+    for row, fine in ((under, True), (spread, True), (even, False), (over, False)):
+        row = row + [0.0] * (V - len(row))
+        for order in (list(range(V)), list(range(V - 1, -1, -1)), torch.randperm(V, generator=U.gen(3)).tolist()):
+            c = plain(torch.tensor(row)[order].expand(N, V), [0.99] * N)
+            tokens, _, _ = run(c)
+            assert B.biv_device_error() == (0 if fine else B.DEVERR_VALUE)
+            want = U.verify(**{k: None if v is None else v[:1] for k, v in c.items()})[0][0] if fine else [0]
+            assert (tokens == want).all()
