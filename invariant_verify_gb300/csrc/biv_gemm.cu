@@ -565,17 +565,22 @@ BIV_DEV unsigned long long tile_row_winner(uint32_t taddr, int cb, int ce, int n
     return best;
 }
 
-// 1 + erf(x / sqrt 2) by Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7: one branch-free
-// form for all x, where erff takes both of its branches in nearly every warp (the
-// epilogue of the last tile is not hidden behind any product).
+// 1 + erf(x / sqrt 2) = erfc(-x / sqrt 2), without branches (the epilogue of the last tile
+// is not hidden behind any product, and erff takes both of its branches in nearly every
+// warp): for x <= 0 and z = |x| / sqrt 2, erfc z = e^(-z^2) t P(t) with t = 1 / (1 + 0.44 z)
+// and P of degree 7, fitted here to a least largest RELATIVE error over 0 <= z <= 10
+// (1.8e-7), so that GELU's negative tail keeps its digits: what is left is the exponent's
+// roundings, (14 + 3 z^2) 2^-24 of the value together.
 BIV_DEV float one_plus_erf_half(float x) {
-    const float z = fabsf(x) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float e = p * t * ex2_approx(-1.4426950408889634f * z * z);      // erfc(z)
+    const float t = __fdividef(1.0f, fmaf(0.44f * 0.70710678118654752f, fabsf(x), 1.0f));
+    float p = fmaf(0.0712231752f, t, -0.277946787f);
+    p = fmaf(p, t, 0.296685352f);
+    p = fmaf(p, t, -0.0201787074f);
+    p = fmaf(p, t, 0.215811205f);
+    p = fmaf(p, t, 0.217313856f);
+    p = fmaf(p, t, 0.248871132f);
+    p = fmaf(p, t, 0.248220955f);
+    const float e = p * t * ex2_approx(-0.72134752f * x * x);
     return x < 0.0f ? e : 2.0f - e;
 }
 
@@ -583,9 +588,10 @@ BIV_DEV float one_plus_erf_half(float x) {
 BIV_DEV float times_sigmoid(float x, float y) { return __fdividef(x, 1.0f + ex2_approx(-1.4426950408889634f * y)); }
 
 // act(x) in fp32, without branches: the epilogue of a CTA's last tile is not hidden
-// behind any product.  Errors stay below 2^-20 of |x|, so the result's one rounding to
-// bf16 is the one that counts.  x/2 (1 + tanh u) = x / (1 + e^-2u) loses nothing to
-// cancellation.
+// behind any product.  Relative errors stay below (24 + 4 |y|) 2^-24, y being the
+// exponential's argument (x^2 / 2 for the erf form; |x|; 2 |u| for the tanh form), and what
+// lies below 2^-126 |x| may be lost: far below a bf16 C's half step of 2^-8, and some units
+// of an fp32 C.  x/2 (1 + tanh u) = x / (1 + e^-2u) loses nothing to cancellation.
 BIV_DEV float activate(float x, int act) {
     switch (act) {
         case BIV_ACT_RELU: return x > 0.0f || x != x ? x : 0.0f;
@@ -605,7 +611,7 @@ BIV_DEV uint4 ld_global_16(const void* p) {
 }
 
 // Sixteen columns of one row: C = act(acc + bias) + residual, one rounding.
-// 1023 x 14336 x 4096 with bias and GELU: 77 us, the plain product 71 (the last tile's
+// 1023 x 14336 x 4096 with bias and GELU: 78 us, the plain product 71 (the last tile's
 // epilogue is not covered by MMAs); operands after the accumulators and the C library's
 // erff: 80.
 struct BiasActRow {
