@@ -113,6 +113,14 @@ int biv_device_error(uint32_t* bits_out);
  * traps, faults or spins without bound.  Not for the hot path. */
 int biv_selftest_wait_timeout(biv_stream_t stream);
 
+/* The same inside a pipeline: biv_softmax (T = 1, dense rows) in its form for
+ * many rows, in which one CTA never asks for its part of `row`.  After the
+ * limit its cluster gives that row and its later ones up (they are not
+ * written), the other rows are right, and BIV_DEVERR_TIMEOUT is raised; about
+ * 4 s.  Requires 2^15 < V <= 2^16, V % 4 == 0, 16-B aligned pointers and more
+ * rows than the device takes at once (BIV_ERR_SHAPE).                       */
+int biv_selftest_softmax_lost_row(const float* logits, int R, int V, float* probs, int row, biv_stream_t stream);
+
 /* --------------------------------------------------------- RMSNorm
  * [DVR] para 1: RMSNorm with a fixed split over the hidden dimension that
  * does not depend on the batch or on how many SMs are busy.

@@ -51,6 +51,7 @@ SIGNATURES = {
     "biv_version": (_I, []),
     "biv_device_error": (_I, [_P]),
     "biv_selftest_wait_timeout": (_I, [_P]),
+    "biv_selftest_softmax_lost_row": (_I, [_P, _I, _I, _P, _I, _P]),
     "biv_rmsnorm": (_I, [_P, _P, _P, _I, _I, _F, _P]),
     "biv_gemm_nosplitk": (_I, [_P, _P, _P, _I, _I, _I, _I, _P]),
     "biv_gemm_nosplitk_bn": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
@@ -218,6 +219,13 @@ def biv_device_error() -> int:
 
 def biv_selftest_wait_timeout(stream=None) -> None:
     _check("biv_selftest_wait_timeout", _load().biv_selftest_wait_timeout(_stream(stream)))
+
+
+def biv_selftest_softmax_lost_row(logits, probs, row: int, stream=None) -> None:
+    """biv_softmax whose part of ``row`` one CTA never asks for (dense fp32 [R, V] each)."""
+    fn = "biv_selftest_softmax_lost_row"
+    _dense(fn, _F32, (logits, probs), (logits.shape, logits.shape), "logits probs")
+    _check(fn, _load().biv_selftest_softmax_lost_row(_ptr(logits), *logits.shape, _ptr(probs), row, _stream(stream)))
 
 
 # ---------------------------------------------------------------- kernels

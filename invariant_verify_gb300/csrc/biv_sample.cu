@@ -73,6 +73,7 @@ BIV_DEV void put_cluster(const void* p, uint32_t rank, unsigned long long x) {
 // batch.  Rows past 8 x 16 x 2048 entries are read twice.  A few rows are bound by
 // latency: 5 x 32000 take 3.6 us.
 constexpr int kMaxCluster = 8;
+constexpr unsigned long long kLandingNs = 1000000ull;      // for a message between two SMs, about 1 us: plenty
 
 // Exponentials of a slice on its own maximum: an infinite maximum's entries share the
 // mass (differences would be NaN), a slice of nothing but -infinity gives zeros.
@@ -190,9 +191,13 @@ softmax_kernel(const float* logits, int V, long long ld, float scale, float* pro
 // the receiving CTA: a cluster barrier's release would wait until the row before has
 // been written out.  Bound by memory: 320 x 128256 take 57 to 58 us, 5.7 TB/s (a cluster
 // a row: 72; cluster barriers: 73).
-template <int NV>
+// A wait that runs out raises its bit and the CTA's flag, and the CTA leaves at the row's
+// next barrier, where all its threads see the flag; its cluster's other CTAs then miss its
+// numbers and leave in the same way, and the cluster's rows from there on are not written.
+// LOSE (the self-test): rank 0 never asks for row `lose`.
+template <int NV, bool LOSE = false>
 __global__ void __launch_bounds__(kThreads, 2)
-softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale, float* probs, long long ld_p) {
+softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale, float* probs, long long ld_p, int lose) {
     constexpr int kSlice = NV * kPerLoad, C = kMaxCluster;
     extern __shared__ __align__(16) float s_x[];           // [kSlice]
     __shared__ float s_m[kWarps], s_l[kWarps];
@@ -217,6 +222,7 @@ softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale
     pdl_trigger();
     auto fetch = [&](int row) {                            // by one thread
         mbar_arrive_expect_tx(&full, static_cast<uint32_t>(n) * 4u);
+        if (LOSE && rank == 0 && row == lose) return;
         if (n > 0)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                              smem_u32(s_x)),
@@ -226,9 +232,10 @@ softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale
     int row = blockIdx.x / C;
     if (tid == 0) fetch(row);                              // the grid holds no more clusters than rows
     cluster_wait();
-    uint32_t heard_phase = 0;
-    for (uint32_t phase = 0; row < R; row += step, phase ^= 1u) {
-        mbar_wait(&full, phase, &abort_flag, &g_sample_err);           // one that runs out raises its bit; the row is lost
+    uint32_t heard_phase = 0, phase = 0;
+    volatile int* const gave_up = &abort_flag;
+    for (; row < R; row += step, phase ^= 1u) {
+        mbar_wait(&full, phase, gave_up, &g_sample_err);
         const float* x = s_x + 4 * tid;
         float4 r[NV];
         float m = -INFINITY;
@@ -238,7 +245,8 @@ softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale
                                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             m = max4(m, r[k]);
         }
-        m = cta_max(m, s_m);                               // its barrier: every thread has read the buffer
+        m = cta_max(m, s_m);                               // its barrier: every thread has read the buffer, or raised the flag
+        if (*gave_up) break;                               // (nothing raises it between that barrier and the next one)
         if (tid == 0 && row + step < R) fetch(row + step);
         const SlicePower power(m, scale);
         float l = 0.0f;
@@ -256,7 +264,7 @@ softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale
                              mapa_shared(&c_ml[phase][rank], tid)),
                          "l"(pack2(m, l)), "r"(mapa_shared(&heard[phase], tid))
                          : "memory");
-        mbar_wait(&heard[phase], heard_phase, &abort_flag, &g_sample_err, false, true);
+        if (!mbar_wait(&heard[phase], heard_phase, gave_up, &g_sample_err, false, true)) continue;
         if (phase) heard_phase ^= 1u;
         const float factor = slice_factor(m, scale, c_ml[phase], C);
         float* p = probs + static_cast<long long>(row) * ld_p + start + 4 * tid;
@@ -264,6 +272,14 @@ softmax_rows_kernel(const float* logits, int R, int V, long long ld, float scale
         for (int k = 0; k < NV; ++k)
             if (4 * tid + k * kPerLoad < n) *reinterpret_cast<float4*>(p + k * kPerLoad) = times(r[k], factor);
     }
+    __syncthreads();
+    if (!*gave_up) return;
+    // Nothing may land here once the CTA has left: its own copy, and the numbers of peers, which
+    // have stopped sending when they come to this barrier (or have left), a moment later.
+    if (row < R && tid == 0) mbar_wait_drain(&full, phase);
+    cluster_started();
+    cluster_wait();
+    for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < kLandingNs;) {}
 }
 
 // T == 0: one CTA per row finds the lowest index of its largest entry and writes the row.
@@ -541,9 +557,9 @@ int launch_softmax(const float* x, int R, int V, long long ld, float scale, floa
 
 // Many rows: as many clusters of softmax_rows_kernel as the device holds at once.
 // *done = false: the rows fit softmax_kernel's one wave (or the device holds none).
-template <int NV>
+template <int NV, bool LOSE = false>
 int launch_softmax_rows(const float* x, int R, int V, long long ld, float scale, float* p, long long ld_p, bool* done,
-                        cudaStream_t s) {
+                        cudaStream_t s, int lose = -1) {
     constexpr int smem = NV * kPerLoad * 4;
     static std::mutex mu;
     static int resident[kMaxDevices] = {};                 // clusters, 0: not yet asked, -1: none
@@ -555,7 +571,7 @@ int launch_softmax_rows(const float* x, int R, int V, long long ld, float scale,
     {
         std::lock_guard<std::mutex> lock(mu);
         if (resident[dev] == 0) {
-            e = cudaFuncSetAttribute(softmax_rows_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = cudaFuncSetAttribute(softmax_rows_kernel<NV, LOSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return cuda_status(e);
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms() / kMaxCluster * kMaxCluster));
@@ -569,7 +585,7 @@ int launch_softmax_rows(const float* x, int R, int V, long long ld, float scale,
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int most = 0;
-            e = cudaOccupancyMaxActiveClusters(&most, softmax_rows_kernel<NV>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&most, softmax_rows_kernel<NV, LOSE>, &cfg);
             if (e != cudaSuccess) return cuda_status(e);
             resident[dev] = most > 0 ? most : -1;
         }
@@ -577,8 +593,8 @@ int launch_softmax_rows(const float* x, int R, int V, long long ld, float scale,
     }
     *done = n > 0 && R > n;
     if (!*done) return BIV_OK;
-    return launch_cluster_pdl(softmax_rows_kernel<NV>, dim3(static_cast<unsigned>(n) * kMaxCluster), dim3(kThreads), smem, s,
-                              kMaxCluster, x, R, V, ld, scale, p, ld_p);
+    return launch_cluster_pdl(softmax_rows_kernel<NV, LOSE>, dim3(static_cast<unsigned>(n) * kMaxCluster), dim3(kThreads), smem, s,
+                              kMaxCluster, x, R, V, ld, scale, p, ld_p, lose);
 }
 
 // Loads a thread and CTAs a row, by V alone: up to four loads a thread, then up to
@@ -629,6 +645,19 @@ extern "C" int biv_softmax(const float* logits, int R, int V, long long ld, floa
     return aligned_rows(logits, ld) && aligned_rows(probs, ld_p)
                ? launch_softmax<true>(logits, R, V, ld, scale, greedy, probs, ld_p, s)
                : launch_softmax<false>(logits, R, V, ld, scale, greedy, probs, ld_p, s);
+}
+
+extern "C" int biv_selftest_softmax_lost_row(const float* logits, int R, int V, float* probs, int row, biv_stream_t stream) {
+    BIV_TRACE_CALL();
+    constexpr int NV = 4;
+    if (R < 1 || row < 0 || row >= R || V % 4 != 0) return BIV_ERR_SHAPE;
+    if (V <= 16 * kPerLoad || V > NV * kPerLoad * kMaxCluster) return BIV_ERR_UNSUPPORTED;
+    if (!logits || !probs) return BIV_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(probs)) return BIV_ERR_ALIGN;
+    bool done = false;
+    const int st = launch_softmax_rows<NV, true>(logits, R, V, V, 1.4426950408889634f, probs, V, &done,
+                                                 reinterpret_cast<cudaStream_t>(stream), row);
+    return st != BIV_OK ? st : done ? BIV_OK : BIV_ERR_SHAPE;
 }
 
 extern "C" int biv_verify_sample(const float* target, const float* draft_probs, const int32_t* draft,
