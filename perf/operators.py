@@ -17,16 +17,6 @@ import torch
 
 own = False
 
-_WORKSPACE = {}
-
-
-def _workspace(n):
-    """One workspace for the whole program, as a server keeps it: grown when a call needs more."""
-    ws = _WORKSPACE.get("ws")
-    if ws is None or ws.numel() < n:
-        ws = _WORKSPACE["ws"] = torch.empty(max(int(n), 1 << 20), dtype=torch.uint8, device="cuda")
-    return ws
-
 
 # ----------------------------------------------------------------- cases
 def listed():
@@ -327,10 +317,13 @@ _PLAIN = {"attn": _plain_attn, "write": _plain_write, "gemm": _plain_gemm, "soft
 # ------------------------------------------------------- the library's calls
 def _own_attn(s):
     from invariant_verify_gb300 import abi as B
-    W, Hq, hd = s["q"].shape
-    n = B.biv_decode_attn_paged_workspace_size(W, Hq, hd, s["page_table"].shape[1], s["k_pages"].shape[2])
+    if "workspace" not in s:
+        # one for each batch shape and stream, as a server keeps it: a call owns its workspace until it is done
+        W, Hq, hd = s["q"].shape
+        n = B.biv_decode_attn_paged_workspace_size(W, Hq, hd, s["page_table"].shape[1], s["k_pages"].shape[2])
+        s["workspace"] = torch.empty(n, dtype=torch.uint8, device=s["q"].device)
     B.biv_decode_attn_paged(s["q"], s["k_pages"], s["v_pages"], s["page_table"], s["row_slot"], s["row_pos"], s["o"],
-                            s["case"]["K"], _workspace(n))
+                            s["case"]["K"], s["workspace"])
     return s["o"]
 
 
