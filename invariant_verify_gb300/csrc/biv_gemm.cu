@@ -1493,9 +1493,13 @@ int launch_gemm(const void* A, const void* B, void* C, int M, int N, int K, int 
 // A and BN / 2 rows of B out of L2 for every k-block instead of M and bn rows, and an
 // SM takes about 120 GB/s.  A pair costs about 2 us more to start, so it pays where A
 // is long (pairs against single CTAs, us): M = 64, N = 4096, K = 14336: 31.7 / 35.5;
-// M = 128 there: 37.3 / 48.0; M = 128, N = 4096, K = 4096: 14.1 / 16.2; but M = 64
-// there: 13.5 / 12.4, K = 1024: 7.1 / 5.5, and with wide tiles (N = 14336, K = 4096,
-// M = 128), whose ring holds few k-blocks: 27.5 / 24.7.  Pair MMAs of M = 128, which read
+// M = 128 there: 37.3 / 48.0; M = 128, N = 4096, K = 4096: 14.1 / 16.3; but M = 64
+// there: 12.7 / 12.3, K = 1024: 7.1 / 5.5, and with wide tiles (N = 14336, K = 4096,
+// M = 128), whose ring holds few k-blocks: 27.5 / 24.7.  The turn, with N = 4096, lies near
+// M K = 2^18.5 = 380000: M = 80, K = 4096 (327680): 13.6 / 13.2; 64 x 5120 (the same): 14.6 / 14.7;
+// 64 x 5632 (360448): 15.6 / 16.1; 96 x 4096 (393216): 13.7 / 14.5.  N = 2048 turns later
+// (96 x 4096: 12.4 / 12.1, the worst point 48 x 8192: 18.7 / 17.5; 112 x 4096: 12.6 / 13.5) and N = 8192
+// earlier (64 x 4096: 15.4 / 16.3).  Pair MMAs of M = 128, which read
 // 64 rows of each CTA's shared memory, instead of M = 256: 1 to 3 % less; what is left at
 // M = 64 is the chain of 896 MMAs on one accumulator, some 58 cycles each (26 us).
 inline int halves_tile_n(int N) {

@@ -23,7 +23,8 @@ struct PageTable {
 // --------------------------------------------------- RoPE + paged write
 // Turns per position of each rotation pair, theta^(-2i/hd) / 2 pi, as 64-bit
 // fractions of a turn: position times this, modulo 2^64, is the angle modulo a
-// full turn with an error of pos * 2^-65 turns.
+// full turn with an error of about pos * 2^-56 turns (the table's doubles: 53 bits
+// of at most 1 / 2 pi, below 2^-65 for pairs that turn slowly).
 struct RopeTurns {
     uint64_t per_pos[128];     // hd / 2 <= 128
 };
@@ -1457,10 +1458,13 @@ int launch_paged_attn(const PagedAttnParams& P, cudaStream_t s) {
     const long long rows = static_cast<long long>(P.rpg) * P.G;
     // Few tiles (of 8 query rows of a request and KV head) and short tables: one launch, with
     // as many CTAs a tile as one round of them holds.  A CTA takes its splits one after the
-    // other, some 3 to 5 us each, so two at most.  32 and 8 heads, us, with two kernels in
-    // brackets: a window of 5 rows, 700 keys, 1 request 6.7 (10.1), 3 requests (C = 4) 7.8 (11.0);
-    // 5 single tokens 6.5 (9.0), of 1500 keys 12.8 (11.7), 9 of them 14.7 (14.5).  In several
-    // rounds (2 windows, C = 8): 12.7 (10.5).
+    // other, some 3 to 5 us each, so two at most.  The host knows the tables' width, not the
+    // lengths, so a wide table sends short requests through two kernels.  32 and 8 heads, us, with
+    // two kernels in brackets: a window of 5 rows, 700 keys, 1 request 6.7 (10.3).  C = 4, under
+    // tables of 2048: 5 single tokens of 700 keys 6.7 (9.0), 1024: 8.7 (10.7), 1500: 12.7 (11.6), 2000: 13.0
+    // (12.6); 9 of them 8.9 (11.6), 11.1 (12.7), 14.5 (14.4), 15.9 (20.6); 3 windows of 5 rows, 700 keys 7.8
+    // (11.1), 1024: 9.3 (11.2), 2000: 13.3 (15.9).  So it may lose a tenth near the middle of its two
+    // turns and gains a quarter below and above.  In several rounds (2 windows, C = 8): 12.7 (10.5).
     const long long tiles = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((rows + 7) / 8), slots = 2LL * num_sms();
     if (P.s_max <= kSmallTurns * 8 && tiles * 8 <= slots)
         return launch_cluster_pdl(paged_attn_small_kernel<HD, 8>, dim3(static_cast<unsigned>(tiles * 8)), dim3(kDirectThreads), 0, s, 8, P);
