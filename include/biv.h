@@ -560,7 +560,8 @@ int biv_softmax(const float* logits, int R, int V, long long ld, float temperatu
  *   tokens[r][0..K]  = d_0 .. d_{n-1}, token, then -1
  *   accept_len[r]    = n + 1 (tokens emitted), new_len[r] = p0[r] + n + 1
  * Sums are taken in 64-bit integers (units of 2^-60), so they are exact to
- * 2^-60 per entry and do not depend on any order.  Entries are clamped to
+ * 2^-60 per entry and do not depend on any order; u * S keeps all of its
+ * bits, and the test for 8 is one of the exact sum.  Entries are clamped to
  * [0, 1] and a NaN counts as 0; u_sample is clamped to [0, 1).  Where no entry
  * is positive, or the entries sum to 8 or more (no distribution: the units
  * would overflow), the token is 0 and BIV_DEVERR_VALUE is raised; a draft
