@@ -569,8 +569,8 @@ BIV_DEV unsigned long long tile_row_winner(uint32_t taddr, int cb, int ce, int n
 // is not hidden behind any product, and erff takes both of its branches in nearly every
 // warp): for x <= 0 and z = |x| / sqrt 2, erfc z = e^(-z^2) t P(t) with t = 1 / (1 + 0.44 z)
 // and P of degree 7, fitted here to a least largest RELATIVE error over 0 <= z <= 10
-// (1.8e-7), so that GELU's negative tail keeps its digits: what is left is the exponent's
-// roundings, (14 + 3 z^2) 2^-24 of the value together.
+// (1.8e-7), so that GELU's negative tail keeps its digits: what is left is the roundings,
+// those of the exponent z^2 above all, below (24 + 4 z^2) 2^-24 of the value together.
 BIV_DEV float one_plus_erf_half(float x) {
     const float t = __fdividef(1.0f, fmaf(0.44f * 0.70710678118654752f, fabsf(x), 1.0f));
     float p = fmaf(0.0712231752f, t, -0.277946787f);

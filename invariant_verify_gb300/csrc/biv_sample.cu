@@ -351,7 +351,7 @@ BIV_DEV unsigned long long warp_sum(unsigned long long x) {
 // weights of its chunk in 64-bit integers, and the warp that holds the border reads
 // the part of its chunk again (from L2) where its kept sums pass the border, down to the
 // entry.  Sums of integers do not depend on their order, so C may follow the batch.
-// 64 requests of 128256 entries: 16.3 us, of which some 10 stream the rows at the rate of
+// 64 requests of 128256 entries: 16.0 us, of which some 10 stream the rows at the rate of
 // memory; the rest are the dependent reads before a request's rows are known and the
 // steps from the sums to the token.
 constexpr int kKeptGoes = 4;           // goes of 512 entries whose sums are kept (64 x 128256 entries, four to a warp: 18.4 -> 16.3 us)
