@@ -528,6 +528,87 @@ int biv_decode_attn_paged(const void* q, const void* k_pages, const void* v_page
                           int Hq, int Hkv, int hd, int n_slots, int max_pages, int n_pages, int page_size,
                           void* workspace, size_t ws_bytes, biv_stream_t stream);
 
+/* --------------------------------------------- a decoding step in 8 bits
+ * Weights, activations and the cache held in e4m3 (4 exponent bits, 3 of the
+ * significand, largest 448) with scales: half the bytes of a step, with the
+ * same invariance.  A value is scale * e4m3; quantisation takes
+ *   scale = max(max |x| / 448, 2^-100),  q = e4m3(x / scale)
+ * (nearest, ties to even).  What is not finite is held as a NaN; in max |x| a
+ * NaN counts as nothing and an infinity as the largest bf16 number.
+ *
+ * biv_quant_e4m3: q = e4m3 [rows, K] of x (bf16, rows ld_x elements apart).
+ *   block_rows = 1 (activations): a scale for 128 values of a row (fewer at
+ *   its end); scales: fp32 [ceil(K/128), rows].  A row does not depend on the
+ *   others.
+ *   block_rows = 128 (weights): a scale for 128 x 128 values; scales: fp32
+ *   [ceil(rows/128), ceil(K/128)].
+ * Requires K % 16 == 0, ld_x >= K, ld_x % 8 == 0, 16-B aligned pointers, q not
+ * x; BIV_ERR_UNSUPPORTED for another block_rows.                            */
+int biv_quant_e4m3(const void* x, long long ld_x, int rows, int K, int block_rows, void* q, float* scales,
+                   biv_stream_t stream);
+
+/* The product of two such matrices with a projection's usual tail:
+ *   C[m][n] = act(sum_b sa[b][m] sb[n / 128][b] sum_{k in block b} A[m][k] B[n][k]
+ *                 + bias[n]) + residual[m][n]
+ * over blocks b of 128 terms.  A block's products are summed by the tensor core,
+ * the blocks in fp32 in increasing order, whatever M, N and the tiles: a row's
+ * bits do not depend on M.  One rounding to C's type (bf16 or fp32, out_dtype).
+ * A: e4m3 [M, K] with a_scales fp32 [ceil(K/128), M]; B: e4m3 [N, K] with
+ * b_scales fp32 [ceil(N/128), ceil(K/128)] (biv_quant_e4m3's layouts); bias: bf16
+ * [N] or NULL; residual: bf16 [M, N] or NULL; act: a biv_act.  C may be the
+ * residual itself when it is bf16; it must not overlap an input in any other way.
+ * B and b_scales are weights in the sense of the conventions above.
+ * Requires N % 8 == 0, K % 16 == 0, 16-B aligned pointers; errors as
+ * biv_gemm_bias_act.                                                        */
+int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B, const float* b_scales, const void* bias,
+                  const void* residual, void* C, int out_dtype, int act, int M, int N, int K, biv_stream_t stream);
+
+/* The paged cache in e4m3.  Pools of pages e4m3 [n_pages, Hkv, page_size, hd],
+ * a bf16 scale for every 16 positions and KV head: [n_pages, Hkv,
+ * page_size / 16], and rings bf16 [n_slots, Hkv, tail, hd], where position p
+ * of a slot lies at p % tail.  A block of 16 positions goes into its page when
+ * its last position is written, quantised as above over its 16 x hd values
+ * with the scale rounded up to bf16; the rows of a block that is not full, and
+ * those that a rejected draft may take back, are in the ring.  A row at
+ * position p reads positions below 16 floor(p / 16) in e4m3 and the others up
+ * to p in bf16: its result depends neither on the window it came in nor on the
+ * drafts behind it.
+ *
+ * biv_rope_kv_write_paged_e4m3: as biv_rope_kv_write_paged (the same angles,
+ * q_out and rows_keep; page table as there), into such a cache.  The rows
+ * [r*K, (r+1)*K) of a group are consecutive positions of one slot, those
+ * without a row (-1) last; groups that write name different slots.  Positions
+ * [16 floor(p / 16), p) before a group's first position p must be among the
+ * last `tail` that were written to the slot (or p % 16 == 0): so a request may
+ * go back by up to tail - 15 positions, or to any multiple of 16.  A row whose
+ * position does not follow the one before, or whose slot is not its group's,
+ * raises BIV_DEVERR_GROUP and is not written, nor is its block; the page
+ * table is read, and has to name a page, only where a block is filled.
+ * Requires tail % 16 == 0, tail >= K + 15, hd == 64 or 128 (else
+ * BIV_ERR_UNSUPPORTED), Hq % Hkv == 0, 32-B aligned pools, 16-B aligned qkv,
+ * q_out and rings, and what biv_rope_kv_write_paged requires of the rest.   */
+int biv_rope_kv_write_paged_e4m3(const void* qkv, void* q_out, void* k_pages, void* v_pages, void* k_scales,
+                                 void* v_scales, void* k_tail, void* v_tail, const int32_t* page_table,
+                                 const int32_t* row_slot, const int32_t* row_pos, const int32_t* rows_keep, int W,
+                                 int K, int Hq, int Hkv, int hd, int n_slots, int max_pages, int n_pages,
+                                 int page_size, int tail, float theta, biv_stream_t stream);
+
+/* biv_decode_attn_paged over such a cache: the same rows, groups, errors,
+ * workspace (biv_decode_attn_paged_workspace_size) and order of sums.  Queries
+ * meet the keys in fp16 after an exact scaling of each row; the softmax
+ * weights meet e4m3 values with 11 bits, an eighth of the rounding of o to
+ * bf16, and the ring's values with 16.  Page ids are read for the e4m3
+ * positions only.  Cache rows up to the group's largest position must hold
+ * finite values; the rest of a ring may hold anything.
+ * Requires tail % 16 == 0, tail >= 16, the pools' alignment as above, and what
+ * biv_decode_attn_paged requires of the rest.                               */
+int biv_decode_attn_paged_e4m3(const void* q, const void* k_pages, const void* v_pages, const void* k_scales,
+                               const void* v_scales, const void* k_tail, const void* v_tail,
+                               const int32_t* page_table, const int32_t* row_slot, const int32_t* row_pos, void* o,
+                               int W, int rows_per_group, int Hq, int Hkv, int hd, int n_slots, int max_pages,
+                               int n_pages, int page_size, int tail, void* workspace, size_t ws_bytes,
+                               biv_stream_t stream);
+
 /* --------------------------------------------- sampled verification
  * For drafters whose tokens were drawn without the shared noise of
  * biv_gumbel_argmax: probabilities of the target and the drafter, and uniform

@@ -89,6 +89,10 @@ SIGNATURES = {
     "biv_rope_kv_write_paged": (_I, [_P] * 8 + [_I] * 9 + [_F, _P]),
     "biv_decode_attn_paged_workspace_size": (_SZ, [_I] * 5),
     "biv_decode_attn_paged": (_I, [_P] * 7 + [_I] * 9 + [_P, _SZ, _P]),
+    "biv_quant_e4m3": (_I, [_P, _LL, _I, _I, _I, _P, _P, _P]),
+    "biv_gemm_e4m3": (_I, [_P] * 7 + [_I] * 5 + [_P]),
+    "biv_rope_kv_write_paged_e4m3": (_I, [_P] * 12 + [_I] * 10 + [_F, _P]),
+    "biv_decode_attn_paged_e4m3": (_I, [_P] * 11 + [_I] * 10 + [_P, _SZ, _P]),
     "biv_softmax": (_I, [_P, _I, _I, _LL, _F, _P, _LL, _P]),
     "biv_verify_sample": (_I, [_P] * 6 + [_I] * 3 + [_P] * 4),
 }
@@ -169,7 +173,7 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
 def _dense(fn: str, dtype, tensors, shapes, names: str) -> None:
@@ -515,6 +519,100 @@ def biv_decode_attn_paged(q, k_pages, v_pages, page_table, row_slot, row_pos, o,
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), row_slot.data_ptr(),
         row_pos.data_ptr(), o.data_ptr(), W, rows_per_group, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size,
         workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        raise BivError(fn, st)
+
+
+def biv_quant_e4m3(x, q, scales, block_rows: int = 1, stream=None) -> None:
+    """q (float8_e4m3fn) and scales of x (bf16; rows may be strided): block_rows 1 for activations
+    (scales fp32 [ceil(K/128), rows]), 128 for weights ([ceil(rows/128), ceil(K/128)])."""
+    fn = "biv_quant_e4m3"
+    rows, K = q.shape
+    _int32(fn, rows, K, block_rows)
+    if x.dtype is not _BF16 or x.shape != (rows, K):
+        raise BivError(fn, 4 if x.dtype is not _BF16 else 2, f"x is {x.dtype} {tuple(x.shape)}, q {tuple(q.shape)}")
+    ld = x.stride(0) if rows > 1 else max(K, 1)
+    if (K > 1 and x.stride(1) != 1) or ld < K:
+        raise BivError(fn, 2, f"x has strides {x.stride()}")
+    if x.get_device() != (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0):
+        raise BivError(fn, 7, "x is not on the current CUDA device")
+    groups = -(-K // 128)
+    _dense(fn, _E4M3, (q,), ((rows, K),), "q")
+    _dense(fn, _F32, (scales,), ((groups, rows) if block_rows == 1 else (-(-rows // 128), groups),), "scales")
+    st = _load().biv_quant_e4m3(x.data_ptr(), ld, rows, K, block_rows, q.data_ptr(), scales.data_ptr(), _stream(stream))
+    if st:
+        raise BivError(fn, st)
+
+
+def biv_gemm_e4m3(A, a_scales, B, b_scales, C_out, bias=None, residual=None, act: str = "none", stream=None) -> None:
+    """C = act(A B^T + bias) + residual of matrices that biv_quant_e4m3 gave; C_out (bf16 or fp32)
+    may be the bf16 residual itself."""
+    fn = "biv_gemm_e4m3"
+    M, K = A.shape
+    N = B.shape[0]
+    _int32(fn, M, N, K)
+    out = C_out.dtype
+    if out is not _BF16 and out is not _F32:
+        raise BivError(fn, 4, f"C is {out}, not bfloat16 or float32")
+    if act not in ACTS:
+        raise BivError(fn, 4, f"act {act!r} is none of {', '.join(ACTS)}")
+    groups = -(-K // 128)
+    _dense(fn, _E4M3, (A, B), ((M, K), (N, K)), "A B")
+    _dense(fn, _F32, (a_scales, b_scales), ((groups, M), (-(-N // 128), groups)), "a_scales b_scales")
+    _dense(fn, _BF16, (bias, residual), ((N,), (M, N)), "bias residual")
+    _dense(fn, out, (C_out,), ((M, N),), "C")
+    st = _load().biv_gemm_e4m3(
+        A.data_ptr(), a_scales.data_ptr(), B.data_ptr(), b_scales.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), C_out.data_ptr(), BIV_F32 if out is _F32 else BIV_BF16,
+        ACTS[act], M, N, K, _stream(stream))
+    if st:
+        raise BivError(fn, st)
+
+
+def _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd):
+    """Checks a cache in e4m3; its n_pages, Hkv, page_size and tail."""
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    tail = k_tail.shape[2]
+    pool, scales, ring = (n_pages, Hkv, page_size, hd), (n_pages, Hkv, page_size // 16), (n_slots, Hkv, tail, hd)
+    _int32(fn, n_pages, Hkv, page_size, tail)
+    _dense(fn, _E4M3, (k_pages, v_pages), (pool, pool), "k_pages v_pages")
+    _dense(fn, _BF16, (k_scales, v_scales, k_tail, v_tail), (scales, scales, ring, ring), "k_scales v_scales k_tail v_tail")
+    return n_pages, Hkv, page_size, tail
+
+
+def biv_rope_kv_write_paged_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot,
+                                 row_pos, theta: float, K: int, rows_keep=None, stream=None) -> None:
+    fn = "biv_rope_kv_write_paged_e4m3"
+    rows = W, Hq, hd = q_out.shape
+    table = n_slots, max_pages = page_table.shape
+    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
+    _int32(fn, W, K, Hq, hd, n_slots, max_pages)
+    _dense(fn, _BF16, (qkv, q_out), ((W, (Hq + 2 * Hkv) * hd), rows), "qkv q_out")
+    _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), (table, (W,), (W,), (W // max(K, 1),)),
+           "page_table row_slot row_pos rows_keep")
+    st = _load().biv_rope_kv_write_paged_e4m3(
+        qkv.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        k_tail.data_ptr(), v_tail.data_ptr(), page_table.data_ptr(), row_slot.data_ptr(), row_pos.data_ptr(),
+        None if rows_keep is None else rows_keep.data_ptr(), W, K, Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size,
+        tail, theta, _stream(stream))
+    if st:
+        raise BivError(fn, st)
+
+
+def biv_decode_attn_paged_e4m3(q, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot, row_pos, o,
+                               rows_per_group: int, workspace, stream=None) -> None:
+    fn = "biv_decode_attn_paged_e4m3"
+    rows = W, Hq, hd = q.shape
+    table = n_slots, max_pages = page_table.shape
+    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
+    _int32(fn, W, rows_per_group, Hq, hd, n_slots, max_pages)
+    _dense(fn, _BF16, (q, o), (rows, rows), "q o")
+    _dense(fn, _I32, (page_table, row_slot, row_pos), (table, (W,), (W,)), "page_table row_slot row_pos")
+    _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")
+    st = _load().biv_decode_attn_paged_e4m3(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), k_tail.data_ptr(),
+        v_tail.data_ptr(), page_table.data_ptr(), row_slot.data_ptr(), row_pos.data_ptr(), o.data_ptr(), W, rows_per_group,
+        Hq, Hkv, hd, n_slots, max_pages, n_pages, page_size, tail, workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if st:
         raise BivError(fn, st)
 

@@ -1,0 +1,719 @@
+// The paged key-value cache held in 8 bits: rotation and write of new rows, and
+// fixed-split decode attention over them.
+//
+// A block of 16 positions is held in e4m3 with one scale for each KV head, and goes
+// into the pages when its last position is written.  Until then, and for as long as a
+// rejected draft may take a request back, its rows lie in bf16 in a ring of `tail`
+// positions a slot (position p at p % tail).  A row at position p reads positions
+// below 16 floor(p / 16) in e4m3 and the rest of its own block in bf16: which form a
+// key has goes by the row's position alone, so a row has the same bits in every
+// window, and a block is always quantised once, from bf16, whole.
+#include "biv_e4m3.cuh"
+#include "biv_paged.cuh"
+
+namespace biv {
+namespace {
+
+constexpr int kHeldBlock = 16;                         // also the keys of an attention step
+
+// Pools of held blocks, their scales [n_pages][Hkv][page_size / 16] and the rings
+// [n_slots][Hkv][tail][hd].
+struct HeldPools {
+    uint8_t* k;
+    uint8_t* v;
+    __nv_bfloat16* k_scales;
+    __nv_bfloat16* v_scales;
+    __nv_bfloat16* k_tail;
+    __nv_bfloat16* v_tail;
+    int tail;
+};
+
+// --------------------------------------------------- RoPE + write
+constexpr int kWriteThreads = 128;
+
+// One CTA per block of 16 positions that a group's rows touch and KV head: it rotates
+// the block's rows of the G query heads and the key head, puts keys and values into the
+// ring and, where the block's last position is among the rows, the whole block into its
+// page: rows of earlier calls come from the ring, so that no CTA waits for another.
+template <int HD>
+__global__ void __launch_bounds__(kWriteThreads)
+rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ q_out, const HeldPools hp,
+                          const PageTable pt, const int32_t* __restrict__ row_slot, const int32_t* __restrict__ row_pos,
+                          const int32_t* __restrict__ rows_keep, int K, int Hq, int Hkv, int chunks,
+                          const __grid_constant__ RopeTurns turns) {
+    constexpr int kHalf = HD / 2, kPerHead = kHalf / 8;
+    __shared__ __align__(16) float s_cs[kHeldBlock][HD];             // cosines, then sines
+    __shared__ __align__(16) __nv_bfloat16 s_kv[2][kHeldBlock][HD];
+    __shared__ int s_pos[kHeldBlock];
+    __shared__ bool s_ok[kHeldBlock];
+    __shared__ int s_page;                                           // of the block if it is full, else -1
+    __shared__ float s_max[kWriteThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int h = blockIdx.x % Hkv, rc = blockIdx.x / Hkv, c = rc % chunks, r = rc / chunks;
+    const int G = Hq / Hkv, heads = Hq + 2 * Hkv;
+    const long long w00 = static_cast<long long>(r) * K;
+    pdl_wait();
+    pdl_trigger();
+    const int p0 = row_pos[w00], slot = row_slot[w00];
+    const int before = c == 0 && p0 >= 0 ? p0 & (kHeldBlock - 1) : 0;               // the block's rows of earlier calls
+    const int j0 = kHeldBlock * c - (p0 >= 0 ? p0 & (kHeldBlock - 1) : 0);          // row of the block's first position
+    if (j0 >= K) return;
+    const int i0 = max(0, -j0), i1 = min(kHeldBlock, K - j0);                       // the block's rows of this call
+    const long long cap = static_cast<long long>(pt.max_pages) << pt.page_shift;
+    const int first = (p0 & ~(kHeldBlock - 1)) + kHeldBlock * c;                    // the block's first position
+    if (tid < 32) {
+        bool ok = false;
+        if (lane >= i0 && lane < i1) {
+            const int j = j0 + lane;
+            const long long w = w00 + j;
+            const int pos = row_pos[w];
+            if (pos != -1 && (!rows_keep || j < rows_keep[r])) {
+                unsigned int bits = 0;
+                if (pos < 0 || pos >= cap || slot < 0 || slot >= pt.n_slots) bits = BIV_DEVERR_INDEX;
+                else if (row_slot[w] != slot || pos - j != p0 || (j > 0 && row_pos[w - 1] != pos - 1)) bits = BIV_DEVERR_GROUP;
+                if (bits) atomicOr(&g_paged_err, bits);
+                ok = bits == 0;
+            }
+            s_pos[lane] = pos;
+            s_ok[lane] = ok;
+        }
+        const uint32_t all = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) {
+            const uint32_t want = (1u << kHeldBlock) - (1u << i0);
+            int page = -1;
+            if ((all & want) == want && i1 == kHeldBlock) {
+                page = pt.table[static_cast<long long>(slot) * pt.max_pages + (first >> pt.page_shift)];
+                if (page < 0 || page >= pt.n_pages) {
+                    atomicOr(&g_paged_err, BIV_DEVERR_INDEX);
+                    page = -1;
+                }
+            }
+            s_page = page;
+        }
+    }
+    for (int e = tid; e < (i1 - i0) * kHalf; e += kWriteThreads) {
+        const int i = i0 + e / kHalf, d = e % kHalf;
+        const uint64_t phase = static_cast<uint64_t>(static_cast<long long>(row_pos[w00 + j0 + i])) * turns.per_pos[d];
+        // the top 32 bits as a signed fraction of half a turn
+        float sn, cs;
+        sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &sn, &cs);
+        s_cs[i][d] = cs;
+        s_cs[i][kHalf + d] = sn;
+    }
+    __syncthreads();
+    const long long ring = (static_cast<long long>(slot) * Hkv + h) * hp.tail;
+    const int items = (G + 2) * kPerHead;                           // of a row: eight pairs each
+    for (int it = tid; it < (i1 - i0) * items; it += kWriteThreads) {
+        const int i = i0 + it / items, u = it % items, x = u / kPerHead, d = (u % kPerHead) * 8;
+        const long long w = w00 + j0 + i;
+        const int head = x < G ? h * G + x : x == G ? Hq + h : Hq + Hkv + h;
+        const __nv_bfloat16* src = qkv + (w * heads + head) * HD;
+        uint4 a = __ldg(reinterpret_cast<const uint4*>(src + d)), b = __ldg(reinterpret_cast<const uint4*>(src + kHalf + d));
+        if (x <= G) {
+            uint32_t* a4 = &a.x;
+            uint32_t* b4 = &b.x;
+            const float* cs = &s_cs[i][d];
+            const float* sn = cs + kHalf;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float al = bf16lo(a4[e]), ah = bf16hi(a4[e]), bl = bf16lo(b4[e]), bh = bf16hi(b4[e]);
+                const float cl = cs[2 * e], ch = cs[2 * e + 1], sl = sn[2 * e], sh = sn[2 * e + 1];
+                a4[e] = pack_bf16x2(al * cl - bl * sl, ah * ch - bh * sh);
+                b4[e] = pack_bf16x2(bl * cl + al * sl, bh * ch + ah * sh);
+            }
+        }
+        if (x < G) {
+            __nv_bfloat16* dst = q_out + (w * Hq + head) * HD;
+            *reinterpret_cast<uint4*>(dst + d) = a;
+            *reinterpret_cast<uint4*>(dst + kHalf + d) = b;
+            continue;
+        }
+        __nv_bfloat16* held = s_kv[x - G][i];
+        *reinterpret_cast<uint4*>(held + d) = a;
+        *reinterpret_cast<uint4*>(held + kHalf + d) = b;
+        if (s_ok[i]) {
+            __nv_bfloat16* dst = (x == G ? hp.k_tail : hp.v_tail) + (ring + s_pos[i] % hp.tail) * HD;
+            *reinterpret_cast<uint4*>(dst + d) = a;
+            *reinterpret_cast<uint4*>(dst + kHalf + d) = b;
+        }
+    }
+    const int page = s_page;
+    if (page < 0) return;
+    for (int e = tid; e < 2 * before * (HD / 8); e += kWriteThreads) {
+        const int x = e & 1, i = (e >> 1) / (HD / 8), d = (e >> 1) % (HD / 8) * 8;
+        *reinterpret_cast<uint4*>(&s_kv[x][i][d]) =
+            *reinterpret_cast<const uint4*>((x ? hp.v_tail : hp.k_tail) + (ring + (first + i) % hp.tail) * HD + d);
+    }
+    __syncthreads();
+    // two warps for the keys, two for the values
+    constexpr int kLoads = kHeldBlock * HD / 8 / 64;
+    const int x = tid >> 6, t = tid & 63;
+    uint4 y[kLoads];
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+        y[e] = reinterpret_cast<const uint4*>(&s_kv[x][0][0])[t + 64 * e];
+        m = fmaxf(m, max_of_halves(max_abs8(y[e])));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0) s_max[tid >> 5] = m;
+    __syncthreads();
+    m = fmaxf(s_max[2 * x], s_max[2 * x + 1]);
+    // the next bf16 number: what the scale is rounded by costs range (at most 2^-7 of it), no precision,
+    // since the values are divided by the number that is held
+    const uint32_t bits = (__float_as_uint(scale_of(m)) + 0xffffu) & 0xffff0000u;
+    const float scale = __uint_as_float(bits), inv = __frcp_rn(scale);
+    const long long at = static_cast<long long>(page) * Hkv + h;
+    const int in_page = first & (pt.page_size - 1);
+    uint8_t* dst = (x ? hp.v : hp.k) + (at * pt.page_size + in_page) * HD;
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) reinterpret_cast<uint2*>(dst)[t + 64 * e] = e4m3x8(y[e], scale, inv);
+    if (t == 0)
+        reinterpret_cast<uint16_t*>(x ? hp.v_scales : hp.k_scales)[(at * pt.page_size + in_page) / kHeldBlock] = static_cast<uint16_t>(bits >> 16);
+}
+
+// ------------------------------------------------------------ attention
+// The split kernels of biv_paged.cu with other keys.  Held keys and values become fp16 in
+// registers, which holds every e4m3 number, and meet fp16 queries and weights in
+// mma.m16n8k16; a step of 16 keys is one block, so the key scale multiplies the step's
+// scores and the value scale its share of the output, both in fp32.  A query row is
+// multiplied by a power of two first, so that its largest element lies in [2^14, 2^15):
+// nothing above 2^-28 of that is rounded.  A weight is at most 2^15 and rounded to 11
+// bits, an eighth of the output's own rounding, and a row's sum adds the rounded weights.
+// The rest of a row's own block comes from the ring, in bf16, with weights of 16 bits.
+//
+// One CTA per item; the split's steps are taken by four warps in turn; a warp reads its
+// keys and values straight from global memory, 32 bytes (keys) and 16 (values) a lane, a
+// whole line for four or eight lanes.  Up to T tiles of 8 query rows share one read.
+
+// D[16 x 8] (+)= A[16 x 16] B[16 x 8], fp16 with fp32 sums.
+BIV_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+BIV_DEV void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+BIV_DEV uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+BIV_DEV float f16_lo(uint32_t x) {
+    float r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(r) : "r"(x));
+    return r;
+}
+BIV_DEV float f16_hi(uint32_t x) {
+    float r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "r"(x));
+    return r;
+}
+
+// N words of held keys or values: read once, so not kept in L1 and first to leave L2.
+template <int N>
+BIV_DEV void ld_held(const uint8_t* p, uint32_t (&r)[N], uint64_t policy) {
+    if constexpr (N == 8)
+        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "l"(p));
+    else if constexpr (N == 4)
+        asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "l"(p), "l"(policy));
+    else
+        asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v2.b32 {%0, %1}, [%2], %3;"
+                     : "=r"(r[0]), "=r"(r[1])
+                     : "l"(p), "l"(policy));
+}
+// N words of the ring: the kernel before may have written them.
+template <int N>
+BIV_DEV void ld_tail(const __nv_bfloat16* p, uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * i);
+        r[i] = v.x;
+        r[i + 1] = v.y;
+        r[i + 2] = v.z;
+        r[i + 3] = v.w;
+    }
+}
+
+// A warp's keys and values of one held step.  Lane (g8, c4): dims [HD / 4 c4, ..) of keys g8 and
+// g8 + 8, dims [HD / 8 g8, ..) of values 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9.
+template <int HD>
+struct HeldKeys {
+    static constexpr int KS = HD / 16;
+    uint32_t k[2][KS];
+    uint32_t v[4][HD / 32];
+
+    BIV_DEV void load_k(const uint8_t* kp, int g8, int c4, uint64_t policy) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) ld_held(kp + (g8 + 8 * r) * HD + HD / 4 * c4, k[r], policy);
+    }
+    BIV_DEV void load_v(const uint8_t* vp, int g8, int c4, uint64_t policy) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld_held(vp + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i], policy);
+    }
+};
+
+// Q of T tiles in the order of the B fragments: [tile][k / 2][lane] holds the lane's two registers of
+// k-steps k and k + 1, as fp16 (times the row's power of two) and as bf16.
+template <int HD, int T>
+struct __align__(16) HeldQ {
+    uint4 f16[T][HD / 32][32];
+    uint4 bf[T][HD / 32][32];
+    float back[T][8];                  // log2(e) / sqrt(hd) over the row's power of two
+};
+
+// A warp's running softmax over T tiles of eight query rows: this lane's columns are rows
+// 2 (lane % 4) and the next of a tile.
+template <int HD, int T>
+struct HeldRows {
+    static constexpr int KS = HD / 16;
+    static constexpr float kSlack = 8.0f;          // as in RowState: a row's reference follows its maximum with slack
+    static constexpr float kLift = 7.0f;           // weights are 2^kLift times as large: up to 2^15, so that fp16 keeps small ones
+    float acc[T][KS][4];
+    float m[T][2], l[T][2], mu[T][2];
+
+    BIV_DEV void clear() {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][k][e] = 0.0f;
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = mu[t][0] = mu[t][1] = 0.0f;
+        }
+    }
+
+    // Scores of a step in units of log 2 to weights in place (without their sum).
+    BIV_DEV void weights(int t, float (&st)[4]) {
+        float x[2] = {fmaxf(st[0], st[2]), fmaxf(st[1], st[3])};
+        if (__any_sync(0xffffffffu, x[0] > m[t][0] + kSlack || x[1] > m[t][1] + kSlack)) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
+                x[0] = fmaxf(x[0], y0);
+                x[1] = fmaxf(x[1], y1);
+            }
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[e] = 1.0f;
+                if (x[e] > m[t][e] + kSlack) {
+                    f[e] = ex2_approx(m[t][e] - x[e]);
+                    m[t][e] = x[e];
+                    mu[t][e] = x[e] - kLift;
+                }
+                l[t][e] *= f[e];
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][k][e] *= f[e & 1];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[e] = ex2_approx(st[e] - mu[t][e & 1]);
+    }
+
+    // One held step: scores, weights and values; key0 its first key, last[t] the lane's rows' last held key.
+    // between(): asked for between the scores and the values, when the keys' registers are free.
+    template <typename F>
+    BIV_DEV void step(HeldKeys<HD>& hk, const HeldQ<HD, T>& q, const float (&back)[T][2], float k_scale, float v_scale,
+                      const int (&last)[T][2], int see, bool bad, int key0, int lane, F&& between) {
+        const int g8 = lane >> 2;
+        float st[T][4];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[t][e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                a[j][0] = e4m3_lo(hk.k[0][k + j]);
+                a[j][1] = e4m3_lo(hk.k[1][k + j]);
+                a[j][2] = e4m3_hi(hk.k[0][k + j]);
+                a[j][3] = e4m3_hi(hk.k[1][k + j]);
+            }
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const uint4 b = q.f16[t][k / 2][lane];
+                mma_f16(st[t], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+                mma_f16(st[t], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+            }
+        }
+        between();
+        uint32_t w[T][2];
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[t][e] *= back[t][e & 1] * k_scale;
+            if (key0 + kStep - 1 > see) mask_step(st[t], last[t], key0, g8);
+            weights(t, st[t]);
+            const uint32_t h0 = pack_f16x2(st[t][0], st[t][1]), h1 = pack_f16x2(st[t][2], st[t][3]);
+            l[t][0] += f16_lo(h0) + f16_lo(h1);
+            l[t][1] += f16_hi(h0) + f16_hi(h1);
+            w[t][0] = transpose8(h0);
+            w[t][1] = transpose8(h1);
+        }
+        if (bad) {                                 // a page out of range: what was read in its place may be NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < HD / 32; ++d) hk.v[i][d] = 0u;
+        }
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) {
+            uint32_t p[2][2];                      // [keys, keys + 8][dims 0 and 1, 2 and 3]: pairs of keys
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                p[i][0] = __byte_perm(hk.v[2 * i][d], hk.v[2 * i + 1][d], 0x5140);
+                p[i][1] = __byte_perm(hk.v[2 * i][d], hk.v[2 * i + 1][d], 0x7362);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t a0 = e4m3_lo(p[0][j]), a1 = e4m3_hi(p[0][j]), a2 = e4m3_lo(p[1][j]), a3 = e4m3_hi(p[1][j]);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    float y[4];
+                    mma_f16_zero(y, a0, a1, a2, a3, w[t][0], w[t][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][2 * d + j][e] = fmaf(v_scale, y[e], acc[t][2 * d + j][e]);
+                }
+            }
+        }
+    }
+
+    // The step whose block is a row's own, from the ring: pos[t] are the rows' positions; rows of other
+    // blocks are left alone; what lies behind key tmax may be anything.
+    BIV_DEV void own_step(const __nv_bfloat16* kt, const __nv_bfloat16* vt, const HeldQ<HD, T>& q, float scale_log2,
+                          const int (&pos)[T][2], int tmax, int key0, int lane) {
+        const int g8 = lane >> 2, c4 = lane & 3;
+        uint32_t k[2][2 * KS];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) ld_tail(kt + (g8 + 8 * r) * HD + HD / 4 * c4, k[r]);
+        uint32_t v[4][KS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld_tail(vt + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (key0 + 2 * c4 + (i & 1) + 8 * (i >> 1) > tmax) {
+#pragma unroll
+                for (int d = 0; d < KS; ++d) v[i][d] = 0u;
+            }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float st[4] = {};
+#pragma unroll
+            for (int j = 0; j < KS; j += 2) {
+                const uint4 b = q.bf[t][j / 2][lane];
+                mma_16816(st, k[0][2 * j], k[1][2 * j], k[0][2 * j + 1], k[1][2 * j + 1], b.x, b.y);
+                mma_16816(st, k[0][2 * j + 2], k[1][2 * j + 2], k[0][2 * j + 3], k[1][2 * j + 3], b.z, b.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = pos[t][e & 1];
+                st[e] = (p | (kStep - 1)) == (key0 | (kStep - 1)) && key0 + g8 + 8 * (e >> 1) <= p ? st[e] * scale_log2 : -INFINITY;
+            }
+            weights(t, st);
+            l[t][0] += st[0] + st[2];
+            l[t][1] += st[1] + st[3];
+            const uint32_t h0 = pack_bf16x2(st[0], st[1]), h1 = pack_bf16x2(st[2], st[3]);
+            const uint32_t hi[2] = {transpose8(h0), transpose8(h1)};
+            const uint32_t low[2] = {transpose8(pack_bf16x2(st[0] - bf16lo(h0), st[1] - bf16hi(h0))),
+                                     transpose8(pack_bf16x2(st[2] - bf16lo(h1), st[3] - bf16hi(h1)))};
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+                const uint32_t a0 = __byte_perm(v[0][d], v[1][d], 0x5410), a1 = __byte_perm(v[0][d], v[1][d], 0x7632);
+                const uint32_t a2 = __byte_perm(v[2][d], v[3][d], 0x5410), a3 = __byte_perm(v[2][d], v[3][d], 0x7632);
+                mma_16816(acc[t][d], a0, a1, a2, a3, hi[0], hi[1]);
+                mma_16816(acc[t][d], a0, a1, a2, a3, low[0], low[1]);
+            }
+        }
+    }
+
+    // As RowState::put_ml and DirectKeys::put: maximum, sum and output of every row; bad: rows that met a
+    // page id out of range.
+    BIV_DEV void put(float2 (*ml)[kClasses][8], float (*o)[kClasses][8][HD + 4], int cls, const uint32_t (&bad)[T], int lane) const {
+        const int g8 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float s[2] = {l[t][0], l[t][1]};
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, s[0], d), y1 = __shfl_xor_sync(0xffffffffu, s[1], d);
+                s[0] += y0;
+                s[1] += y1;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (g8 == 0) ml[t][cls][2 * c4 + e] = make_float2(m[t][e], (bad[t] >> e) & 1u ? -INFINITY : s[e]);
+#pragma unroll
+                for (int k = 0; k < KS; k += 2)
+                    *reinterpret_cast<float4*>(&o[t][cls][2 * c4 + e][HD / 8 * g8 + 2 * k]) =
+                        make_float4(acc[t][k][e], acc[t][k][e + 2], acc[t][k + 1][e], acc[t][k + 1][e + 2]);
+            }
+        }
+    }
+};
+
+// A 16-byte piece of a query row: as it is, and times the row's power of two.  The HD / 8
+// threads of a row stand side by side in a warp.
+template <int HD, int T>
+BIV_DEV void put_q(HeldQ<HD, T>& q, const uint4& x, int row, int piece, float scale_log2) {
+    uint32_t m = max_abs8(x);
+    m = __float_as_uint(max_of_halves(m));
+#pragma unroll
+    for (int d = HD / 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    // exponent field e: 2^(141 - e) takes the largest to [2^14, 2^15)
+    const uint32_t e = min(max(m >> 23, 15u), 254u);
+    const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23);
+    const int d0 = piece * 8, c4 = d0 / (HD / 4), kk = d0 % (HD / 4) / 8;
+    uint4 y;
+    y.x = pack_f16x2(bf16lo(x.x) * up, bf16hi(x.x) * up);
+    y.y = pack_f16x2(bf16lo(x.y) * up, bf16hi(x.y) * up);
+    y.z = pack_f16x2(bf16lo(x.z) * up, bf16hi(x.z) * up);
+    y.w = pack_f16x2(bf16lo(x.w) * up, bf16hi(x.w) * up);
+    q.f16[row / 8][kk][(row % 8) * 4 + c4] = y;
+    q.bf[row / 8][kk][(row % 8) * 4 + c4] = x;
+    if (piece == 0) q.back[row / 8][row % 8] = scale_log2 * down;
+}
+
+template <int HD, int T>
+struct __align__(16) HeldSmem {
+    float o[T][kClasses][8][HD + 4];       // rows padded against bank conflicts
+    HeldQ<HD, T> q;
+    float2 ml[T][kClasses][8];
+    int pos[8 * T];
+    LiveTable table;
+};
+
+constexpr int kHeldThreads = 32 * kClasses;
+
+// Where the pool's rows of a 16-key step start, in elements.
+template <int HD>
+BIV_DEV long long held_at(const PagedAttnParams& P, int page, int kvh, int key0) {
+    return ((static_cast<long long>(page) * P.Hkv + kvh) * P.pt.page_size + (key0 & (P.pt.page_size - 1))) * HD;
+}
+
+template <int HD, int T>
+__global__ void __launch_bounds__(kHeldThreads, T == 1 ? 4 : T == 2 ? 3 : 2) paged_attn_held_kernel(const PagedAttnParams P, const HeldPools hp) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    HeldSmem<HD, T>& sm = *reinterpret_cast<HeldSmem<HD, T>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
+    const int g8 = lane >> 2, c4 = lane & 3;
+    const Items I(P, sm.table, 8 * T);
+    const uint64_t policy = policy_evict_first();
+    pdl_wait();
+    pdl_trigger();
+    I.zero_rows<HD>();
+    AttnItem it;
+    for (bool more = I.first(it); more; more = I.next(it, it)) {
+        const int key_lo = it.split * kSplit, r0 = it.tile * 8 * T;
+        __syncthreads();                           // the item before has been joined
+        // positions and queries of the tile's rows
+        for (int i = tid; i < 8 * T; i += kHeldThreads) {
+            int j, head;
+            row_head(P, r0 + i, j, head);
+            sm.pos[i] = r0 + i < it.rows ? I.pos_of(it.w0 + j) : -1;
+        }
+        for (int e = tid; e < 8 * T * (HD / 8); e += kHeldThreads) {
+            const int row = e / (HD / 8), piece = e % (HD / 8);
+            int j, head;
+            row_head(P, r0 + row < it.rows ? r0 + row : 0, j, head);           // rows past the group's read its first row and are never used
+            const uint4 x = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + piece * 8);
+            put_q(sm.q, x, row, piece, P.scale_log2);
+        }
+        __syncthreads();
+        int pos[T][2], last[T][2], tmax = -1, tmin = 0x7fffffff, all = 0x7fffffff;
+        float back[T][2];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                pos[t][e] = sm.pos[8 * t + 2 * c4 + e];
+                back[t][e] = sm.q.back[t][2 * c4 + e];
+                last[t][e] = pos[t][e] < 0 ? -1 : (pos[t][e] & ~(kStep - 1)) - 1;
+                tmax = max(tmax, pos[t][e]);
+                if (pos[t][e] >= 0) tmin = min(tmin, pos[t][e]);
+                if (pos[t][e] >= key_lo) all = min(all, last[t][e]);
+            }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, d));
+            tmin = min(tmin, __shfl_xor_sync(0xffffffffu, tmin, d));
+            all = min(all, __shfl_xor_sync(0xffffffffu, all, d));
+        }
+        if (tmax < key_lo) continue;               // no row of the tile has keys here
+        const int held_last = (tmax & ~(kStep - 1)) - 1;
+        const int nsteps = held_last < 0 ? 0 : Items::steps_to(held_last, it.split);
+        const int my_steps = (nsteps - cls + kClasses - 1) / kClasses;
+        // lane i: page and scales of this class's i-th step
+        int page = 0;
+        uint32_t bad = 0;
+        float ks = 0.0f, vs = 0.0f;
+        if (lane < my_steps)
+            page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
+                              ((key_lo + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
+        bad = bad_pages(P, page);
+        if (lane < my_steps) {
+            const long long s = held_at<HD>(P, page, it.kvh, key_lo + kStep * (cls + kClasses * lane)) / (kStep * HD);
+            ks = __bfloat162float(hp.k_scales[s]);
+            vs = __bfloat162float(hp.v_scales[s]);
+        }
+        HeldKeys<HD> keys;
+        auto at = [&](int i) { return held_at<HD>(P, __shfl_sync(0xffffffffu, page, i), it.kvh, key_lo + kStep * (cls + kClasses * i)); };
+        if (my_steps > 0) {
+            const long long a = at(0);
+            keys.load_k(hp.k + a, g8, c4, policy);
+            keys.load_v(hp.v + a, g8, c4, policy);
+        }
+        HeldRows<HD, T> rs;
+        rs.clear();
+        uint32_t bad_rows[T] = {};
+#pragma unroll 1
+        for (int i = 0; i < my_steps; ++i) {
+            const int key0 = key_lo + kStep * (cls + kClasses * i);
+            const bool step_bad = (bad >> i) & 1u;
+            if (step_bad) {
+#pragma unroll
+                for (int t = 0; t < T; ++t) bad_rows[t] |= (last[t][0] >= key0 ? 1u : 0u) | (last[t][1] >= key0 ? 2u : 0u);
+            }
+            long long next = 0;
+            const bool here = i + 1 < my_steps;
+            rs.step(keys, sm.q, back, __shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i), last, all, step_bad, key0, lane, [&] {
+                if (here) {
+                    next = at(i + 1);
+                    keys.load_k(hp.k + next, g8, c4, policy);
+                }
+            });
+            if (here) keys.load_v(hp.v + next, g8, c4, policy);
+        }
+        // the rows' own blocks, from the ring
+        const int b1 = min(kSteps - 1, (tmax - key_lo) / kStep);
+        for (int b = max(0, (tmin - key_lo) / kStep); b <= b1; ++b)
+            if ((b & (kClasses - 1)) == cls) {
+                const int key0 = key_lo + kStep * b;
+                const long long a = ((static_cast<long long>(I.slot_of(it.w0)) * P.Hkv + it.kvh) * hp.tail + key0 % hp.tail) * HD;
+                rs.own_step(hp.k_tail + a, hp.v_tail + a, sm.q, P.scale_log2, pos, tmax, key0, lane);
+            }
+        rs.put(sm.ml, sm.o, cls, bad_rows, lane);
+        __syncthreads();
+        for (int x4 = tid; x4 < 8 * T * (HD / 4); x4 += kHeldThreads) {
+            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4, row_pos = sm.pos[row];
+            if (row_pos < key_lo) continue;
+            int j, head;
+            row_head(P, r0 + row, j, head);
+            join_row<HD>(P, sm.o[row / 8], sm.ml[row / 8], row % 8, d, row_pos, static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head, it.split);
+        }
+    }
+}
+
+template <int HD, int T>
+int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
+    static DeviceOnce once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int st = once.run(dev, [] {
+        return cuda_status(cudaFuncSetAttribute(paged_attn_held_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                static_cast<int>(sizeof(HeldSmem<HD, T>))));
+    });
+    if (st != BIV_OK) return st;
+    const long long n_groups = (P.W + P.rpg - 1) / P.rpg, tiles = (static_cast<long long>(P.rpg) * P.G + 8 * T - 1) / (8 * T);
+    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, (T == 1 ? 4LL : T == 2 ? 3LL : 2LL) * num_sms());
+    return launch_pdl(paged_attn_held_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(kHeldThreads), sizeof(HeldSmem<HD, T>), s, P, hp);
+}
+
+template <int HD>
+int launch_held_attn(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
+    // as few passes over the keys as four tiles allow, each with as few tiles as they then need
+    const long long rows = static_cast<long long>(P.rpg) * P.G, passes = (rows + 31) / 32, T = (rows + 8 * passes - 1) / (8 * passes);
+    const int st = T == 1 ? launch_held<HD, 1>(P, hp, s) : T == 2 ? launch_held<HD, 2>(P, hp, s)
+                 : T == 3 ? launch_held<HD, 3>(P, hp, s) : launch_held<HD, 4>(P, hp, s);
+    if (st != BIV_OK || P.s_max == 1) return st;
+    return launch_combine<HD>(P, s);
+}
+
+// What both calls ask of the pools.
+int check_held(const HeldPools& hp, const void* const (&p)[6]) {
+    for (const void* x : p)
+        if (!x) return BIV_ERR_NULL;
+    for (int i = 0; i < 6; ++i)
+        if (i == 2 || i == 3 ? (reinterpret_cast<uintptr_t>(p[i]) & 1u) != 0 : i < 2 ? (reinterpret_cast<uintptr_t>(p[i]) & 31u) != 0 : !aligned16(p[i]))
+            return BIV_ERR_ALIGN;
+    return BIV_OK;
+}
+
+}  // namespace
+}  // namespace biv
+
+using namespace biv;
+
+extern "C" int biv_rope_kv_write_paged_e4m3(const void* qkv, void* q_out, void* k_pages, void* v_pages, void* k_scales,
+                                            void* v_scales, void* k_tail, void* v_tail, const int32_t* page_table,
+                                            const int32_t* row_slot, const int32_t* row_pos, const int32_t* rows_keep, int W,
+                                            int K, int Hq, int Hkv, int hd, int n_slots, int max_pages, int n_pages,
+                                            int page_size, int tail, float theta, biv_stream_t stream) {
+    BIV_TRACE_CALL();
+    if (W < 0 || K < 1 || Hq <= 0 || Hkv <= 0 || hd <= 0 || W % K != 0 || Hq % Hkv != 0 || Hq > (1 << 20)) return BIV_ERR_SHAPE;
+    PageTable pt;
+    int st = check_pages(n_slots, max_pages, n_pages, page_size, &pt);
+    if (st != BIV_OK) return st;
+    if (hd != 64 && hd != 128) return BIV_ERR_UNSUPPORTED;
+    if (tail % kHeldBlock != 0 || tail < K + kHeldBlock - 1LL) return BIV_ERR_SHAPE;
+    const int chunks = (K + kHeldBlock - 2) / kHeldBlock + 1;
+    const long long grid = static_cast<long long>(W / K) * chunks * Hkv;
+    if (grid > 0x7fffffffLL) return BIV_ERR_SHAPE;
+    if (!(theta > 1.0f) || !std::isfinite(theta)) return BIV_ERR_VALUE;
+    if (W == 0) return BIV_OK;
+    if (!qkv || !q_out || !page_table || !row_slot || !row_pos) return BIV_ERR_NULL;
+    const HeldPools hp{static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages), static_cast<__nv_bfloat16*>(k_scales),
+                       static_cast<__nv_bfloat16*>(v_scales), static_cast<__nv_bfloat16*>(k_tail), static_cast<__nv_bfloat16*>(v_tail), tail};
+    st = check_held(hp, {k_pages, v_pages, k_scales, v_scales, k_tail, v_tail});
+    if (st != BIV_OK) return st;
+    if (!aligned16(qkv) || !aligned16(q_out)) return BIV_ERR_ALIGN;
+    pt.table = page_table;
+    const RopeTurns& turns = rope_turns(theta, hd);
+    return launch_pdl(hd == 128 ? rope_kv_write_held_kernel<128> : rope_kv_write_held_kernel<64>, dim3(static_cast<unsigned>(grid)),
+                      dim3(kWriteThreads), 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(qkv),
+                      static_cast<__nv_bfloat16*>(q_out), hp, pt, row_slot, row_pos, rows_keep, K, Hq, Hkv, chunks, turns);
+}
+
+extern "C" int biv_decode_attn_paged_e4m3(const void* q, const void* k_pages, const void* v_pages, const void* k_scales,
+                                          const void* v_scales, const void* k_tail, const void* v_tail,
+                                          const int32_t* page_table, const int32_t* row_slot, const int32_t* row_pos, void* o,
+                                          int W, int rows_per_group, int Hq, int Hkv, int hd, int n_slots, int max_pages,
+                                          int n_pages, int page_size, int tail, void* workspace, size_t ws_bytes,
+                                          biv_stream_t stream) {
+    BIV_TRACE_CALL();
+    if (W < 0 || rows_per_group <= 0 || Hq <= 0 || Hkv <= 0 || hd <= 0 || Hq % Hkv != 0) return BIV_ERR_SHAPE;
+    PagedAttnParams P;
+    int st = check_pages(n_slots, max_pages, n_pages, page_size, &P.pt);
+    if (st != BIV_OK) return st;
+    if (hd != 64 && hd != 128) return BIV_ERR_UNSUPPORTED;
+    if (static_cast<long long>(W) * Hq > 0x7fffffffLL || tail < kHeldBlock || tail % kHeldBlock != 0) return BIV_ERR_SHAPE;
+    if (W == 0) return BIV_OK;
+    if (!q || !page_table || !row_slot || !row_pos || !o || !workspace) return BIV_ERR_NULL;
+    auto out = [](const void* x) { return const_cast<void*>(x); };
+    const HeldPools hp{static_cast<uint8_t*>(out(k_pages)), static_cast<uint8_t*>(out(v_pages)), static_cast<__nv_bfloat16*>(out(k_scales)),
+                       static_cast<__nv_bfloat16*>(out(v_scales)), static_cast<__nv_bfloat16*>(out(k_tail)), static_cast<__nv_bfloat16*>(out(v_tail)), tail};
+    st = check_held(hp, {k_pages, v_pages, k_scales, v_scales, k_tail, v_tail});
+    if (st != BIV_OK) return st;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return BIV_ERR_ALIGN;
+    if (ws_bytes < biv_decode_attn_paged_workspace_size(W, Hq, hd, max_pages, page_size)) return BIV_ERR_SHAPE;
+    if (o == q) return BIV_ERR_VALUE;
+    fill_attn(P, q, o, page_table, row_slot, row_pos, W, rows_per_group, Hq, Hkv, hd, max_pages, page_size, workspace);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return hd == 128 ? launch_held_attn<128>(P, hp, s) : launch_held_attn<64>(P, hp, s);
+}
