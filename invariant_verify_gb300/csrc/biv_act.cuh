@@ -4,7 +4,6 @@
 #include "biv_common.cuh"
 
 namespace biv {
-namespace {
 
 // Bias, activation and residual of an epilogue.
 struct BiasActArgs {
@@ -12,6 +11,8 @@ struct BiasActArgs {
     const __nv_bfloat16* residual;    // [M, N] or null; may be C itself
     int act;                          // BIV_ACT_*
 };
+
+namespace {
 
 // 1 + erf(x / sqrt 2) = erfc(-x / sqrt 2), without branches (the epilogue of the last tile
 // is not hidden behind any product, and erff takes both of its branches in nearly every

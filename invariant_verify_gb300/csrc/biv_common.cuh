@@ -342,6 +342,12 @@ BIV_DEV void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 
+// The same where no memory is handed over with it (accumulators in TMEM are, by the tcgen05
+// fences): no release at cluster scope, which waits for the thread's stores.
+BIV_DEV void mbar_arrive_remote(uint32_t bar_cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
+}
+
 // Phase probe with acquire at cluster scope (for barriers other CTAs of the
 // cluster arrive on).
 BIV_DEV bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {

@@ -5,25 +5,27 @@
 // The tensor core sums one k-block of 128 terms (four MMAs of K = 32) into an
 // accumulator in TMEM that starts at zero; the epilogue warps read it, multiply it by the
 // two scales and add it to fp32 sums in their registers, block by block in increasing k.
-// That order, and a row's bits, do not depend on M, on the tile or on which operand lies
-// along the accumulator's lanes.  So the work of the CUDA cores goes with the tensor
-// core's: 256 x 256 a pair and k-block are 128 fused multiply-adds a thread.
+// That order, and a row's bits, do not depend on M or on the tile.  So the work of the CUDA
+// cores goes with the tensor core's: 128 x 256 a CTA and k-block are 128 fused multiply-adds
+// a thread (in pairs, fma.rn.f32x2, they take nearly twice as long), some 360 cycles with
+// the reads of TMEM, beside 517 of the MMAs.
 //
-// Kernel layout (320 threads, one CTA per SM, persistent over tiles), as in biv_gemm.cu:
-//   warp 0      TMA producer: boxes of KS k-blocks, 128-byte swizzle
-//   warp 1      TMEM allocator + MMA issuer
-//   warps 2..9  sums and stores, two warps per TMEM lane quarter (half of the columns each)
-// TMEM holds two sets of 256 columns, each of `nb` k-blocks' accumulators (nb BN <= 256):
-// while the epilogue reads one, the other is filled.
+// A row of A is a lane of the accumulator, so that a thread's scale is one number for 128
+// columns.  (With the weights along the lanes M need not be a multiple of 128, but every column
+// has its own scale, from shared memory: 840 cycles a k-block instead of 590.)
 //
-// Two forms:
-//   rows    (M <= 128, and N small enough for one wave) one CTA per tile: the rows of A along
-//           the lanes, BN columns of C: the weights stream once, as many CTAs as SMs.
-//   columns a pair of CTAs per tile (cta_group::2): 256 rows of the WEIGHTS along the lanes
-//           (one scale for a CTA and k-block), BN rows of A as the tile's columns: M is cut into
-//           multiples of 32 instead of 128 (320 rows are two tiles of 160, not 512), and a
-//           warp's lanes are consecutive n of one row of C, so that it stores whole lines.
+// Kernel layout (384 or 640 threads, one CTA per SM, persistent over tiles):
+//   warp 0      TMA producer: boxes of NB k-blocks, 128-byte swizzle
+//   warps 1, 2  MMA issuers, which take the stages in turn: one warp's waits and commits take some 300
+//               cycles a k-block, in which the MMAs that it has queued run out.  Stages and sets are even
+//               in number, so that each has its own, and every wait is for the phase after one that the
+//               same warp has seen: a parity cannot tell phases apart that are two away
+//   warps 4..   sums and stores: two or four warps per TMEM lane quarter, which share the columns
+// TMEM holds kSets sets of NB k-blocks' accumulators: one is read while others are filled.
+// CG = 1: a CTA per tile of 128 rows.  CG = 2: a pair per tile of 256 (cta_group::2): each CTA copies its
+// 128 rows of A and half of the BN rows of B, the even one issues the MMAs.
 #include <algorithm>
+#include <cstdlib>
 
 #include "biv_act.cuh"
 
@@ -34,145 +36,236 @@ BIV_DEFINE_ERR_WORD(g_gemm8_err)
 
 constexpr int kLanes = 128;                   // rows of an accumulator in one CTA
 constexpr int kBK = 128;                      // a k-block: 128 e4m3, one swizzle row and one scale
-constexpr int kSetCols = 256;
 constexpr int kMaxStages = 16;
-constexpr int kEpilogue = 256;                // epilogue threads
-constexpr int kRowSets = 4;                   // k-blocks of a set, at most, in the rows form
+constexpr int kIssuers = 2;
 constexpr int kBarBytes = 512;
-constexpr int kScaleFloats = kRowSets * kLanes + kRowSets * 4;        // of a set: see Scales
-constexpr int kRing = 227 * 1024 - 1024 - kBarBytes - 2 * kScaleFloats * 4 - 1024;
+constexpr int kPageBlocks = 16;               // k-blocks whose scales are copied at once
+constexpr int kPageFloats = kPageBlocks * (kLanes + 4);
 constexpr int kSlack = kLanes * kBK;          // an MMA may read 128 rows past the last stage
-constexpr int kParts = 8;                     // 16 columns each: a thread's half of 256
+constexpr int kMaxSmem = 227 * 1024 - 1024;
+constexpr int kRing = kMaxSmem - 1024 - kBarBytes - 2 * kPageFloats * 4;
 
 struct Gemm8Args {
-    int M, N, K, KB;                          // k-blocks
-    int BN, KS, stages, nb;
-    int xr, yr;                               // rows of a CTA's boxes: along the lanes, along the columns
-    int y_tiles, work;
-    int three_d;                              // K % 128 == 0: a box may hold several k-blocks
-    uint32_t idesc;
     const float* sa;                          // [KB][M]
     const float* sb;                          // [ceil(N / 128)][KB]
+    void* C;
+    BiasActArgs ba;
+    int M, N, K, KB;                          // k-blocks
+    int f32;
+    int BN, stages;                           // tile width, stages
+    int xr, yr;                               // rows of a CTA's boxes of A and of B
+    int m_tiles, tiles;
+    int boxes;                                // of a stage and operand: 1, or all where K % 128 != 0
+    uint32_t idesc;
 };
 
-// A barrier of the epilogue threads and a vote: true if every one says so.
-BIV_DEV bool set_all(bool ok) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(ok ? 1u : 0u)
-                 : "memory");
-    return r != 0;
+// WG: warpgroups that sum; PARTS: 16-column parts of a thread, its share of BN.  Registers: every thread starts
+// with kStart, then the first warpgroup keeps kFew, so that the others can have kMany.
+template <int WG, int PARTS>
+struct Form {
+    static constexpr int kEpilogue = 128 * WG, kThreads = 128 + kEpilogue, kCols = 16 * WG * PARTS;          // the widest BN
+    static constexpr int kStart = WG == 2 ? 168 : 96, kFew = WG == 2 ? 40 : 64, kMany = WG == 2 ? 232 : 104;
+    static_assert(kThreads * kStart <= 65536 && 128 * kFew + kEpilogue * kMany <= kThreads * kStart, "more registers than the CTA holds");
+    // K-blocks of a stage, whose accumulators are a set: the sets are taken in turn.
+    static constexpr int kBlocks = kCols <= 64 ? 4 : kCols <= 128 ? 2 : 1;
+    static constexpr int kSets = kCols <= 32 ? 4 : 2;
+    static constexpr int kSetCols = 512 / kSets;
+    // A barrier of the summing threads and a vote: true if every one says so.
+    BIV_DEV static bool all_say(bool ok) {
+        uint32_t r;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(r)
+                     : "r"(ok ? 1u : 0u), "n"(kEpilogue)
+                     : "memory");
+        return r != 0;
+    }
+};
+
+// The four MMAs of a k-block into an accumulator that starts at zero, by one elected lane of a converged warp
+// (one election for the four: 7 % of a small product's time).  +32 bytes along K inside the swizzle
+// row are +2 in the descriptors' 16-byte units.
+#define BIV_MMA_BLOCK(CG)                                                                                       \
+    "{\n\t.reg .pred e, pt, pf;\n\t.reg .b64 x1, x2, x3, y1, y2, y3;\n\t"                                        \
+    "setp.eq.u32 pt, 0, 0;\n\tsetp.ne.u32 pf, 0, 0;\n\t"                                                        \
+    "add.s64 x1, %1, 2;\n\tadd.s64 y1, %2, 2;\n\tadd.s64 x2, %1, 4;\n\tadd.s64 y2, %2, 4;\n\t"                   \
+    "add.s64 x3, %1, 6;\n\tadd.s64 y3, %2, 6;\n\telect.sync _|e, 0xffffffff;\n\t"                               \
+    "@e tcgen05.mma.cta_group::" CG ".kind::f8f6f4 [%0], %1, %2, %3, pf;\n\t"                                   \
+    "@e tcgen05.mma.cta_group::" CG ".kind::f8f6f4 [%0], x1, y1, %3, pt;\n\t"                                   \
+    "@e tcgen05.mma.cta_group::" CG ".kind::f8f6f4 [%0], x2, y2, %3, pt;\n\t"                                   \
+    "@e tcgen05.mma.cta_group::" CG ".kind::f8f6f4 [%0], x3, y3, %3, pt;\n\t}\n"
+template <int CG>
+BIV_DEV void mma_block(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc) {
+    if constexpr (CG == 2)
+        asm volatile(BIV_MMA_BLOCK("2")::"r"(d), "l"(x), "l"(y), "r"(idesc) : "memory");
+    else
+        asm volatile(BIV_MMA_BLOCK("1")::"r"(d), "l"(x), "l"(y), "r"(idesc) : "memory");
 }
 
-template <bool COLS, bool F32>
-__global__ void __launch_bounds__(64 + kEpilogue, 1)
-gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, void* __restrict__ C,
-                 const Gemm8Args g, const BiasActArgs ba) {
+// Arrive once on `bar` (of both CTAs of a pair) when the MMAs issued so far by the elected lane complete.
+template <int CG>
+BIV_DEV void commit(uint64_t* bar) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        umma_commit_elect(bar);
+}
+
+// A bounded wait of a whole warp for one barrier or two (shared-memory addresses).  The loops hold nothing but
+// the polls: a k-block takes some 600 cycles, and what stands between a phase and the work behind it is seen
+// in each.
+BIV_DEV bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+BIV_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    bool ok;
+    int polls = kFastPolls;
+#pragma unroll 1
+    do ok = poll(bar, parity);
+    while (!ok && --polls);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return __all_sync(0xffffffffu, mbar_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, &g_gemm8_err));
+}
+BIV_DEV bool warp_wait(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort_flag) {
+    bool ok;
+    int polls = kFastPolls;
+#pragma unroll 1
+    do ok = poll(bar0, parity0);
+    while (!ok && --polls);
+#pragma unroll 1
+    while (ok && !(ok = poll(bar1, parity1)) && --polls > 0) ok = true;
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return warp_wait(bar0, parity0, abort_flag) && warp_wait(bar1, parity1, abort_flag);
+}
+BIV_DEV float ld_shared(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+
+// Four bytes to shared memory, zero where there are none to read.
+BIV_DEV void copy_4(float* dst, const float* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
+template <int CG, int WG, int PARTS>
+__global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                                                                const Gemm8Args g) {
+    using Q = Form<WG, PARTS>;
+    constexpr int NB = Q::kBlocks;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int CG = COLS ? 2 : 1;
-    const int X_BYTES = g.KS * g.xr * kBK, STAGE = X_BYTES + g.KS * g.yr * kBK, S = g.stages;
+    const int A_BYTES = NB * g.xr * kBK, STAGE = A_BYTES + NB * g.yr * kBK, S = g.stages;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * STAGE + (g.xr < kLanes ? kSlack : 0));
     uint64_t* empty = full + kMaxStages;
-    uint64_t* tfull = empty + kMaxStages;     // [2]
-    uint64_t* tempty = tfull + 2;             // [2]
-    uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* tfull = empty + kMaxStages;     // [kSets]
+    uint64_t* tempty = tfull + Q::kSets;      // [kSets]
+    uint64_t* drain = tempty + Q::kSets;      // [kIssuers]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + kIssuers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float(*s_scale)[kScaleFloats] = reinterpret_cast<float(*)[kScaleFloats]>(reinterpret_cast<uint8_t*>(full) + kBarBytes);   // [2]
+    float(*s_page)[kPageFloats] = reinterpret_cast<float(*)[kPageFloats]>(reinterpret_cast<uint8_t*>(full) + kBarBytes);   // [2]
 
-    const int rank = COLS ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int unit = static_cast<int>(blockIdx.x) / CG, n_units = static_cast<int>(gridDim.x) / CG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_stages = (g.KB + g.KS - 1) / g.KS;                   // of a tile
+    const int n_stages = (g.KB + NB - 1) / NB;                   // of a tile
     // epilogue warps with rows to read: all, or those of the quarters that M reaches
-    const int readers = COLS ? 16 : 2 * min(4, (g.M + 31) / 32);
+    const int readers = WG * (CG == 2 ? 8 : min(4, (g.M + 31) / 32));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < Q::kSets; ++a) {
             mbar_init(&tfull[a], 1);
             mbar_init(&tempty[a], readers);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < kIssuers; ++i) mbar_init(&drain[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
-        prefetch_tensormap(&tmX);
-        prefetch_tensormap(&tmY);
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
     }
     if (warp == 1) {
-        if constexpr (COLS) {
-            tmem_alloc_pair(tmem_slot, 2 * kSetCols);
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(tmem_slot, 512);
             tmem_relinquish_pair();
         } else {
-            tmem_alloc(tmem_slot, 2 * kSetCols);
+            tmem_alloc(tmem_slot, 512);
             tmem_relinquish();
         }
     }
     tc_fence_before();
-    if constexpr (COLS)
+    if constexpr (CG == 2)
         cluster_sync();
     else
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    const uint64_t pol_w = !COLS || g.y_tiles == 1 ? policy_evict_first() : policy_evict_normal();   // weights: read once
-    const uint64_t pol_a = policy_evict_last();                                                      // activations: by every CTA
-    const uint32_t tx = static_cast<uint32_t>(STAGE);
-    // the X or Y box of a stage of tile t
-    auto load = [&](const CUtensorMap* map, uint8_t* dst, int stage, int row, int sb, uint64_t pol) {
-        const int c0 = g.three_d ? 0 : sb * kBK, c2 = g.three_d ? sb * g.KS : 0;
-        if constexpr (COLS)
-            tma_load_3d_pair(dst, map, mapa_shared(&full[stage], 0), c0, row, c2, pol);
-        else
-            tma_load_3d(dst, map, &full[stage], c0, row, c2, pol);
+    // weights: read once, or by the CTAs of all rows at about the same time; activations: by every CTA
+    const uint64_t pol_w = g.m_tiles == 1 ? policy_evict_first() : policy_evict_normal(), pol_a = policy_evict_last();
+    auto load = [&](const CUtensorMap* map, uint8_t* dst, int stage, int row, int rows, int sb, uint64_t pol) {
+        for (int j = 0; j < g.boxes; ++j) {
+            const int c0 = g.boxes == 1 && g.K % kBK == 0 ? 0 : (sb * NB + j) * kBK, c2 = g.K % kBK == 0 ? sb * NB : 0;
+            if constexpr (CG == 2)
+                tma_load_3d_pair(dst + j * rows * kBK, map, mapa_shared(&full[stage], 0), c0, row, c2, pol);
+            else
+                tma_load_3d(dst + j * rows * kBK, map, &full[stage], c0, row, c2, pol);
+        }
     };
-    auto load_x = [&](int t, int sb, int stage) {
-        load(&tmX, smem + stage * STAGE, stage, (t / g.y_tiles) * (kLanes * CG) + rank * kLanes, sb, COLS ? pol_w : pol_a);
+    // tile t: rows (t % m_tiles), columns (t / m_tiles)
+    auto load_a = [&](int t, int sb, int stage) {
+        load(&tmA, smem + stage * STAGE, stage, (t % g.m_tiles) * (kLanes * CG) + rank * kLanes, g.xr, sb, pol_a);
     };
-    auto load_y = [&](int t, int sb, int stage) {
-        load(&tmY, smem + stage * STAGE + X_BYTES, stage, (t % g.y_tiles) * g.BN + rank * g.yr, sb, COLS ? pol_a : pol_w);
+    auto load_b = [&](int t, int sb, int stage) {
+        load(&tmB, smem + stage * STAGE + A_BYTES, stage, (t / g.m_tiles) * g.BN + rank * g.yr, g.yr, sb, pol_w);
     };
     auto expect = [&](int stage) {            // a pair's copies all complete on the even CTA's barrier
-        if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * tx);
+        if (rank == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(CG * STAGE));
     };
     // The weights are no output of the previous kernel: the first stages' are asked for before waiting for it.
     int early = 0;
-    if (warp == 0 && lane == 0 && unit < g.work) {
+    if (warp == 0 && lane == 0 && unit < g.tiles) {
         early = min(S, n_stages);
         for (int sb = 0; sb < early; ++sb) {
             expect(sb);
-            if constexpr (COLS)
-                load_x(unit, sb, sb);
-            else
-                load_y(unit, sb, sb);
+            load_b(unit, sb, sb);
         }
     }
     pdl_wait();
     pdl_trigger();
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Q::kFew));
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
             bool ok = true;
-            for (int t = unit; t < g.work && ok; t += n_units)
+            for (int t = unit; t < g.tiles && ok; t += n_units)
                 for (int sb = 0; sb < n_stages; ++sb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &g_gemm8_err, true, COLS)) {
-                        ok = false;
-                        break;
+                    ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, &g_gemm8_err);
+                    if (!ok) break;
+                    if (t != unit || sb >= early) {
+                        expect(stage);
+                        load_b(t, sb, stage);
                     }
-                    const bool asked = t == unit && sb < early;
-                    if (!asked) expect(stage);
-                    if (!(COLS && asked)) load_x(t, sb, stage);
-                    if (!(!COLS && asked)) load_y(t, sb, stage);
+                    load_a(t, sb, stage);
                     ++issued;
                     if (++stage == S) {
                         stage = 0;
@@ -191,273 +284,221 @@ gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                     }
                 }
             }
-        }
-    } else if (warp == 1) {
-        // --------------------------------------------------- MMA issuer
-        if (rank == 0) {
-            int stage = 0, set = 0;
+        } else if ((warp == 1 || warp == 2) && rank == 0) {
+            // -------------------------------------------------- MMA issuers
+            const int me = warp - 1;
+            const int units_tiles = unit < g.tiles ? (g.tiles - unit + n_units - 1) / n_units : 0;
+            const long long all = static_cast<long long>(units_tiles) * n_stages;
+            int stage = me, set = me, sb = me % n_stages;            // sb: the stage's place in its tile
             uint32_t phase = 0, set_phase = 0;
             bool ok = true, any = false;
-            auto commit_set = [&]() {
-                if constexpr (COLS) {
-                    umma_commit_pair_elect(mapa_shared(&tfull[set], 0));
-                    umma_commit_pair_elect(mapa_shared(&tfull[set], 1));
-                } else {
-                    umma_commit_elect(&tfull[set]);
-                }
-                set ^= 1;
-                if (set == 0) set_phase ^= 1u;
-            };
-            for (int t = unit; t < g.work && ok; t += n_units) {
-                int in_set = 0;                                      // k-blocks of the present set
-                for (int sb = 0; sb < n_stages && ok; ++sb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, &g_gemm8_err, true, COLS));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t x_addr = smem_u32(smem + stage * STAGE), y_addr = x_addr + static_cast<uint32_t>(X_BYTES);
-                    const int nkb = min(g.KS, g.KB - sb * g.KS);
-                    for (int j = 0; j < nkb; ++j) {
-                        if (in_set == 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(&tempty[set], set_phase ^ 1u, abort_flag, &g_gemm8_err, true, COLS));
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        const uint32_t d = tmem_base + static_cast<uint32_t>(set * kSetCols + in_set * g.BN);
-                        const uint64_t x = sw128_kmajor_desc(x_addr + static_cast<uint32_t>(j * g.xr * kBK));
-                        const uint64_t y = sw128_kmajor_desc(y_addr + static_cast<uint32_t>(j * g.yr * kBK));
+            const uint32_t full0 = smem_u32(full), tempty0 = smem_u32(tempty);
+            const uint64_t a0 = sw128_kmajor_desc(smem_u32(smem)), b0 = sw128_kmajor_desc(smem_u32(smem + A_BYTES));
+            const uint32_t a_step = static_cast<uint32_t>(g.xr * kBK / 16), b_step = static_cast<uint32_t>(g.yr * kBK / 16);      // of a k-block
+            for (long long c = me; c < all; c += kIssuers) {
+                ok = warp_wait(full0 + 8u * stage, phase, tempty0 + 8u * set, set_phase ^ 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = static_cast<uint32_t>(stage * (STAGE / 16)), d = tmem_base + static_cast<uint32_t>(set * Q::kSetCols);
+                const int nkb = NB == 1 ? 1 : min(NB, g.KB - sb * NB);
 #pragma unroll
-                        for (int k = 0; k < kBK / 32; ++k) {
-                            // +32 bytes along K inside the swizzle row = +2 in 16-byte units
-                            if constexpr (COLS)
-                                umma_f8_pair_elect(d, x + 2u * k, y + 2u * k, g.idesc, k > 0 ? 1u : 0u);
-                            else
-                                umma_f8_elect(d, x + 2u * k, y + 2u * k, g.idesc, k > 0 ? 1u : 0u);
-                        }
-                        any = true;
-                        if (++in_set == g.nb || sb * g.KS + j + 1 == g.KB) {
-                            commit_set();
-                            in_set = 0;
-                        }
-                    }
-                    if (!ok) break;
-                    if constexpr (COLS) {
-                        umma_commit_pair_elect(mapa_shared(&empty[stage], 0));
-                        umma_commit_pair_elect(mapa_shared(&empty[stage], 1));
-                    } else {
-                        umma_commit_elect(&empty[stage]);
-                    }
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                for (int j = 0; j < NB; ++j)
+                    if (j < nkb) mma_block<CG>(d + static_cast<uint32_t>(j * g.BN), a0 + at + j * a_step, b0 + at + j * b_step, g.idesc);
+                commit<CG>(&tfull[set]);
+                commit<CG>(&empty[stage]);
+                any = true;
+                if ((stage += kIssuers) >= S) {
+                    stage = me;
+                    phase ^= 1u;
                 }
+                if ((set += kIssuers) >= Q::kSets) {
+                    set = me;
+                    set_phase ^= 1u;
+                }
+                for (sb += kIssuers; sb >= n_stages;) sb -= n_stages;
             }
-            if (!ok && any) {
-                // all MMAs issued so far have finished
-                if constexpr (COLS)
-                    umma_commit_pair_elect(mapa_shared(drain, 0));
-                else
-                    umma_commit_elect(drain);
-                if (lane == 0) mbar_wait_drain(drain, 0);
+            if (!ok && any) {                 // all MMAs issued so far have finished
+                commit<CG>(&drain[me]);
+                if (lane == 0) mbar_wait_drain(&drain[me], 0);
             }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------- sums and stores
-        const int q = warp & 3, half = (warp - 2) >> 2, tid = static_cast<int>(threadIdx.x) - 64;
-        const int hc = (g.BN / 2 + 15) / 16 * 16;
-        const int cb = half ? hc : 0, ce = half ? g.BN : hc;           // this warp's columns of the tile
-        const bool reads = COLS || q * 32 < g.M;
-        const int parts = reads ? (ce - cb + 15) / 16 : 0;
-        const int sets = (g.KB + g.nb - 1) / g.nb;
-        // Scales of set s of tile t, one to three numbers a thread.  Columns form: [k-block][column]
-        // sa times the CTA's sb.  Rows form: [k-block][row] sa, then [k-block][4] sb of the tile's 128-column blocks.
-        float pre[3];
-        auto fetch = [&](int t, int s) {
-            pre[0] = pre[1] = pre[2] = 0.0f;
-            if constexpr (COLS) {
-                const int kb = s * g.nb + tid / g.BN, col = tid % g.BN;
-                const int m = (t % g.y_tiles) * g.BN + col, n0 = (t / g.y_tiles) * (2 * kLanes) + rank * kLanes;
-                if (tid / g.BN < g.nb && kb < g.KB && m < g.M && n0 < g.N)
-                    pre[0] = g.sa[static_cast<long long>(kb) * g.M + m] * __ldg(g.sb + static_cast<long long>(n0 / 128) * g.KB + kb);
-            } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Q::kMany));
+        const int q = warp & 3, tid = static_cast<int>(threadIdx.x) - 128;
+        const int cb = (warp / 4 - 1) * 16 * PARTS;                     // this warp's first column of the tile
+        const bool reads = CG == 2 || q * 32 < g.M;
+        const int sets = n_stages, pages = (g.KB + kPageBlocks - 1) / kPageBlocks;
+        constexpr int kPageSets = kPageBlocks / NB;
+        // Scales of a page of tile t: [k-block][row] sa, then [k-block][4] sb of the tile's 128-column blocks.
+        auto fetch = [&](int t, int page, float* dst) {
+            const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + (tid & (kLanes - 1)), kb0 = page * kPageBlocks;
+            int kb = kb0 + tid / kLanes;
+            const float* src = g.sa + static_cast<long long>(kb) * g.M + row;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int kl = (tid + i * kEpilogue) / kLanes, row = tid % kLanes, kb = s * g.nb + kl;
-                    if (kl < g.nb && kb < g.KB && row < g.M) pre[i] = g.sa[static_cast<long long>(kb) * g.M + row];
-                }
-                const int kl = tid / 4, kb = s * g.nb + kl, nblk = t * g.BN / 128 + tid % 4;
-                if (kl < g.nb && kb < g.KB && nblk < (g.N + 127) / 128) pre[2] = __ldg(g.sb + static_cast<long long>(nblk) * g.KB + kb);
+            for (int i = 0; i < kPageBlocks / WG; ++i, kb += WG, src += static_cast<long long>(WG) * g.M) {
+                const bool in = kb < g.KB && row < g.M;
+                copy_4(dst + i * Q::kEpilogue + tid, in ? src : g.sa, in);
             }
-        };
-        auto put = [&](float* dst) {
-            if constexpr (COLS) {
-                dst[tid] = pre[0];
-            } else {
-                dst[tid] = pre[0];
-                dst[tid + kEpilogue] = pre[1];
-                if (tid < 4 * kRowSets) dst[kRowSets * kLanes + tid] = pre[2];
+            if (tid < 4 * kPageBlocks) {
+                const int nblk = (t / g.m_tiles) * g.BN / 128 + (tid & 3);
+                kb = kb0 + tid / 4;
+                const bool in = kb < g.KB && nblk < (g.N + 127) / 128;
+                copy_4(dst + kPageBlocks * kLanes + tid, in ? g.sb + static_cast<long long>(nblk) * g.KB + kb : g.sb, in);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        int set = 0;
+        const uint32_t tfull0 = smem_u32(tfull), pages0 = smem_u32(&s_page[0][0]);
+        uint32_t freed = smem_u32(tempty);    // the sets' barriers where the MMAs are issued
+        if constexpr (CG == 2) freed = mapa_shared(tempty, 0);
+        int set = 0, buf = 0;
         uint32_t set_phase = 0;
         bool ok = true;                       // a wait ran out: the warps leave together, at the next vote
-        if (unit < g.work) fetch(unit, 0);
-        for (int t = unit; t < g.work; t += n_units) {
-            const int col0 = (t % g.y_tiles) * g.BN;
-            float acc[kParts][16];
+        if (unit < g.tiles) fetch(unit, 0, s_page[0]);
+        for (int t = unit; t < g.tiles; t += n_units) {
+            const int n0 = (t / g.m_tiles) * g.BN;
+            float acc[PARTS][16];
 #pragma unroll
-            for (int i = 0; i < kParts; ++i)
+            for (int i = 0; i < PARTS; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+            // of the first columns of each part: which of the tile's 128-column blocks of weights
+            const int blk = (n0 + cb) / 128 - n0 / 128, turn = (128 - (n0 + cb) % 128) / 16;         // the first one, and its parts
             for (int s = 0; s < sets; ++s) {
-                float* scale = s_scale[set];
-                put(scale);
-                if (!(ok = set_all(ok))) break;
-                if (s + 1 < sets)
-                    fetch(t, s + 1);
-                else if (t + n_units < g.work)
-                    fetch(t + n_units, 0);
-                if (reads) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&tfull[set], set_phase, abort_flag, &g_gemm8_err, false, COLS));
-                    tc_fence_after();
-                    const int nkb = ok ? min(g.nb, g.KB - s * g.nb) : 0;
-                    for (int kl = 0; kl < nkb; ++kl) {
-                        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * kSetCols + kl * g.BN + cb);
-                        const float row_scale = COLS ? 0.0f : scale[kl * kLanes + q * 32 + lane];
-#pragma unroll
-                        for (int i = 0; i < kParts; ++i)
-                            if (i < parts) {
-                                uint32_t r[16];
-                                tmem_ld16_sync(taddr + static_cast<uint32_t>(16 * i), r);
-                                if constexpr (COLS) {
-                                    const float4* sc = reinterpret_cast<const float4*>(scale + kl * g.BN + cb + 16 * i);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float4 x = sc[e];
-                                        acc[i][4 * e] = fmaf(__uint_as_float(r[4 * e]), x.x, acc[i][4 * e]);
-                                        acc[i][4 * e + 1] = fmaf(__uint_as_float(r[4 * e + 1]), x.y, acc[i][4 * e + 1]);
-                                        acc[i][4 * e + 2] = fmaf(__uint_as_float(r[4 * e + 2]), x.z, acc[i][4 * e + 2]);
-                                        acc[i][4 * e + 3] = fmaf(__uint_as_float(r[4 * e + 3]), x.w, acc[i][4 * e + 3]);
-                                    }
-                                } else {
-                                    const float x = row_scale * scale[kRowSets * kLanes + kl * 4 + (col0 + cb + 16 * i) / 128 - col0 / 128];
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) acc[i][e] = fmaf(__uint_as_float(r[e]), x, acc[i][e]);
-                                }
-                            }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (COLS)
-                            mbar_arrive_cluster(mapa_shared(&tempty[set], 0));
-                        else
-                            mbar_arrive(&tempty[set]);
-                    }
+                const int in_page = s % kPageSets, nkb = min(NB, g.KB - s * NB);
+                if (in_page == 0) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    if (!(ok = Q::all_say(ok))) break;                    // this page has landed, and the one before it is read
+                    const int page = s / kPageSets + 1;
+                    buf ^= 1;
+                    if (page < pages)
+                        fetch(t, page, s_page[buf]);
+                    else if (t + n_units < g.tiles)
+                        fetch(t + n_units, 0, s_page[buf]);
                 }
-                set ^= 1;
-                if (set == 0) set_phase ^= 1u;
-            }
-            if (!ok) continue;                // to the vote, or to the end
-            if constexpr (COLS) {
-                // lane: n; columns: rows m of C
-                const int n = (t / g.y_tiles) * (2 * kLanes) + rank * kLanes + q * 32 + lane;
-                const float bias = ba.bias && n < g.N ? __bfloat162float(ba.bias[n]) : 0.0f;
+                if (reads) {
+                    const uint32_t row_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + in_page * NB * kLanes + q * 32 + lane) * 4u;
+                    const uint32_t col_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + kPageBlocks * kLanes + in_page * NB * 4 + blk) * 4u;
+                    const bool here = warp_wait(tfull0 + 8u * set, set_phase, abort_flag);
+                    ok = ok && here;
+                    tc_fence_after();
+                    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * Q::kSetCols + cb);
 #pragma unroll
-                for (int i = 0; i < kParts; ++i)
-                    if (i < parts) {
+                    for (int kl = 0; kl < NB; ++kl)
+                        if (kl < nkb) {
+                            // the warp's columns lie in two 128-column blocks of weights at most
+                            const float mine = ld_shared(row_scale + kl * kLanes * 4u);
+                            const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = mine * ld_shared(col_scale + kl * 16u + 4u);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const int m = col0 + cb + 16 * i + e;
-                            float v0 = acc[i][e] + bias, v1 = acc[i][e + 1] + bias;
-                            if (ba.act != BIV_ACT_NONE) {
-                                v0 = activate(v0, ba.act);
-                                v1 = activate(v1, ba.act);
-                            }
-                            if constexpr (F32) {
-                                if (n < g.N) {
-                                    const long long at = static_cast<long long>(m) * g.N + n;
-                                    if (m < g.M) static_cast<float*>(C)[at] = v0 + (ba.residual ? __bfloat162float(ba.residual[at]) : 0.0f);
-                                    if (m + 1 < g.M)
-                                        static_cast<float*>(C)[at + g.N] = v1 + (ba.residual ? __bfloat162float(ba.residual[at + g.N]) : 0.0f);
+                            for (int i = 0; i < PARTS; i += 2) {
+                                const uint32_t at = taddr + static_cast<uint32_t>(kl * g.BN + 16 * i);
+                                uint32_t r[32];
+                                if (i + 1 < PARTS) {
+                                    tmem_ld32_sync(at, r);
+                                } else {
+                                    uint32_t h[16];
+                                    tmem_ld16_sync(at, h);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) r[e] = h[e];
                                 }
-                            } else {
-                                // even lanes store n, n + 1 of row m, odd lanes n - 1, n of row m + 1
-                                const bool odd = lane & 1;
-                                const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                                float lo = odd ? other : v0, hi = odd ? v1 : other;
-                                const int row = m + (odd ? 1 : 0), n2 = n & ~1;
-                                if (row < g.M && n2 < g.N) {
-                                    uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(C) + static_cast<long long>(row) * g.N + n2);
-                                    if (ba.residual) {
-                                        const uint32_t x = *reinterpret_cast<const volatile uint32_t*>(ba.residual + static_cast<long long>(row) * g.N + n2);
-                                        lo += bf16lo(x);
-                                        hi += bf16hi(x);
+                                if (i + 2 >= PARTS && kl + 1 == nkb) {         // the set has been read
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        if constexpr (CG == 2)
+                                            mbar_arrive_remote(freed + 8u * set);
+                                        else
+                                            mbar_arrive(&tempty[set]);
                                     }
-                                    *at = pack_bf16x2(lo, hi);
                                 }
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (i + h < PARTS) {
+                                        const float x = i + h < turn ? x0 : x1;
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            acc[i + h < PARTS ? i + h : 0][e] = fmaf(__uint_as_float(r[16 * h + e]), x, acc[i + h < PARTS ? i + h : 0][e]);
+                                    }
                             }
                         }
-                    }
-            } else {
-                const int row = q * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < kParts; ++i)
-                    if (i < parts) {
-                        const BiasActRow operands(row < g.M, row, col0 + cb + 16 * i, g.N, ba);
-                        operands.template store<F32>([&](int e) { return acc[i][e]; }, C, ba);
-                    }
+                }
+                if (++set == Q::kSets) {
+                    set = 0;
+                    set_phase ^= 1u;
+                }
             }
+            if (!ok || !reads) continue;      // to the vote, or to the end
+            const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + q * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i)
+                if (cb + 16 * i < g.BN) {
+                    const BiasActRow operands(row < g.M, row, n0 + cb + 16 * i, g.N, g.ba);
+                    auto value = [&](int e) { return acc[i][e]; };
+                    if (g.f32)
+                        operands.template store<true>(value, g.C, g.ba);
+                    else
+                        operands.template store<false>(value, g.C, g.ba);
+                }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     tc_fence_before();
-    if constexpr (COLS) {
+    if constexpr (CG == 2) {
         // neither CTA leaves while the other may still read its shared memory or signal its barriers
         cluster_sync();
         tc_fence_after();
-        if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kSetCols);
+        if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
     } else {
         __syncthreads();
         tc_fence_after();
-        if (warp == 1) tmem_dealloc(tmem_base, 2 * kSetCols);
+        if (warp == 1) tmem_dealloc(tmem_base, 512);
     }
 }
 
 // ---------------------------------------------------------------- host side
-// e4m3 [rows, K] in boxes [KS][box_rows][128 bytes], 128-byte swizzle; zeros past the ends.
-bool encode_e4m3(CUtensorMap* map, const void* base, int rows, int K, int box_rows, int ks, bool three_d) {
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// e4m3 [rows, K] in boxes [ks][box_rows][128 bytes], 128-byte swizzle; zeros past the ends.  Where K is no
+// multiple of 128 a box holds one k-block.
+bool encode_e4m3(CUtensorMap* map, const void* base, int rows, int K, int box_rows, int ks) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
+    const bool whole = K % kBK == 0;
     const cuuint64_t ld = static_cast<cuuint64_t>(K);
-    const cuuint64_t dims[3] = {three_d ? kBK : ld, static_cast<cuuint64_t>(rows), three_d ? ld / kBK : 1};
+    const cuuint64_t dims[3] = {whole ? kBK : ld, static_cast<cuuint64_t>(rows), whole ? ld / kBK : 1};
     const cuuint64_t strides[2] = {ld, kBK};
-    const cuuint32_t box[3] = {kBK, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(ks)}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {kBK, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(whole ? ks : 1)}, estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
-
-// The kernel's opt-in shared memory and how many of its CTAs (pairs) run at once.
-template <bool COLS, bool F32>
-int setup_e4m3(int dev, int* units) {
+// Once per device and kernel: its opt-in shared memory, the registers it starts with (those that the sums'
+// warps take are the ones that the others give up), and how many units (CTAs, or pairs) run at once.
+template <int CG, int WG, int PARTS>
+int setup_e4m3(int* out) {
     static std::mutex mu;
-    static int known[kMaxDevices] = {};
+    static int units[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
     if (dev < 0 || dev >= kMaxDevices) return BIV_ERR_DEVICE;
     std::lock_guard<std::mutex> lock(mu);
-    if (known[dev] == 0) {
-        auto kern = gemm_e4m3_kernel<COLS, F32>;
-        const int smem = 227 * 1024 - 1024;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (units[dev] == 0) {
+        auto kern = gemm_e4m3_kernel<CG, WG, PARTS>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return cuda_status(e);
+        cudaFuncAttributes attrs;
+        e = cudaFuncGetAttributes(&attrs, kern);
+        if (e != cudaSuccess) return cuda_status(e);
+        if (attrs.numRegs != Form<WG, PARTS>::kStart) return BIV_ERR_DEVICE;
         int n = num_sms();
-        if (COLS) {
+        if (CG == 2) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms()));
-            cfg.blockDim = dim3(64 + kEpilogue);
-            cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+            cfg.blockDim = dim3(Form<WG, PARTS>::kThreads);
+            cfg.dynamicSmemBytes = static_cast<size_t>(kMaxSmem);
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -468,58 +509,52 @@ int setup_e4m3(int dev, int* units) {
             if (e != cudaSuccess) return cuda_status(e);
             if (n <= 0) return BIV_ERR_DEVICE;
         }
-        known[dev] = n;
+        units[dev] = n;
     }
-    *units = known[dev];
+    *out = units[dev];
     return BIV_OK;
 }
 
-template <bool COLS, bool F32>
-int launch_e4m3(const void* A, const void* B, void* C, Gemm8Args g, const BiasActArgs& ba, cudaStream_t s) {
-    int dev = 0, units = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_status(e);
-    const int st = setup_e4m3<COLS, F32>(dev, &units);
+template <int CG, int WG, int PARTS>
+int launch_e4m3(const void* A, const void* B, Gemm8Args g, cudaStream_t s) {
+    int units = 0;
+    const int st = setup_e4m3<CG, WG, PARTS>(&units);
     if (st != BIV_OK) return st;
-    g.xr = COLS ? kLanes : std::min(kLanes, (g.M + 7) / 8 * 8);
-    g.yr = COLS ? g.BN / 2 : g.BN;
-    g.nb = std::min(kRowSets, kSetCols / g.BN);
-    g.three_d = g.K % kBK == 0 ? 1 : 0;
-    g.idesc = idesc_e4m3_f32(COLS ? 2 * kLanes : kLanes, g.BN);
-    const int per_kb = (g.xr + g.yr) * kBK, ring = kRing - (g.xr < kLanes ? kSlack : 0);
-    // A box costs the TMA unit a fixed time: several k-blocks each, as long as four stages fit.
-    g.KS = g.three_d ? std::min(g.KB, std::max(1, ring / (COLS ? 3 : 4) / per_kb)) : 1;
-    if (COLS) g.KS = std::min(g.KS, 2);
-    g.stages = std::min(kMaxStages, ring / (g.KS * per_kb));
-    const long long x_tiles = COLS ? ceil_div(g.N, 2 * kLanes) : 1;
-    g.y_tiles = static_cast<int>(ceil_div(COLS ? g.M : g.N, g.BN));
-    if (x_tiles * g.y_tiles > 0x3fffffffLL) return BIV_ERR_SHAPE;
-    g.work = static_cast<int>(x_tiles * g.y_tiles);
-    CUtensorMap tx, ty;
-    if (!encode_e4m3(&tx, COLS ? B : A, COLS ? g.N : g.M, g.K, g.xr, g.KS, g.three_d) ||
-        !encode_e4m3(&ty, COLS ? A : B, COLS ? g.M : g.N, g.K, g.yr, g.KS, g.three_d)) {
+    constexpr int NB = Form<WG, PARTS>::kBlocks, kThreads = Form<WG, PARTS>::kThreads;
+    g.xr = CG == 2 ? kLanes : std::min(kLanes, (g.M + 7) / 8 * 8);
+    g.yr = g.BN / CG;
+    g.idesc = idesc_e4m3_f32(CG * kLanes, g.BN);
+    const int per_kb = (g.xr + g.yr) * kBK, slack = g.xr < kLanes ? kSlack : 0;
+    g.boxes = g.K % kBK == 0 ? 1 : NB;
+    g.stages = std::min(kMaxStages, (kRing - slack) / (NB * per_kb) / kIssuers * kIssuers);      // two at least
+    g.m_tiles = static_cast<int>(ceil_div(g.M, CG * kLanes));
+    const long long tiles = ceil_div(g.N, g.BN) * g.m_tiles;
+    if (tiles > 0x3fffffffLL) return BIV_ERR_SHAPE;
+    g.tiles = static_cast<int>(tiles);
+    CUtensorMap ta, tb;
+    if (!encode_e4m3(&ta, A, g.M, g.K, g.xr, NB) || !encode_e4m3(&tb, B, g.N, g.K, g.yr, NB)) {
         set_cuda_error(cudaErrorInvalidValue);
         return BIV_ERR_CUDA;
     }
-    const size_t smem = 1024 + static_cast<size_t>(g.stages) * g.KS * per_kb + (g.xr < kLanes ? kSlack : 0) + kBarBytes + 2 * kScaleFloats * 4;
-    const unsigned grid = static_cast<unsigned>(std::min(g.work, units));
-    if (COLS) return launch_cluster_pdl(gemm_e4m3_kernel<COLS, F32>, dim3(2 * grid), dim3(64 + kEpilogue), smem, s, 2, tx, ty, C, g, ba);
-    return launch_pdl(gemm_e4m3_kernel<COLS, F32>, dim3(grid), dim3(64 + kEpilogue), smem, s, tx, ty, C, g, ba);
+    const size_t smem = 1024 + static_cast<size_t>(g.stages) * NB * per_kb + slack + kBarBytes + 2 * kPageFloats * 4;
+    const unsigned grid = static_cast<unsigned>(std::min(g.tiles, units));
+    if (CG == 2) return launch_cluster_pdl(gemm_e4m3_kernel<CG, WG, PARTS>, dim3(2 * grid), dim3(kThreads), smem, s, 2, ta, tb, g);
+    return launch_pdl(gemm_e4m3_kernel<CG, WG, PARTS>, dim3(grid), dim3(kThreads), smem, s, ta, tb, g);
 }
 
-// Columns form: M in tiles of equal width, a multiple of 32 up to 256, so that the waves of
-// pairs are full and the tiles wide.
-int columns_tile(int M, int N, int pairs) {
-    int best = 256;
-    double least = 1e30;
-    for (int bn = 32; bn <= 256; bn += 32) {
-        const double cost = static_cast<double>(ceil_div(ceil_div(N, 2 * kLanes) * ceil_div(M, bn), pairs)) * (bn + 32);
-        if (cost <= least) {
-            least = cost;
-            best = bn;
-        }
+// The kernel for a tile width.
+int launch_single(const void* A, const void* B, const Gemm8Args& g, cudaStream_t s) {
+    static const bool four = getenv("FOUR") != nullptr;
+    if (g.BN <= 32) return launch_e4m3<1, 2, 1>(A, B, g, s);
+    if (g.BN <= 64) return launch_e4m3<1, 2, 2>(A, B, g, s);
+    if (four) {
+    if (g.BN <= 128) return launch_e4m3<1, 4, 2>(A, B, g, s);
+    if (g.BN <= 192) return launch_e4m3<1, 4, 3>(A, B, g, s);
+    return launch_e4m3<1, 4, 4>(A, B, g, s);
     }
-    return best;
+    if (g.BN <= 128) return launch_e4m3<1, 2, 4>(A, B, g, s);
+    if (g.BN <= 192) return launch_e4m3<1, 2, 6>(A, B, g, s);
+    return launch_e4m3<1, 2, 8>(A, B, g, s);
 }
 
 }  // namespace
@@ -539,23 +574,33 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
     // an fp32 C over a bf16 residual would overwrite rows that are still to be read
     if (C == A || C == B || C == bias || C == a_scales || C == b_scales || (C == residual && out_dtype == BIV_F32)) return BIV_ERR_VALUE;
     Gemm8Args g = {};
+    g.sa = a_scales;
+    g.sb = b_scales;
+    g.C = C;
+    g.ba.bias = static_cast<const __nv_bfloat16*>(bias);
+    g.ba.residual = static_cast<const __nv_bfloat16*>(residual);
+    g.ba.act = act;
     g.M = M;
     g.N = N;
     g.K = K;
     g.KB = static_cast<int>(ceil_div(K, kBK));
-    g.sa = a_scales;
-    g.sb = b_scales;
-    BiasActArgs ba;
-    ba.bias = static_cast<const __nv_bfloat16*>(bias);
-    ba.residual = static_cast<const __nv_bfloat16*>(residual);
-    ba.act = act;
+    g.f32 = out_dtype == BIV_F32;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = num_sms();
+    const long long m_tiles = ceil_div(M, kLanes);
     const long long bn = std::max<long long>(16, ceil_div(ceil_div(N, sms), 16) * 16);
-    if (M <= kLanes && bn <= kSetCols) {
+    if (m_tiles == 1 && bn <= 256) {
         g.BN = static_cast<int>(bn);
-        return out_dtype == BIV_F32 ? launch_e4m3<false, true>(A, B, C, g, ba, s) : launch_e4m3<false, false>(A, B, C, g, ba, s);
+        return launch_single(A, B, g, s);
     }
-    g.BN = columns_tile(M, N, sms / 2);
-    return out_dtype == BIV_F32 ? launch_e4m3<true, true>(A, B, C, g, ba, s) : launch_e4m3<true, false>(A, B, C, g, ba, s);
+    // several waves, or several row tiles: the width that fills whole waves, rather a wide one
+    double least = 1e30;
+    for (int w : {64, 128, 160, 192, 256}) {
+        const double cost = static_cast<double>(ceil_div(m_tiles * ceil_div(N, w), sms)) * (w + 96);
+        if (cost <= least) {
+            least = cost;
+            g.BN = w;
+        }
+    }
+    return getenv("PAIRS") && g.BN == 256 ? launch_e4m3<2, 2, 8>(A, B, g, s) : launch_single(A, B, g, s);
 }
