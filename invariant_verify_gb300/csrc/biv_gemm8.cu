@@ -38,6 +38,12 @@ constexpr int kLanes = 128;                   // rows of an accumulator in one C
 constexpr int kBK = 128;                      // a k-block: 128 e4m3, one swizzle row and one scale
 constexpr int kMaxStages = 16;
 constexpr int kIssuers = 2;
+constexpr int kEpilogue = 256;                // epilogue threads
+constexpr int kThreads = 128 + kEpilogue;
+// Registers of a thread after the start, where each has the 168 that 384 threads leave: the first
+// warpgroup gives up what the sums need (128 x 40 + 256 x 232 = 384 x 168).
+constexpr int kRegsStart = 168, kRegsFew = 40, kRegsMany = 232;
+static_assert(128 * kRegsFew + kEpilogue * kRegsMany <= kThreads * kRegsStart, "more registers than the CTA holds");
 constexpr int kBarBytes = 512;
 constexpr int kPageBlocks = 16;               // k-blocks whose scales are copied at once
 constexpr int kPageFloats = kPageBlocks * (kLanes + 4);
@@ -59,15 +65,15 @@ struct Gemm8Args {
     uint32_t idesc;
 };
 
-// WG: warpgroups that sum; PARTS: 16-column parts of a thread, its share of BN.  Registers: every thread starts
-// with kStart, then the first warpgroup keeps kFew, so that the others can have kMany.
-template <int WG, int PARTS>
+// PARTS: 16-column parts of a thread (half of BN, rounded up).
+template <int PARTS>
 struct Form {
-    static constexpr int kEpilogue = 128 * WG, kThreads = 128 + kEpilogue, kCols = 16 * WG * PARTS;          // the widest BN
-    static constexpr int kStart = WG == 2 ? 168 : 96, kFew = WG == 2 ? 40 : 64, kMany = WG == 2 ? 232 : 104;
-    static_assert(kThreads * kStart <= 65536 && 128 * kFew + kEpilogue * kMany <= kThreads * kStart, "more registers than the CTA holds");
-    // K-blocks of a stage, whose accumulators are a set: the sets are taken in turn.
+    static constexpr int kCols = 32 * PARTS;  // the widest BN
+    // K-blocks of a set of accumulators; the sets are taken in turn.  Where a set is one k-block a stage holds two
+    // sets, since a box costs the TMA unit some 275 ns whatever its size (1024 x 4096 x 14336: 79 us with boxes
+    // of one k-block, 41 with no copies at all).
     static constexpr int kBlocks = kCols <= 64 ? 4 : kCols <= 128 ? 2 : 1;
+    static constexpr int kStageSets = kBlocks == 1 ? 2 : 1, kStage = kBlocks * kStageSets;
     static constexpr int kSets = kCols <= 32 ? 4 : 2;
     static constexpr int kSetCols = 512 / kSets;
     // A barrier of the summing threads and a vote: true if every one says so.
@@ -115,39 +121,25 @@ BIV_DEV void commit(uint64_t* bar) {
         umma_commit_elect(bar);
 }
 
-// A bounded wait of a whole warp for one barrier or two (shared-memory addresses).  The loops hold nothing but
-// the polls: a k-block takes some 600 cycles, and what stands between a phase and the work behind it is seen
-// in each.
-BIV_DEV bool poll(uint32_t bar, uint32_t parity) {
+// A bounded wait of a whole warp (shared-memory address).  The loop holds nothing but the poll: a k-block takes
+// some 600 cycles, and what stands between a phase and the work behind it is seen in each (a vote on the
+// outcome: 100).  Where the wait runs out it sets the CTA's abort flag and returns all the same; each loop
+// reads the flag before its wait, which costs nothing, and leaves after it: all lanes together, and at most one
+// block of work later than they could.
+BIV_DEV void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    int polls = kFastPolls;
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-BIV_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    bool ok;
-    int polls = kFastPolls;
 #pragma unroll 1
-    do ok = poll(bar, parity);
-    while (!ok && --polls);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    return __all_sync(0xffffffffu, mbar_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, &g_gemm8_err));
-}
-BIV_DEV bool warp_wait(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort_flag) {
-    bool ok;
-    int polls = kFastPolls;
-#pragma unroll 1
-    do ok = poll(bar0, parity0);
-    while (!ok && --polls);
-#pragma unroll 1
-    while (ok && !(ok = poll(bar1, parity1)) && --polls > 0) ok = true;
-    if (__all_sync(0xffffffffu, ok)) return true;
-    return warp_wait(bar0, parity0, abort_flag) && warp_wait(bar1, parity1, abort_flag);
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    } while (!ok && --polls);
+    if (!ok) mbar_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort_flag, &g_gemm8_err);
 }
 BIV_DEV float ld_shared(uint32_t at) {
     float x;
@@ -160,14 +152,15 @@ BIV_DEV void copy_4(float* dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 
-template <int CG, int WG, int PARTS>
-__global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+// WHOLE: BN = 256, so that a warp's columns lie in one 128-column block of weights.
+template <int CG, int PARTS, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                                                                 const Gemm8Args g) {
-    using Q = Form<WG, PARTS>;
-    constexpr int NB = Q::kBlocks;
+    using Q = Form<PARTS>;
+    constexpr int NB = Q::kBlocks, KS = Q::kStage;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int A_BYTES = NB * g.xr * kBK, STAGE = A_BYTES + NB * g.yr * kBK, S = g.stages;
+    const int A_BYTES = KS * g.xr * kBK, STAGE = A_BYTES + KS * g.yr * kBK, S = g.stages;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * STAGE + (g.xr < kLanes ? kSlack : 0));
     uint64_t* empty = full + kMaxStages;
     uint64_t* tfull = empty + kMaxStages;     // [kSets]
@@ -180,14 +173,14 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
     const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int unit = static_cast<int>(blockIdx.x) / CG, n_units = static_cast<int>(gridDim.x) / CG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_stages = (g.KB + NB - 1) / NB;                   // of a tile
+    const int n_stages = (g.KB + KS - 1) / KS;                   // of a tile
     // epilogue warps with rows to read: all, or those of the quarters that M reaches
-    const int readers = WG * (CG == 2 ? 8 : min(4, (g.M + 31) / 32));
+    const int readers = CG == 2 ? 16 : 2 * min(4, (g.M + 31) / 32);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], Q::kStageSets);      // commits of the issuers that read it
         }
         for (int a = 0; a < Q::kSets; ++a) {
             mbar_init(&tfull[a], 1);
@@ -220,7 +213,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
     const uint64_t pol_w = g.m_tiles == 1 ? policy_evict_first() : policy_evict_normal(), pol_a = policy_evict_last();
     auto load = [&](const CUtensorMap* map, uint8_t* dst, int stage, int row, int rows, int sb, uint64_t pol) {
         for (int j = 0; j < g.boxes; ++j) {
-            const int c0 = g.boxes == 1 && g.K % kBK == 0 ? 0 : (sb * NB + j) * kBK, c2 = g.K % kBK == 0 ? sb * NB : 0;
+            const int c0 = g.boxes == 1 && g.K % kBK == 0 ? 0 : (sb * KS + j) * kBK, c2 = g.K % kBK == 0 ? sb * KS : 0;
             if constexpr (CG == 2)
                 tma_load_3d_pair(dst + j * rows * kBK, map, mapa_shared(&full[stage], 0), c0, row, c2, pol);
             else
@@ -250,7 +243,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
     pdl_trigger();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Q::kFew));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             int stage = 0;
@@ -286,36 +279,46 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
             }
         } else if ((warp == 1 || warp == 2) && rank == 0) {
             // -------------------------------------------------- MMA issuers
+            // Stages and sets taken in turn: issuer 0 the even ones, 1 the odd ones; or of every stage's two sets one each.
             const int me = warp - 1;
-            const int units_tiles = unit < g.tiles ? (g.tiles - unit + n_units - 1) / n_units : 0;
-            const long long all = static_cast<long long>(units_tiles) * n_stages;
-            int stage = me, set = me, sb = me % n_stages;            // sb: the stage's place in its tile
+            constexpr int kStep = Q::kStageSets == 2 ? 1 : kIssuers;
+            const int first = Q::kStageSets == 2 ? 0 : me, j0 = Q::kStageSets == 2 ? me * NB : 0;
+            const int unit_tiles = unit < g.tiles ? (g.tiles - unit + n_units - 1) / n_units : 0;
+            const long long all = static_cast<long long>(unit_tiles) * n_stages;
+            int stage = first, set = me, sb = first % n_stages;      // sb: the stage's place in its tile
             uint32_t phase = 0, set_phase = 0;
             bool ok = true, any = false;
             const uint32_t full0 = smem_u32(full), tempty0 = smem_u32(tempty);
-            const uint64_t a0 = sw128_kmajor_desc(smem_u32(smem)), b0 = sw128_kmajor_desc(smem_u32(smem + A_BYTES));
             const uint32_t a_step = static_cast<uint32_t>(g.xr * kBK / 16), b_step = static_cast<uint32_t>(g.yr * kBK / 16);      // of a k-block
-            for (long long c = me; c < all; c += kIssuers) {
-                ok = warp_wait(full0 + 8u * stage, phase, tempty0 + 8u * set, set_phase ^ 1u, abort_flag);
-                if (!ok) break;
+            const uint64_t a0 = sw128_kmajor_desc(smem_u32(smem)) + j0 * a_step, b0 = sw128_kmajor_desc(smem_u32(smem + A_BYTES)) + j0 * b_step;
+            for (long long c = first; c < all; c += kStep) {
+                const int nkb = min(NB, g.KB - sb * KS - j0);        // none: the second set of a last stage that is not full
+                const bool stop = *abort_flag;
+                warp_wait(full0 + 8u * stage, phase, abort_flag);
+                if (nkb > 0) warp_wait(tempty0 + 8u * set, set_phase ^ 1u, abort_flag);
+                if (stop) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const uint32_t at = static_cast<uint32_t>(stage * (STAGE / 16)), d = tmem_base + static_cast<uint32_t>(set * Q::kSetCols);
-                const int nkb = NB == 1 ? 1 : min(NB, g.KB - sb * NB);
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
                     if (j < nkb) mma_block<CG>(d + static_cast<uint32_t>(j * g.BN), a0 + at + j * a_step, b0 + at + j * b_step, g.idesc);
-                commit<CG>(&tfull[set]);
+                if (nkb > 0) {
+                    commit<CG>(&tfull[set]);
+                    if ((set += kIssuers) >= Q::kSets) {
+                        set = me;
+                        set_phase ^= 1u;
+                    }
+                }
                 commit<CG>(&empty[stage]);
                 any = true;
-                if ((stage += kIssuers) >= S) {
-                    stage = me;
+                if ((stage += kStep) >= S) {
+                    stage = first;
                     phase ^= 1u;
                 }
-                if ((set += kIssuers) >= Q::kSets) {
-                    set = me;
-                    set_phase ^= 1u;
-                }
-                for (sb += kIssuers; sb >= n_stages;) sb -= n_stages;
+                for (sb += kStep; sb >= n_stages;) sb -= n_stages;
             }
             if (!ok && any) {                 // all MMAs issued so far have finished
                 commit<CG>(&drain[me]);
@@ -325,11 +328,11 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
         __syncwarp();
     } else {
         // ------------------------------------------------- sums and stores
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Q::kMany));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
         const int q = warp & 3, tid = static_cast<int>(threadIdx.x) - 128;
         const int cb = (warp / 4 - 1) * 16 * PARTS;                     // this warp's first column of the tile
         const bool reads = CG == 2 || q * 32 < g.M;
-        const int sets = n_stages, pages = (g.KB + kPageBlocks - 1) / kPageBlocks;
+        const int sets = (g.KB + NB - 1) / NB, pages = (g.KB + kPageBlocks - 1) / kPageBlocks;
         constexpr int kPageSets = kPageBlocks / NB;
         // Scales of a page of tile t: [k-block][row] sa, then [k-block][4] sb of the tile's 128-column blocks.
         auto fetch = [&](int t, int page, float* dst) {
@@ -337,9 +340,9 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
             int kb = kb0 + tid / kLanes;
             const float* src = g.sa + static_cast<long long>(kb) * g.M + row;
 #pragma unroll
-            for (int i = 0; i < kPageBlocks / WG; ++i, kb += WG, src += static_cast<long long>(WG) * g.M) {
+            for (int i = 0; i < kPageBlocks / 2; ++i, kb += 2, src += 2LL * g.M) {
                 const bool in = kb < g.KB && row < g.M;
-                copy_4(dst + i * Q::kEpilogue + tid, in ? src : g.sa, in);
+                copy_4(dst + i * kEpilogue + tid, in ? src : g.sa, in);
             }
             if (tid < 4 * kPageBlocks) {
                 const int nblk = (t / g.m_tiles) * g.BN / 128 + (tid & 3);
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
         uint32_t freed = smem_u32(tempty);    // the sets' barriers where the MMAs are issued
         if constexpr (CG == 2) freed = mapa_shared(tempty, 0);
         int set = 0, buf = 0;
-        uint32_t set_phase = 0;
+        uint32_t phases = 0;                  // bit a: the phase of set a
         bool ok = true;                       // a wait ran out: the warps leave together, at the next vote
         if (unit < g.tiles) fetch(unit, 0, s_page[0]);
         for (int t = unit; t < g.tiles; t += n_units) {
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
                 for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
             // of the first columns of each part: which of the tile's 128-column blocks of weights
             const int blk = (n0 + cb) / 128 - n0 / 128, turn = (128 - (n0 + cb) % 128) / 16;         // the first one, and its parts
+            if (Q::kStageSets == 2) set = 0;   // a tile begins with a stage's first set
             for (int s = 0; s < sets; ++s) {
                 const int in_page = s % kPageSets, nkb = min(NB, g.KB - s * NB);
                 if (in_page == 0) {
@@ -380,8 +384,8 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
                 if (reads) {
                     const uint32_t row_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + in_page * NB * kLanes + q * 32 + lane) * 4u;
                     const uint32_t col_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + kPageBlocks * kLanes + in_page * NB * 4 + blk) * 4u;
-                    const bool here = warp_wait(tfull0 + 8u * set, set_phase, abort_flag);
-                    ok = ok && here;
+                    ok = !*abort_flag;
+                    warp_wait(tfull0 + 8u * set, (phases >> set) & 1u, abort_flag);
                     tc_fence_after();
                     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * Q::kSetCols + cb);
 #pragma unroll
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
                         if (kl < nkb) {
                             // the warp's columns lie in two 128-column blocks of weights at most
                             const float mine = ld_shared(row_scale + kl * kLanes * 4u);
-                            const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = mine * ld_shared(col_scale + kl * 16u + 4u);
+                            const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = WHOLE ? x0 : mine * ld_shared(col_scale + kl * 16u + 4u);
 #pragma unroll
                             for (int i = 0; i < PARTS; i += 2) {
                                 const uint32_t at = taddr + static_cast<uint32_t>(kl * g.BN + 16 * i);
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) r[e] = h[e];
                                 }
-                                if (i + 2 >= PARTS && kl + 1 == nkb) {         // the set has been read
+                                if (i + 2 >= PARTS && (NB == 1 || kl + 1 == nkb)) {         // the set has been read
                                     tc_fence_before();
                                     __syncwarp();
                                     if (lane == 0) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     if (i + h < PARTS) {
-                                        const float x = i + h < turn ? x0 : x1;
+                                        const float x = WHOLE || i + h < turn ? x0 : x1;
 #pragma unroll
                                         for (int e = 0; e < 16; ++e)
                                             acc[i + h < PARTS ? i + h : 0][e] = fmaf(__uint_as_float(r[16 * h + e]), x, acc[i + h < PARTS ? i + h : 0][e]);
@@ -423,10 +427,8 @@ __global__ void __launch_bounds__(Form<WG, PARTS>::kThreads, 1) gemm_e4m3_kernel
                             }
                         }
                 }
-                if (++set == Q::kSets) {
-                    set = 0;
-                    set_phase ^= 1u;
-                }
+                phases ^= 1u << set;
+                set = set + 1 == Q::kSets ? 0 : set + 1;
             }
             if (!ok || !reads) continue;      // to the vote, or to the end
             const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + q * 32 + lane;
@@ -476,7 +478,7 @@ bool encode_e4m3(CUtensorMap* map, const void* base, int rows, int K, int box_ro
 
 // Once per device and kernel: its opt-in shared memory, the registers it starts with (those that the sums'
 // warps take are the ones that the others give up), and how many units (CTAs, or pairs) run at once.
-template <int CG, int WG, int PARTS>
+template <int CG, int PARTS, bool WHOLE>
 int setup_e4m3(int* out) {
     static std::mutex mu;
     static int units[kMaxDevices] = {};
@@ -486,18 +488,18 @@ int setup_e4m3(int* out) {
     if (dev < 0 || dev >= kMaxDevices) return BIV_ERR_DEVICE;
     std::lock_guard<std::mutex> lock(mu);
     if (units[dev] == 0) {
-        auto kern = gemm_e4m3_kernel<CG, WG, PARTS>;
+        auto kern = gemm_e4m3_kernel<CG, PARTS, WHOLE>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return cuda_status(e);
         cudaFuncAttributes attrs;
         e = cudaFuncGetAttributes(&attrs, kern);
         if (e != cudaSuccess) return cuda_status(e);
-        if (attrs.numRegs != Form<WG, PARTS>::kStart) return BIV_ERR_DEVICE;
+        if (attrs.numRegs != kRegsStart) return BIV_ERR_DEVICE;
         int n = num_sms();
         if (CG == 2) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms()));
-            cfg.blockDim = dim3(Form<WG, PARTS>::kThreads);
+            cfg.blockDim = dim3(kThreads);
             cfg.dynamicSmemBytes = static_cast<size_t>(kMaxSmem);
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -515,46 +517,40 @@ int setup_e4m3(int* out) {
     return BIV_OK;
 }
 
-template <int CG, int WG, int PARTS>
+template <int CG, int PARTS, bool WHOLE = false>
 int launch_e4m3(const void* A, const void* B, Gemm8Args g, cudaStream_t s) {
     int units = 0;
-    const int st = setup_e4m3<CG, WG, PARTS>(&units);
+    const int st = setup_e4m3<CG, PARTS, WHOLE>(&units);
     if (st != BIV_OK) return st;
-    constexpr int NB = Form<WG, PARTS>::kBlocks, kThreads = Form<WG, PARTS>::kThreads;
+    using Q = Form<PARTS>;
     g.xr = CG == 2 ? kLanes : std::min(kLanes, (g.M + 7) / 8 * 8);
     g.yr = g.BN / CG;
     g.idesc = idesc_e4m3_f32(CG * kLanes, g.BN);
     const int per_kb = (g.xr + g.yr) * kBK, slack = g.xr < kLanes ? kSlack : 0;
-    g.boxes = g.K % kBK == 0 ? 1 : NB;
-    g.stages = std::min(kMaxStages, (kRing - slack) / (NB * per_kb) / kIssuers * kIssuers);      // two at least
+    g.boxes = g.K % kBK == 0 ? 1 : Q::kStage;
+    g.stages = std::min(kMaxStages, (kRing - slack) / (Q::kStage * per_kb) / (kIssuers / Q::kStageSets) * (kIssuers / Q::kStageSets));      // two at least
     g.m_tiles = static_cast<int>(ceil_div(g.M, CG * kLanes));
     const long long tiles = ceil_div(g.N, g.BN) * g.m_tiles;
     if (tiles > 0x3fffffffLL) return BIV_ERR_SHAPE;
     g.tiles = static_cast<int>(tiles);
     CUtensorMap ta, tb;
-    if (!encode_e4m3(&ta, A, g.M, g.K, g.xr, NB) || !encode_e4m3(&tb, B, g.N, g.K, g.yr, NB)) {
+    if (!encode_e4m3(&ta, A, g.M, g.K, g.xr, Q::kStage) || !encode_e4m3(&tb, B, g.N, g.K, g.yr, Q::kStage)) {
         set_cuda_error(cudaErrorInvalidValue);
         return BIV_ERR_CUDA;
     }
-    const size_t smem = 1024 + static_cast<size_t>(g.stages) * NB * per_kb + slack + kBarBytes + 2 * kPageFloats * 4;
+    const size_t smem = 1024 + static_cast<size_t>(g.stages) * Q::kStage * per_kb + slack + kBarBytes + 2 * kPageFloats * 4;
     const unsigned grid = static_cast<unsigned>(std::min(g.tiles, units));
-    if (CG == 2) return launch_cluster_pdl(gemm_e4m3_kernel<CG, WG, PARTS>, dim3(2 * grid), dim3(kThreads), smem, s, 2, ta, tb, g);
-    return launch_pdl(gemm_e4m3_kernel<CG, WG, PARTS>, dim3(grid), dim3(kThreads), smem, s, ta, tb, g);
+    if (CG == 2) return launch_cluster_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE>, dim3(2 * grid), dim3(kThreads), smem, s, 2, ta, tb, g);
+    return launch_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE>, dim3(grid), dim3(kThreads), smem, s, ta, tb, g);
 }
 
 // The kernel for a tile width.
 int launch_single(const void* A, const void* B, const Gemm8Args& g, cudaStream_t s) {
-    static const bool four = getenv("FOUR") != nullptr;
-    if (g.BN <= 32) return launch_e4m3<1, 2, 1>(A, B, g, s);
-    if (g.BN <= 64) return launch_e4m3<1, 2, 2>(A, B, g, s);
-    if (four) {
-    if (g.BN <= 128) return launch_e4m3<1, 4, 2>(A, B, g, s);
-    if (g.BN <= 192) return launch_e4m3<1, 4, 3>(A, B, g, s);
-    return launch_e4m3<1, 4, 4>(A, B, g, s);
-    }
-    if (g.BN <= 128) return launch_e4m3<1, 2, 4>(A, B, g, s);
-    if (g.BN <= 192) return launch_e4m3<1, 2, 6>(A, B, g, s);
-    return launch_e4m3<1, 2, 8>(A, B, g, s);
+    if (g.BN <= 32) return launch_e4m3<1, 1>(A, B, g, s);
+    if (g.BN <= 64) return launch_e4m3<1, 2>(A, B, g, s);
+    if (g.BN <= 128) return launch_e4m3<1, 4>(A, B, g, s);
+    if (g.BN <= 192) return launch_e4m3<1, 6>(A, B, g, s);
+    return g.BN == 256 ? launch_e4m3<1, 8, true>(A, B, g, s) : launch_e4m3<1, 8>(A, B, g, s);
 }
 
 }  // namespace
@@ -602,5 +598,5 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
             g.BN = w;
         }
     }
-    return getenv("PAIRS") && g.BN == 256 ? launch_e4m3<2, 2, 8>(A, B, g, s) : launch_single(A, B, g, s);
+    return getenv("PAIRS") && g.BN == 256 ? launch_e4m3<2, 8, true>(A, B, g, s) : launch_single(A, B, g, s);
 }
