@@ -25,7 +25,6 @@
 // CG = 1: a CTA per tile of 128 rows.  CG = 2: a pair per tile of 256 (cta_group::2): each CTA copies its
 // 128 rows of A and half of the BN rows of B, the even one issues the MMAs.
 #include <algorithm>
-#include <cstdlib>
 
 #include "biv_act.cuh"
 
@@ -212,8 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
     // weights: read once, or by the CTAs of all rows at about the same time; activations: by every CTA
     const uint64_t pol_w = g.m_tiles == 1 ? policy_evict_first() : policy_evict_normal(), pol_a = policy_evict_last();
     auto load = [&](const CUtensorMap* map, uint8_t* dst, int stage, int row, int rows, int sb, uint64_t pol) {
+        const bool whole = g.K % kBK == 0;
         for (int j = 0; j < g.boxes; ++j) {
-            const int c0 = g.boxes == 1 && g.K % kBK == 0 ? 0 : (sb * KS + j) * kBK, c2 = g.K % kBK == 0 ? sb * KS : 0;
+            const int c0 = whole ? 0 : (sb * KS + j) * kBK, c2 = whole ? sb * KS : 0;
             if constexpr (CG == 2)
                 tma_load_3d_pair(dst + j * rows * kBK, map, mapa_shared(&full[stage], 0), c0, row, c2, pol);
             else
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
             for (int i = 0; i < PARTS; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-            // of the first columns of each part: which of the tile's 128-column blocks of weights
+            // the warp's columns lie in two 128-column blocks of weights at most: the first one, and its parts
             const int blk = (n0 + cb) / 128 - n0 / 128, turn = (128 - (n0 + cb) % 128) / 16;         // the first one, and its parts
             if (Q::kStageSets == 2) set = 0;   // a tile begins with a stage's first set
             for (int s = 0; s < sets; ++s) {
@@ -391,7 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
 #pragma unroll
                     for (int kl = 0; kl < NB; ++kl)
                         if (kl < nkb) {
-                            // the warp's columns lie in two 128-column blocks of weights at most
                             const float mine = ld_shared(row_scale + kl * kLanes * 4u);
                             const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = WHOLE ? x0 : mine * ld_shared(col_scale + kl * 16u + 4u);
 #pragma unroll
@@ -598,5 +597,7 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
             g.BN = w;
         }
     }
-    return getenv("PAIRS") && g.BN == 256 ? launch_e4m3<2, 8, true>(A, B, g, s) : launch_single(A, B, g, s);
+    // Pairs take B out of L2 once for 256 rows, where that pads M no further: 1023 x 14336 x 4096: 68.7 us (single
+    // CTAs: 72.2), 1024 x 4096 x 14336: 67.2 (71.7); but 320 x 128256 x 4096, with 512 rows for 384: 360 (267).
+    return g.BN == 256 && m_tiles % 2 == 0 ? launch_e4m3<2, 8, true>(A, B, g, s) : launch_single(A, B, g, s);
 }

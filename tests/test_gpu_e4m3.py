@@ -90,7 +90,7 @@ def product(A, Bm, out, **kw):
 # both forms; widths of one tile, of several, of a last one that is not full; k-blocks that fill sets and stages
 # and that do not; K that is no multiple of 128
 SHAPES = [(1, 8, 16), (1, 64, 128), (3, 136, 272), (8, 6144, 1024), (31, 200, 640), (33, 4096, 384), (64, 2048, 5120), (100, 1000, 896),
-          (128, 256, 2048), (129, 256, 128), (160, 136, 208), (255, 1024, 1024), (300, 520, 1152), (320, 2560, 512), (513, 264, 400)]
+          (128, 256, 2048), (129, 256, 128), (160, 136, 208), (255, 1024, 1024), (300, 520, 1152), (320, 2560, 512), (513, 264, 400), (500, 28672, 144)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -129,12 +129,13 @@ def test_gemm_onto_its_residual(M):
     assert same_bits(x, want)
 
 
-@pytest.mark.parametrize("N,K", [(520, 1040), (4096, 1408)])
+# 28672: 256 columns a tile, pairs of CTAs where the number of 128-row tiles is even
+@pytest.mark.parametrize("N,K", [(520, 1040), (4096, 1408), (28672, 400)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_gemm_rows_do_not_depend_on_m(N, K, out):
     A, Bm, bias, res = matrices(600, N, K, 9)
     full = product(A, Bm, out, bias=bias.cuda(), residual=res.cuda())
-    for M in (1, 2, 7, 33, 64, 127, 128, 129, 161, 256, 257, 333):
+    for M in (1, 2, 7, 33, 64, 127, 128, 129, 161, 256, 257, 333, 512):
         for first in (0, 600 - M):
             part = (A[0][first:first + M], A[1][:, first:first + M].contiguous(), None)
             got = product(part, Bm, out, bias=bias.cuda(), residual=res[first:first + M].cuda())
