@@ -130,7 +130,8 @@ def _binding(lib):
                       RuntimeWarning, stacklevel=3)
         return _NoBinding()
     _biv_torch.bind(*(C.cast(getattr(lib, "biv_" + n), C.c_void_p).value for n in (
-        "rope_kv_write_paged", "decode_attn_paged", "gemm_bias_act", "softmax", "verify_sample")))
+        "rope_kv_write_paged", "decode_attn_paged", "gemm_bias_act", "softmax", "verify_sample", "quant_e4m3", "gemm_e4m3",
+        "rope_kv_write_paged_e4m3", "decode_attn_paged_e4m3")))
     return _biv_torch
 
 
@@ -527,6 +528,8 @@ def biv_quant_e4m3(x, q, scales, block_rows: int = 1, stream=None) -> None:
     """q (float8_e4m3fn) and scales of x (bf16; rows may be strided): block_rows 1 for activations
     (scales fp32 [ceil(K/128), rows]), 128 for weights ([ceil(rows/128), ceil(K/128)])."""
     fn = "biv_quant_e4m3"
+    if stream is None and _done(fn, (_fast or _load_fast()).quant_e4m3(x, q, scales, block_rows)):
+        return
     rows, K = q.shape
     _int32(fn, rows, K, block_rows)
     if x.dtype is not _BF16 or x.shape != (rows, K):
@@ -548,6 +551,8 @@ def biv_gemm_e4m3(A, a_scales, B, b_scales, C_out, bias=None, residual=None, act
     """C = act(A B^T + bias) + residual of matrices that biv_quant_e4m3 gave; C_out (bf16 or fp32)
     may be the bf16 residual itself."""
     fn = "biv_gemm_e4m3"
+    if stream is None and act in ACTS and _done(fn, (_fast or _load_fast()).gemm_e4m3(A, a_scales, B, b_scales, C_out, bias, residual, ACTS[act])):
+        return
     M, K = A.shape
     N = B.shape[0]
     _int32(fn, M, N, K)
@@ -583,10 +588,13 @@ def _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
 def biv_rope_kv_write_paged_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot,
                                  row_pos, theta: float, K: int, rows_keep=None, stream=None) -> None:
     fn = "biv_rope_kv_write_paged_e4m3"
+    if stream is None and rows_keep is None and _done(fn, (_fast or _load_fast()).rope_kv_write_paged_e4m3(
+            qkv, q_out, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot, row_pos, theta, K)):
+        return
     rows = W, Hq, hd = q_out.shape
     table = n_slots, max_pages = page_table.shape
-    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
     _int32(fn, W, K, Hq, hd, n_slots, max_pages)
+    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
     _dense(fn, _BF16, (qkv, q_out), ((W, (Hq + 2 * Hkv) * hd), rows), "qkv q_out")
     _dense(fn, _I32, (page_table, row_slot, row_pos, rows_keep), (table, (W,), (W,), (W // max(K, 1),)),
            "page_table row_slot row_pos rows_keep")
@@ -602,10 +610,13 @@ def biv_rope_kv_write_paged_e4m3(qkv, q_out, k_pages, v_pages, k_scales, v_scale
 def biv_decode_attn_paged_e4m3(q, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot, row_pos, o,
                                rows_per_group: int, workspace, stream=None) -> None:
     fn = "biv_decode_attn_paged_e4m3"
+    if stream is None and _done(fn, (_fast or _load_fast()).decode_attn_paged_e4m3(
+            q, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table, row_slot, row_pos, o, rows_per_group, workspace)):
+        return
     rows = W, Hq, hd = q.shape
     table = n_slots, max_pages = page_table.shape
-    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
     _int32(fn, W, rows_per_group, Hq, hd, n_slots, max_pages)
+    n_pages, Hkv, page_size, tail = _held(fn, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, n_slots, hd)
     _dense(fn, _BF16, (q, o), (rows, rows), "q o")
     _dense(fn, _I32, (page_table, row_slot, row_pos), (table, (W,), (W,)), "page_table row_slot row_pos")
     _dense(fn, workspace.dtype, (workspace,), (workspace.shape,), "workspace")

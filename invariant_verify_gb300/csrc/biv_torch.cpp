@@ -22,6 +22,7 @@ namespace {
 constexpr auto kBF16 = c10::ScalarType::BFloat16;
 constexpr auto kF32 = c10::ScalarType::Float;
 constexpr auto kI32 = c10::ScalarType::Int;
+constexpr auto kE4M3 = c10::ScalarType::Float8_e4m3fn;
 
 // Entry points of the loaded library, in the order in which bind() takes them.
 struct {
@@ -30,6 +31,10 @@ struct {
     decltype(&biv_gemm_bias_act) gemm_bias_act;
     decltype(&biv_softmax) softmax;
     decltype(&biv_verify_sample) verify_sample;
+    decltype(&biv_quant_e4m3) quant_e4m3;
+    decltype(&biv_gemm_e4m3) gemm_e4m3;
+    decltype(&biv_rope_kv_write_paged_e4m3) rope_kv_write_paged_e4m3;
+    decltype(&biv_decode_attn_paged_e4m3) decode_attn_paged_e4m3;
 } g_lib;
 
 // One call's arguments: every look at them may find that the call is not for this file.
@@ -212,11 +217,111 @@ PyObject* verify_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// Addresses of the five entry points of the library that abi.py has loaded.
+// x (dense), q, scales, block_rows
+PyObject* quant_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return answer(a, n, 4, [](Args& x) -> long {
+        const at::Tensor* q = x.tensor(1, kE4M3, 2);
+        if (!x.ok) return -1;
+        const int64_t rows = x.size(q, 0), K = x.size(q, 1), groups = (K + 127) / 128;
+        const int block = x.integer(3);
+        void* in = x.data(0, kBF16, {rows, K});
+        void* scales = block == 1 ? x.data(2, kF32, {groups, rows}) : x.data(2, kF32, {(rows + 127) / 128, groups});
+        if (!x.ok) return -1;
+        const biv_stream_t s = x.stream();
+        void* q_at = q->data_ptr();
+        return unlocked([&] { return g_lib.quant_e4m3(in, K, rows, K, block, q_at, static_cast<float*>(scales), s); });
+    });
+}
+
+// A, a_scales, B, b_scales, C, bias, residual, act (its number)
+PyObject* gemm_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return answer(a, n, 8, [](Args& x) -> long {
+        const at::Tensor *A = x.tensor(0, kE4M3, 2), *B = x.tensor(2, kE4M3, 2), *out = x.tensor(4);
+        if (!x.ok) return -1;
+        const int64_t M = x.size(A, 0), K = x.size(A, 1), N = x.size(B, 0), groups = (K + 127) / 128;
+        const c10::ScalarType type = out->scalar_type();
+        if (B->size(1) != K || (type != kBF16 && type != kF32)) return -1;
+        void *sa = x.data(1, kF32, {groups, M}), *sb = x.data(3, kF32, {(N + 127) / 128, groups}), *C = x.data(4, type, {M, N});
+        void *bias = x.data_or_none(5, kBF16, {N}), *residual = x.data_or_none(6, kBF16, {M, N});
+        const int act = x.integer(7);
+        if (!x.ok) return -1;
+        const biv_stream_t s = x.stream();
+        void *A_at = A->data_ptr(), *B_at = B->data_ptr();
+        return unlocked([&] {
+            return g_lib.gemm_e4m3(A_at, static_cast<float*>(sa), B_at, static_cast<float*>(sb), bias, residual, C, type == kF32 ? BIV_F32 : BIV_BF16,
+                                   act, M, N, K, s);
+        });
+    });
+}
+
+// A cache in e4m3 from argument i on: k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, page_table.
+struct Held {
+    void* at[6];
+    const int32_t* table;
+    int64_t n_pages, Hkv, page, n_slots, max_pages, tail;
+
+    Held(Args& x, int i, int64_t hd) {
+        const at::Tensor *k = x.tensor(i, kE4M3, 4), *ring = x.tensor(i + 4, kBF16, 4), *t = x.tensor(i + 6, kI32, 2);
+        n_pages = x.size(k, 0), Hkv = x.size(k, 1), page = x.size(k, 2);
+        tail = x.size(ring, 2), n_slots = x.size(t, 0), max_pages = x.size(t, 1);
+        for (int p = 0; p < 2; ++p) {
+            at[p] = x.data(i + p, kE4M3, {n_pages, Hkv, page, hd});
+            at[2 + p] = x.data(i + 2 + p, kBF16, {n_pages, Hkv, page / 16});
+            at[4 + p] = x.data(i + 4 + p, kBF16, {n_slots, Hkv, tail, hd});
+        }
+        table = x.ok ? static_cast<const int32_t*>(t->data_ptr()) : nullptr;
+    }
+};
+
+// qkv, q_out, the cache (7), row_slot, row_pos, theta, K
+PyObject* rope_kv_write_paged_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return answer(a, n, 13, [](Args& x) -> long {
+        const at::Tensor* q = x.tensor(1, kBF16, 3);
+        if (!x.ok) return -1;
+        const int64_t W = x.size(q, 0), Hq = x.size(q, 1), hd = x.size(q, 2);
+        const Held c(x, 2, hd);
+        if (!x.ok) return -1;
+        void *qkv = x.data(0, kBF16, {W, (Hq + 2 * c.Hkv) * hd}), *slot = x.data(9, kI32, {W}), *pos = x.data(10, kI32, {W});
+        const float theta = x.number(11);
+        const int K = x.integer(12);
+        if (!x.ok) return -1;
+        const biv_stream_t s = x.stream();
+        void* q_at = q->data_ptr();
+        return unlocked([&] {
+            return g_lib.rope_kv_write_paged_e4m3(qkv, q_at, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4], c.at[5], c.table, static_cast<int32_t*>(slot),
+                                                  static_cast<int32_t*>(pos), nullptr, W, K, Hq, c.Hkv, hd, c.n_slots, c.max_pages, c.n_pages, c.page,
+                                                  c.tail, theta, s);
+        });
+    });
+}
+
+// q, the cache (7), row_slot, row_pos, o, rows_per_group, workspace
+PyObject* decode_attn_paged_e4m3(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return answer(a, n, 13, [](Args& x) -> long {
+        const at::Tensor *q = x.tensor(0, kBF16, 3), *ws = x.tensor(12);
+        if (!x.ok || !ws->is_contiguous()) return -1;
+        const int64_t W = x.size(q, 0), Hq = x.size(q, 1), hd = x.size(q, 2);
+        const Held c(x, 1, hd);
+        if (!x.ok) return -1;
+        void *slot = x.data(8, kI32, {W}), *pos = x.data(9, kI32, {W}), *o = x.data(10, kBF16, {W, Hq, hd});
+        const int rpg = x.integer(11);
+        if (!x.ok) return -1;
+        const biv_stream_t s = x.stream();
+        void *q_at = q->data_ptr(), *ws_at = ws->data_ptr();
+        const size_t ws_bytes = ws->nbytes();
+        return unlocked([&] {
+            return g_lib.decode_attn_paged_e4m3(q_at, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4], c.at[5], c.table, static_cast<int32_t*>(slot),
+                                                static_cast<int32_t*>(pos), o, W, rpg, Hq, c.Hkv, hd, c.n_slots, c.max_pages, c.n_pages, c.page, c.tail,
+                                                ws_at, ws_bytes, s);
+        });
+    });
+}
+
+// Addresses of the nine entry points of the library that abi.py has loaded.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* at[5];
-    if (n != 5) return PyErr_Format(PyExc_TypeError, "five addresses");
-    for (int i = 0; i < 5; ++i) {
+    void* at[9];
+    if (n != 9) return PyErr_Format(PyExc_TypeError, "nine addresses");
+    for (int i = 0; i < 9; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -225,12 +330,16 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_lib.gemm_bias_act = reinterpret_cast<decltype(&biv_gemm_bias_act)>(at[2]);
     g_lib.softmax = reinterpret_cast<decltype(&biv_softmax)>(at[3]);
     g_lib.verify_sample = reinterpret_cast<decltype(&biv_verify_sample)>(at[4]);
+    g_lib.quant_e4m3 = reinterpret_cast<decltype(&biv_quant_e4m3)>(at[5]);
+    g_lib.gemm_e4m3 = reinterpret_cast<decltype(&biv_gemm_e4m3)>(at[6]);
+    g_lib.rope_kv_write_paged_e4m3 = reinterpret_cast<decltype(&biv_rope_kv_write_paged_e4m3)>(at[7]);
+    g_lib.decode_attn_paged_e4m3 = reinterpret_cast<decltype(&biv_decode_attn_paged_e4m3)>(at[8]);
     Py_RETURN_NONE;
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(rope_kv_write_paged), FAST(decode_attn_paged), FAST(gemm_bias_act), FAST(softmax), FAST(verify_sample),
-                          FAST(bind), {nullptr, nullptr, 0, nullptr}};
+                          FAST(quant_e4m3), FAST(gemm_e4m3), FAST(rope_kv_write_paged_e4m3), FAST(decode_attn_paged_e4m3), FAST(bind), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_biv_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

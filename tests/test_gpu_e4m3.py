@@ -523,3 +523,67 @@ def test_a_step_of_single_tokens_is_a_window():
         outs.append(torch.cat(rows))
     assert same_bits(outs[0], outs[1]) and same_bits(outs[0], outs[2])
     no_error()
+
+
+# ------------------------------------------------- the binding's way and abi.py's
+def calls(seed=0):
+    """name -> arguments, and the indexes of the outputs and of the tensors whose last dimension is theirs to choose."""
+    g = U.gen(seed)
+    b = lambda *shape: U.bf16(g, *shape).cuda()  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    A, Bm, bias, res = matrices(5, 72, 144, seed)
+    x = b(40, 272)
+    cache = Cache(2, 2, 64, 16, 32, 3)
+    for t in (*cache.pages, *cache.scales, *cache.tails):
+        t.view(torch.uint8).zero_()
+    ws = torch.empty(B.biv_decode_attn_paged_workspace_size(2, 4, 64, 3, 16), dtype=torch.uint8, device="cuda")
+    slot, pos = i32([0, 1]), i32([15, 40])
+    return {
+        "biv_quant_e4m3": ([x, torch.zeros(40, 272, device="cuda").to(E.E4M3), torch.zeros(3, 40, device="cuda")], (1, 2), ()),
+        "biv_gemm_e4m3": ([A[0].cuda(), A[1].cuda(), Bm[0].cuda(), Bm[1].cuda(), torch.zeros(5, 72, device="cuda"), bias.cuda(), res.cuda()], (4,), ()),
+        "biv_rope_kv_write_paged_e4m3": ([b(2, 8 * 64), torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"), *cache.args(), slot, pos, 1e4, 1],
+                                         (1, 2, 3, 4, 5, 6, 7), (8,)),
+        "biv_decode_attn_paged_e4m3": ([b(2, 4, 64), *[b(*t.shape).to(t.dtype) for t in cache.args()[:6]], cache.table, slot, pos,
+                                        torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"), 1, ws], (10,), (7, 12)),
+    }
+
+
+NAMES = ["biv_quant_e4m3", "biv_gemm_e4m3", "biv_rope_kv_write_paged_e4m3", "biv_decode_attn_paged_e4m3"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_both_ways_agree(name):
+    def run(**kw):
+        args, out, _ = calls()[name]
+        torch.cuda.synchronize()
+        getattr(B, name)(*args, **kw)
+        torch.cuda.synchronize()
+        no_error()
+        return [raw(args[i]).clone() for i in out]
+
+    direct = run()
+    assert all(bool((x != 0).any()) for x in direct[:2])
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream().cuda_stream):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(direct, run(stream=stream)))
+
+
+@pytest.mark.parametrize("fault", ["type", "shape", "stride", "device"])
+@pytest.mark.parametrize("name", NAMES)
+def test_a_fault_has_its_status(name, fault):
+    good, _, own = calls()[name]
+    for at, x in enumerate(good):
+        if not isinstance(x, torch.Tensor) or at in own:
+            continue
+        if fault == "type":
+            bad, status = x.to(torch.float64), 4
+        elif fault == "device":
+            bad, status = x.cpu(), 7
+        elif fault == "stride":
+            bad, status = torch.zeros(*x.shape, 2, device="cuda").to(x.dtype)[..., 0], 2
+        else:
+            bad, status = torch.zeros(*x.shape[:-1], x.shape[-1] + 16, device="cuda").to(x.dtype), 2
+        args = list(good)
+        args[at] = bad
+        with pytest.raises(B.BivError) as e:
+            getattr(B, name)(*args)
+        assert e.value.status == status, (at, str(e.value))
