@@ -236,13 +236,8 @@ BIV_DEV void ld_held(const uint8_t* p, uint32_t (&r)[N], uint64_t policy) {
 template <int N>
 BIV_DEV void ld_tail(const __nv_bfloat16* p, uint32_t (&r)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * i);
-        r[i] = v.x;
-        r[i + 1] = v.y;
-        r[i + 2] = v.z;
-        r[i + 3] = v.w;
-    }
+    for (int i = 0; i < N; i += 4)
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]) : "l"(p + 2 * i));
 }
 
 // A warp's keys and values of one held step.  Lane (g8, c4): dims [HD / 4 c4, ..) of keys g8 and
@@ -402,29 +397,35 @@ struct HeldRows {
         uint32_t k[2][2 * KS];
 #pragma unroll
         for (int r = 0; r < 2; ++r) ld_tail(kt + (g8 + 8 * r) * HD + HD / 4 * c4, k[r]);
-        uint32_t v[4][KS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ld_tail(vt + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (key0 + 2 * c4 + (i & 1) + 8 * (i >> 1) > tmax) {
-#pragma unroll
-                for (int d = 0; d < KS; ++d) v[i][d] = 0u;
-            }
+        float s4[T][4];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float st[4] = {};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s4[t][e] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KS; j += 2) {
                 const uint4 b = q.bf[t][j / 2][lane];
-                mma_16816(st, k[0][2 * j], k[1][2 * j], k[0][2 * j + 1], k[1][2 * j + 1], b.x, b.y);
-                mma_16816(st, k[0][2 * j + 2], k[1][2 * j + 2], k[0][2 * j + 3], k[1][2 * j + 3], b.z, b.w);
+                mma_16816(s4[t], k[0][2 * j], k[1][2 * j], k[0][2 * j + 1], k[1][2 * j + 1], b.x, b.y);
+                mma_16816(s4[t], k[0][2 * j + 2], k[1][2 * j + 2], k[0][2 * j + 3], k[1][2 * j + 3], b.z, b.w);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int p = pos[t][e & 1];
-                st[e] = (p | (kStep - 1)) == (key0 | (kStep - 1)) && key0 + g8 + 8 * (e >> 1) <= p ? st[e] * scale_log2 : -INFINITY;
+                s4[t][e] = (p | (kStep - 1)) == (key0 | (kStep - 1)) && key0 + g8 + 8 * (e >> 1) <= p ? s4[t][e] * scale_log2 : -INFINITY;
             }
+        }
+        uint32_t v[4][KS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ld_tail(vt + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i]);
+            if (key0 + 2 * c4 + (i & 1) + 8 * (i >> 1) > tmax) {
+#pragma unroll
+                for (int d = 0; d < KS; ++d) v[i][d] = 0u;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float(&st)[4] = s4[t];
             weights(t, st);
             l[t][0] += st[0] + st[2];
             l[t][1] += st[1] + st[3];
@@ -444,7 +445,7 @@ struct HeldRows {
 
     // As RowState::put_ml and DirectKeys::put: maximum, sum and output of every row; bad: rows that met a
     // page id out of range.
-    BIV_DEV void put(float2 (*ml)[kClasses][8], float (*o)[kClasses][8][HD + 4], int cls, const uint32_t (&bad)[T], int lane) const {
+    BIV_DEV void put(float2 (*ml)[kClasses][8], float (*o)[kClasses][8][HD + 4], int cls, const uint32_t (&bad)[T], int rows, int lane) const {
         const int g8 = lane >> 2, c4 = lane & 3;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -457,6 +458,7 @@ struct HeldRows {
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                if (8 * t + 2 * c4 + e >= rows) continue;              // nobody's
                 if (g8 == 0) ml[t][cls][2 * c4 + e] = make_float2(m[t][e], (bad[t] >> e) & 1u ? -INFINITY : s[e]);
 #pragma unroll
                 for (int k = 0; k < KS; k += 2)
@@ -494,7 +496,7 @@ struct __align__(16) HeldSmem {
     float o[T][kClasses][8][HD + 4];       // rows padded against bank conflicts
     HeldQ<HD, T> q;
     float2 ml[T][kClasses][8];
-    int pos[8 * T];
+    int pos[2][8 * T];
     LiveTable table;
 };
 
@@ -506,8 +508,16 @@ BIV_DEV long long held_at(const PagedAttnParams& P, int page, int kvh, int key0)
     return ((static_cast<long long>(page) * P.Hkv + kvh) * P.pt.page_size + (key0 & (P.pt.page_size - 1))) * HD;
 }
 
+// Pages and scales of a class's steps of a split: lane i has its i-th.
+struct HeldSteps {
+    int n;                             // steps of this class
+    int page;
+    uint32_t bad;                      // bit i: the page id of step i is out of range
+    float k_scale, v_scale;
+};
+
 template <int HD, int T>
-__global__ void __launch_bounds__(kHeldThreads, T == 1 ? 4 : T == 2 ? 3 : 2) paged_attn_held_kernel(const PagedAttnParams P, const HeldPools hp) {
+__global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_kernel(const PagedAttnParams P, const HeldPools hp) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     HeldSmem<HD, T>& sm = *reinterpret_cast<HeldSmem<HD, T>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
@@ -517,31 +527,90 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 4 : T == 2 ? 3 : 2) pag
     pdl_wait();
     pdl_trigger();
     I.zero_rows<HD>();
-    AttnItem it;
-    for (bool more = I.first(it); more; more = I.next(it, it)) {
-        const int key_lo = it.split * kSplit, r0 = it.tile * 8 * T;
-        __syncthreads();                           // the item before has been joined
-        // positions and queries of the tile's rows
-        for (int i = tid; i < 8 * T; i += kHeldThreads) {
-            int j, head;
-            row_head(P, r0 + i, j, head);
-            sm.pos[i] = r0 + i < it.rows ? I.pos_of(it.w0 + j) : -1;
+
+    // An item's pages (asked for an item ahead), then its scales and the keys of its first step (asked for during
+    // the last step of the item before).
+    auto pages_of = [&](const AttnItem& it, HeldSteps& st) {
+        const int last = (I.largest_pos(it, it.tile * 8 * T, 8 * T) & ~(kStep - 1)) - 1;      // -1 & ~15 is -16
+        const int nsteps = last < 0 ? 0 : Items::steps_to(last, it.split);
+        st.n = (nsteps - cls + kClasses - 1) / kClasses;
+        st.page = 0;
+        if (lane < st.n)
+            st.page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
+                                 ((it.split * kSplit + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
+    };
+    auto scales_of = [&](const AttnItem& it, HeldSteps& st) {
+        st.bad = bad_pages(P, st.page);
+        if (lane < st.n) {
+            const long long at = held_at<HD>(P, st.page, it.kvh, it.split * kSplit + kStep * (cls + kClasses * lane)) / (kStep * HD);
+            st.k_scale = __bfloat162float(hp.k_scales[at]);
+            st.v_scale = __bfloat162float(hp.v_scales[at]);
         }
-        for (int e = tid; e < 8 * T * (HD / 8); e += kHeldThreads) {
-            const int row = e / (HD / 8), piece = e % (HD / 8);
-            int j, head;
-            row_head(P, r0 + row < it.rows ? r0 + row : 0, j, head);           // rows past the group's read its first row and are never used
-            const uint4 x = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + piece * 8);
-            put_q(sm.q, x, row, piece, P.scale_log2);
+    };
+    auto step_at = [&](const AttnItem& it, const HeldSteps& st, int i) {
+        return held_at<HD>(P, __shfl_sync(0xffffffffu, st.page, i), it.kvh, it.split * kSplit + kStep * (cls + kClasses * i));
+    };
+    constexpr int kPieces = 8 * T * (HD / 8), kMine = (kPieces + kHeldThreads - 1) / kHeldThreads;       // 16-byte pieces of a tile's queries
+    auto queries_of = [&](const AttnItem& it, uint4 (&x)[kMine], int (&row_pos)[1]) {
+        const int r0 = it.tile * 8 * T;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int e = tid + i * kHeldThreads, row = r0 + e / (HD / 8);
+            if (e < kPieces) {
+                int j, head;
+                row_head(P, row < it.rows ? row : 0, j, head);         // rows past the group's read its first row and are never used
+                x[i] = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head) * HD + e % (HD / 8) * 8);
+            }
         }
-        __syncthreads();
+        if (tid < 8 * T) {
+            int j, head;
+            row_head(P, r0 + tid, j, head);
+            row_pos[0] = r0 + tid < it.rows ? I.pos_of(it.w0 + j) : -1;
+        }
+    };
+    auto put_queries = [&](const uint4 (&x)[kMine], const int (&row_pos)[1], int buf) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int e = tid + i * kHeldThreads;
+            if (e < kPieces) put_q(sm.q, x[i], e / (HD / 8), e % (HD / 8), P.scale_log2);
+        }
+        if (tid < 8 * T) sm.pos[buf][tid] = row_pos[0];
+    };
+
+    AttnItem cur, nxt;
+    if (!I.first(cur)) return;
+    HeldSteps steps, next_steps;
+    HeldKeys<HD> keys;
+    {
+        uint4 x[kMine];
+        int row_pos[1];
+        pages_of(cur, steps);
+        queries_of(cur, x, row_pos);
+        scales_of(cur, steps);
+        if (steps.n > 0) {
+            const long long at = step_at(cur, steps, 0);
+            keys.load_k(hp.k + at, g8, c4, policy);
+            keys.load_v(hp.v + at, g8, c4, policy);
+        }
+        put_queries(x, row_pos, 0);
+    }
+    for (int buf = 0;; buf ^= 1) {
+        __syncthreads();                           // the tile's queries and positions are there, the item before has been joined
+        const bool more = I.next(cur, nxt);
+        uint4 next_q[kMine];
+        int next_pos[1];
+        if (more) {
+            pages_of(nxt, next_steps);
+            queries_of(nxt, next_q, next_pos);
+        }
+        const int key_lo = cur.split * kSplit;
         int pos[T][2], last[T][2], tmax = -1, tmin = 0x7fffffff, all = 0x7fffffff;
         float back[T][2];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                pos[t][e] = sm.pos[8 * t + 2 * c4 + e];
+                pos[t][e] = sm.pos[buf][8 * t + 2 * c4 + e];
                 back[t][e] = sm.q.back[t][2 * c4 + e];
                 last[t][e] = pos[t][e] < 0 ? -1 : (pos[t][e] & ~(kStep - 1)) - 1;
                 tmax = max(tmax, pos[t][e]);
@@ -554,68 +623,74 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 4 : T == 2 ? 3 : 2) pag
             tmin = min(tmin, __shfl_xor_sync(0xffffffffu, tmin, d));
             all = min(all, __shfl_xor_sync(0xffffffffu, all, d));
         }
-        if (tmax < key_lo) continue;               // no row of the tile has keys here
-        const int held_last = (tmax & ~(kStep - 1)) - 1;
-        const int nsteps = held_last < 0 ? 0 : Items::steps_to(held_last, it.split);
-        const int my_steps = (nsteps - cls + kClasses - 1) / kClasses;
-        // lane i: page and scales of this class's i-th step
-        int page = 0;
-        uint32_t bad = 0;
-        float ks = 0.0f, vs = 0.0f;
-        if (lane < my_steps)
-            page = P.pt.table[static_cast<long long>(I.slot_of(it.w0)) * P.pt.max_pages +
-                              ((key_lo + kStep * (cls + kClasses * lane)) >> P.pt.page_shift)];
-        bad = bad_pages(P, page);
-        if (lane < my_steps) {
-            const long long s = held_at<HD>(P, page, it.kvh, key_lo + kStep * (cls + kClasses * lane)) / (kStep * HD);
-            ks = __bfloat162float(hp.k_scales[s]);
-            vs = __bfloat162float(hp.v_scales[s]);
-        }
-        HeldKeys<HD> keys;
-        auto at = [&](int i) { return held_at<HD>(P, __shfl_sync(0xffffffffu, page, i), it.kvh, key_lo + kStep * (cls + kClasses * i)); };
-        if (my_steps > 0) {
-            const long long a = at(0);
-            keys.load_k(hp.k + a, g8, c4, policy);
-            keys.load_v(hp.v + a, g8, c4, policy);
-        }
         HeldRows<HD, T> rs;
         rs.clear();
         uint32_t bad_rows[T] = {};
+        // the rows' own blocks that are this class's: first the first of them, in the order of steps
+        const int own1 = tmax < key_lo ? -1 : min(kSteps - 1, (tmax - key_lo) / kStep);
+        int own = max(0, (tmin - key_lo) / kStep);
+        own += (cls - own) & (kClasses - 1);
+        const bool has_own = own <= own1;
+        // what is asked for of the next item: during the last step, but after the own blocks, which need the registers
+        auto next_keys = [&]() {
+            if (more) {
+                scales_of(nxt, next_steps);
+                if (next_steps.n > 0) {
+                    const long long next = step_at(nxt, next_steps, 0);
+                    keys.load_k(hp.k + next, g8, c4, policy);
+                    keys.load_v(hp.v + next, g8, c4, policy);
+                }
+            }
+        };
 #pragma unroll 1
-        for (int i = 0; i < my_steps; ++i) {
+        for (int i = 0; i < steps.n; ++i) {
             const int key0 = key_lo + kStep * (cls + kClasses * i);
-            const bool step_bad = (bad >> i) & 1u;
+            const bool step_bad = (steps.bad >> i) & 1u;
             if (step_bad) {
 #pragma unroll
                 for (int t = 0; t < T; ++t) bad_rows[t] |= (last[t][0] >= key0 ? 1u : 0u) | (last[t][1] >= key0 ? 2u : 0u);
             }
+            // the keys of this class's next step, or of its first step of the next item
             long long next = 0;
-            const bool here = i + 1 < my_steps;
-            rs.step(keys, sm.q, back, __shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i), last, all, step_bad, key0, lane, [&] {
-                if (here) {
-                    next = at(i + 1);
-                    keys.load_k(hp.k + next, g8, c4, policy);
-                }
-            });
-            if (here) keys.load_v(hp.v + next, g8, c4, policy);
+            const bool here = i + 1 < steps.n, there = !here && more && !has_own;
+            bool load = here;
+            rs.step(keys, sm.q, back, __shfl_sync(0xffffffffu, steps.k_scale, i), __shfl_sync(0xffffffffu, steps.v_scale, i), last, all, step_bad, key0, lane,
+                    [&] {
+                        if (here) {
+                            next = step_at(cur, steps, i + 1);
+                        } else if (there) {
+                            scales_of(nxt, next_steps);
+                            load = next_steps.n > 0;
+                            if (load) next = step_at(nxt, next_steps, 0);
+                        }
+                        if (load) keys.load_k(hp.k + next, g8, c4, policy);
+                    });
+            if (load) keys.load_v(hp.v + next, g8, c4, policy);
         }
-        // the rows' own blocks, from the ring
-        const int b1 = min(kSteps - 1, (tmax - key_lo) / kStep);
-        for (int b = max(0, (tmin - key_lo) / kStep); b <= b1; ++b)
-            if ((b & (kClasses - 1)) == cls) {
-                const int key0 = key_lo + kStep * b;
-                const long long a = ((static_cast<long long>(I.slot_of(it.w0)) * P.Hkv + it.kvh) * hp.tail + key0 % hp.tail) * HD;
+        if (has_own) {
+            for (; own <= own1; own += kClasses) {
+                const int key0 = key_lo + kStep * own;
+                const long long a = ((static_cast<long long>(I.slot_of(cur.w0)) * P.Hkv + cur.kvh) * hp.tail + key0 % hp.tail) * HD;
                 rs.own_step(hp.k_tail + a, hp.v_tail + a, sm.q, P.scale_log2, pos, tmax, key0, lane);
             }
-        rs.put(sm.ml, sm.o, cls, bad_rows, lane);
+            next_keys();
+        } else if (steps.n == 0) {
+            next_keys();
+        }
+        const int r0 = cur.tile * 8 * T;
+        rs.put(sm.ml, sm.o, cls, bad_rows, cur.rows - r0, lane);
         __syncthreads();
         for (int x4 = tid; x4 < 8 * T * (HD / 4); x4 += kHeldThreads) {
-            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4, row_pos = sm.pos[row];
+            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4, row_pos = sm.pos[buf][row];
             if (row_pos < key_lo) continue;
             int j, head;
             row_head(P, r0 + row, j, head);
-            join_row<HD>(P, sm.o[row / 8], sm.ml[row / 8], row % 8, d, row_pos, static_cast<long long>(it.w0 + j) * P.Hq + it.kvh * P.G + head, it.split);
+            join_row<HD>(P, sm.o[row / 8], sm.ml[row / 8], row % 8, d, row_pos, static_cast<long long>(cur.w0 + j) * P.Hq + cur.kvh * P.G + head, cur.split);
         }
+        if (!more) break;
+        put_queries(next_q, next_pos, buf ^ 1);    // nobody reads this item's any more
+        cur = nxt;
+        steps = next_steps;
     }
 }
 
@@ -631,7 +706,7 @@ int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
     });
     if (st != BIV_OK) return st;
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg, tiles = (static_cast<long long>(P.rpg) * P.G + 8 * T - 1) / (8 * T);
-    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, (T == 1 ? 4LL : T == 2 ? 3LL : 2LL) * num_sms());
+    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, (T == 1 ? 3LL : 2LL) * num_sms());
     return launch_pdl(paged_attn_held_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(kHeldThreads), sizeof(HeldSmem<HD, T>), s, P, hp);
 }
 
