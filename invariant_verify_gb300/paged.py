@@ -17,6 +17,10 @@ its pages lie.
 Projections may carry a bias (``l{l}.bqkv``, ``l{l}.bo``, ``l{l}.bdown`` beside the
 weights of ``synth.decoder_weights``); the residual is added in the epilogues of
 the two projections that end on it.
+
+Either half of a step's bytes may be held in 8 bits: the cache (a pool with a ``tail``) and
+any of the weights (the verifier's ``held``).  The rows' independence of their window,
+neighbours, drafts and pages stays.
 """
 from __future__ import annotations
 
@@ -33,14 +37,28 @@ class PagePool:
     [0, length); ``release`` takes a slot's pages back.  Both copy the slot's row
     to the device on the current stream and raise before anything has changed if
     the pool or the table is too small.
+
+    With ``tail`` (a multiple of 16, or None) the pages are e4m3 with a bf16 scale for 16
+    positions and a head (``k_scales``, ``v_scales``), and the last ``tail`` positions
+    of a slot lie in bf16 rings (``k_tail``, ``v_tail``).
     """
 
     def __init__(self, n_pages: int, page_size: int, layers: int, Hkv: int, hd: int, n_slots: int, max_pages: int,
-                 device="cuda"):
+                 device="cuda", tail: int | None = None):
         shape = (n_pages, Hkv, page_size, hd)
-        self.page_size, self.max_pages = page_size, max_pages
-        self.k = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(layers)]
-        self.v = [torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(layers)]
+        self.page_size, self.max_pages, self.tail = page_size, max_pages, tail
+        if tail is not None and (tail < 16 or tail % 16 or page_size % 16):
+            raise ValueError(f"a cache in e4m3 needs a tail and pages of multiples of 16 positions, not {tail} and {page_size}")
+
+        def pools(shape, dtype=torch.bfloat16):
+            size = torch.empty(0, dtype=dtype).element_size()
+            return [torch.zeros((*shape[:-1], shape[-1] * size), dtype=torch.uint8, device=device).view(dtype) for _ in range(layers)]
+
+        dtype = torch.bfloat16 if tail is None else torch.float8_e4m3fn
+        self.k, self.v = pools(shape, dtype), pools(shape, dtype)
+        if tail is not None:
+            self.k_scales, self.v_scales = (pools((n_pages, Hkv, page_size // 16)) for _ in range(2))
+            self.k_tail, self.v_tail = (pools((n_slots, Hkv, tail, hd)) for _ in range(2))
         self.table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device)
         self.free = list(range(n_pages - 1, -1, -1))
         self.pages: list[list[int]] = [[] for _ in range(n_slots)]
@@ -55,6 +73,12 @@ class PagePool:
         if more > 0:
             self.pages[slot] += [self.free.pop() for _ in range(more)]
             self._show(slot)
+
+    def layer(self, l: int) -> tuple:
+        """Layer l's cache in the order in which the writes and attention calls take it."""
+        if self.tail is None:
+            return self.k[l], self.v[l]
+        return self.k[l], self.v[l], self.k_scales[l], self.v_scales[l], self.k_tail[l], self.v_tail[l]
 
     def release(self, slot: int) -> None:
         self.free += reversed(self.pages[slot])
@@ -75,17 +99,36 @@ class PagedVerifier:
     the caller, so that ``capture`` can put the step into a CUDA graph.  Results:
     ``emitted`` int32 [N, K + 1] (-1 behind a request's last token),
     ``accept_len`` and ``new_len`` int32 [N], ``probs`` fp32 [W, vocab].
+
+    ``held`` names the weights that are kept in e4m3 with a scale for 128 x 128 values
+    (of ``HELD``; "lm_head" among them): their products take the rows in e4m3 as well.  A
+    pool with a tail needs tail >= K + 16, and is prefilled by up to tail - 15 tokens at a time.
     """
 
+    HELD = ("wqkv", "wo", "wgu", "wdown", "lm_head")
+
     def __init__(self, cfg, weights: dict, pool: PagePool, N: int, K: int, temperature: float | None = None,
-                 device="cuda"):
+                 device="cuda", held: tuple = ()):
+        if not set(held) <= set(self.HELD):
+            raise ValueError(f"held: {sorted(set(held) - set(self.HELD))} not among {self.HELD}")
+        if pool.tail is not None and pool.tail < K + 16:
+            raise ValueError(f"a window of {K + 1} rows needs a tail of {K + 16} positions, the pool has {pool.tail}")
         self.cfg, self.pool, self.N, self.K = cfg, pool, N, K
         self.rows = K + 1
         self.W = W = N * (K + 1)
         self.temperature = cfg.temperature if temperature is None else temperature
         dev = torch.device(device)
-        self.w = {k: v.to(dev).contiguous() for k, v in weights.items()}
-        for l in range(cfg.layers):
+        self.w, self.w8, self.rows8 = {}, {}, {}
+        for k, v in weights.items():
+            v = v.to(dev).contiguous()
+            if k.split(".")[-1] in held:
+                self.w8[k] = self._matrix8(*v.shape, 128, dev)
+                B.biv_quant_e4m3(v, *self.w8[k], 128)
+                if v.shape[1] not in self.rows8:
+                    self.rows8[v.shape[1]] = self._matrix8(W, v.shape[1], 1, dev)
+            else:
+                self.w[k] = v
+        for l in range(cfg.layers if "wgu" not in held else 0):
             wgu = self.w[f"l{l}.wgu"]
             self.w[f"l{l}.wgu_packed"] = torch.empty_like(wgu)
             B.biv_swiglu_pack_weights(wgu, self.w[f"l{l}.wgu_packed"])
@@ -98,6 +141,7 @@ class PagedVerifier:
         self.q = torch.empty(W, cfg.Hq, cfg.hd, **bf)
         self.o = torch.empty(W, cfg.Hq, cfg.hd, **bf)
         self.act = torch.empty(W, cfg.ffn, **bf)
+        self.gu = torch.empty(W, 2 * cfg.ffn, **bf) if "wgu" in held else None
         self.logits = torch.empty(W, cfg.vocab, **f32)
         self.probs = torch.empty(W, cfg.vocab, **f32)
         self.tokens = torch.zeros(W, **i32)
@@ -112,6 +156,13 @@ class PagedVerifier:
         self.new_len = torch.empty(N, **i32)
         ws = B.biv_decode_attn_paged_workspace_size(W, cfg.Hq, cfg.hd, pool.max_pages, pool.page_size)
         self.workspace = torch.empty(ws, device=dev, dtype=torch.uint8)
+
+    @staticmethod
+    def _matrix8(rows, K, block, dev):
+        """An e4m3 matrix and its scales."""
+        groups, blocks = -(-K // 128), rows if block == 1 else -(-rows // 128)
+        return (torch.empty(rows, K, device=dev, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                torch.empty((groups, rows) if block == 1 else (blocks, groups), device=dev))
 
     # -------------------------------------------------------------- inputs
     def set_window(self, slots, last, p0, draft, u_accept=None, u_sample=None) -> None:
@@ -138,28 +189,56 @@ class PagedVerifier:
             self.u_sample[:n].copy_(torch.as_tensor(u_sample))
 
     # -------------------------------------------------------------- stages
-    def forward(self) -> None:
-        """Final normalised hidden state of every window row (``h``); the rows' K and V are in their pages."""
-        c, w, p = self.cfg, self.w, self.pool
+    def project(self, x, name: str, out, bias=None, residual=None) -> None:
+        """out = x w^T (+ bias) (+ residual) with the weight ``name``, in the type in which it is held."""
+        if name in self.w8:
+            x8 = self.rows8[x.shape[1]]
+            B.biv_quant_e4m3(x, *x8, 1)
+            B.biv_gemm_e4m3(*x8, *self.w8[name], out, bias=bias, residual=residual)
+        else:
+            B.biv_gemm_bias_act(x, self.w[name], out, bias=bias, residual=residual)
+
+    def attend(self, l: int, group: int) -> None:
+        """Layer l's K and V of the window into the cache, and its attention.  A cache in e4m3 takes
+        a slot's rows in one group: ``group`` rows from each multiple of it on, as far as they go evenly."""
+        c, p = self.cfg, self.pool
+        at = (p.table, self.row_slot, self.row_pos)
+        if p.tail is None:
+            B.biv_rope_kv_write_paged(self.qkv, self.q, *p.layer(l), *at, c.rope_theta, self.rows)
+            B.biv_decode_attn_paged(self.q, *p.layer(l), *at, self.o, self.rows, self.workspace)
+        else:
+            n = self.W // group * group
+            B.biv_rope_kv_write_paged_e4m3(self.qkv[:n], self.q[:n], *p.layer(l), p.table, self.row_slot[:n], self.row_pos[:n],
+                                           c.rope_theta, group)
+            B.biv_decode_attn_paged_e4m3(self.q, *p.layer(l), *at, self.o, self.rows, self.workspace)
+
+    def forward(self, group: int | None = None) -> None:
+        """Final normalised hidden state of every window row (``h``); the rows' K and V are in their pages.
+        ``group``: the rows of a window that are one request's, in their order (K + 1 unless given)."""
+        c, w = self.cfg, self.w
         W = self.W
         B.biv_embed_rmsnorm(w["embed"], self.tokens, w["l0.attn_norm"], self.x, self.h, c.eps)
         for l in range(c.layers):
-            B.biv_gemm_bias_act(self.h, w[f"l{l}.wqkv"], self.qkv, bias=w.get(f"l{l}.bqkv"))
-            B.biv_rope_kv_write_paged(self.qkv, self.q, p.k[l], p.v[l], p.table, self.row_slot, self.row_pos,
-                                      c.rope_theta, self.rows)
-            B.biv_decode_attn_paged(self.q, p.k[l], p.v[l], p.table, self.row_slot, self.row_pos, self.o, self.rows,
-                                    self.workspace)
-            B.biv_gemm_bias_act(self.o.view(W, -1), w[f"l{l}.wo"], self.x, bias=w.get(f"l{l}.bo"), residual=self.x)
+            self.project(self.h, f"l{l}.wqkv", self.qkv, bias=w.get(f"l{l}.bqkv"))
+            self.attend(l, group or self.rows)
+            self.project(self.o.view(W, -1), f"l{l}.wo", self.x, bias=w.get(f"l{l}.bo"), residual=self.x)
             B.biv_rmsnorm(self.x, w[f"l{l}.ffn_norm"], self.h, c.eps)
-            B.biv_gemm_swiglu(self.h, w[f"l{l}.wgu_packed"], self.act)
-            B.biv_gemm_bias_act(self.act, w[f"l{l}.wdown"], self.x, bias=w.get(f"l{l}.bdown"), residual=self.x)
+            if self.gu is None:
+                B.biv_gemm_swiglu(self.h, w[f"l{l}.wgu_packed"], self.act)
+            else:
+                self.project(self.h, f"l{l}.wgu", self.gu)
+                B.biv_silu_mul(self.gu, self.act)
+            self.project(self.act, f"l{l}.wdown", self.x, bias=w.get(f"l{l}.bdown"), residual=self.x)
             gain = w["final_norm"] if l + 1 == c.layers else w[f"l{l + 1}.attn_norm"]
             B.biv_rmsnorm(self.x, gain, self.h, c.eps)
 
     def verify(self, draft_probs=None) -> None:
         """Probabilities of every row and the verified tokens.  ``draft_probs``: fp32
         [N * K, vocab], or None for a drafter that is certain of its tokens."""
-        B.biv_gemm_nosplitk(self.h, self.w["lm_head"], self.logits)
+        if "lm_head" in self.w8:
+            self.project(self.h, "lm_head", self.logits)
+        else:
+            B.biv_gemm_nosplitk(self.h, self.w["lm_head"], self.logits)
         B.biv_softmax(self.logits, self.probs, self.temperature)
         B.biv_verify_sample(self.probs, draft_probs, self.draft, self.u_accept, self.u_sample, self.p0, self.emitted,
                             self.accept_len, self.new_len)
@@ -183,19 +262,21 @@ class PagedVerifier:
 
     def prefill(self, slot: int, prompt) -> None:
         """K and V of a prompt's tokens at positions 0.. of ``slot``: full windows of
-        W rows, the last one padded with empty seats."""
+        W rows (of tail - 15, if the pool's tail holds no more), the last one padded
+        with empty seats."""
         prompt = torch.as_tensor(prompt, dtype=torch.int32, device="cpu")
         self.pool.reserve(slot, prompt.numel())
         self.row_slot.fill_(slot)
-        for a in range(0, prompt.numel(), self.W):
-            part = prompt[a:a + self.W]
+        window = self.W if self.pool.tail is None else min(self.W, self.pool.tail - 15)
+        for a in range(0, prompt.numel(), window):
+            part = prompt[a:a + window]
             pos = torch.full((self.W,), -1, dtype=torch.int32)
             tokens = torch.zeros(self.W, dtype=torch.int32)
             pos[:part.numel()] = torch.arange(a, a + part.numel(), dtype=torch.int32)
             tokens[:part.numel()] = part
             self.row_pos.copy_(pos)
             self.tokens.copy_(tokens)
-            self.forward()
+            self.forward(window)
 
 
 @torch.no_grad()
