@@ -29,7 +29,8 @@ struct HeldPools {
 };
 
 // --------------------------------------------------- RoPE + write
-constexpr int kWriteThreads = 128;
+constexpr int kWriteThreads = 256;
+constexpr int kWriteBatch = 3;
 
 // One CTA per block of 16 positions that a group's rows touch and KV head: it rotates
 // the block's rows of the G query heads and the key head, puts keys and values into the
@@ -91,6 +92,27 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
             s_page = page;
         }
     }
+    // a thread's next kWriteBatch pieces (eight pairs each): the first ones' loads run under the sines
+    const int items = (G + 2) * kPerHead, n_items = (i1 - i0) * items;
+    uint4 a[kWriteBatch], b[kWriteBatch];
+    int row[kWriteBatch], piece[kWriteBatch];
+    auto load = [&](int it0) {
+#pragma unroll
+        for (int n = 0; n < kWriteBatch; ++n) {
+            const int it = it0 + n * kWriteThreads;
+            row[n] = -1;
+            if (it < n_items) {
+                row[n] = i0 + it / items;
+                piece[n] = it % items;
+                const int x = piece[n] / kPerHead, d = (piece[n] % kPerHead) * 8;
+                const int head = x < G ? h * G + x : x == G ? Hq + h : Hq + Hkv + h;
+                const __nv_bfloat16* src = qkv + ((w00 + j0 + row[n]) * heads + head) * HD + d;
+                a[n] = __ldg(reinterpret_cast<const uint4*>(src));
+                b[n] = __ldg(reinterpret_cast<const uint4*>(src + kHalf));
+            }
+        }
+    };
+    load(tid);
     for (int e = tid; e < (i1 - i0) * kHalf; e += kWriteThreads) {
         const int i = i0 + e / kHalf, d = e % kHalf;
         const uint64_t phase = static_cast<uint64_t>(static_cast<long long>(row_pos[w00 + j0 + i])) * turns.per_pos[d];
@@ -102,40 +124,37 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
     }
     __syncthreads();
     const long long ring = (static_cast<long long>(slot) * Hkv + h) * hp.tail;
-    const int items = (G + 2) * kPerHead;                           // of a row: eight pairs each
-    for (int it = tid; it < (i1 - i0) * items; it += kWriteThreads) {
-        const int i = i0 + it / items, u = it % items, x = u / kPerHead, d = (u % kPerHead) * 8;
-        const long long w = w00 + j0 + i;
-        const int head = x < G ? h * G + x : x == G ? Hq + h : Hq + Hkv + h;
-        const __nv_bfloat16* src = qkv + (w * heads + head) * HD;
-        uint4 a = __ldg(reinterpret_cast<const uint4*>(src + d)), b = __ldg(reinterpret_cast<const uint4*>(src + kHalf + d));
-        if (x <= G) {
-            uint32_t* a4 = &a.x;
-            uint32_t* b4 = &b.x;
-            const float* cs = &s_cs[i][d];
-            const float* sn = cs + kHalf;
+    for (int it0 = tid; it0 < n_items;) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float al = bf16lo(a4[e]), ah = bf16hi(a4[e]), bl = bf16lo(b4[e]), bh = bf16hi(b4[e]);
-                const float cl = cs[2 * e], ch = cs[2 * e + 1], sl = sn[2 * e], sh = sn[2 * e + 1];
-                a4[e] = pack_bf16x2(al * cl - bl * sl, ah * ch - bh * sh);
-                b4[e] = pack_bf16x2(bl * cl + al * sl, bh * ch + ah * sh);
+        for (int n = 0; n < kWriteBatch; ++n) {
+            if (row[n] < 0) continue;
+            const int i = row[n], x = piece[n] / kPerHead, d = (piece[n] % kPerHead) * 8;
+            if (x <= G) {
+                uint32_t* a4 = &a[n].x;
+                uint32_t* b4 = &b[n].x;
+                const float* cs = &s_cs[i][d];
+                const float* sn = cs + kHalf;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float al = bf16lo(a4[e]), ah = bf16hi(a4[e]), bl = bf16lo(b4[e]), bh = bf16hi(b4[e]);
+                    const float cl = cs[2 * e], ch = cs[2 * e + 1], sl = sn[2 * e], sh = sn[2 * e + 1];
+                    a4[e] = pack_bf16x2(al * cl - bl * sl, ah * ch - bh * sh);
+                    b4[e] = pack_bf16x2(bl * cl + al * sl, bh * ch + ah * sh);
+                }
             }
+            __nv_bfloat16* dst = x < G ? q_out + ((w00 + j0 + i) * Hq + h * G + x) * HD
+                                       : (x == G ? hp.k_tail : hp.v_tail) + (ring + s_pos[i] % hp.tail) * HD;
+            if (x >= G) {
+                __nv_bfloat16* held = s_kv[x - G][i];
+                *reinterpret_cast<uint4*>(held + d) = a[n];
+                *reinterpret_cast<uint4*>(held + kHalf + d) = b[n];
+                if (!s_ok[i]) continue;
+            }
+            *reinterpret_cast<uint4*>(dst + d) = a[n];
+            *reinterpret_cast<uint4*>(dst + kHalf + d) = b[n];
         }
-        if (x < G) {
-            __nv_bfloat16* dst = q_out + (w * Hq + head) * HD;
-            *reinterpret_cast<uint4*>(dst + d) = a;
-            *reinterpret_cast<uint4*>(dst + kHalf + d) = b;
-            continue;
-        }
-        __nv_bfloat16* held = s_kv[x - G][i];
-        *reinterpret_cast<uint4*>(held + d) = a;
-        *reinterpret_cast<uint4*>(held + kHalf + d) = b;
-        if (s_ok[i]) {
-            __nv_bfloat16* dst = (x == G ? hp.k_tail : hp.v_tail) + (ring + s_pos[i] % hp.tail) * HD;
-            *reinterpret_cast<uint4*>(dst + d) = a;
-            *reinterpret_cast<uint4*>(dst + kHalf + d) = b;
-        }
+        it0 += kWriteBatch * kWriteThreads;
+        load(it0);
     }
     const int page = s_page;
     if (page < 0) return;
@@ -145,21 +164,22 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
             *reinterpret_cast<const uint4*>((x ? hp.v_tail : hp.k_tail) + (ring + (first + i) % hp.tail) * HD + d);
     }
     __syncthreads();
-    // two warps for the keys, two for the values
-    constexpr int kLoads = kHeldBlock * HD / 8 / 64;
-    const int x = tid >> 6, t = tid & 63;
+    // half of the warps for the keys, half for the values
+    constexpr int kSide = kWriteThreads / 2, kLoads = kHeldBlock * HD / 8 / kSide;
+    const int x = tid / kSide, t = tid % kSide;
     uint4 y[kLoads];
     float m = 0.0f;
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-        y[e] = reinterpret_cast<const uint4*>(&s_kv[x][0][0])[t + 64 * e];
+        y[e] = reinterpret_cast<const uint4*>(&s_kv[x][0][0])[t + kSide * e];
         m = fmaxf(m, max_of_halves(max_abs8(y[e])));
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (lane == 0) s_max[tid >> 5] = m;
     __syncthreads();
-    m = fmaxf(s_max[2 * x], s_max[2 * x + 1]);
+#pragma unroll
+    for (int n = 0; n < kSide / 32; ++n) m = fmaxf(m, s_max[kSide / 32 * x + n]);
     // the next bf16 number: what the scale is rounded by costs range (at most 2^-7 of it), no precision,
     // since the values are divided by the number that is held
     const uint32_t bits = (__float_as_uint(scale_of(m)) + 0xffffu) & 0xffff0000u;
@@ -168,7 +188,7 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
     const int in_page = first & (pt.page_size - 1);
     uint8_t* dst = (x ? hp.v : hp.k) + (at * pt.page_size + in_page) * HD;
 #pragma unroll
-    for (int e = 0; e < kLoads; ++e) reinterpret_cast<uint2*>(dst)[t + 64 * e] = e4m3x8(y[e], scale, inv);
+    for (int e = 0; e < kLoads; ++e) reinterpret_cast<uint2*>(dst)[t + kSide * e] = e4m3x8(y[e], scale, inv);
     if (t == 0)
         reinterpret_cast<uint16_t*>(x ? hp.v_scales : hp.k_scales)[(at * pt.page_size + in_page) / kHeldBlock] = static_cast<uint16_t>(bits >> 16);
 }
