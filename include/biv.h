@@ -594,10 +594,10 @@ int biv_rope_kv_write_paged_e4m3(const void* qkv, void* q_out, void* k_pages, vo
                                  int page_size, int tail, float theta, biv_stream_t stream);
 
 /* biv_decode_attn_paged over such a cache: the same rows, groups, errors,
- * workspace (biv_decode_attn_paged_workspace_size) and order of sums.  Queries
- * meet the keys in fp16 after an exact scaling of each row; the softmax
- * weights meet e4m3 values with 11 bits, an eighth of the rounding of o to
- * bf16, and the ring's values with 16.  Page ids are read for the e4m3
+ * workspace (biv_decode_attn_paged_workspace_size) and joins, with splits of
+ * 512 keys.  Queries meet the keys in fp16 after an exact scaling of each row;
+ * the softmax weights meet e4m3 values with 11 bits, an eighth of the rounding
+ * of o to bf16, and the ring's values with 16.  Page ids are read for the e4m3
  * positions only.  Cache rows up to the group's largest position must hold
  * finite values; the rest of a ring may hold anything.
  * Requires tail % 16 == 0, tail >= 16, the pools' alignment as above, and what

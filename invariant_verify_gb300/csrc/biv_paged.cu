@@ -1,5 +1,7 @@
 // The paged key-value cache: rotation and write of new rows into pages, and
 // fixed-split decode attention over them.
+#define BIV_PAGED_SPLIT BIV_KV_SPLIT
+#define BIV_PAGED_ROWS 2048
 #include "biv_paged.cuh"
 
 namespace biv {

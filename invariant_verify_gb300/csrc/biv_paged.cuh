@@ -14,7 +14,7 @@ namespace {
 
 BIV_DEFINE_ERR_WORD(g_paged_err)
 
-constexpr int kSplit = BIV_KV_SPLIT;
+constexpr int kSplit = BIV_PAGED_SPLIT;                // keys of a split: the including file says
 
 // Where a pool's rows lie: page p, KV head h, offset t is row (p * Hkv + h) *
 // page_size + t of hd elements.
@@ -88,7 +88,7 @@ constexpr int kSteps = kSplit / kStep;                 // steps of a split
 constexpr int kStepsPerClass = kSteps / kClasses;
 constexpr int kDirectThreads = 32 * kClasses;
 constexpr int kMaxGroups = 1024;       // entries of the table of live splits; more groups share entries
-constexpr int kMaxRows = 2048;         // rows whose positions are kept in shared memory; with more they are read again
+constexpr int kMaxRows = BIV_PAGED_ROWS;     // rows whose positions are kept in shared memory; with more they are read again
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 with fp32 sums.
 BIV_DEV void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -423,8 +423,8 @@ BIV_DEV float join4(float c0, float c1, float c2, float c3) { return __fadd_rn(_
 
 // Four dims of a row from the classes' shares o[class][row], ml[class][row]; the row's
 // maximum and sum.
-template <int HD>
-BIV_DEV float4 join_dims(const float (*o)[8][HD + 4], const float2 (*ml)[8], int row, int d, float& mx, float& sum) {
+template <int HD, int R>
+BIV_DEV float4 join_dims(const float (*o)[R][HD + 4], const float2 (*ml)[R], int row, int d, float& mx, float& sum) {
     float2 c[kClasses];
     float4 y[kClasses];
 #pragma unroll
@@ -448,8 +448,8 @@ BIV_DEV float4 join_dims(const float (*o)[8][HD + 4], const float2 (*ml)[8], int
 
 // Dims d .. d + 3 of one row of a split, joined: a row's only split is finished here,
 // others go to the workspace.
-template <int HD>
-BIV_DEV void join_row(const PagedAttnParams& P, const float (*o)[8][HD + 4], const float2 (*ml)[8], int row, int d, int pos,
+template <int HD, int R>
+BIV_DEV void join_row(const PagedAttnParams& P, const float (*o)[R][HD + 4], const float2 (*ml)[R], int row, int d, int pos,
                       long long pair, int split) {
     float mx, sum;
     const float4 x = join_dims<HD>(o, ml, row, d, mx, sum);

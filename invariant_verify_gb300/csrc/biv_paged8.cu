@@ -9,6 +9,8 @@
 // key has goes by the row's position alone, so a row has the same bits in every
 // window, and a block is always quantised once, from bf16, whole.
 #include "biv_e4m3.cuh"
+#define BIV_PAGED_SPLIT 512
+#define BIV_PAGED_ROWS 512                             // so that three CTAs of 73 KB share an SM
 #include "biv_paged.cuh"
 
 namespace biv {
@@ -203,9 +205,16 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
 // bits, an eighth of the output's own rounding, and a row's sum adds the rounded weights.
 // The rest of a row's own block comes from the ring, in bf16, with weights of 16 bits.
 //
-// One CTA per item; the split's steps are taken by four warps in turn; a warp reads its
-// keys and values straight from global memory, 32 bytes (keys) and 16 (values) a lane, a
-// whole line for four or eight lanes.  Up to T tiles of 8 query rows share one read.
+// One CTA per item; the split's steps are taken by four warps in turn, whose keys and values
+// are copied to shared memory three steps ahead, over the items' ends; an item's pages, scales
+// and queries are asked for during the item before.  Up to T tiles of 8 query rows share
+// one read.  What bounds it is the instructions of a step (395 with their share of the item's,
+// 64 of them conversions) at 12 warps an SM, not bytes: 512 keys a split instead of 256
+// halve the items' share, at the cost of a call that is one short row.  Measured with (256, 512)
+// keys a split: one row of 131071 keys 64.5, 54.5 us (5.0 TB/s; 4.3 and 3.4 before the copies,
+// when the keys went straight to registers), 64 rows of some 1300 47.8, 41.8 us, 32 windows of
+// five 68.8, 57.4 us, one row of 700 8.0, 9.9 us.  Two steps at once (more independent
+// work a warp, fewer warps) took 20 % longer.
 
 // D[16 x 8] (+)= A[16 x 16] B[16 x 8], fp16 with fp32 sums.
 BIV_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -236,22 +245,6 @@ BIV_DEV float f16_hi(uint32_t x) {
     return r;
 }
 
-// N words of held keys or values: read once, so not kept in L1 and first to leave L2.
-template <int N>
-BIV_DEV void ld_held(const uint8_t* p, uint32_t (&r)[N], uint64_t policy) {
-    if constexpr (N == 8)
-        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "l"(p));
-    else if constexpr (N == 4)
-        asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "l"(p), "l"(policy));
-    else
-        asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v2.b32 {%0, %1}, [%2], %3;"
-                     : "=r"(r[0]), "=r"(r[1])
-                     : "l"(p), "l"(policy));
-}
 // N words of the ring: the kernel before may have written them.
 template <int N>
 BIV_DEV void ld_tail(const __nv_bfloat16* p, uint32_t (&r)[N]) {
@@ -260,23 +253,60 @@ BIV_DEV void ld_tail(const __nv_bfloat16* p, uint32_t (&r)[N]) {
         asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]) : "l"(p + 2 * i));
 }
 
-// A warp's keys and values of one held step.  Lane (g8, c4): dims [HD / 4 c4, ..) of keys g8 and
-// g8 + 8, dims [HD / 8 g8, ..) of values 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9.
-template <int HD>
-struct HeldKeys {
-    static constexpr int KS = HD / 16;
-    uint32_t k[2][KS];
-    uint32_t v[4][HD / 32];
+// A warp's keys and values of a step on their way to registers: 16 x hd bytes each, copied to shared memory
+// kSlots - 1 steps ahead.  A 16-byte piece lies at its place XORed with its line's number,
+// so that the eight lanes that are served at once meet all banks: lane (g8, c4) reads
+// dims [hd / 4 c4, ..) of keys g8 and g8 + 8 and dims [hd / 8 g8, ..) of values 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9.
+constexpr int kSlots = 3;
 
-    BIV_DEV void load_k(const uint8_t* kp, int g8, int c4, uint64_t policy) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) ld_held(kp + (g8 + 8 * r) * HD + HD / 4 * c4, k[r], policy);
+template <int HD>
+struct __align__(128) HeldSlot {
+    static constexpr int KS = HD / 16;
+    static constexpr int kBytes = kHeldBlock * HD;
+    uint8_t k[kBytes], v[kBytes];
+
+    // Where piece c (16 bytes) of a key lies.
+    static BIV_DEV int at(int key, int c) {
+        if constexpr (HD == 128) return key * 128 + ((c ^ (key & 7)) << 4);
+        const int line = key >> 1;
+        return line * 128 + ((((key & 1) * 4 + c) ^ (2 * (line & 3))) << 4);
     }
-    BIV_DEV void load_v(const uint8_t* vp, int g8, int c4, uint64_t policy) {
+    BIV_DEV void copy(const uint8_t* kp, const uint8_t* vp, int lane, uint64_t policy) {
+        constexpr int kRow = HD / 16;              // pieces of a key
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ld_held(vp + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i], policy);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < kBytes / 512; ++e) {
+                const int i = lane + 32 * e;
+                asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(x ? v : k) + at(i / kRow, i % kRow)),
+                             "l"((x ? vp : kp) + 16 * i), "l"(policy)
+                             : "memory");
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Keys g8 + 8 r of k-steps 4 u .. 4 u + 3.
+    BIV_DEV void load_k(uint32_t (&w)[4], int r, int u, int g8, int c4) const {
+        const uint4 x = *reinterpret_cast<const uint4*>(k + at(g8 + 8 * r, KS / 4 * c4 + u));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    }
+    BIV_DEV void load_v(uint32_t (&w)[HD / 32], int i, int g8, int c4) const {
+        const int key = 2 * c4 + (i & 1) + 8 * (i >> 1);
+        if constexpr (HD == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + at(key, g8));
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(v + at(key, g8 >> 1) + (g8 & 1) * 8);
+            w[0] = x.x, w[1] = x.y;
+        }
     }
 };
+
+// Waits for all of this thread's groups of copies but the newest `but`.
+BIV_DEV void wait_copies(int but) {
+    if (but >= 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (but == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
 
 // Q of T tiles in the order of the B fragments: [tile][k / 2][lane] holds the lane's two registers of
 // k-steps k and k + 1, as fp16 (times the row's power of two) and as bf16.
@@ -340,34 +370,40 @@ struct HeldRows {
     }
 
     // One held step: scores, weights and values; key0 its first key, last[t] the lane's rows' last held key.
-    // between(): asked for between the scores and the values, when the keys' registers are free.
-    template <typename F>
-    BIV_DEV void step(HeldKeys<HD>& hk, const HeldQ<HD, T>& q, const float (&back)[T][2], float k_scale, float v_scale,
-                      const int (&last)[T][2], int see, bool bad, int key0, int lane, F&& between) {
-        const int g8 = lane >> 2;
+    BIV_DEV void step(const HeldSlot<HD>& slot, const HeldQ<HD, T>& q, const float (&back)[T][2], float k_scale, float v_scale,
+                      const int (&last)[T][2], int see, bool bad, int key0, int lane) {
+        const int g8 = lane >> 2, c4 = lane & 3;
         float st[T][4];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) st[t][e] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-            uint32_t a[2][4];
+        for (int u = 0; u < KS / 4; ++u) {
+            uint32_t hk[2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                a[j][0] = e4m3_lo(hk.k[0][k + j]);
-                a[j][1] = e4m3_lo(hk.k[1][k + j]);
-                a[j][2] = e4m3_hi(hk.k[0][k + j]);
-                a[j][3] = e4m3_hi(hk.k[1][k + j]);
-            }
+            for (int r = 0; r < 2; ++r) slot.load_k(hk[r], r, u, g8, c4);
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const uint4 b = q.f16[t][k / 2][lane];
-                mma_f16(st[t], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
-                mma_f16(st[t], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+            for (int k = 0; k < 4; k += 2) {
+                uint32_t a[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    a[j][0] = e4m3_lo(hk[0][k + j]);
+                    a[j][1] = e4m3_lo(hk[1][k + j]);
+                    a[j][2] = e4m3_hi(hk[0][k + j]);
+                    a[j][3] = e4m3_hi(hk[1][k + j]);
+                }
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const uint4 b = q.f16[t][2 * u + k / 2][lane];
+                    mma_f16(st[t], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+                    mma_f16(st[t], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+                }
             }
         }
-        between();
+        uint32_t hv[4][HD / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) slot.load_v(hv[i], i, g8, c4);
         uint32_t w[T][2];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -385,15 +421,15 @@ struct HeldRows {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int d = 0; d < HD / 32; ++d) hk.v[i][d] = 0u;
+                for (int d = 0; d < HD / 32; ++d) hv[i][d] = 0u;
         }
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d) {
             uint32_t p[2][2];                      // [keys, keys + 8][dims 0 and 1, 2 and 3]: pairs of keys
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                p[i][0] = __byte_perm(hk.v[2 * i][d], hk.v[2 * i + 1][d], 0x5140);
-                p[i][1] = __byte_perm(hk.v[2 * i][d], hk.v[2 * i + 1][d], 0x7362);
+                p[i][0] = __byte_perm(hv[2 * i][d], hv[2 * i + 1][d], 0x5140);
+                p[i][1] = __byte_perm(hv[2 * i][d], hv[2 * i + 1][d], 0x7362);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -417,6 +453,12 @@ struct HeldRows {
         uint32_t k[2][2 * KS];
 #pragma unroll
         for (int r = 0; r < 2; ++r) ld_tail(kt + (g8 + 8 * r) * HD + HD / 4 * c4, k[r]);
+        uint32_t v[4][KS];
+        auto load_v = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ld_tail(vt + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i]);
+        };
+        if constexpr (T <= 2) load_v();            // the registers allow it
         float s4[T][4];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -434,10 +476,9 @@ struct HeldRows {
                 s4[t][e] = (p | (kStep - 1)) == (key0 | (kStep - 1)) && key0 + g8 + 8 * (e >> 1) <= p ? s4[t][e] * scale_log2 : -INFINITY;
             }
         }
-        uint32_t v[4][KS];
+        if constexpr (T > 2) load_v();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            ld_tail(vt + (2 * c4 + (i & 1) + 8 * (i >> 1)) * HD + HD / 8 * g8, v[i]);
             if (key0 + 2 * c4 + (i & 1) + 8 * (i >> 1) > tmax) {
 #pragma unroll
                 for (int d = 0; d < KS; ++d) v[i][d] = 0u;
@@ -463,29 +504,19 @@ struct HeldRows {
         }
     }
 
-    // As RowState::put_ml and DirectKeys::put: maximum, sum and output of every row; bad: rows that met a
-    // page id out of range.
-    BIV_DEV void put(float2 (*ml)[kClasses][8], float (*o)[kClasses][8][HD + 4], int cls, const uint32_t (&bad)[T], int rows, int lane) const {
+    // As RowState::put_ml and DirectKeys::put: maximum, sum and output of tile t's rows 2 c4 + e; bad: those that
+    // met a page id out of range.
+    BIV_DEV void put(int t, int e, float2 (*ml)[4], float (*o)[4][HD + 4], int cls, uint32_t bad, int rows, int lane) const {
         const int g8 = lane >> 2, c4 = lane & 3;
+        float s = l[t][e];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            float s[2] = {l[t][0], l[t][1]};
+        for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (2 * c4 + e >= rows) return;            // nobody's
+        if (g8 == 0) ml[cls][c4] = make_float2(m[t][e], (bad >> e) & 1u ? -INFINITY : s);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                const float y0 = __shfl_xor_sync(0xffffffffu, s[0], d), y1 = __shfl_xor_sync(0xffffffffu, s[1], d);
-                s[0] += y0;
-                s[1] += y1;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (8 * t + 2 * c4 + e >= rows) continue;              // nobody's
-                if (g8 == 0) ml[t][cls][2 * c4 + e] = make_float2(m[t][e], (bad[t] >> e) & 1u ? -INFINITY : s[e]);
-#pragma unroll
-                for (int k = 0; k < KS; k += 2)
-                    *reinterpret_cast<float4*>(&o[t][cls][2 * c4 + e][HD / 8 * g8 + 2 * k]) =
-                        make_float4(acc[t][k][e], acc[t][k][e + 2], acc[t][k + 1][e], acc[t][k + 1][e + 2]);
-            }
-        }
+        for (int k = 0; k < KS; k += 2)
+            *reinterpret_cast<float4*>(&o[cls][c4][HD / 8 * g8 + 2 * k]) =
+                make_float4(acc[t][k][e], acc[t][k][e + 2], acc[t][k + 1][e], acc[t][k + 1][e + 2]);
     }
 };
 
@@ -513,9 +544,10 @@ BIV_DEV void put_q(HeldQ<HD, T>& q, const uint4& x, int row, int piece, float sc
 
 template <int HD, int T>
 struct __align__(16) HeldSmem {
-    float o[T][kClasses][8][HD + 4];       // rows padded against bank conflicts
+    HeldSlot<HD> slots[kClasses][kSlots];
+    float o[kClasses][4][HD + 4];          // of half a tile; rows padded against bank conflicts
     HeldQ<HD, T> q;
-    float2 ml[T][kClasses][8];
+    float2 ml[kClasses][4];
     int pos[2][8 * T];
     LiveTable table;
 };
@@ -536,9 +568,13 @@ struct HeldSteps {
     float k_scale, v_scale;
 };
 
+// CTAs an SM: three of up to two tiles, two of more (the accumulators' registers: three of
+// three tiles spill, 32 windows of five 81 us for 57; two of one tile: 64 rows 48 us for 42).
+constexpr int held_ctas(int T) { return T <= 2 ? 3 : 2; }
+
 template <int HD, int T>
-__global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_kernel(const PagedAttnParams P, const HeldPools hp) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+__global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_kernel(const PagedAttnParams P, const HeldPools hp) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     HeldSmem<HD, T>& sm = *reinterpret_cast<HeldSmem<HD, T>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;
@@ -548,8 +584,8 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_
     pdl_trigger();
     I.zero_rows<HD>();
 
-    // An item's pages (asked for an item ahead), then its scales and the keys of its first step (asked for during
-    // the last step of the item before).
+    // An item's pages (asked for an item ahead), then its scales and the copies of its first steps (asked for
+    // during the last steps of the item before).
     auto pages_of = [&](const AttnItem& it, HeldSteps& st) {
         const int last = (I.largest_pos(it, it.tile * 8 * T, 8 * T) & ~(kStep - 1)) - 1;      // -1 & ~15 is -16
         const int nsteps = last < 0 ? 0 : Items::steps_to(last, it.split);
@@ -600,18 +636,24 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_
     AttnItem cur, nxt;
     if (!I.first(cur)) return;
     HeldSteps steps, next_steps;
-    HeldKeys<HD> keys;
+    // copies under way lie in slots [tail_slot, tail_slot + flying) mod kSlots, oldest first
+    HeldSlot<HD>* const slots = sm.slots[cls];
+    int tail_slot = 0, flying = 0, asked = 0;          // asked: steps of the item whose copies were begun
+    auto ask = [&](const AttnItem& it, const HeldSteps& st, int i) {
+        const long long at = step_at(it, st, i);
+        int slot = tail_slot + flying;
+        slot -= slot >= kSlots ? kSlots : 0;
+        slots[slot].copy(hp.k + at, hp.v + at, lane, policy);
+        ++flying;
+    };
     {
         uint4 x[kMine];
         int row_pos[1];
         pages_of(cur, steps);
         queries_of(cur, x, row_pos);
         scales_of(cur, steps);
-        if (steps.n > 0) {
-            const long long at = step_at(cur, steps, 0);
-            keys.load_k(hp.k + at, g8, c4, policy);
-            keys.load_v(hp.v + at, g8, c4, policy);
-        }
+        asked = min(steps.n, kSlots);
+        for (int i = 0; i < asked; ++i) ask(cur, steps, i);
         put_queries(x, row_pos, 0);
     }
     for (int buf = 0;; buf ^= 1) {
@@ -650,16 +692,16 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_
         const int own1 = tmax < key_lo ? -1 : min(kSteps - 1, (tmax - key_lo) / kStep);
         int own = max(0, (tmin - key_lo) / kStep);
         own += (cls - own) & (kClasses - 1);
-        const bool has_own = own <= own1;
-        // what is asked for of the next item: during the last step, but after the own blocks, which need the registers
-        auto next_keys = [&]() {
-            if (more) {
-                scales_of(nxt, next_steps);
-                if (next_steps.n > 0) {
-                    const long long next = step_at(nxt, next_steps, 0);
-                    keys.load_k(hp.k + next, g8, c4, policy);
-                    keys.load_v(hp.v + next, g8, c4, policy);
-                }
+        int next_asked = 0;
+        bool looked_up = false;
+        // the next step's copies, of this item or of the next
+        auto ask_ahead = [&]() {
+            if (asked < steps.n) {
+                ask(cur, steps, asked++);
+            } else if (more) {
+                if (!looked_up) scales_of(nxt, next_steps);
+                looked_up = true;
+                if (next_asked < next_steps.n) ask(nxt, next_steps, next_asked++);
             }
         };
 #pragma unroll 1
@@ -670,47 +712,42 @@ __global__ void __launch_bounds__(kHeldThreads, T == 1 ? 3 : 2) paged_attn_held_
 #pragma unroll
                 for (int t = 0; t < T; ++t) bad_rows[t] |= (last[t][0] >= key0 ? 1u : 0u) | (last[t][1] >= key0 ? 2u : 0u);
             }
-            // the keys of this class's next step, or of its first step of the next item
-            long long next = 0;
-            const bool here = i + 1 < steps.n, there = !here && more && !has_own;
-            bool load = here;
-            rs.step(keys, sm.q, back, __shfl_sync(0xffffffffu, steps.k_scale, i), __shfl_sync(0xffffffffu, steps.v_scale, i), last, all, step_bad, key0, lane,
-                    [&] {
-                        if (here) {
-                            next = step_at(cur, steps, i + 1);
-                        } else if (there) {
-                            scales_of(nxt, next_steps);
-                            load = next_steps.n > 0;
-                            if (load) next = step_at(nxt, next_steps, 0);
-                        }
-                        if (load) keys.load_k(hp.k + next, g8, c4, policy);
-                    });
-            if (load) keys.load_v(hp.v + next, g8, c4, policy);
+            wait_copies(flying - 1);
+            __syncwarp();                          // the step before has been read, this one's copies of all lanes are there
+            if (flying < kSlots) ask_ahead();
+            rs.step(slots[tail_slot], sm.q, back, __shfl_sync(0xffffffffu, steps.k_scale, i), __shfl_sync(0xffffffffu, steps.v_scale, i), last, all, step_bad, key0, lane);
+            tail_slot = tail_slot + 1 == kSlots ? 0 : tail_slot + 1;
+            --flying;
         }
-        if (has_own) {
-            for (; own <= own1; own += kClasses) {
-                const int key0 = key_lo + kStep * own;
-                const long long a = ((static_cast<long long>(I.slot_of(cur.w0)) * P.Hkv + cur.kvh) * hp.tail + key0 % hp.tail) * HD;
-                rs.own_step(hp.k_tail + a, hp.v_tail + a, sm.q, P.scale_log2, pos, tmax, key0, lane);
-            }
-            next_keys();
-        } else if (steps.n == 0) {
-            next_keys();
+        __syncwarp();
+#pragma unroll 1
+        for (int i = flying; i < kSlots; ++i) ask_ahead();
+        for (; own <= own1; own += kClasses) {
+            const int key0 = key_lo + kStep * own;
+            const long long a = ((static_cast<long long>(I.slot_of(cur.w0)) * P.Hkv + cur.kvh) * hp.tail + key0 % hp.tail) * HD;
+            rs.own_step(hp.k_tail + a, hp.v_tail + a, sm.q, P.scale_log2, pos, tmax, key0, lane);
         }
         const int r0 = cur.tile * 8 * T;
-        rs.put(sm.ml, sm.o, cls, bad_rows, cur.rows - r0, lane);
-        __syncthreads();
-        for (int x4 = tid; x4 < 8 * T * (HD / 4); x4 += kHeldThreads) {
-            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4, row_pos = sm.pos[buf][row];
-            if (row_pos < key_lo) continue;
-            int j, head;
-            row_head(P, r0 + row, j, head);
-            join_row<HD>(P, sm.o[row / 8], sm.ml[row / 8], row % 8, d, row_pos, static_cast<long long>(cur.w0 + j) * P.Hq + cur.kvh * P.G + head, cur.split);
-        }
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (t + e > 0) __syncthreads();    // the rows before have been joined
+                rs.put(t, e, sm.ml, sm.o, cls, bad_rows[t], cur.rows - r0 - 8 * t, lane);
+                __syncthreads();
+                for (int x4 = tid; x4 < 4 * (HD / 4); x4 += kHeldThreads) {
+                    const int row = x4 / (HD / 4), in_tile = 2 * row + e, d = (x4 % (HD / 4)) * 4, row_pos = sm.pos[buf][8 * t + in_tile];
+                    if (row_pos < key_lo) continue;
+                    int j, head;
+                    row_head(P, r0 + 8 * t + in_tile, j, head);
+                    join_row<HD>(P, sm.o, sm.ml, row, d, row_pos, static_cast<long long>(cur.w0 + j) * P.Hq + cur.kvh * P.G + head, cur.split);
+                }
+            }
         if (!more) break;
         put_queries(next_q, next_pos, buf ^ 1);    // nobody reads this item's any more
         cur = nxt;
         steps = next_steps;
+        asked = next_asked;
     }
 }
 
@@ -726,13 +763,14 @@ int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
     });
     if (st != BIV_OK) return st;
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg, tiles = (static_cast<long long>(P.rpg) * P.G + 8 * T - 1) / (8 * T);
-    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, (T == 1 ? 3LL : 2LL) * num_sms());
+    const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, static_cast<long long>(held_ctas(T)) * num_sms());
     return launch_pdl(paged_attn_held_kernel<HD, T>, dim3(static_cast<unsigned>(grid)), dim3(kHeldThreads), sizeof(HeldSmem<HD, T>), s, P, hp);
 }
 
 template <int HD>
 int launch_held_attn(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
-    // as few passes over the keys as four tiles allow, each with as few tiles as they then need
+    // as few passes over the keys as four tiles allow, each with as few tiles as they then need: 20 query rows
+    // (windows of five, G = 4) in one pass of three tiles 57 us, in two of two 71
     const long long rows = static_cast<long long>(P.rpg) * P.G, passes = (rows + 31) / 32, T = (rows + 8 * passes - 1) / (8 * passes);
     const int st = T == 1 ? launch_held<HD, 1>(P, hp, s) : T == 2 ? launch_held<HD, 2>(P, hp, s)
                  : T == 3 ? launch_held<HD, 3>(P, hp, s) : launch_held<HD, 4>(P, hp, s);

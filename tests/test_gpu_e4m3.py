@@ -414,6 +414,23 @@ def test_attention_of_a_long_context():
     no_error()
 
 
+@pytest.mark.parametrize("N,K", [(1100, 1), (150, 4)])
+def test_attention_of_many_rows(N, K):
+    """More rows, and more groups, than a CTA keeps a table of; requests share slots."""
+    lengths = [4, 40, 515, 77]
+    pool = E.HeldPool(lengths, 1, 64, 16, seed=7)
+    q = U.bf16(U.gen(8), N * K, 2, 64, std=1.5)
+    slot = [r % 4 for r in range(N) for _ in range(K)]
+    pos = [lengths[r % 4] - K + j for r in range(N) for j in range(K)]
+    for w in range(0, N * K, 37):
+        pos[w] = -1
+    o = attend(pool, q, slot, pos, K)
+    check_attention(o, q, pool, slot, pos)
+    some = slice(5 * K, 9 * K)
+    assert same_bits(attend(pool, q[some], slot[some], pos[some], K), o[some])
+    no_error()
+
+
 def test_attention_does_not_depend_on_pages():
     """Page size, ring and the pages' order are where keys lie, no more."""
     q, outs = U.bf16(U.gen(4), 2, 8, 64), []
