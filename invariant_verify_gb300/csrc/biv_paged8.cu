@@ -751,16 +751,167 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
     }
 }
 
+// ---- small calls: a cluster of C CTAs per (request, KV head, 8 query rows), CTA c taking split c;
+// the partials stay in shared memory, and CTA c joins query rows c, c + C, ... of all
+// splits.  One launch, no table of items and no workspace where the two kernels would mostly wait.
+// The same steps, joins and bits.
+template <int HD>
+struct __align__(128) HeldSmallSmem {
+    HeldSlot<HD> slots[kClasses][kSlots];
+    float o[kClasses][4][HD + 4];          // of half a tile
+    float part[8][HD];                     // the split's outputs
+    float2 part_ml[8];
+    HeldQ<HD, 1> q;
+    float2 ml[kClasses][4];
+};
+
+template <int HD, int C>
+__global__ void __launch_bounds__(kHeldThreads, 3) paged_attn_held_small_kernel(const PagedAttnParams P, const HeldPools hp) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    HeldSmallSmem<HD>& sm = *reinterpret_cast<HeldSmallSmem<HD>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
+    const int g8 = lane >> 2, c4 = lane & 3;
+    const int split = static_cast<int>(cluster_ctarank()), key_lo = split * kSplit;
+    const int tiles = (P.rpg * P.G + 7) / 8, p = blockIdx.x / C / tiles, tile = blockIdx.x / C - p * tiles;
+    const int grp = p / P.Hkv, kvh = p - grp * P.Hkv;
+    const int w0 = grp * P.rpg, r0 = 8 * tile, rows = min(8, min(P.rpg, P.W - w0) * P.G - r0);   // none: a last group that is not full
+    const uint64_t policy = policy_evict_first();
+    int pos[1][2], last[1][2], tmax = -1, tmin = 0x7fffffff, all = 0x7fffffff;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * c4 + e;
+        pos[0][e] = i < rows ? usable_pos(P, w0 + (r0 + i) / P.G, split == 0 && kvh == 0) : -1;
+        last[0][e] = pos[0][e] < 0 ? -1 : (pos[0][e] & ~(kStep - 1)) - 1;
+        tmax = max(tmax, pos[0][e]);
+        if (pos[0][e] >= 0) tmin = min(tmin, pos[0][e]);
+        if (pos[0][e] >= key_lo) all = min(all, last[0][e]);
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        tmax = max(tmax, __shfl_xor_sync(0xffffffffu, tmax, d));
+        tmin = min(tmin, __shfl_xor_sync(0xffffffffu, tmin, d));
+        all = min(all, __shfl_xor_sync(0xffffffffu, all, d));
+    }
+    const int held = (tmax & ~(kStep - 1)) - 1, nsteps = held < 0 ? 0 : Items::steps_to(held, split);      // -1 & ~15 is -16
+    HeldSteps steps;
+    steps.n = (nsteps - cls + kClasses - 1) / kClasses;
+    steps.page = 0;
+    const int lane_key = key_lo + kStep * (cls + kClasses * lane);
+    if (lane < steps.n) steps.page = P.pt.table[static_cast<long long>(P.row_slot[w0]) * P.pt.max_pages + (lane_key >> P.pt.page_shift)];
+    steps.bad = bad_pages(P, steps.page);
+    pdl_wait();
+    pdl_trigger();
+    HeldSlot<HD>* const slots = sm.slots[cls];
+    auto ask = [&](int i) {
+        const long long at = held_at<HD>(P, __shfl_sync(0xffffffffu, steps.page, i), kvh, key_lo + kStep * (cls + kClasses * i));
+        slots[i % kSlots].copy(hp.k + at, hp.v + at, lane, policy);
+    };
+    int asked = min(steps.n, kSlots);
+    for (int i = 0; i < asked; ++i) ask(i);
+    if (lane < steps.n) {
+        const long long at = held_at<HD>(P, steps.page, kvh, lane_key) / (kStep * HD);
+        steps.k_scale = __bfloat162float(hp.k_scales[at]);
+        steps.v_scale = __bfloat162float(hp.v_scales[at]);
+    }
+    if (tid < HD) {                                // 8 rows of HD / 8 pieces; rows past the group's read its first row and are never used
+        const int row = tid / (HD / 8), d = tid % (HD / 8), i = row < rows ? r0 + row : 0;
+        const uint4 x = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(w0 + i / P.G) * P.Hq + kvh * P.G + i % P.G) * HD + d * 8);
+        put_q(sm.q, x, row, d, P.scale_log2);
+    }
+    __syncthreads();
+    float back[1][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) back[0][e] = sm.q.back[0][2 * c4 + e];
+    HeldRows<HD, 1> rs;
+    rs.clear();
+    uint32_t bad_rows = 0;
+#pragma unroll 1
+    for (int i = 0; i < steps.n; ++i) {
+        const int key0 = key_lo + kStep * (cls + kClasses * i);
+        const bool step_bad = (steps.bad >> i) & 1u;
+        if (step_bad) bad_rows |= (last[0][0] >= key0 ? 1u : 0u) | (last[0][1] >= key0 ? 2u : 0u);
+        wait_copies(asked - i - 1);
+        __syncwarp();                              // the step before has been read, this one's copies of all lanes are there
+        if (asked - i < kSlots && asked < steps.n) ask(asked++);
+        rs.step(slots[i % kSlots], sm.q, back, __shfl_sync(0xffffffffu, steps.k_scale, i), __shfl_sync(0xffffffffu, steps.v_scale, i), last, all, step_bad,
+                key0, lane);
+    }
+    const int own1 = tmax < key_lo ? -1 : min(kSteps - 1, (tmax - key_lo) / kStep);
+    int own = max(0, (tmin - key_lo) / kStep);
+    own += (cls - own) & (kClasses - 1);
+    for (; own <= own1; own += kClasses) {
+        const int key0 = key_lo + kStep * own;
+        const long long a = ((static_cast<long long>(P.row_slot[w0]) * P.Hkv + kvh) * hp.tail + key0 % hp.tail) * HD;
+        rs.own_step(hp.k_tail + a, hp.v_tail + a, sm.q, P.scale_log2, pos, tmax, key0, lane);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (e > 0) __syncthreads();                // the rows before have been joined
+        rs.put(0, e, sm.ml, sm.o, cls, bad_rows, rows, lane);
+        __syncthreads();
+        for (int x4 = tid; x4 < 4 * (HD / 4); x4 += kHeldThreads) {
+            const int row = x4 / (HD / 4), d = (x4 % (HD / 4)) * 4;
+            if (2 * row + e >= rows) continue;
+            float mx, sum;
+            *reinterpret_cast<float4*>(&sm.part[2 * row + e][d]) = join_dims<HD>(sm.o, sm.ml, row, d, mx, sum);
+            if (d == 0) sm.part_ml[2 * row + e] = make_float2(mx, sum);
+        }
+    }
+    cluster_sync();
+    // query rows split, split + C, ..., joined as the combine kernel does (up to 16 splits: one block)
+    for (int r = split; r < rows; r += C) {
+        const int w = w0 + (r0 + r) / P.G;
+        const int row_pos = usable_pos(P, w, false), ns = row_pos < 0 ? 0 : row_pos / kSplit + 1;
+        const long long pair = static_cast<long long>(w) * P.Hq + kvh * P.G + (r0 + r) % P.G;
+        const float2 mine = lane < ns ? ld_cluster(&sm.part_ml[r], lane) : make_float2(-INFINITY, 0.0f);
+        float x[C] = {};
+        if (tid < HD) {
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (k < ns) x[k] = ld_cluster(&sm.part[r][tid], k);
+        }
+        float m = mine.x, l;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float f_lane = lane < ns ? ex2_approx(mine.x - m) : 0.0f;
+        l = mine.y * f_lane;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const bool broken = __any_sync(0xffffffffu, lane < ns && mine.y == -1.0f);
+        float acc = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const float f = __shfl_sync(0xffffffffu, f_lane, k);
+            if (k < ns) acc = fmaf(x[k], f, acc);
+        }
+        if (tid < HD) P.o[pair * HD + tid] = __float2bfloat16_rn(broken || ns == 0 ? 0.0f : acc * (1.0f / l));
+    }
+    cluster_sync();                                // nobody leaves while its shared memory is read
+}
+
+template <typename F>
+int allow_smem(F* kernel, size_t bytes) {
+    return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+}
+
+template <int HD, int C>
+int launch_held_small(const PagedAttnParams& P, const HeldPools& hp, long long tiles, cudaStream_t s) {
+    static DeviceOnce once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int st = once.run(dev, [] { return allow_smem(paged_attn_held_small_kernel<HD, C>, sizeof(HeldSmallSmem<HD>)); });
+    if (st != BIV_OK) return st;
+    return launch_cluster_pdl(paged_attn_held_small_kernel<HD, C>, dim3(static_cast<unsigned>(tiles * C)), dim3(kHeldThreads), sizeof(HeldSmallSmem<HD>), s, C, P, hp);
+}
+
 template <int HD, int T>
 int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
     static DeviceOnce once;
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_status(e);
-    const int st = once.run(dev, [] {
-        return cuda_status(cudaFuncSetAttribute(paged_attn_held_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                static_cast<int>(sizeof(HeldSmem<HD, T>))));
-    });
+    const int st = once.run(dev, [] { return allow_smem(paged_attn_held_kernel<HD, T>, sizeof(HeldSmem<HD, T>)); });
     if (st != BIV_OK) return st;
     const long long n_groups = (P.W + P.rpg - 1) / P.rpg, tiles = (static_cast<long long>(P.rpg) * P.G + 8 * T - 1) / (8 * T);
     const long long grid = std::min<long long>(n_groups * P.Hkv * P.s_max * tiles, static_cast<long long>(held_ctas(T)) * num_sms());
@@ -769,6 +920,12 @@ int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
 
 template <int HD>
 int launch_held_attn(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
+    // few tiles (of 8 query rows of a request and KV head) and short tables: one launch, with a CTA for every split
+    // that the tables may need, if one round of CTAs holds them
+    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((static_cast<long long>(P.rpg) * P.G + 7) / 8), slots = 3LL * num_sms();
+    if (P.s_max <= 2 && small * 2 <= slots) return launch_held_small<HD, 2>(P, hp, small, s);
+    if (P.s_max <= 4 && small * 4 <= slots) return launch_held_small<HD, 4>(P, hp, small, s);
+    if (P.s_max <= 8 && small * 8 <= slots) return launch_held_small<HD, 8>(P, hp, small, s);
     // as few passes over the keys as four tiles allow, each with as few tiles as they then need: 20 query rows
     // (windows of five, G = 4) in one pass of three tiles 57 us, in two of two 71
     const long long rows = static_cast<long long>(P.rpg) * P.G, passes = (rows + 31) / 32, T = (rows + 8 * passes - 1) / (8 * passes);

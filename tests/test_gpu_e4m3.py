@@ -431,6 +431,24 @@ def test_attention_of_many_rows(N, K):
     no_error()
 
 
+@pytest.mark.parametrize("K,hd,Hq,Hkv", [(1, 128, 8, 2), (5, 128, 8, 2), (3, 64, 16, 1)])
+@pytest.mark.parametrize("cap", [512, 1024, 2048, 4096])
+def test_attention_does_not_depend_on_the_tables_width(K, hd, Hq, Hkv, cap):
+    """A table's width says how a call is split among CTAs, no more: tables of one to eight splits and of twenty."""
+    lengths = [n for n in (K, 16, 100, 511, 512, 513, 528, 1000, 1537, 2048, 3100, 4096) if n <= cap]
+    q, outs = U.bf16(U.gen(4), len(lengths) * K, Hq, hd, std=1.5), []
+    slot = [r for r in range(len(lengths)) for _ in range(K)]
+    pos = [n - K + j for n in lengths for j in range(K)]
+    pos[2 * K] = -1
+    for wide in (cap, 10240):
+        pool = E.HeldPool(lengths, Hkv, hd, 16, seed=5, cap=wide)
+        outs.append(attend(pool, q, slot, pos, K))
+    if K == 1:
+        check_attention(outs[0], q, pool, slot, pos)
+    assert same_bits(outs[0], outs[1])
+    no_error()
+
+
 def test_attention_does_not_depend_on_pages():
     """Page size, ring and the pages' order are where keys lie, no more."""
     q, outs = U.bf16(U.gen(4), 2, 8, 64), []
