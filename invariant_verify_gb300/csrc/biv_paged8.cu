@@ -920,12 +920,15 @@ int launch_held(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
 
 template <int HD>
 int launch_held_attn(const PagedAttnParams& P, const HeldPools& hp, cudaStream_t s) {
-    // few tiles (of 8 query rows of a request and KV head) and short tables: one launch, with a CTA for every split
-    // that the tables may need, if one round of CTAs holds them
-    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((static_cast<long long>(P.rpg) * P.G + 7) / 8), slots = 3LL * num_sms();
-    if (P.s_max <= 2 && small * 2 <= slots) return launch_held_small<HD, 2>(P, hp, small, s);
-    if (P.s_max <= 4 && small * 4 <= slots) return launch_held_small<HD, 4>(P, hp, small, s);
-    if (P.s_max <= 8 && small * 8 <= slots) return launch_held_small<HD, 8>(P, hp, small, s);
+    // Few tiles (of 8 query rows of a request and KV head) and short tables: one launch, with a CTA for every split
+    // that the tables may need, if one round of CTAs holds them.  32 and 8 heads, us, with two kernels in
+    // brackets: one token of 700 keys 7.0 (10.1), a window of five 7.9 (14.9), three such 10.9 (17.3); C = 2, 28
+    // tokens of 700 (448 CTAs) 13.5 (15.4); C = 4, nine (288) 10.4 (13.2), 2048 keys 11.9 (14.3), but fourteen
+    // (448) 15.7 (13.8): of larger clusters three CTAs an SM are no single round.
+    const long long small = (P.W + P.rpg - 1LL) / P.rpg * P.Hkv * ((static_cast<long long>(P.rpg) * P.G + 7) / 8);
+    if (P.s_max <= 2 && small * 2 <= 3LL * num_sms()) return launch_held_small<HD, 2>(P, hp, small, s);
+    if (P.s_max <= 4 && small * 4 <= 2LL * num_sms()) return launch_held_small<HD, 4>(P, hp, small, s);
+    if (P.s_max <= 8 && small * 8 <= 2LL * num_sms()) return launch_held_small<HD, 8>(P, hp, small, s);
     // as few passes over the keys as four tiles allow, each with as few tiles as they then need: 20 query rows
     // (windows of five, G = 4) in one pass of three tiles 57 us, in two of two 71
     const long long rows = static_cast<long long>(P.rpg) * P.G, passes = (rows + 31) / 32, T = (rows + 8 * passes - 1) / (8 * passes);
