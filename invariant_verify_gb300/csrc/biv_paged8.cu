@@ -339,32 +339,37 @@ struct HeldRows {
         }
     }
 
-    // Scores of a step in units of log 2 to weights in place (without their sum).
-    BIV_DEV void weights(int t, float (&st)[4]) {
+    // Whether this lane's scores of a step ask for another reference.
+    BIV_DEV bool above(int t, const float (&st)[4]) const {
+        return fmaxf(st[0], st[2]) > m[t][0] + kSlack || fmaxf(st[1], st[3]) > m[t][1] + kSlack;
+    }
+    // The references of the rows whose scores pass theirs by more than the slack.
+    BIV_DEV void refer(int t, const float (&st)[4]) {
         float x[2] = {fmaxf(st[0], st[2]), fmaxf(st[1], st[3])};
-        if (__any_sync(0xffffffffu, x[0] > m[t][0] + kSlack || x[1] > m[t][1] + kSlack)) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
-                x[0] = fmaxf(x[0], y0);
-                x[1] = fmaxf(x[1], y1);
-            }
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                f[e] = 1.0f;
-                if (x[e] > m[t][e] + kSlack) {
-                    f[e] = ex2_approx(m[t][e] - x[e]);
-                    m[t][e] = x[e];
-                    mu[t][e] = x[e] - kLift;
-                }
-                l[t][e] *= f[e];
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][k][e] *= f[e & 1];
+        for (int d = 4; d < 32; d <<= 1) {
+            const float y0 = __shfl_xor_sync(0xffffffffu, x[0], d), y1 = __shfl_xor_sync(0xffffffffu, x[1], d);
+            x[0] = fmaxf(x[0], y0);
+            x[1] = fmaxf(x[1], y1);
         }
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            f[e] = 1.0f;
+            if (x[e] > m[t][e] + kSlack) {
+                f[e] = ex2_approx(m[t][e] - x[e]);
+                m[t][e] = x[e];
+                mu[t][e] = x[e] - kLift;
+            }
+            l[t][e] *= f[e];
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][k][e] *= f[e & 1];
+    }
+    // Scores of a step in units of log 2 to weights in place (without their sum).
+    BIV_DEV void weights(int t, float (&st)[4]) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[e] = ex2_approx(st[e] - mu[t][e & 1]);
     }
@@ -405,11 +410,20 @@ struct HeldRows {
 #pragma unroll
         for (int i = 0; i < 4; ++i) slot.load_v(hv[i], i, g8, c4);
         uint32_t w[T][2];
+        bool up = false;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) st[t][e] *= back[t][e & 1] * k_scale;
             if (key0 + kStep - 1 > see) mask_step(st[t], last[t], key0, g8);
+            up |= above(t, st[t]);
+        }
+        if (__any_sync(0xffffffffu, up)) {         // one vote for all tiles: a row that need not move keeps its bits
+#pragma unroll
+            for (int t = 0; t < T; ++t) refer(t, st[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
             weights(t, st[t]);
             const uint32_t h0 = pack_f16x2(st[t][0], st[t][1]), h1 = pack_f16x2(st[t][2], st[t][3]);
             l[t][0] += f16_lo(h0) + f16_lo(h1);
@@ -487,6 +501,7 @@ struct HeldRows {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             float(&st)[4] = s4[t];
+            if (__any_sync(0xffffffffu, above(t, st))) refer(t, st);
             weights(t, st);
             l[t][0] += st[0] + st[2];
             l[t][1] += st[1] + st[3];
