@@ -24,8 +24,8 @@ TORCH_LIB = os.path.join(HERE, "_biv_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["biv_api.cu", "biv_gemm.cu", "biv_select.cu", "biv_attn.cu", "biv_rowops.cu", "biv_draft.cu",
-           "biv_paged.cu", "biv_sample.cu", "biv_quant8.cu", 
-           "biv_gemm8.cu", "biv_paged8.cu"]
+           "biv_paged.cu", "biv_sample.cu", "biv_quant8.cu", "biv_gemm8.cu",
+           "biv_paged8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE]

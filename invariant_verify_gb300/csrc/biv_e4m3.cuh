@@ -46,7 +46,7 @@ BIV_DEV float scale_of(float amax) {
 
 // Eight bf16 numbers over s (inv: its inverse) as e4m3.  x inv alone falls beside a tie of the
 // quotient too often (one value in 10^3, where x and the largest of its block are small multiples
-// of one another); one correction makes it the quotient.  An infinity leaves it as a NaN.
+// of one another); one correction by its remainder (Markstein's) makes it the quotient.  An infinity leaves it as a NaN.
 BIV_DEV float over(float x, float s, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, s, x), inv, q);
