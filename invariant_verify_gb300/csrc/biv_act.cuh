@@ -79,33 +79,40 @@ struct BiasActRow {
             if (in[h] && ba.residual) rs[h] = ld_global_16(ba.residual + at + 8 * h);
         }
     }
+    // Columns 8 h .. 8 h + 7; v(e): accumulator of column e.
+    template <typename V>
+    BIV_DEV void values(int h, V&& v, const BiasActArgs& ba, float (&x)[8]) const {
+        const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = v(8 * h + e);
+            if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
+        }
+        if (ba.act != BIV_ACT_NONE) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
+        }
+        if (ba.residual) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
+        }
+    }
+    static BIV_DEV uint4 pack8(const float (&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
     template <bool F32, typename V>
-    BIV_DEV void store(V&& v, void* C, const BiasActArgs& ba) const {      // v(e): accumulator of column e
+    BIV_DEV void store(V&& v, void* C, const BiasActArgs& ba) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (!in[h]) continue;
-            const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
             float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = v(8 * h + e);
-                if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
-            }
-            if (ba.act != BIV_ACT_NONE) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
-            }
-            if (ba.residual) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
-            }
+            values(h, v, ba, x);
             if constexpr (F32) {
                 float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at + 8 * h);
                 dst[0] = make_float4(x[0], x[1], x[2], x[3]);
                 dst[1] = make_float4(x[4], x[5], x[6], x[7]);
             } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at + 8 * h) =
-                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(C) + at + 8 * h) = pack8(x);
             }
         }
     }

@@ -57,6 +57,7 @@ struct Gemm8Args {
     BiasActArgs ba;
     int M, N, K, KB;                          // k-blocks
     int f32;
+    int wide;                                 // C's rows are 32-byte aligned
     int BN, stages;                           // tile width, stages
     int xr, yr;                               // rows of a CTA's boxes of A and of B
     int m_tiles, tiles;
@@ -149,6 +150,60 @@ BIV_DEV float ld_shared(uint32_t at) {
 // Four bytes to shared memory, zero where there are none to read.
 BIV_DEV void copy_4(float* dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
+// Eight words to memory, 32-byte aligned.
+BIV_DEV void st_global_32(void* p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+                 "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
+// A thread's row: PARTS x 16 columns from col0 on (the first `cols` of them) to C.
+template <bool F32, int PARTS>
+BIV_DEV void put_row(const float (&acc)[PARTS][16], int row, int col0, int cols, const Gemm8Args& g) {
+    if (row >= g.M) return;
+    const bool plain = !g.ba.bias && !g.ba.residual && g.ba.act == BIV_ACT_NONE;
+    uint8_t* dst = static_cast<uint8_t*>(g.C) + (static_cast<long long>(row) * g.N + col0) * (F32 ? 4 : 2);
+    const int n = min(cols, g.N - col0);       // columns that there are: a multiple of 8
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        if (16 * i >= n) break;
+        float x[2][8];
+        if (plain) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e >> 3][e & 7] = acc[i][e];
+        } else {
+            const BiasActRow operands(true, row, col0 + 16 * i, g.N, g.ba);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) operands.values(h, [&](int e) { return acc[i][e]; }, g.ba, x[h]);
+        }
+        uint8_t* at = dst + 16 * i * (F32 ? 4 : 2);
+        if constexpr (F32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (16 * i + 8 * h >= n) break;
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(x[h][e]);
+                if (g.wide) {
+                    st_global_32(at + 32 * h, y);
+                } else {
+                    *reinterpret_cast<uint4*>(at + 32 * h) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(at + 32 * h + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        } else {
+            const uint4 a = BiasActRow::pack8(x[0]), b = BiasActRow::pack8(x[1]);
+            if (g.wide && 16 * i + 8 < n) {
+                const uint32_t y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                st_global_32(at, y);
+            } else {
+                *reinterpret_cast<uint4*>(at) = a;
+                if (16 * i + 8 < n) *reinterpret_cast<uint4*>(at + 16) = b;
+            }
+        }
+    }
 }
 
 // WHOLE: BN = 256, so that a warp's columns lie in one 128-column block of weights.
@@ -431,16 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
             }
             if (!ok || !reads) continue;      // to the vote, or to the end
             const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + q * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i)
-                if (cb + 16 * i < g.BN) {
-                    const BiasActRow operands(row < g.M, row, n0 + cb + 16 * i, g.N, g.ba);
-                    auto value = [&](int e) { return acc[i][e]; };
-                    if (g.f32)
-                        operands.template store<true>(value, g.C, g.ba);
-                    else
-                        operands.template store<false>(value, g.C, g.ba);
-                }
+            if (g.f32)
+                put_row<true, PARTS>(acc, row, n0 + cb, g.BN - cb, g);
+            else
+                put_row<false, PARTS>(acc, row, n0 + cb, g.BN - cb, g);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -580,6 +629,7 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
     g.K = K;
     g.KB = static_cast<int>(ceil_div(K, kBK));
     g.f32 = out_dtype == BIV_F32;
+    g.wide = reinterpret_cast<uintptr_t>(C) % 32 == 0 && (g.f32 || N % 16 == 0);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = num_sms();
     const long long m_tiles = ceil_div(M, kLanes);
