@@ -31,13 +31,14 @@
  *     call time.  They skip the offending row and set a bit in the library's
  *     device error word, read with biv_device_error().
  *   - Inputs are never modified, except the caches of biv_kv_overwrite, the
- *     pages of biv_rope_kv_write_paged and the caller-provided workspaces.
+ *     pages of biv_rope_kv_write_paged, the pages, scales and rings of
+ *     biv_rope_kv_write_paged_e4m3 and the caller-provided workspaces.
  *   - Kernels launch with programmatic dependent launch: a kernel may start
  *     while the previous libbiv kernel on the same stream is finishing, and
  *     waits for it before reading that kernel's outputs.  A few inputs that
  *     are never a step's intermediate results are read before that wait:
- *     GEMM weights (B operands), the row_slot / row_pos arrays of attention
- *     (of the paged attention also page_table, and no cache rows) and the
+ *     GEMM weights (B operands and their scales), the row_slot / row_pos arrays
+ *     of attention (of the paged ones also page_table, and no cache rows) and the
  *     cache rows of each attention row group below the group's smallest
  *     position (the requests' committed context).  They must not be
  *     written by the immediately preceding libbiv kernel on the stream

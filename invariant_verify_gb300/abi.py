@@ -5,7 +5,7 @@ pointers, sizes and the current CUDA stream to the C entry point of the same
 name, and raises ``BivError`` on a non-zero status.  There is no fallback:
 if ``libbiv.so`` has not been built, loading raises immediately.
 
-The paged and sampled calls, whose small cases take less time on the GPU than
+The paged, sampled and e4m3 calls, whose small cases take less time on the GPU than
 ctypes and these checks on the host, go through ``_biv_torch.so`` first
 (``csrc/biv_torch.cpp``: the same checks and the same entry points); what it
 does not take (a named stream, rows_keep, strided rows, a tensor at fault)

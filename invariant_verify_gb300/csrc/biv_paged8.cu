@@ -38,6 +38,10 @@ constexpr int kWriteBatch = 3;
 // the block's rows of the G query heads and the key head, puts keys and values into the
 // ring and, where the block's last position is among the rows, the whole block into its
 // page: rows of earlier calls come from the ring, so that no CTA waits for another.
+// Bound by its chain of dependent steps (position, rows, rotation, largest, page), which too few
+// CTAs an SM hide: 2047 rows of 32 and 8 heads 15.4 us (3.5 TB/s read and written), 8 rows
+// 3.9 us with the launch.  128 threads, with the rows asked for after the sines: 20.1; more CTAs an
+// SM by fewer registers: 17.3 (five), 20.3 (six).
 template <int HD>
 __global__ void __launch_bounds__(kWriteThreads)
 rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ q_out, const HeldPools hp,
@@ -210,11 +214,11 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
 // and queries are asked for during the item before.  Up to T tiles of 8 query rows share
 // one read.  What bounds it is the instructions of a step (395 with their share of the item's,
 // 64 of them conversions) at 12 warps an SM, not bytes: 512 keys a split instead of 256
-// halve the items' share, at the cost of a call that is one short row.  Measured with (256, 512)
-// keys a split: one row of 131071 keys 64.5, 54.5 us (5.0 TB/s; 4.3 and 3.4 before the copies,
-// when the keys went straight to registers), 64 rows of some 1300 47.8, 41.8 us, 32 windows of
-// five 68.8, 57.4 us, one row of 700 8.0, 9.9 us.  Two steps at once (more independent
-// work a warp, fewer warps) took 20 % longer.
+// halve the items' share, at the cost of a call that is one short row (which the clusters below
+// pay back).  Measured with (256, 512) keys a split: one row of 131071 keys 64.5, 54.5 us (4.9 TB/s;
+// 67.4, 61.7 before the copies, when the keys went straight to registers), 64 rows of some 1400 keys
+// 47.8, 41.8 us, 32 windows of five 68.8, 56.0 us, one row of 700 8.0, 9.9 us.  Two steps at once
+// (more independent work a warp, fewer warps) took 20 % longer.
 
 // D[16 x 8] (+)= A[16 x 16] B[16 x 8], fp16 with fp32 sums.
 BIV_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -769,7 +773,8 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
 // ---- small calls: a cluster of C CTAs per (request, KV head, 8 query rows), CTA c taking split c;
 // the partials stay in shared memory, and CTA c joins query rows c, c + C, ... of all
 // splits.  One launch, no table of items and no workspace where the two kernels would mostly wait.
-// The same steps, joins and bits.
+// The same steps, joins and bits.  One row of 700 keys: 6.9 us, 9.9 with the two kernels; the chain of
+// a class's eight steps bounds it.
 template <int HD>
 struct __align__(128) HeldSmallSmem {
     HeldSlot<HD> slots[kClasses][kSlots];
