@@ -578,7 +578,8 @@ int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B, const flo
  * biv_rope_kv_write_paged_e4m3: as biv_rope_kv_write_paged (the same angles,
  * q_out and rows_keep; page table as there), into such a cache.  The rows
  * [r*K, (r+1)*K) of a group are consecutive positions of one slot, those
- * without a row (-1) last; groups that write name different slots.  Positions
+ * without a row (-1) last; groups that write name different slots (else
+ * BIV_DEVERR_GROUP: what such a slot then holds is undefined).  Positions
  * [16 floor(p / 16), p) before a group's first position p must be among the
  * last `tail` that were written to the slot (or p % 16 == 0): so a request may
  * go back by up to tail - 15 positions, or to any multiple of 16.  A row whose

@@ -46,7 +46,7 @@ template <int HD>
 __global__ void __launch_bounds__(kWriteThreads)
 rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* __restrict__ q_out, const HeldPools hp,
                           const PageTable pt, const int32_t* __restrict__ row_slot, const int32_t* __restrict__ row_pos,
-                          const int32_t* __restrict__ rows_keep, int K, int Hq, int Hkv, int chunks,
+                          const int32_t* __restrict__ rows_keep, int groups, int K, int Hq, int Hkv, int chunks,
                           const __grid_constant__ RopeTurns turns) {
     constexpr int kHalf = HD / 2, kPerHead = kHalf / 8;
     __shared__ __align__(16) float s_cs[kHeldBlock][HD];             // cosines, then sines
@@ -66,6 +66,13 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
     const int j0 = kHeldBlock * c - (p0 >= 0 ? p0 & (kHeldBlock - 1) : 0);          // row of the block's first position
     if (j0 >= K) return;
     const int i0 = max(0, -j0), i1 = min(kHeldBlock, K - j0);                       // the block's rows of this call
+    // A slot that two groups write: neither sees the other's rows when it fills a block.
+    if (h == 0 && c == 0) {
+        auto writes = [&](long long g) { return row_pos[g * K] >= 0 && (!rows_keep || rows_keep[g] > 0); };
+        bool twice = false;
+        for (int g = tid; g < groups; g += kWriteThreads) twice |= g != r && row_slot[static_cast<long long>(g) * K] == slot && writes(g) && writes(r);
+        if (twice) atomicOr(&g_paged_err, BIV_DEVERR_GROUP);
+    }
     const long long cap = static_cast<long long>(pt.max_pages) << pt.page_shift;
     const int first = (p0 & ~(kHeldBlock - 1)) + kHeldBlock * c;                    // the block's first position
     if (tid < 32) {
@@ -1000,7 +1007,7 @@ extern "C" int biv_rope_kv_write_paged_e4m3(const void* qkv, void* q_out, void* 
     const RopeTurns& turns = rope_turns(theta, hd);
     return launch_pdl(hd == 128 ? rope_kv_write_held_kernel<128> : rope_kv_write_held_kernel<64>, dim3(static_cast<unsigned>(grid)),
                       dim3(kWriteThreads), 0, reinterpret_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(qkv),
-                      static_cast<__nv_bfloat16*>(q_out), hp, pt, row_slot, row_pos, rows_keep, K, Hq, Hkv, chunks, turns);
+                      static_cast<__nv_bfloat16*>(q_out), hp, pt, row_slot, row_pos, rows_keep, W / K, K, Hq, Hkv, chunks, turns);
 }
 
 extern "C" int biv_decode_attn_paged_e4m3(const void* q, const void* k_pages, const void* v_pages, const void* k_scales,

@@ -129,6 +129,22 @@ def test_gemm_onto_its_residual(M):
     assert same_bits(x, want)
 
 
+@pytest.mark.parametrize("M,N,K,out", [(5, 72, 144, torch.float32), (130, 304, 256, torch.bfloat16), (70, 96, 256, torch.float32), (9, 1040, 128, torch.bfloat16)])
+def test_gemm_into_rows_of_16_bytes(M, N, K, out):
+    """C sixteen bytes off a 32-byte boundary: the bits that it has on one, and nothing beside it."""
+    A, Bm, bias, res = matrices(M, N, K, 3)
+    on = torch.zeros(M, N, dtype=out, device="cuda")
+    room = torch.full((M * N + 64,), 7.0, dtype=out, device="cuda")
+    step = 16 // on.element_size()
+    off = room[step:step + M * N].view(M, N)
+    assert on.data_ptr() % 32 == 0 and off.data_ptr() % 32 == 16
+    for C in (on, off):
+        B.biv_gemm_e4m3(A[0].cuda(), A[1].cuda(), Bm[0].cuda(), Bm[1].cuda(), C, bias=bias.cuda(), residual=res.cuda(), act="gelu")
+    assert same_bits(on, off)
+    assert (room[:step] == 7).all() and (room[step + M * N:] == 7).all()
+    no_error()
+
+
 # 28672: 256 columns a tile, pairs of CTAs where the number of 128-row tiles is even
 @pytest.mark.parametrize("N,K", [(520, 1040), (4096, 1408), (28672, 400)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -322,6 +338,28 @@ def test_write_keeps_rows():
     x[~rows] = 0
     assert check_write(cache, x, slot, kept, Hq, 1e4, q2, before) == {(0, 0)}
     no_error()
+
+
+@pytest.mark.parametrize("groups", [2, 300])
+def test_write_of_a_slot_by_two_groups(groups):
+    """Neither would see the other's rows when it fills a block: the error word says so.  Empty groups, and those that keep
+    no row, may name any slot."""
+    K, Hq, Hkv, hd = 4, 2, 1, 64
+    cache = Cache(groups, Hkv, hd, 16, 32, 2)
+    qkv = U.bf16(U.gen(1), groups * K, (Hq + 2 * Hkv) * hd)
+    pos = [j for _ in range(groups) for j in range(K)]
+    slots = list(range(groups))
+    slots[-1] = 0
+    rows = lambda s: [x for x in s for _ in range(K)]  # noqa: E731
+    cache.write(qkv, rows(range(groups)), pos, Hq, 1e4, K)
+    no_error()
+    cache.write(qkv, rows(slots), pos[:-K] + [-1] * K, Hq, 1e4, K)
+    no_error()
+    cache.write(qkv, rows(slots), pos, Hq, 1e4, K, keep=[K] * (groups - 1) + [0])
+    no_error()
+    cache.write(qkv, rows(slots), pos, Hq, 1e4, K)
+    torch.cuda.synchronize()
+    assert B.biv_device_error() == B.DEVERR_GROUP
 
 
 @pytest.mark.parametrize("fault,bit", [("slot", B.DEVERR_INDEX), ("far", B.DEVERR_INDEX), ("negative", B.DEVERR_INDEX), ("page", B.DEVERR_INDEX),
