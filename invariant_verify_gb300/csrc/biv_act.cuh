@@ -79,23 +79,31 @@ struct BiasActRow {
             if (in[h] && ba.residual) rs[h] = ld_global_16(ba.residual + at + 8 * h);
         }
     }
-    // Columns 8 h .. 8 h + 7; v(e): accumulator of column e.
-    template <typename V>
-    BIV_DEV void values(int h, V&& v, const BiasActArgs& ba, float (&x)[8]) const {
-        const uint32_t b4[4] = {bs[h].x, bs[h].y, bs[h].z, bs[h].w}, r4[4] = {rs[h].x, rs[h].y, rs[h].z, rs[h].w};
+    // Columns 8 h .. 8 h + 8 N - 1; v(e): accumulator of column e.  An activation's steps run side by side for all
+    // of them: 1023 x 14336 x 4096 in e4m3 with (relu, gelu, gelu_tanh, silu) 63.8, 84.9, 70.6, 69.1 us for N = 2,
+    // 72.2, 94.2, 77.7, 75.3 with one column after the other (62.0 without an activation).
+    template <int N, typename V>
+    BIV_DEV void values(int h, V&& v, const BiasActArgs& ba, float (&x)[N][8]) const {
+        auto all = [&](auto f) {                   // f(value, half, column of it), all of them side by side
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = v(8 * h + e);
-            if (ba.bias) x[e] += (e & 1) ? bf16hi(b4[e >> 1]) : bf16lo(b4[e >> 1]);
-        }
-        if (ba.act != BIV_ACT_NONE) {
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = activate(x[e], ba.act);
+                for (int e = 0; e < 8; ++e) x[n][e] = f(x[n][e], h + n, e);
+        };
+        auto of = [](const uint4& y, int e) {
+            const uint32_t w = e < 2 ? y.x : e < 4 ? y.y : e < 6 ? y.z : y.w;
+            return (e & 1) ? bf16hi(w) : bf16lo(w);
+        };
+        all([&](float, int k, int e) { return v(8 * k + e); });
+        if (ba.bias) all([&](float y, int k, int e) { return y + of(bs[k], e); });
+        switch (ba.act) {
+            case BIV_ACT_NONE: break;
+            case BIV_ACT_RELU: all([](float y, int, int) { return activate(y, BIV_ACT_RELU); }); break;
+            case BIV_ACT_GELU: all([](float y, int, int) { return activate(y, BIV_ACT_GELU); }); break;
+            case BIV_ACT_GELU_TANH: all([](float y, int, int) { return activate(y, BIV_ACT_GELU_TANH); }); break;
+            default: all([](float y, int, int) { return activate(y, BIV_ACT_SILU); }); break;
         }
-        if (ba.residual) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += (e & 1) ? bf16hi(r4[e >> 1]) : bf16lo(r4[e >> 1]);
-        }
+        if (ba.residual) all([&](float y, int k, int e) { return y + of(rs[k], e); });
     }
     static BIV_DEV uint4 pack8(const float (&x)[8]) {
         return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
@@ -105,8 +113,9 @@ struct BiasActRow {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (!in[h]) continue;
-            float x[8];
-            values(h, v, ba, x);
+            float y[1][8];
+            values(h, v, ba, y);
+            const float(&x)[8] = y[0];
             if constexpr (F32) {
                 float4* dst = reinterpret_cast<float4*>(static_cast<float*>(C) + at + 8 * h);
                 dst[0] = make_float4(x[0], x[1], x[2], x[3]);
