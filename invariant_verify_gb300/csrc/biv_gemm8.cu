@@ -71,16 +71,17 @@ struct Gemm8Args {
     uint32_t idesc;
 };
 
-// PARTS: 16-column parts of a thread (half of BN, rounded up).
-template <int PARTS>
+// PARTS: 16-column parts of a thread (half of BN, rounded up).  DEEP: sets of one k-block, four of them, where two of two
+// would fit as well.
+template <int PARTS, bool DEEP>
 struct Form {
     static constexpr int kCols = 32 * PARTS;  // the widest BN
     // K-blocks of a set of accumulators; the sets are taken in turn.  Where a set is one k-block a stage holds two
     // sets, since a box costs the TMA unit some 275 ns whatever its size (1024 x 4096 x 14336: 79 us with boxes
     // of one k-block, 41 with no copies at all).
-    static constexpr int kBlocks = kCols <= 64 ? 4 : kCols <= 128 ? 2 : 1;
+    static constexpr int kBlocks = kCols <= 64 ? 4 : kCols <= 128 && !DEEP ? 2 : 1;
     static constexpr int kStageSets = kBlocks == 1 ? 2 : 1, kStage = kBlocks * kStageSets;
-    static constexpr int kSets = kCols <= 32 ? 4 : 2;
+    static constexpr int kSets = kCols <= 32 || DEEP ? 4 : 2;
     static constexpr int kSetCols = 512 / kSets;
     // A barrier of the summing threads and a vote: true if every one says so.
     BIV_DEV static bool all_say(bool ok) {
@@ -213,10 +214,10 @@ BIV_DEV void put_row(const float (&acc)[PARTS][16], int row, int col0, int cols,
 }
 
 // WHOLE: BN = 256, so that a warp's columns lie in one 128-column block of weights.
-template <int CG, int PARTS, bool WHOLE>
+template <int CG, int PARTS, bool WHOLE, bool DEEP>
 __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                                                                 const Gemm8Args g) {
-    using Q = Form<PARTS>;
+    using Q = Form<PARTS, DEEP>;
     constexpr int NB = Q::kBlocks, KS = Q::kStage;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -416,7 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
         const uint32_t tfull0 = smem_u32(tfull), pages0 = smem_u32(&s_page[0][0]);
         uint32_t freed = smem_u32(tempty);    // the sets' barriers where the MMAs are issued
         if constexpr (CG == 2) freed = mapa_shared(tempty, 0);
-        int set = 0, buf = 0;
+        // The set of a tile's next k-blocks: in turn, or where a stage holds two, in turn among the even ones for its
+        // first and among the odd ones for its second, which a tile's last stage may lack.
+        int next[2] = {0, 1}, buf = 0;
         uint32_t phases = 0;                  // bit a: the phase of set a
         bool ok = true;                       // a wait ran out: the warps leave together, at the next vote
         if (unit < g.tiles) fetch(unit, 0, s_page[0]);
@@ -429,7 +432,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
                 for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
             // the warp's columns lie in two 128-column blocks of weights at most: the first one, and its parts
             const int blk = (n0 + cb) / 128 - n0 / 128, turn = (128 - (n0 + cb) % 128) / 16;         // the first one, and its parts
-            if (Q::kStageSets == 2) set = 0;   // a tile begins with a stage's first set
             for (int s = 0; s < sets; ++s) {
                 const int in_page = s % kPageSets, nkb = min(NB, g.KB - s * NB);
                 if (in_page == 0) {
@@ -442,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
                     else if (t + n_units < g.tiles)
                         fetch(t + n_units, 0, s_page[buf]);
                 }
+                const int second = Q::kStageSets == 2 ? s & 1 : 0, set = second ? next[1] : next[0];
                 if (reads) {
                     const uint32_t row_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + in_page * NB * kLanes + q * 32 + lane) * 4u;
                     const uint32_t col_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + kPageBlocks * kLanes + in_page * NB * 4 + blk) * 4u;
@@ -488,7 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
                         }
                 }
                 phases ^= 1u << set;
-                set = set + 1 == Q::kSets ? 0 : set + 1;
+                const int after = (set + Q::kStageSets) & (Q::kSets - 1);
+                if (second) next[1] = after;
+                else next[0] = after;
             }
             if (!ok || !reads) continue;      // to the vote, or to the end
             const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + q * 32 + lane;
@@ -532,7 +537,7 @@ bool encode_e4m3(CUtensorMap* map, const void* base, int rows, int K, int box_ro
 
 // Once per device and kernel: its opt-in shared memory, the registers it starts with (those that the sums'
 // warps take are the ones that the others give up), and how many units (CTAs, or pairs) run at once.
-template <int CG, int PARTS, bool WHOLE>
+template <int CG, int PARTS, bool WHOLE, bool DEEP>
 int setup_e4m3(int* out) {
     static std::mutex mu;
     static int units[kMaxDevices] = {};
@@ -542,7 +547,7 @@ int setup_e4m3(int* out) {
     if (dev < 0 || dev >= kMaxDevices) return BIV_ERR_DEVICE;
     std::lock_guard<std::mutex> lock(mu);
     if (units[dev] == 0) {
-        auto kern = gemm_e4m3_kernel<CG, PARTS, WHOLE>;
+        auto kern = gemm_e4m3_kernel<CG, PARTS, WHOLE, DEEP>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return cuda_status(e);
         cudaFuncAttributes attrs;
@@ -571,12 +576,12 @@ int setup_e4m3(int* out) {
     return BIV_OK;
 }
 
-template <int CG, int PARTS, bool WHOLE = false>
+template <int CG, int PARTS, bool WHOLE = false, bool DEEP = false>
 int launch_e4m3(const void* A, const void* B, Gemm8Args g, cudaStream_t s) {
     int units = 0;
-    const int st = setup_e4m3<CG, PARTS, WHOLE>(&units);
+    const int st = setup_e4m3<CG, PARTS, WHOLE, DEEP>(&units);
     if (st != BIV_OK) return st;
-    using Q = Form<PARTS>;
+    using Q = Form<PARTS, DEEP>;
     g.xr = CG == 2 ? kLanes : std::min(kLanes, (g.M + 7) / 8 * 8);
     g.yr = g.BN / CG;
     g.idesc = idesc_e4m3_f32(CG * kLanes, g.BN);
@@ -594,15 +599,18 @@ int launch_e4m3(const void* A, const void* B, Gemm8Args g, cudaStream_t s) {
     }
     const size_t smem = 1024 + static_cast<size_t>(g.stages) * Q::kStage * per_kb + slack + kBarBytes + 2 * kPageFloats * 4;
     const unsigned grid = static_cast<unsigned>(std::min(g.tiles, units));
-    if (CG == 2) return launch_cluster_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE>, dim3(2 * grid), dim3(kThreads), smem, s, 2, ta, tb, g);
-    return launch_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE>, dim3(grid), dim3(kThreads), smem, s, ta, tb, g);
+    if (CG == 2) return launch_cluster_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE, DEEP>, dim3(2 * grid), dim3(kThreads), smem, s, 2, ta, tb, g);
+    return launch_pdl(gemm_e4m3_kernel<CG, PARTS, WHOLE, DEEP>, dim3(grid), dim3(kThreads), smem, s, ta, tb, g);
 }
 
 // The kernel for a tile width.
 int launch_single(const void* A, const void* B, const Gemm8Args& g, cudaStream_t s) {
     if (g.BN <= 32) return launch_e4m3<1, 1>(A, B, g, s);
     if (g.BN <= 64) return launch_e4m3<1, 2>(A, B, g, s);
-    if (g.BN <= 128) return launch_e4m3<1, 4>(A, B, g, s);
+    // four sets of one k-block hide an accumulator's way to the sums and back better, two of two cost fewer steps on it:
+    // 14336 x 4096 (two of two in brackets) 80 rows 16.6 us (15.5), 96: 16.7 (15.7), 128: 16.3 (17.8); 128 x 16384 x 14336
+    // 46.7 (55.2), 256 x 8192 x 4096 16.6 (18.1)
+    if (g.BN <= 128) return g.M <= 96 ? launch_e4m3<1, 4>(A, B, g, s) : launch_e4m3<1, 4, false, true>(A, B, g, s);
     if (g.BN <= 192) return launch_e4m3<1, 6>(A, B, g, s);
     return g.BN == 256 ? launch_e4m3<1, 8, true>(A, B, g, s) : launch_e4m3<1, 8>(A, B, g, s);
 }
