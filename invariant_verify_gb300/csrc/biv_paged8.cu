@@ -224,7 +224,7 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
 // halve the items' share, at the cost of a call that is one short row (which the clusters below
 // pay back).  Measured with (256, 512) keys a split: one row of 131071 keys 64.5, 54.5 us (4.9 TB/s;
 // 67.4, 61.7 before the copies, when the keys went straight to registers), 64 rows of some 1400 keys
-// 47.8, 41.8 us, 32 windows of five 68.8, 56.0 us, one row of 700 8.0, 9.9 us.  Two steps at once
+// 47.8, 41.8 us, 32 windows of five 68.8, 57.4 us, one row of 700 8.0, 9.9 us.  Two steps at once
 // (more independent work a warp, fewer warps) took 20 % longer.
 
 // D[16 x 8] (+)= A[16 x 16] B[16 x 8], fp16 with fp32 sums.
@@ -282,16 +282,16 @@ struct __align__(128) HeldSlot {
         const int line = key >> 1;
         return line * 128 + ((((key & 1) * 4 + c) ^ (2 * (line & 3))) << 4);
     }
-    BIV_DEV void copy(const uint8_t* kp, const uint8_t* vp, int lane, uint64_t policy) {
-        constexpr int kRow = HD / 16;              // pieces of a key
+    // Where a lane's first piece of a step goes (pieces lane, lane + 32, ... of the keys and of the values are its own).
+    static BIV_DEV int first(int lane) { return at(lane / (HD / 16), lane % (HD / 16)); }
+    BIV_DEV void copy(const uint8_t* kp, const uint8_t* vp, int first, uint64_t policy) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < kBytes / 512; ++e) {
-                const int i = lane + 32 * e;
-                asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(x ? v : k) + at(i / kRow, i % kRow)),
-                             "l"((x ? vp : kp) + 16 * i), "l"(policy)
-                             : "memory");
+                // four lines further: bit 2 of a line's number is bit 6 of the place (hd = 64: the pattern repeats)
+                const uint32_t to = smem_u32(x ? v : k) + (HD == 128 && (e & 1) ? first ^ 64 : first) + 512 * e;
+                asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"((x ? vp : kp) + 512 * e), "l"(policy) : "memory");
             }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
@@ -569,7 +569,7 @@ BIV_DEV void put_q(HeldQ<HD, T>& q, const uint4& x, int row, int piece, float sc
 }
 
 template <int HD, int T>
-struct __align__(16) HeldSmem {
+struct __align__(128) HeldSmem {
     HeldSlot<HD> slots[kClasses][kSlots];
     float o[kClasses][4][HD + 4];          // of half a tile; rows padded against bank conflicts
     HeldQ<HD, T> q;
@@ -590,6 +590,7 @@ BIV_DEV long long held_at(const PagedAttnParams& P, int page, int kvh, int key0)
 struct HeldSteps {
     int n;                             // steps of this class
     int page;
+    long long at;                      // of the step in its pool
     uint32_t bad;                      // bit i: the page id of step i is out of range
     float k_scale, v_scale;
 };
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
     extern __shared__ __align__(128) uint8_t smem_raw[];
     HeldSmem<HD, T>& sm = *reinterpret_cast<HeldSmem<HD, T>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
-    const int g8 = lane >> 2, c4 = lane & 3;
+    const int c4 = lane & 3;
     const Items I(P, sm.table, 8 * T);
     const uint64_t policy = policy_evict_first();
     pdl_wait();
@@ -624,13 +625,11 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
     auto scales_of = [&](const AttnItem& it, HeldSteps& st) {
         st.bad = bad_pages(P, st.page);
         if (lane < st.n) {
-            const long long at = held_at<HD>(P, st.page, it.kvh, it.split * kSplit + kStep * (cls + kClasses * lane)) / (kStep * HD);
+            st.at = held_at<HD>(P, st.page, it.kvh, it.split * kSplit + kStep * (cls + kClasses * lane));
+            const long long at = st.at / (kStep * HD);
             st.k_scale = __bfloat162float(hp.k_scales[at]);
             st.v_scale = __bfloat162float(hp.v_scales[at]);
         }
-    };
-    auto step_at = [&](const AttnItem& it, const HeldSteps& st, int i) {
-        return held_at<HD>(P, __shfl_sync(0xffffffffu, st.page, i), it.kvh, it.split * kSplit + kStep * (cls + kClasses * i));
     };
     constexpr int kPieces = 8 * T * (HD / 8), kMine = (kPieces + kHeldThreads - 1) / kHeldThreads;       // 16-byte pieces of a tile's queries
     auto queries_of = [&](const AttnItem& it, uint4 (&x)[kMine], int (&row_pos)[1]) {
@@ -664,12 +663,13 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
     HeldSteps steps, next_steps;
     // copies under way lie in slots [tail_slot, tail_slot + flying) mod kSlots, oldest first
     HeldSlot<HD>* const slots = sm.slots[cls];
+    const int first = HeldSlot<HD>::first(lane);
     int tail_slot = 0, flying = 0, asked = 0;          // asked: steps of the item whose copies were begun
-    auto ask = [&](const AttnItem& it, const HeldSteps& st, int i) {
-        const long long at = step_at(it, st, i);
+    auto ask = [&](const HeldSteps& st, int i) {
+        const long long at = __shfl_sync(0xffffffffu, st.at, i) + 16 * lane;
         int slot = tail_slot + flying;
         slot -= slot >= kSlots ? kSlots : 0;
-        slots[slot].copy(hp.k + at, hp.v + at, lane, policy);
+        slots[slot].copy(hp.k + at, hp.v + at, first, policy);
         ++flying;
     };
     {
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
         queries_of(cur, x, row_pos);
         scales_of(cur, steps);
         asked = min(steps.n, kSlots);
-        for (int i = 0; i < asked; ++i) ask(cur, steps, i);
+        for (int i = 0; i < asked; ++i) ask(steps, i);
         put_queries(x, row_pos, 0);
     }
     for (int buf = 0;; buf ^= 1) {
@@ -723,11 +723,11 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
         // the next step's copies, of this item or of the next
         auto ask_ahead = [&]() {
             if (asked < steps.n) {
-                ask(cur, steps, asked++);
+                ask(steps, asked++);
             } else if (more) {
                 if (!looked_up) scales_of(nxt, next_steps);
                 looked_up = true;
-                if (next_asked < next_steps.n) ask(nxt, next_steps, next_asked++);
+                if (next_asked < next_steps.n) ask(next_steps, next_asked++);
             }
         };
 #pragma unroll 1
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kHeldThreads, 3) paged_attn_held_small_kernel(
     extern __shared__ __align__(128) uint8_t smem_raw[];
     HeldSmallSmem<HD>& sm = *reinterpret_cast<HeldSmallSmem<HD>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, cls = tid >> 5;
-    const int g8 = lane >> 2, c4 = lane & 3;
+    const int c4 = lane & 3;
     const int split = static_cast<int>(cluster_ctarank()), key_lo = split * kSplit;
     const int tiles = (P.rpg * P.G + 7) / 8, p = blockIdx.x / C / tiles, tile = blockIdx.x / C - p * tiles;
     const int grp = p / P.Hkv, kvh = p - grp * P.Hkv;
@@ -829,9 +829,10 @@ __global__ void __launch_bounds__(kHeldThreads, 3) paged_attn_held_small_kernel(
     pdl_wait();
     pdl_trigger();
     HeldSlot<HD>* const slots = sm.slots[cls];
+    const int first = HeldSlot<HD>::first(lane);
     auto ask = [&](int i) {
-        const long long at = held_at<HD>(P, __shfl_sync(0xffffffffu, steps.page, i), kvh, key_lo + kStep * (cls + kClasses * i));
-        slots[i % kSlots].copy(hp.k + at, hp.v + at, lane, policy);
+        const long long at = held_at<HD>(P, __shfl_sync(0xffffffffu, steps.page, i), kvh, key_lo + kStep * (cls + kClasses * i)) + 16 * lane;
+        slots[i % kSlots].copy(hp.k + at, hp.v + at, first, policy);
     };
     int asked = min(steps.n, kSlots);
     for (int i = 0; i < asked; ++i) ask(i);
