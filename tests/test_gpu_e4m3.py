@@ -105,6 +105,22 @@ def test_gemm(M, N, K, out):
     no_error()
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 12000, 400), (97, 12000, 400), (128, 19200, 640), (128, 12000, 128), (256, 8192, 272), (300, 12904, 528), (128, 24000, 272)])
+def test_gemm_of_middle_widths(M, N, K):
+    """Tiles of 65 to 192 columns, on both sides of the row count that chooses their form; two of them to a CTA; odd numbers of k-blocks."""
+    A, Bm, bias, res = matrices(M, N, K, 9)
+    C = product(A, Bm, torch.float32, bias=bias.cuda(), residual=res.cuda()).cpu().double()
+    want, size = E.gemm(A[0], A[2], Bm[0], Bm[2])
+    y = want + bias.double() + res.double()
+    tol = E.gemm_tolerance(size, K) + (want.abs() + 2 * (want + bias.double()).abs() + 2 * y.abs()) * E.F32_STEP
+    bad = ~((C - y).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), ((C - y).abs() / tol).max())
+    rows = slice(3, 40)                                     # another form, the same bits
+    few = product([x[rows] if x.shape[0] == M else x[:, rows] for x in A], Bm, torch.float32, bias=bias.cuda(), residual=res[rows].cuda())
+    assert same_bits(few.cpu().double(), C[rows])
+    no_error()
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 136, 272), (70, 264, 384), (200, 264, 400)])
 @pytest.mark.parametrize("act", list(B.ACTS))
 def test_gemm_tail(M, N, K, act):
