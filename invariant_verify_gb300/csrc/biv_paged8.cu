@@ -595,6 +595,15 @@ struct HeldSteps {
     float k_scale, v_scale;
 };
 
+// The scales of a lane's step at element `at` of the pools.  Those of a page out of range stay 0: page 0's, read in its
+// place, may be NaN, which times the zeros of the rows that do not reach the page would be NaN too.
+template <int HD>
+BIV_DEV void scales_at(const HeldPools& hp, HeldSteps& st, int lane, long long at) {
+    if ((st.bad >> lane) & 1u) return;
+    st.k_scale = __bfloat162float(hp.k_scales[at / (kStep * HD)]);
+    st.v_scale = __bfloat162float(hp.v_scales[at / (kStep * HD)]);
+}
+
 // CTAs an SM: three of up to two tiles, two of more (the accumulators' registers: three of
 // three tiles spill, 32 windows of five 81 us for 57; two of one tile: 64 rows 48 us for 42).
 constexpr int held_ctas(int T) { return T <= 2 ? 3 : 2; }
@@ -624,11 +633,10 @@ __global__ void __launch_bounds__(kHeldThreads, held_ctas(T)) paged_attn_held_ke
     };
     auto scales_of = [&](const AttnItem& it, HeldSteps& st) {
         st.bad = bad_pages(P, st.page);
+        st.k_scale = st.v_scale = 0.0f;
         if (lane < st.n) {
             st.at = held_at<HD>(P, st.page, it.kvh, it.split * kSplit + kStep * (cls + kClasses * lane));
-            const long long at = st.at / (kStep * HD);
-            st.k_scale = __bfloat162float(hp.k_scales[at]);
-            st.v_scale = __bfloat162float(hp.v_scales[at]);
+            scales_at<HD>(hp, st, lane, st.at);
         }
     };
     constexpr int kPieces = 8 * T * (HD / 8), kMine = (kPieces + kHeldThreads - 1) / kHeldThreads;       // 16-byte pieces of a tile's queries
@@ -836,11 +844,8 @@ __global__ void __launch_bounds__(kHeldThreads, 3) paged_attn_held_small_kernel(
     };
     int asked = min(steps.n, kSlots);
     for (int i = 0; i < asked; ++i) ask(i);
-    if (lane < steps.n) {
-        const long long at = held_at<HD>(P, steps.page, kvh, lane_key) / (kStep * HD);
-        steps.k_scale = __bfloat162float(hp.k_scales[at]);
-        steps.v_scale = __bfloat162float(hp.v_scales[at]);
-    }
+    steps.k_scale = steps.v_scale = 0.0f;
+    if (lane < steps.n) scales_at<HD>(hp, steps, lane, held_at<HD>(P, steps.page, kvh, lane_key));
     if (tid < HD) {                                // 8 rows of HD / 8 pieces; rows past the group's read its first row and are never used
         const int row = tid / (HD / 8), d = tid % (HD / 8), i = row < rows ? r0 + row : 0;
         const uint4 x = *reinterpret_cast<const uint4*>(P.q + (static_cast<long long>(w0 + i / P.G) * P.Hq + kvh * P.G + i % P.G) * HD + d * 8);
