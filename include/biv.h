@@ -583,9 +583,10 @@ int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B, const flo
  * [16 floor(p / 16), p) before a group's first position p must be among the
  * last `tail` that were written to the slot (or p % 16 == 0): so a request may
  * go back by up to tail - 15 positions, or to any multiple of 16.  A row whose
- * position does not follow the one before, or whose slot is not its group's,
- * raises BIV_DEVERR_GROUP and is not written, nor is its block; the page
- * table is read, and has to name a page, only where a block is filled.
+ * position does not follow the one before, whose group's first row has none, or
+ * whose slot is not its group's, raises BIV_DEVERR_GROUP and is not written, nor
+ * is its block; the page table is read, and has to name a page, only where a
+ * block is filled.
  * Requires tail % 16 == 0, tail >= K + 15, hd == 64 or 128 (else
  * BIV_ERR_UNSUPPORTED), Hq % Hkv == 0, 32-B aligned pools, 16-B aligned qkv,
  * q_out and rings, and what biv_rope_kv_write_paged requires of the rest.   */

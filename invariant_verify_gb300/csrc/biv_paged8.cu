@@ -84,7 +84,7 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
             if (pos != -1 && (!rows_keep || j < rows_keep[r])) {
                 unsigned int bits = 0;
                 if (pos < 0 || pos >= cap || slot < 0 || slot >= pt.n_slots) bits = BIV_DEVERR_INDEX;
-                else if (row_slot[w] != slot || pos - j != p0 || (j > 0 && row_pos[w - 1] != pos - 1)) bits = BIV_DEVERR_GROUP;
+                else if (p0 < 0 || row_slot[w] != slot || pos - j != p0 || (j > 0 && row_pos[w - 1] != pos - 1)) bits = BIV_DEVERR_GROUP;
                 if (bits) atomicOr(&g_paged_err, bits);
                 ok = bits == 0;
             }
