@@ -8,7 +8,7 @@ namespace biv {
 namespace {
 
 constexpr float kE4M3Max = 448.0f;
-constexpr float kLeastScale = 7.888609052210118e-31f;      // 2^-100: its inverse and products of two stay in fp32's range
+constexpr float kLeastScale = 7.888609052210118e-31f;      // 2^-100: its inverse is in fp32's range
 
 // Two numbers, rounded to nearest even; what passes 448 is held as 448, a NaN as NaN.
 BIV_DEV uint32_t pack_e4m3x2(float lo, float hi) {

@@ -31,8 +31,10 @@
 // CG = 1: a CTA per tile of 128 rows.  CG = 2: a pair per tile of 256 (cta_group::2): each CTA copies its
 // 128 rows of A and half of the BN rows of B, the even one issues the MMAs.
 #include <algorithm>
+#include <type_traits>
 
 #include "biv_act.cuh"
+#include "biv_e4m3.cuh"
 
 namespace biv {
 namespace {
@@ -52,6 +54,8 @@ static_assert(128 * kRegsFew + kEpilogue * kRegsMany <= kThreads * kRegsStart, "
 constexpr int kBarBytes = 512;
 constexpr int kPageBlocks = 16;               // k-blocks whose scales are copied at once
 constexpr int kPageFloats = kPageBlocks * (kLanes + 4);
+// A scale that, times the quantiser's least, is a normal number: 2^-26.
+constexpr float kMuchLarger = 1.4901161193847656e-08f;
 constexpr int kSlack = kLanes * kBK;          // an MMA may read 128 rows past the last stage
 constexpr int kMaxSmem = 227 * 1024 - 1024;
 constexpr int kRing = kMaxSmem - 1024 - kBarBytes - 2 * kPageFloats * 4;
@@ -158,6 +162,38 @@ BIV_DEV float ld_shared(uint32_t at) {
 BIV_DEV void copy_4(float* dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
+
+// What a block's sums are multiplied by: scale * lift is the product a * b of its two scales.  lift is 1, and scale
+// a * b itself, where that is a normal number; a product below them (down to 2^-200) loses bits, one above is infinite
+// (and times a sum of zero NaN), though the sums, of 2^-18 to 2^25, may bring the result back.  There lift is a power of
+// two, by which a sum is multiplied first: 2^-80 exactly, and 2^112 exactly or, if that is infinite, the result is too.
+struct BlockScale {
+    float scale, lift;
+    BIV_DEV BlockScale(float a, float b) : scale(a * b), lift(1.0f) {
+        const uint32_t bits = __float_as_uint(scale) << 1;
+        if (bits - 0x01000000u >= 0xfe000000u) {
+            const bool small = fabsf(scale) < 1.0f;
+            lift = small ? 8.271806125530277e-25f : 5.192296858534828e+33f;                    // 2^-80, 2^112
+            const float part = small ? 1.099511627776e+12f : 1.3877787807814457e-17f;          // 2^40, 2^-56
+            scale = (a * part) * (b * part);
+            // both the quantiser's least: sums times 2^-200 are less than half of the smallest number, and their sign is
+            // not to turn a sum of 0 to -0 on such a page and not on another
+            if (small && fabsf(scale) < 1.504632769052528e-36f) scale = 0.0f;                  // 2^-119
+        }
+    }
+};
+
+// The smallest and the largest of the scales above `skip`, which lie in the order of their bits; zeros (rows and columns
+// that there are none of) aside, and what is below zero, or not finite, counts as too large.
+struct ScaleRange {
+    uint32_t skip;                           // its bits
+    uint32_t over = 0xffffffffu, hi = 0u;    // by how much the smallest lies over skip, less one; the largest
+    BIV_DEV void add(float x) {
+        over = min(over, __float_as_uint(x) - skip - 1u);
+        hi = max(hi, __float_as_uint(x));
+    }
+    BIV_DEV bool within(float least) const { return over >= __float_as_uint(least) - skip - 1u && hi < __float_as_uint(9.223372036854775808e18f); }      // 2^63
+};
 
 // Eight words to memory, 32-byte aligned: a thread has a row, so that a warp's store meets 32 lines whatever its
 // width (16 bytes: 320 x 128256 x 4096 267 us, 234 so; through shared memory to 64 bytes a row 247).
@@ -432,68 +468,130 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_e4m3_kernel(const __grid_con
                 for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
             // the warp's columns lie in two 128-column blocks of weights at most: the first one, and its parts
             const int blk = (n0 + cb) / 128 - n0 / 128, turn = (128 - (n0 + cb) % 128) / 16;         // the first one, and its parts
-            for (int s = 0; s < sets; ++s) {
-                const int in_page = s % kPageSets, nkb = min(NB, g.KB - s * NB);
-                if (in_page == 0) {
-                    asm volatile("cp.async.wait_group 0;" ::: "memory");
-                    if (!(ok = Q::all_say(ok))) break;                    // this page has landed, and the one before it is read
-                    const int page = s / kPageSets + 1;
-                    buf ^= 1;
-                    if (page < pages)
-                        fetch(t, page, s_page[buf]);
-                    else if (t + n_units < g.tiles)
-                        fetch(t + n_units, 0, s_page[buf]);
+            auto set_read = [&](int set) {    // the MMAs may have it again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_remote(freed + 8u * set);
+                    else
+                        mbar_arrive(&tempty[set]);
                 }
-                const int second = Q::kStageSets == 2 ? s & 1 : 0, set = second ? next[1] : next[0];
-                if (reads) {
-                    const uint32_t row_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + in_page * NB * kLanes + q * 32 + lane) * 4u;
-                    const uint32_t col_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + kPageBlocks * kLanes + in_page * NB * 4 + blk) * 4u;
-                    ok = !*abort_flag;
-                    warp_wait(tfull0 + 8u * set, (phases >> set) & 1u, abort_flag);
-                    tc_fence_after();
-                    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * Q::kSetCols + cb);
+            };
+            // The sets [s0, s1) of a page.  lifted: products of its scales lie outside the normal numbers; then the sums go
+            // through memory, so that the other loop has the registers as if it were alone (1023 x 14336 x 4096: 59.6 us; one
+            // loop with a branch in it 67.2, two that share the sums' registers 61.7, without the check 58.9; 625
+            // with far scales everywhere).
+            auto page_sets = [&](auto lifted, int s0, int s1) {
+#pragma unroll 1
+                for (int s = s0; s < s1; ++s) {
+                    const int in_page = s - s0, nkb = min(NB, g.KB - s * NB);
+                    const int second = Q::kStageSets == 2 ? s & 1 : 0, set = second ? next[1] : next[0];
+                    if (reads) {
+                        const uint32_t row_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + in_page * NB * kLanes + q * 32 + lane) * 4u;
+                        const uint32_t col_scale = pages0 + static_cast<uint32_t>((buf ^ 1) * kPageFloats + kPageBlocks * kLanes + in_page * NB * 4 + blk) * 4u;
+                        ok = !*abort_flag;
+                        warp_wait(tfull0 + 8u * set, (phases >> set) & 1u, abort_flag);
+                        tc_fence_after();
+                        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * Q::kSetCols + cb);
+                        if constexpr (lifted) {
+                            float4 sums[4 * PARTS];
 #pragma unroll
-                    for (int kl = 0; kl < NB; ++kl)
-                        if (kl < nkb) {
-                            const float mine = ld_shared(row_scale + kl * kLanes * 4u);
-                            const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = WHOLE ? x0 : mine * ld_shared(col_scale + kl * 16u + 4u);
-#pragma unroll
-                            for (int i = 0; i < PARTS; i += 2) {
-                                const uint32_t at = taddr + static_cast<uint32_t>(kl * g.BN + 16 * i);
-                                uint32_t r[32];
-                                if (i + 1 < PARTS) {
-                                    tmem_ld32_sync(at, r);
-                                } else {
-                                    uint32_t h[16];
-                                    tmem_ld16_sync(at, h);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) r[e] = h[e];
-                                }
-                                if (i + 2 >= PARTS && (NB == 1 || kl + 1 == nkb)) {         // the set has been read
-                                    tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) {
-                                        if constexpr (CG == 2)
-                                            mbar_arrive_remote(freed + 8u * set);
-                                        else
-                                            mbar_arrive(&tempty[set]);
-                                    }
-                                }
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    if (i + h < PARTS) {
-                                        const float x = WHOLE || i + h < turn ? x0 : x1;
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e)
-                                            acc[i + h < PARTS ? i + h : 0][e] = fmaf(__uint_as_float(r[16 * h + e]), x, acc[i + h < PARTS ? i + h : 0][e]);
-                                    }
+                            for (int i = 0; i < 4 * PARTS; ++i) {
+                                const float* x = &acc[i / 4][i % 4 * 4];
+                                sums[i] = make_float4(x[0], x[1], x[2], x[3]);
                             }
+#pragma unroll 1
+                            for (int kl = 0; kl < nkb; ++kl) {
+                                const float mine = ld_shared(row_scale + kl * kLanes * 4u);
+                                const BlockScale x0(mine, ld_shared(col_scale + kl * 16u)), x1(mine, ld_shared(col_scale + kl * 16u + (WHOLE ? 0u : 4u)));
+#pragma unroll 1
+                                for (int i = 0; i < PARTS; ++i) {
+                                    uint32_t r[16];
+                                    tmem_ld16_sync(taddr + static_cast<uint32_t>(kl * g.BN + 16 * i), r);
+                                    const float x = i < turn ? x0.scale : x1.scale, lift = i < turn ? x0.lift : x1.lift;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        float4& y = sums[4 * i + e];
+                                        y.x = fmaf(__uint_as_float(r[4 * e]) * lift, x, y.x);
+                                        y.y = fmaf(__uint_as_float(r[4 * e + 1]) * lift, x, y.y);
+                                        y.z = fmaf(__uint_as_float(r[4 * e + 2]) * lift, x, y.z);
+                                        y.w = fmaf(__uint_as_float(r[4 * e + 3]) * lift, x, y.w);
+                                    }
+                                }
+                            }
+                            set_read(set);
+#pragma unroll
+                            for (int i = 0; i < 4 * PARTS; ++i) {
+                                float* x = &acc[i / 4][i % 4 * 4];
+                                x[0] = sums[i].x, x[1] = sums[i].y, x[2] = sums[i].z, x[3] = sums[i].w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int kl = 0; kl < NB; ++kl)
+                                if (kl < nkb) {
+                                    const float mine = ld_shared(row_scale + kl * kLanes * 4u);
+                                    const float x0 = mine * ld_shared(col_scale + kl * 16u), x1 = WHOLE ? x0 : mine * ld_shared(col_scale + kl * 16u + 4u);
+#pragma unroll
+                                    for (int i = 0; i < PARTS; i += 2) {
+                                        const uint32_t at = taddr + static_cast<uint32_t>(kl * g.BN + 16 * i);
+                                        uint32_t r[32];
+                                        if (i + 1 < PARTS) {
+                                            tmem_ld32_sync(at, r);
+                                        } else {
+                                            uint32_t h[16];
+                                            tmem_ld16_sync(at, h);
+#pragma unroll
+                                            for (int e = 0; e < 16; ++e) r[e] = h[e];
+                                        }
+                                        if (i + 2 >= PARTS && (NB == 1 || kl + 1 == nkb)) set_read(set);
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h)
+                                            if (i + h < PARTS) {
+                                                const float x = WHOLE || i + h < turn ? x0 : x1;
+#pragma unroll
+                                                for (int e = 0; e < 16; ++e)
+                                                    acc[i + h < PARTS ? i + h : 0][e] = fmaf(__uint_as_float(r[16 * h + e]), x, acc[i + h < PARTS ? i + h : 0][e]);
+                                            }
+                                    }
+                                }
                         }
+                    }
+                    phases ^= 1u << set;
+                    const int after = (set + Q::kStageSets) & (Q::kSets - 1);
+                    if (second) next[1] = after;
+                    else next[0] = after;
                 }
-                phases ^= 1u << set;
-                const int after = (set + Q::kStageSets) & (Q::kSets - 1);
-                if (second) next[1] = after;
-                else next[0] = after;
+            };
+            for (int s = 0; s < sets; s += kPageSets) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                // The vote: this page has landed, and the one before it is read.  And its products of scales are normal, as those of
+                // most pages are: the scales of rows are the quantiser's least (rows of zeros have it) or above, and those of
+                // weights are not small.  (Or the other way round; or the least of both meet, whose product makes nothing, and
+                // the others are not small: blocks of zeros among the weights.)
+                const float* landed = s_page[buf];            // this thread's own copies
+                auto ranges = [&](float skip, auto&& fits) {
+                    ScaleRange ra{__float_as_uint(skip)}, rb = ra;
+#pragma unroll
+                    for (int i = 0; i < kPageBlocks / 2; ++i) ra.add(landed[i * kEpilogue + tid]);
+                    if (tid < 4 * kPageBlocks) rb.add(landed[kPageBlocks * kLanes + tid]);
+                    return fits(ra, rb);
+                };
+                bool plain = Q::all_say(ok && ranges(0.0f, [](auto& ra, auto& rb) { return ra.within(kLeastScale) && rb.within(kMuchLarger); }));
+                if (!plain) {
+                    const bool least = ok && ranges(0.0f, [](auto& ra, auto& rb) { return ra.within(kLeastScale) && rb.within(kLeastScale); });
+                    plain = Q::all_say(least && ranges(kLeastScale, [](auto& ra, auto& rb) { return ra.within(kMuchLarger) && rb.within(kMuchLarger); })) ||
+                            Q::all_say(least && ranges(0.0f, [](auto& ra, auto&) { return ra.within(kMuchLarger); }));
+                    if (!plain && !(ok = Q::all_say(ok))) break;
+                }
+                const int page = s / kPageSets + 1;
+                buf ^= 1;
+                if (page < pages)
+                    fetch(t, page, s_page[buf]);
+                else if (t + n_units < g.tiles)
+                    fetch(t + n_units, 0, s_page[buf]);
+                if (plain) page_sets(std::false_type{}, s, min(s + kPageSets, sets));
+                else page_sets(std::true_type{}, s, min(s + kPageSets, sets));
             }
             if (!ok || !reads) continue;      // to the vote, or to the end
             const int row = (t % g.m_tiles) * (kLanes * CG) + rank * kLanes + q * 32 + lane;
