@@ -554,15 +554,16 @@ int biv_quant_e4m3(const void* x, long long ld_x, int rows, int K, int block_row
  * over blocks b of 128 terms.  A block's products are summed by the tensor core,
  * the blocks in fp32 in increasing order, whatever M, N and the tiles: a row's
  * bits do not depend on M.  One rounding to C's type (bf16 or fp32, out_dtype).
- * Scales may be of any size from 2^-100 on: where sa sb is no normal fp32 number the
- * sums are scaled exactly, at a cost (at most ten times a call's time).
+ * Scales may be of any size from 2^-100 to 2^119, as biv_quant_e4m3 gives them: where
+ * sa sb is no normal fp32 number the sums are scaled exactly, at a cost (at most ten
+ * times a call's time).
  * A: e4m3 [M, K] with a_scales fp32 [ceil(K/128), M]; B: e4m3 [N, K] with
  * b_scales fp32 [ceil(N/128), ceil(K/128)] (biv_quant_e4m3's layouts); bias: bf16
  * [N] or NULL; residual: bf16 [M, N] or NULL; act: a biv_act.  C may be the
  * residual itself when it is bf16; it must not overlap an input in any other way.
  * B and b_scales are weights in the sense of the conventions above.
- * Requires N % 8 == 0, K % 16 == 0, 16-B aligned pointers; errors as
- * biv_gemm_bias_act.                                                        */
+ * Requires N % 8 == 0, K % 16 == 0, M, N and K of at most 2^31 - 256, 16-B aligned
+ * pointers; errors as biv_gemm_bias_act.                                    */
 int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B, const float* b_scales, const void* bias,
                   const void* residual, void* C, int out_dtype, int act, int M, int N, int K, biv_stream_t stream);
 

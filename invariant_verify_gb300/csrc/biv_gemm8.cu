@@ -722,6 +722,9 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
                              const void* residual, void* C, int out_dtype, int act, int M, int N, int K, biv_stream_t stream) {
     BIV_TRACE_CALL();
     if (M < 0 || N <= 0 || K <= 0 || N % 8 != 0 || K % 16 != 0) return BIV_ERR_SHAPE;
+    // rows, columns and terms are rounded up to whole tiles and stages in 32 bits
+    constexpr int kMost = 0x7fffffff - 255;
+    if (M > kMost || N > kMost || K > kMost) return BIV_ERR_SHAPE;
     if ((out_dtype != BIV_BF16 && out_dtype != BIV_F32) || act < BIV_ACT_NONE || act > BIV_ACT_SILU) return BIV_ERR_VALUE;
     if (M == 0) return BIV_OK;
     if (!A || !a_scales || !B || !b_scales || !C) return BIV_ERR_NULL;

@@ -102,7 +102,7 @@ extern "C" int biv_quant_e4m3(const void* x, long long ld_x, int rows, int K, in
     if (rows < 0 || K <= 0 || K % 16 != 0 || ld_x < K || ld_x % 8 != 0) return BIV_ERR_SHAPE;
     if (block_rows != 1 && block_rows != kGroup) return BIV_ERR_UNSUPPORTED;
     QuantArgs a = {};
-    a.groups = (K + kGroup - 1) / kGroup;
+    a.groups = (K - 1) / kGroup + 1;               // no sum that passes 31 bits
     const long long blocks = (static_cast<long long>(rows) + block_rows - 1) / block_rows * a.groups;
     if (blocks > (block_rows == 1 ? 0x7fffffffLL * (kRowThreads / 16) / 2 : 0x7fffffffLL)) return BIV_ERR_SHAPE;
     if (rows == 0) return BIV_OK;
