@@ -200,7 +200,7 @@ class PagedVerifier:
 
     def attend(self, l: int, group: int) -> None:
         """Layer l's K and V of the window into the cache, and its attention.  A cache in e4m3 takes
-        a slot's rows in one group: ``group`` rows from each multiple of it on, as far as they go evenly."""
+        a slot's rows in one group: ``group`` rows from each multiple of it on; rows behind the last whole group are not written."""
         c, p = self.cfg, self.pool
         at = (p.table, self.row_slot, self.row_pos)
         if p.tail is None:
@@ -214,13 +214,19 @@ class PagedVerifier:
 
     def forward(self, group: int | None = None) -> None:
         """Final normalised hidden state of every window row (``h``); the rows' K and V are in their pages.
-        ``group``: the rows of a window that are one request's, in their order (K + 1 unless given)."""
+        ``group``: the rows of a window that are one request's, in their order (K + 1 unless given); whole groups make up the window."""
+        if group is not None and (group < 1 or self.W % group):
+            raise ValueError(f"a window of {self.W} rows is not made up of groups of {group}")
+        self._forward(group or self.rows)
+
+    def _forward(self, group: int) -> None:
+        """``forward``, whose rows behind the last whole group have no position."""
         c, w = self.cfg, self.w
         W = self.W
         B.biv_embed_rmsnorm(w["embed"], self.tokens, w["l0.attn_norm"], self.x, self.h, c.eps)
         for l in range(c.layers):
             self.project(self.h, f"l{l}.wqkv", self.qkv, bias=w.get(f"l{l}.bqkv"))
-            self.attend(l, group or self.rows)
+            self.attend(l, group)
             self.project(self.o.view(W, -1), f"l{l}.wo", self.x, bias=w.get(f"l{l}.bo"), residual=self.x)
             B.biv_rmsnorm(self.x, w[f"l{l}.ffn_norm"], self.h, c.eps)
             if self.gu is None:
@@ -276,7 +282,7 @@ class PagedVerifier:
             tokens[:part.numel()] = part
             self.row_pos.copy_(pos)
             self.tokens.copy_(tokens)
-            self.forward(window)
+            self._forward(window)
 
 
 @torch.no_grad()
