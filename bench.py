@@ -214,11 +214,14 @@ def profile_traffic(name):
 
 
 def kernel_source_sha256():
-    """Hash of the sources the GEMM kernels (and the fused selection) are built from."""
+    """Hash of the sources the GEMM kernels (and the fused selection) are built from: the file and
+    every header of the library that it includes, in the order in which they are met."""
     csrc = os.path.join(ROOT, "invariant_verify_gb300", "csrc")
-    h = hashlib.sha256()
-    for name in ("biv_gemm.cu", "biv_gumbel.cuh", "biv_common.cuh"):
-        h.update(open(os.path.join(csrc, name), "rb").read())
+    h, files = hashlib.sha256(), ["biv_gemm.cu"]
+    for name in files:
+        text = open(os.path.join(csrc, name), "rb").read()
+        h.update(text)
+        files += [x for x in dict.fromkeys(re.findall(r'^#include "(\w+\.cuh)"', text.decode(), re.M)) if x not in files]
     return h.hexdigest()
 
 
