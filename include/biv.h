@@ -534,8 +534,9 @@ int biv_decode_attn_paged(const void* q, const void* k_pages, const void* v_page
  * significand, largest 448) with scales: half the bytes of a step, with the
  * same invariance.  A value is scale * e4m3; quantisation takes
  *   scale = max(max |x| / 448, 2^-100),  q = e4m3(x / scale)
- * (nearest, ties to even).  What is not finite is held as a NaN; in max |x| a
- * NaN counts as nothing and an infinity as the largest bf16 number.
+ * (both quotients rounded to fp32, q from there to nearest, ties to even).  What is
+ * not finite is held as a NaN; in max |x| a NaN counts as nothing and an infinity as
+ * the largest bf16 number.
  *
  * biv_quant_e4m3: q = e4m3 [rows, K] of x (bf16, rows ld_x elements apart).
  *   block_rows = 1 (activations): a scale for 128 values of a row (fewer at
