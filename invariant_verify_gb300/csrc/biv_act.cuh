@@ -80,8 +80,8 @@ struct BiasActRow {
         }
     }
     // Columns 8 h .. 8 h + 8 N - 1; v(e): accumulator of column e.  An activation's steps run side by side for all
-    // of them: 1023 x 14336 x 4096 in e4m3 with (relu, gelu, gelu_tanh, silu) 63.8, 84.9, 70.6, 69.1 us for N = 2,
-    // 72.2, 94.2, 77.7, 75.3 with one column after the other (62.0 without an activation).
+    // of them: 1023 x 14336 x 4096 in e4m3 with (relu, gelu, gelu_tanh, silu) 61.5, 84.1, 67.2, 66.7 us for N = 2,
+    // 63.9, 91.1, 71.6, 73.5 for N = 1 twice (59.8 without an activation).
     template <int N, typename V>
     BIV_DEV void values(int h, V&& v, const BiasActArgs& ba, float (&x)[N][8]) const {
         auto all = [&](auto f) {                   // f(value, half, column of it), all of them side by side

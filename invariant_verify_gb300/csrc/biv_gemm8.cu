@@ -14,11 +14,15 @@
 // columns.  (With the weights along the lanes M need not be a multiple of 128, but every column
 // has its own scale, from shared memory: 840 cycles a k-block instead of 590.)
 //
-// What it comes to: 1024 x 4096 x 14336 65 us (1.85 PFLOP/s, tensor pipe busy for 47 % of an active SM's time):
-// a k-block takes 1130 cycles, because an accumulator's way from the MMAs to the sums and back (some 1000
-// cycles) is hidden only by the other one; without the sums 49 us, without copies 62.  320 x 128256 x 4096
-// (fp32 C) 234 us: 48 KB a k-block and SM out of L2 (195 us with no stores, 197 with copies alone) and stores.
-// 64 x 4096 x 14336 20.9 us, 8 x 6144 x 4096 10.1: the chain of narrow MMAs, 340 cycles a k-block.
+// What it comes to, and what is left of it without the copies, without the MMAs, without the sums; copies alone, MMAs
+// alone, the hand-overs of stages and sets alone (us; these three without the stores):
+//   1024 x 4096 x 14336 (1.91 PFLOP/s)    62.9; 57.1, 55.4, 45.3; 32.6, 35.6, 25.1
+//   320 x 128256 x 4096, fp32 C          236.1; 215.5, 196.1, 200.5; 120.5, 103.5, 66.4
+//   64 x 4096 x 14336                     20.8; 18.8, 18.7, 18.4; 16.0, 16.2, 9.1
+//   8 x 6144 x 4096                        9.4; 7.6, 8.3, 8.0; 6.1, 6.1, 3.7
+// So no part alone bounds it.  Wide tiles: an accumulator's way from the MMAs to the sums and back is hidden only by the
+// other one.  The head: that, stages of 96 KB of which two fit, and the stores.  Few rows: a CTA's copies (56 boxes of some
+// 280 ns for 64 x 4096 x 14336) and its narrow MMAs take three quarters of the time each, on the same hand-overs.
 //
 // Kernel layout (384 threads, one CTA per SM, persistent over tiles):
 //   warp 0      TMA producer: boxes of NB k-blocks, 128-byte swizzle
@@ -81,8 +85,8 @@ template <int PARTS, bool DEEP>
 struct Form {
     static constexpr int kCols = 32 * PARTS;  // the widest BN
     // K-blocks of a set of accumulators; the sets are taken in turn.  Where a set is one k-block a stage holds two
-    // sets, since a box costs the TMA unit some 275 ns whatever its size (1024 x 4096 x 14336: 79 us with boxes
-    // of one k-block, 41 with no copies at all).
+    // sets, since a box costs the TMA unit some 280 ns whatever its size (1024 x 4096 x 14336: with boxes of one k-block
+    // 79 us where this took 65).
     static constexpr int kBlocks = kCols <= 64 ? 4 : kCols <= 128 && !DEEP ? 2 : 1;
     static constexpr int kStageSets = kBlocks == 1 ? 2 : 1, kStage = kBlocks * kStageSets;
     static constexpr int kSets = kCols <= 32 || DEEP ? 4 : 2;
@@ -196,7 +200,7 @@ struct ScaleRange {
 };
 
 // Eight words to memory, 32-byte aligned: a thread has a row, so that a warp's store meets 32 lines whatever its
-// width (16 bytes: 320 x 128256 x 4096 267 us, 234 so; through shared memory to 64 bytes a row 247).
+// width (16 bytes: 320 x 128256 x 4096 271 us, 237 so; through shared memory to 64 bytes a row 247 where this took 234).
 BIV_DEV void st_global_32(void* p, const uint32_t (&x)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
                  "r"(x[6]), "r"(x[7])
@@ -706,8 +710,9 @@ int launch_single(const void* A, const void* B, const Gemm8Args& g, cudaStream_t
     if (g.BN <= 32) return launch_e4m3<1, 1>(A, B, g, s);
     if (g.BN <= 64) return launch_e4m3<1, 2>(A, B, g, s);
     // four sets of one k-block hide an accumulator's way to the sums and back better, two of two cost fewer steps on it:
-    // 14336 x 4096 (two of two in brackets) 80 rows 16.6 us (15.5), 96: 16.7 (15.7), 128: 16.3 (17.8); 128 x 16384 x 14336
-    // 46.7 (55.2), 256 x 8192 x 4096 16.6 (18.1)
+    // 14336 x 4096 (two of two in brackets) 8 rows 15.5 us (14.6), 80: 15.3 (15.3), 96: 15.4 (15.5), 128: 15.6 (17.4);
+    // 256 x 8192 x 4096 15.8 (17.9); 16384 x 14336 8 rows 43.9 (43.3), 80: 44.9 (44.5), 128: 46.2 (56.2), but also 96:
+    // 45.2 (55.5), and 80 x 19200 x 4096 17.0 (19.3): between 65 and 96 rows it goes by N as well
     if (g.BN <= 128) return g.M <= 96 ? launch_e4m3<1, 4>(A, B, g, s) : launch_e4m3<1, 4, false, true>(A, B, g, s);
     if (g.BN <= 192) return launch_e4m3<1, 6>(A, B, g, s);
     return g.BN == 256 ? launch_e4m3<1, 8, true>(A, B, g, s) : launch_e4m3<1, 8>(A, B, g, s);
@@ -753,9 +758,10 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
         g.BN = static_cast<int>(bn);
         return launch_single(A, B, g, s);
     }
-    // several waves, or several row tiles: the width that fills whole waves, rather a wide one.  (64, 128, 192, 256)
-    // columns, us: 320 x 14336 x 4096 47.9, 49.0, 43.3, 48.9 (160, which is taken: 40.7); 256 x 8192 x 4096 21.5,
-    // 18.7, 22.5, 23.6; 160 x 4096 x 4096 12.2, 17.8, 21.1, 22.8; 128 x 128256 x 4096 152, 135, 129, 128
+    // several waves, or several row tiles: the width that fills whole waves, rather a wide one.  (64, 128, 160, 192, 256)
+    // columns, us, and which is taken: 320 x 14336 x 4096 44.7, 40.6, 36.4, 38.5, 44.9 (160); 256 x 8192 x 4096 20.2, 15.7,
+    // 19.8, 21.1, 23.3 (128); 160 x 4096 x 4096 11.5, 14.9, 19.3, 20.4, 22.6 (64); 513 x 14336 x 4096 69.2, 53.4, 52.7, 55.3,
+    // 44.8 (256); 128 x 128256 x 4096 128, 100, 113, 104, 105 (256)
     double least = 1e30;
     for (int w : {64, 128, 160, 192, 256}) {
         const double cost = static_cast<double>(ceil_div(m_tiles * ceil_div(N, w), sms)) * (w + 96);
@@ -764,8 +770,8 @@ extern "C" int biv_gemm_e4m3(const void* A, const float* a_scales, const void* B
             g.BN = w;
         }
     }
-    // Pairs take B out of L2 once for 256 rows, where that pads M no further (measured with 16-byte stores): 1023 x
-    // 14336 x 4096: 68.7 us (single CTAs: 72.2), 1024 x 4096 x 14336: 67.2 (71.7); but 320 x 128256 x 4096, with
-    // 512 rows for 384: 360 (267).
+    // Pairs take B out of L2 once for 256 rows, where that pads M no further: 1023 x 14336 x 4096 59.8 us (single CTAs:
+    // 67.0), 1024 x 4096 x 14336 63.0 (71.5); but 320 x 128256 x 4096, with 512 rows for 384: 294 (237), and 513 x 14336 x
+    // 4096 56.8 (44.8).
     return g.BN == 256 && m_tiles % 2 == 0 ? launch_e4m3<2, 8, true>(A, B, g, s) : launch_single(A, B, g, s);
 }

@@ -102,7 +102,9 @@ class PagedVerifier:
 
     ``held`` names the weights that are kept in e4m3 with a scale for 128 x 128 values
     (of ``HELD``; "lm_head" among them): their products take the rows in e4m3 as well.  A
-    pool with a tail needs tail >= K + 16, and is prefilled by up to tail - 15 tokens at a time.
+    pool with a tail needs tail >= K + 16, and is prefilled by up to tail - 15 tokens at a time:
+    for whole windows of prompt it needs N (K + 1) + 16 (2047 tokens through two 8B-shaped layers by windows of
+    320 rows: 4.0 ms; by the 17 rows that tail = 32 leaves: 56 ms).
     """
 
     HELD = ("wqkv", "wo", "wgu", "wdown", "lm_head")
