@@ -556,8 +556,8 @@ int biv_quant_e4m3(const void* x, long long ld_x, int rows, int K, int block_row
  * the blocks in fp32 in increasing order, whatever M, N and the tiles: a row's
  * bits do not depend on M.  One rounding to C's type (bf16 or fp32, out_dtype).
  * Scales may be of any size from 2^-100 to 2^119, as biv_quant_e4m3 gives them: where
- * sa sb is no normal fp32 number the sums are scaled exactly, at a cost (at most ten
- * times a call's time).
+ * sa sb is no normal fp32 number the sums are scaled exactly, at a cost (some ten times
+ * the time of a large call all of whose scales are so).
  * A: e4m3 [M, K] with a_scales fp32 [ceil(K/128), M]; B: e4m3 [N, K] with
  * b_scales fp32 [ceil(N/128), ceil(K/128)] (biv_quant_e4m3's layouts); bias: bf16
  * [N] or NULL; residual: bf16 [M, N] or NULL; act: a biv_act.  C may be the
