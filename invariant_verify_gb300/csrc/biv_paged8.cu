@@ -67,13 +67,13 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
     if (j0 >= K) return;
     const int i0 = max(0, -j0), i1 = min(kHeldBlock, K - j0);                       // the block's rows of this call
     // A slot that two groups write: neither sees the other's rows when it fills a block.
+    const uint32_t cap = static_cast<uint32_t>(pt.max_pages) << pt.page_shift;      // below 2^31
     if (h == 0 && c == 0) {
-        auto writes = [&](long long g) { return row_pos[g * K] >= 0 && (!rows_keep || rows_keep[g] > 0); };
+        auto writes = [&](long long g) { return static_cast<uint32_t>(row_pos[g * K]) < cap && (!rows_keep || rows_keep[g] > 0); };
         bool twice = false;
         for (int g = tid; g < groups; g += kWriteThreads) twice |= g != r && row_slot[static_cast<long long>(g) * K] == slot && writes(g) && writes(r);
-        if (twice) atomicOr(&g_paged_err, BIV_DEVERR_GROUP);
+        if (twice && slot >= 0 && slot < pt.n_slots) atomicOr(&g_paged_err, BIV_DEVERR_GROUP);
     }
-    const long long cap = static_cast<long long>(pt.max_pages) << pt.page_shift;
     const int first = (p0 & ~(kHeldBlock - 1)) + kHeldBlock * c;                    // the block's first position
     if (tid < 32) {
         bool ok = false;
@@ -83,7 +83,7 @@ rope_kv_write_held_kernel(const __nv_bfloat16* __restrict__ qkv, __nv_bfloat16* 
             const int pos = row_pos[w];
             if (pos != -1 && (!rows_keep || j < rows_keep[r])) {
                 unsigned int bits = 0;
-                if (pos < 0 || pos >= cap || slot < 0 || slot >= pt.n_slots) bits = BIV_DEVERR_INDEX;
+                if (static_cast<uint32_t>(pos) >= cap || slot < 0 || slot >= pt.n_slots) bits = BIV_DEVERR_INDEX;
                 else if (p0 < 0 || row_slot[w] != slot || pos - j != p0 || (j > 0 && row_pos[w - 1] != pos - 1)) bits = BIV_DEVERR_GROUP;
                 if (bits) atomicOr(&g_paged_err, bits);
                 ok = bits == 0;
