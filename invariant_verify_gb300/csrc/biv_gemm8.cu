@@ -223,7 +223,7 @@ BIV_DEV void put_row(const float (&acc)[PARTS][16], int row, int col0, int cols,
             for (int e = 0; e < 16; ++e) x[e >> 3][e & 7] = acc[i][e];
         } else {
             const BiasActRow operands(true, row, col0 + 16 * i, g.N, g.ba);
-            operands.values(0, [&](int e) { return acc[i][e]; }, g.ba, x);
+            operands.values([&](int e) { return acc[i][e]; }, g.ba, x);
         }
         uint8_t* at = dst + 16 * i * (F32 ? 4 : 2);
         if constexpr (F32) {
